@@ -89,6 +89,15 @@ extern "C" {
 /* 16-bit element types of features and weights (the *_dtype entry points). */
 #define SUBMCONV_DTYPE_F16 0  /* IEEE binary16 */
 #define SUBMCONV_DTYPE_BF16 1 /* bfloat16 (the top 16 bits of a binary32) */
+/* layer norm only */
+#define SUBMCONV_DTYPE_F32 2 /* IEEE binary32 */
+
+/* Activations of the dense layers. */
+#define SUBMCONV_ACT_NONE 0
+#define SUBMCONV_ACT_RELU 1      /* max(z, 0) */
+#define SUBMCONV_ACT_SILU 2      /* z / (1 + exp(-z)) */
+#define SUBMCONV_ACT_GELU 3      /* z/2 (1 + erf(z / sqrt 2)) */
+#define SUBMCONV_ACT_GELU_TANH 4 /* z/2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) */
 
 /* Flags of submconv_weights_create. */
 #define SUBMCONV_PREP_INPUT_GRAD 1u /* prepare the flipped, transposed kernel of the input gradient */
@@ -507,6 +516,130 @@ int submconv_downsample_free(submconv_down_t plan);
  */
 int submconv_subdivide(const int32_t* coords, int64_t n, const uint16_t* feats, int32_t cdim,
                        int32_t* out_coords, uint16_t* out_feats, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Dense layers on site features: what a block of a sparse model runs on the
+ * rows between its convolutions (layer norm, point-wise linear layers, the
+ * gated feed-forward block), forward and backward.
+ *
+ * Activations (x, grad_out, residual) may be rows of a wider matrix: `ld` is
+ * the number of elements between rows, at least the number of columns (it is
+ * not read for a single row) and at most 2^22. Every other matrix is densely
+ * packed. Any width is taken; widths, strides and pointers in multiples of 16
+ * bytes are read in place, others through zero-padded copies in the
+ * workspace. n = 0 is allowed: outputs per row are then empty, gradients of
+ * parameters zeros. The matrix layers take fp16 or bf16 data and fp32
+ * biases, accumulate in fp32 and round each stored tensor once; weight
+ * gradients are rounded to the data's type, bias gradients are fp32 and sum
+ * unrounded terms. Nothing is summed by atomics: results are bitwise
+ * reproducible. All calls are asynchronous on `stream` and allocate nothing;
+ * a workspace (16-byte aligned, of the bytes its query gives) is scratch
+ * that the stream's order protects. The *_workspace_bytes queries run on the
+ * host; `aligned` nonzero asks for the case that every 16-bit pointer starts
+ * on 16 bytes and every row stride is a multiple of 8, zero for any.
+ * ---------------------------------------------------------------------- */
+
+/*
+ * submconv_layer_norm -- y = (x - m) r weight + bias over the cdim channels of
+ * each row, m the row's mean, r = 1 / sqrt(mean (x - m)^2 + eps).
+ * x [n,cdim] of `dtype` (SUBMCONV_DTYPE_F16, _BF16 or _F32), row stride ldx;
+ * y [n,cdim] of the same type. weight and bias [cdim] fp32, either NULL for 1
+ * and 0. mean and rstd [n] fp32 receive m and r, either may be NULL. cdim up
+ * to 8192. Statistics and arithmetic are fp32 (the variance about the mean).
+ */
+int submconv_layer_norm(const void* x, int64_t ldx, int64_t n, int32_t cdim, const float* weight,
+                        const float* bias, float eps, void* y, float* mean, float* rstd,
+                        int32_t dtype, hipStream_t stream);
+
+/* Workspace of submconv_layer_norm_backward (fp32 sums per workgroup);
+ * negative on a bad argument. */
+int64_t submconv_layer_norm_backward_workspace_bytes(int64_t n, int32_t cdim);
+
+/*
+ * submconv_layer_norm_backward -- with xh = (x - mean) rstd and d = grad_out
+ * weight: grad_x = rstd (d - mean(d) - xh mean(d xh)) per row (of `dtype`),
+ * grad_weight = sum over rows of grad_out xh, grad_bias = sum of grad_out
+ * (fp32 [cdim]). mean and rstd as the forward wrote them. Any of the three
+ * results may be NULL; without grad_weight and grad_bias no workspace is
+ * used.
+ */
+int submconv_layer_norm_backward(const void* grad_out, int64_t ldg, const void* x, int64_t ldx,
+                                 int64_t n, int32_t cdim, const float* mean, const float* rstd,
+                                 const float* weight, void* grad_x, float* grad_weight,
+                                 float* grad_bias, int32_t dtype, void* workspace,
+                                 int64_t workspace_bytes, hipStream_t stream);
+
+/* Workspace of submconv_linear (0 is possible); negative on a bad argument. */
+int64_t submconv_linear_workspace_bytes(int64_t n, int32_t cin, int32_t cout, int32_t aligned);
+
+/*
+ * submconv_linear -- out = act(z) + residual, z = x W + bias.
+ * x [n,cin] (row stride ldx), W [cin,cout], bias [cout] fp32 or NULL, residual
+ * [n,cout] (row stride ldr) or NULL, out [n,cout] dense, pre [n,cout] dense or
+ * NULL: z rounded to the data's type, for the backward pass. `act`
+ * SUBMCONV_ACT_*, `dtype` fp16 or bf16. Bias, activation and residual are
+ * applied in fp32 before the one rounding. out may be the residual itself.
+ */
+int submconv_linear(const uint16_t* x, int64_t ldx, int64_t n, const uint16_t* W, const float* bias,
+                    const uint16_t* residual, int64_t ldr, uint16_t* out, uint16_t* pre,
+                    int32_t cin, int32_t cout, int32_t act, int32_t dtype, void* workspace,
+                    int64_t workspace_bytes, hipStream_t stream);
+
+/* Workspace of submconv_linear_backward with every gradient asked for. */
+int64_t submconv_linear_backward_workspace_bytes(int64_t n, int32_t cin, int32_t cout, int32_t act,
+                                                 int32_t aligned);
+
+/*
+ * submconv_linear_backward -- dz = grad_out act'(pre); grad_x = dz W^T [n,cin]
+ * and grad_w = x^T dz [cin,cout] of the data's type, grad_b = sum over rows of
+ * dz (fp32 [cout]). Any of them may be NULL. pre [n,cout] as the forward wrote
+ * it (not read for SUBMCONV_ACT_NONE). The residual's gradient is grad_out.
+ * dz is rounded to the data's type before its two products.
+ */
+int submconv_linear_backward(const uint16_t* grad_out, int64_t ldg, int64_t n, const uint16_t* x,
+                             int64_t ldx, const uint16_t* W, const uint16_t* pre, uint16_t* grad_x,
+                             uint16_t* grad_w, float* grad_b, int32_t cin, int32_t cout,
+                             int32_t act, int32_t dtype, void* workspace, int64_t workspace_bytes,
+                             hipStream_t stream);
+
+/* Workspace of submconv_gated_ffn (the hidden rows h among it). */
+int64_t submconv_gated_ffn_workspace_bytes(int64_t n, int32_t cin, int32_t hidden, int32_t cout,
+                                           int32_t aligned);
+
+/*
+ * submconv_gated_ffn -- [g | u] = x W_in + b_in, h = act(g) u, out = h W_out +
+ * b_out + residual. W_in [cin,2*hidden]: the gate's columns, then the up
+ * projection's; b_in [2*hidden] fp32 or NULL; W_out [hidden,cout]; b_out [cout]
+ * fp32 or NULL; residual [n,cout] (row stride ldr) or NULL; out [n,cout];
+ * pre [n,2*hidden] or NULL: [g | u] rounded to the data's type, for the
+ * backward pass. h is rounded to the data's type between the two products.
+ */
+int submconv_gated_ffn(const uint16_t* x, int64_t ldx, int64_t n, const uint16_t* W_in,
+                       const float* b_in, const uint16_t* W_out, const float* b_out,
+                       const uint16_t* residual, int64_t ldr, uint16_t* out, uint16_t* pre,
+                       int32_t cin, int32_t hidden, int32_t cout, int32_t act, int32_t dtype,
+                       void* workspace, int64_t workspace_bytes, hipStream_t stream);
+
+/* Workspace of submconv_gated_ffn_backward with every gradient asked for. */
+int64_t submconv_gated_ffn_backward_workspace_bytes(int64_t n, int32_t cin, int32_t hidden,
+                                                    int32_t cout, int32_t aligned);
+
+/*
+ * submconv_gated_ffn_backward -- with dh = grad_out W_out^T, du = dh act(g),
+ * dg = dh u act'(g): grad_x = [dg | du] W_in^T [n,cin], grad_w_in = x^T [dg | du]
+ * [cin,2*hidden], grad_w_out = h^T grad_out [hidden,cout] of the data's type,
+ * grad_b_in = sums of [dg | du] (fp32 [2*hidden]), grad_b_out = sums of
+ * grad_out (fp32 [cout]). Any of them may be NULL. h is formed again from pre
+ * [n,2*hidden], as the forward wrote it. dg, du and h are rounded to the
+ * data's type before their products.
+ */
+int submconv_gated_ffn_backward(const uint16_t* grad_out, int64_t ldg, int64_t n, const uint16_t* x,
+                                int64_t ldx, const uint16_t* W_in, const uint16_t* W_out,
+                                const uint16_t* pre, uint16_t* grad_x, uint16_t* grad_w_in,
+                                float* grad_b_in, uint16_t* grad_w_out, float* grad_b_out,
+                                int32_t cin, int32_t hidden, int32_t cout, int32_t act,
+                                int32_t dtype, void* workspace, int64_t workspace_bytes,
+                                hipStream_t stream);
 
 /* Message for a status code (static string). */
 const char* submconv_status_string(int status);

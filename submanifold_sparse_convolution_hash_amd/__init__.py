@@ -27,7 +27,9 @@ __all__ = [
     "forward_kernel", "backward_input",
     "backward_weight", "backward_bias", "SubMConv3dFunction", "SubMConv3d", "library_path", "load_library",
     "abi_version", "release_scratch", "FLAG_MORTON", "downsample", "subdivide", "MaskedPlan", "masked_plan",
-    "forward_masked",
+    "forward_masked", "layer_norm", "layer_norm_backward", "linear", "linear_backward", "gated_ffn",
+    "gated_ffn_backward", "LayerNormFunction", "LinearFunction", "GatedFeedForwardFunction", "LayerNorm",
+    "Linear", "GatedFeedForward",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -99,6 +101,21 @@ def load_library():
         "submconv_forward": ([P, P, P, P, P, I32, I32, I32, P], ctypes.c_int),
         "submconv_forward_dtype": ([P, P, P, P, P, I32, I32, I32, I32, P], ctypes.c_int),
         "submconv_backward_input_dtype": ([P, P, P, P, I32, I32, I32, I32, P], ctypes.c_int),
+        "submconv_layer_norm": ([P, I64, I64, I32, P, P, ctypes.c_float, P, P, P, I32, P], ctypes.c_int),
+        "submconv_layer_norm_backward_workspace_bytes": ([I64, I32], I64),
+        "submconv_layer_norm_backward": ([P, I64, P, I64, I64, I32, P, P, P, P, P, P, I32, P, I64, P],
+                                         ctypes.c_int),
+        "submconv_linear_workspace_bytes": ([I64, I32, I32, I32], I64),
+        "submconv_linear": ([P, I64, I64, P, P, P, I64, P, P, I32, I32, I32, I32, P, I64, P], ctypes.c_int),
+        "submconv_linear_backward_workspace_bytes": ([I64, I32, I32, I32, I32], I64),
+        "submconv_linear_backward": ([P, I64, I64, P, I64, P, P, P, P, P, I32, I32, I32, I32, P, I64, P],
+                                     ctypes.c_int),
+        "submconv_gated_ffn_workspace_bytes": ([I64, I32, I32, I32, I32], I64),
+        "submconv_gated_ffn": ([P, I64, I64, P, P, P, P, P, I64, P, P, I32, I32, I32, I32, I32, P, I64, P],
+                               ctypes.c_int),
+        "submconv_gated_ffn_backward_workspace_bytes": ([I64, I32, I32, I32, I32], I64),
+        "submconv_gated_ffn_backward": ([P, I64, I64, P, I64, P, P, P, P, P, P, P, P, I32, I32, I32, I32, I32, P,
+                                         I64, P], ctypes.c_int),
         "submconv_status_string": ([ctypes.c_int], ctypes.c_char_p),
         "submconv_last_error": ([], ctypes.c_char_p),
         "submconv_abi_version": ([], ctypes.c_int),
@@ -632,3 +649,8 @@ class SubMConv3d(torch.nn.Module):
 
     def forward(self, kmap: KernelMap, feats: torch.Tensor) -> torch.Tensor:
         return forward(kmap, feats, bias=self.bias, prepared=self.prepared())
+
+
+from .dense import (  # noqa: E402  (dense.py uses this module's helpers)
+    GatedFeedForward, GatedFeedForwardFunction, LayerNorm, LayerNormFunction, Linear, LinearFunction, gated_ffn,
+    gated_ffn_backward, layer_norm, layer_norm_backward, linear, linear_backward)

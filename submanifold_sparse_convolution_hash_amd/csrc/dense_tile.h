@@ -1,0 +1,474 @@
+// Tiled 16-bit matrix products on MFMA for the dense layers (linear, gated
+// feed-forward): out[m][n] = sum_k A(m, k) B(k, n), fp32 accumulation.
+//
+// A workgroup of WM x WN waves owns a BM x BN tile of the output and walks k
+// in steps of 64. Each step's two operand tiles go straight from memory into
+// LDS (buffer_load ... lds, 16 bytes a lane), STAGES buffers in turn, so
+// that the loads of the coming steps are in flight while the waves multiply
+// the current one; buffer bounds give zeros past the last row and the last k.
+// An operand is read either with k contiguous in memory (x, and a weight
+// matrix under its transpose) by ds_read_b128, or with k as the row index (a
+// weight matrix as it is stored, both operands of a weight gradient) by
+// ds_read_b64_tr_b16, which transposes 4 x 16 pieces on the way out of LDS:
+// no operand is ever transposed in memory.
+//
+// v_mfma_f32_16x16x32 takes n as its row index and m as its column index, so
+// that a lane ends with 4 consecutive n of one m; v_permlane16_swap then pairs
+// two accumulators into 8 consecutive n, the 16 bytes of one store.
+#pragma once
+
+#include <type_traits>
+
+#include "lane_ops.h"
+#include "submconv_internal.h"
+
+namespace submconv {
+namespace {
+
+typedef _Float16 half8 __attribute__((ext_vector_type(8)));
+typedef _Float16 half4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef short v4s __attribute__((ext_vector_type(4)));
+typedef float float4v __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) void lds_void;
+typedef __attribute__((address_space(3))) v4s lds_v4s;
+
+constexpr int kStepK = 64;                  // k per LDS buffer
+constexpr uint32_t kOobOff = 0x80000000u;   // past every buffer's bound
+constexpr int64_t kMaxLd = int64_t{1} << 22;  // row strides: a tile's byte offsets fit 31 bits
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t tile_rsrc(const void* base, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), static_cast<short>(0),
+                                           static_cast<int>(bytes), 0x00020000);
+}
+
+// ---- 16-bit elements ----
+
+template <bool BF16>
+__device__ __forceinline__ float to_f32(uint16_t v) {
+  if constexpr (BF16) return __builtin_bit_cast(float, static_cast<uint32_t>(v) << 16);
+  else return static_cast<float>(__builtin_bit_cast(_Float16, v));
+}
+template <bool BF16>
+__device__ __forceinline__ uint16_t to_16(float v) {  // round to nearest even
+  if constexpr (BF16) return __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
+  else return __builtin_bit_cast(uint16_t, static_cast<_Float16>(v));
+}
+template <bool BF16>
+__device__ __forceinline__ u32x2 pack4(float4v v) {
+  if constexpr (BF16) {
+    bf16x4 h;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) h[e] = static_cast<__bf16>(v[e]);
+    return __builtin_bit_cast(u32x2, h);
+  } else {
+    half4 h;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) h[e] = static_cast<_Float16>(v[e]);
+    return __builtin_bit_cast(u32x2, h);
+  }
+}
+template <bool BF16>
+__device__ __forceinline__ float4v unpack4(u32x2 v) {
+  float4v r;
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    r[2 * e] = to_f32<BF16>(static_cast<uint16_t>(v[e]));
+    r[2 * e + 1] = to_f32<BF16>(static_cast<uint16_t>(v[e] >> 16));
+  }
+  return r;
+}
+
+template <bool BF16>
+__device__ __forceinline__ float4v mfma16(half8 a, half8 b, float4v c) {
+  if constexpr (BF16)
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
+                                                   __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+
+// ---- 8 columns of a 16-bit matrix row ----
+
+// Row `row`'s columns n .. n + 7, zeros past n_end. `vec`: the matrix starts
+// on 16 bytes, its rows are 16-byte multiples apart and n_end is one of 8.
+__device__ __forceinline__ u32x4 load_piece(const uint16_t* row, int64_t n, int64_t n_end, bool vec) {
+  if (vec) return *reinterpret_cast<const u32x4*>(row + n);
+  u32x4 r = {};
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if (n + e < n_end) r[e >> 1] |= static_cast<uint32_t>(row[n + e]) << (16 * (e & 1));
+  return r;
+}
+
+// The rows m0 .. of a 16-bit matrix that an epilogue reads or writes, through
+// a buffer whose bound ends with the matrix: lanes outside it load zeros and
+// store nothing, without a branch.
+struct RowsView {
+  __amdgpu_buffer_rsrc_t r;
+  uint32_t ld2, n_end;
+  bool vec;
+  __device__ __forceinline__ RowsView(const uint16_t* p, int64_t ld, int64_t m0, int64_t M,
+                                      int64_t N, int tile_rows, bool vec_)
+      : ld2(static_cast<uint32_t>(ld) * 2u), n_end(static_cast<uint32_t>(N)), vec(vec_) {
+    const int64_t left = M - m0 < tile_rows ? M - m0 : tile_rows;
+    r = tile_rsrc(p ? p + m0 * ld : nullptr,
+                  p && left > 0 ? static_cast<uint32_t>((left - 1) * ld + N) * 2u : 0u);
+  }
+  __device__ __forceinline__ u32x4 load(uint32_t m, uint32_t n) const {
+    const uint32_t off = m * ld2 + n * 2u;
+    if (vec)
+      return __builtin_bit_cast(u32x4,
+                                __builtin_amdgcn_raw_buffer_load_b128(r, n < n_end ? off : kOobOff, 0, 0));
+    u32x4 v = {};
+#pragma unroll
+    for (uint32_t e = 0; e < 8; ++e)
+      v[e >> 1] |= static_cast<uint32_t>(static_cast<uint16_t>(__builtin_amdgcn_raw_buffer_load_b16(
+                       r, n + e < n_end ? off + 2u * e : kOobOff, 0, 0)))
+                   << (16 * (e & 1));
+    return v;
+  }
+  __device__ __forceinline__ void store(uint32_t m, uint32_t n, u32x4 v) const {
+    const uint32_t off = m * ld2 + n * 2u;
+    if (vec) {
+      __builtin_amdgcn_raw_buffer_store_b128(v, r, n < n_end ? off : kOobOff, 0, 0);
+      return;
+    }
+#pragma unroll
+    for (uint32_t e = 0; e < 8; ++e)
+      __builtin_amdgcn_raw_buffer_store_b16(static_cast<uint16_t>(v[e >> 1] >> (16 * (e & 1))), r,
+                                            n + e < n_end ? off + 2u * e : kOobOff, 0, 0);
+  }
+};
+
+// Four consecutive values of an fp32 vector of n_end, zeros past it.
+__device__ __forceinline__ float4v load_bias4(__amdgpu_buffer_rsrc_t r, uint32_t n) {
+  float4v v;
+#pragma unroll
+  for (uint32_t e = 0; e < 4; ++e)
+    v[e] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(r, (n + e) * 4u, 0, 0));
+  return v;
+}
+
+// Two accumulators' packed quads (n blocks j and j + 1; lane group g = lane /
+// 16 holds n = 4 g .. 4 g + 3) <-> 8 consecutive n: lane group g then holds n
+// block j + (g & 1), columns 8 (g >> 1) ... The exchange is its own inverse.
+__device__ __forceinline__ u32x4 join_quads(u32x2 p, u32x2 q) {
+  const u32x2 a = lane_rows_swap(p[0], q[0]), b = lane_rows_swap(p[1], q[1]);
+  return u32x4{a[0], b[0], a[1], b[1]};
+}
+__device__ __forceinline__ void split_quads(u32x4 v, u32x2& p, u32x2& q) {
+  const u32x2 a = lane_rows_swap(v[0], v[2]), b = lane_rows_swap(v[1], v[3]);
+  p = u32x2{a[0], b[0]};
+  q = u32x2{a[1], b[1]};
+}
+
+// ---- activations ----
+
+enum Act : int { kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3, kActGeluTanh = 4 };
+
+constexpr float kSqrtHalf = 0.70710678118654752f;
+constexpr float kInvSqrt2Pi = 0.39894228040143268f;
+constexpr float kTwoSqrt2OverPi = 1.5957691216057308f;  // 2 sqrt(2 / pi)
+
+__device__ __forceinline__ float logistic(float z) {
+  return __builtin_amdgcn_rcpf(1.0f + __expf(-z));
+}
+// gelu_tanh = z / 2 (1 + tanh t) = z logistic(2 t): no cancellation for z < 0
+__device__ __forceinline__ float tanh_arg(float z) {
+  return kTwoSqrt2OverPi * (z + 0.044715f * z * z * z);
+}
+template <int ACT>
+__device__ __forceinline__ float act_value(float z) {
+  if constexpr (ACT == kActRelu) return z < 0.0f ? 0.0f : z;  // a NaN stays one
+  else if constexpr (ACT == kActSilu) return z * logistic(z);
+  else if constexpr (ACT == kActGelu) return 0.5f * z * (1.0f + erff(z * kSqrtHalf));
+  else if constexpr (ACT == kActGeluTanh) return z * logistic(tanh_arg(z));
+  else return z;
+}
+// value and derivative
+template <int ACT>
+__device__ __forceinline__ void act_both(float z, float& a, float& d) {
+  if constexpr (ACT == kActRelu) {
+    a = z < 0.0f ? 0.0f : z;
+    d = z > 0.0f ? 1.0f : 0.0f;
+  } else if constexpr (ACT == kActSilu) {
+    const float p = logistic(z);
+    a = z * p;
+    d = p + a * (1.0f - p);
+  } else if constexpr (ACT == kActGelu) {
+    const float c = 0.5f * (1.0f + erff(z * kSqrtHalf));
+    a = z * c;
+    d = c + z * kInvSqrt2Pi * __expf(-0.5f * z * z);
+  } else if constexpr (ACT == kActGeluTanh) {
+    const float p = logistic(tanh_arg(z));
+    a = z * p;
+    d = p + a * (1.0f - p) * kTwoSqrt2OverPi * (1.0f + 0.134145f * z * z);
+  } else {
+    a = z;
+    d = 1.0f;
+  }
+}
+// runs f<ACT>() for a uniform run-time activation
+template <typename F>
+__device__ __forceinline__ void with_act(int act, F&& f) {
+  switch (act) {
+    case kActRelu: f(std::integral_constant<int, kActRelu>{}); break;
+    case kActSilu: f(std::integral_constant<int, kActSilu>{}); break;
+    case kActGelu: f(std::integral_constant<int, kActGelu>{}); break;
+    case kActGeluTanh: f(std::integral_constant<int, kActGeluTanh>{}); break;
+    default: f(std::integral_constant<int, kActNone>{}); break;
+  }
+}
+
+// ---- operand tiles ----
+
+typedef uint32_t rsrc4 __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ rsrc4 load_rsrc(const void* base, uint32_t bytes) {
+  const uint64_t a = reinterpret_cast<uint64_t>(base);
+  return rsrc4{static_cast<uint32_t>(a), static_cast<uint32_t>(a >> 32) & 0xFFFFu, bytes, 0x00020000u};
+}
+
+// 16 bytes a lane from r + voff to LDS byte `lds` + 16 lane. Written as
+// assembly, without an output register, because for the builtin the compiler
+// waits for every such load before the next LDS read, of whatever buffer;
+// Tile::run waits for them by count instead. m0 needs no clobber: the
+// compiler writes it right before each of its own uses.
+__device__ __forceinline__ void load_to_lds(rsrc4 r, uint32_t voff, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds),
+               "v"(voff), "s"(r));
+}
+// The wait states between a vector instruction that writes a scalar register
+// and a load that reads it, which the compiler does not place before assembly.
+__device__ __forceinline__ void settle_rsrc(rsrc4& r) { asm volatile("s_nop 4" : "+s"(r)); }
+__device__ __forceinline__ uint32_t lds_addr(const char* p) {
+  return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_void*)p));
+}
+
+// One operand: R rows of the tile (m or n) by k. `ld`: elements between
+// memory rows. All of p, ld, `rows` of a KRow operand and k of a KCol
+// one are multiples of 8 elements, so a 16-byte piece is inside or outside.
+struct Operand {
+  const uint16_t* p;
+  int64_t ld;
+  int64_t rows;  // m or n extent
+  int64_t k;     // k extent; a product's k is the k-contiguous operand's, whose
+                 // zeros may go up to 7 past the memory rows of a KRow one
+};
+
+// The k-contiguous form. LDS: row r is 128 bytes, its piece c (8 k) in slot c
+// ^ ((r / 2) % 8), so that the 16 rows a read pass takes fall on distinct
+// banks.
+template <int R, int NT>
+struct LoadKCol {
+  static constexpr int SL = R * 8 / NT;
+  static_assert(R * 8 % NT == 0 && NT / 8 % 16 == 0, "slots");
+  const uint16_t* base;
+  uint32_t bytes;
+  uint32_t voff[SL];
+  int kc;
+  __device__ __forceinline__ void init(const Operand& o, int64_t row0, int64_t k_end, int tid) {
+    const int64_t left = o.rows - row0;
+    base = o.p + row0 * o.ld;
+    bytes = left > 0 ? static_cast<uint32_t>(((left < R ? left : R) - 1) * o.ld + k_end) * 2u : 0u;
+    const int r0 = tid >> 3;
+    kc = ((tid & 7) ^ ((r0 >> 1) & 7)) * 8;
+#pragma unroll
+    for (int i = 0; i < SL; ++i)
+      voff[i] = static_cast<uint32_t>((r0 + i * (NT / 8)) * o.ld + kc) * 2u;
+  }
+  __device__ __forceinline__ void issue(uint32_t lds, int64_t k0, int64_t k_end, int wave) const {
+    rsrc4 r = load_rsrc(base, bytes);
+    settle_rsrc(r);
+    const bool in = k0 + kc < k_end;
+#pragma unroll
+    for (int i = 0; i < SL; ++i)
+      load_to_lds(r, in ? voff[i] + static_cast<uint32_t>(k0) * 2u : kOobOff,
+                  lds + (i * NT + wave * 64) * 16);
+  }
+};
+
+// The form with k as the memory row. LDS: k row r is 2 R bytes; its 32-byte
+// pair of pieces p sits at p ^ f(r), f(r) = r % 4 + 4 (r / 8 % 2), so that the
+// 8 k rows that a transposed read takes at a time fall on distinct banks.
+// PAIR: the tile's columns are R / 2 of the first half of the matrix (gate)
+// and the R / 2 at the same place of its second half (up, `half` further on).
+template <int R, int NT, bool PAIR>
+struct LoadKRow {
+  static constexpr int CH = R / 8;  // pieces per k row
+  static constexpr int SL = kStepK * CH / NT;
+  static constexpr int KS = NT / CH;  // k rows between a thread's slots
+  static_assert(kStepK * CH % NT == 0, "slots");
+  const uint16_t* p;
+  int64_t ld, width, k_rows;
+  uint32_t voff[SL];
+  static __device__ __forceinline__ int swz(int k) {
+    return (((k & 3) | ((k >> 3 & 1) << 2)) << 1) & (CH - 1);
+  }
+  __device__ __forceinline__ void init(const Operand& o, int64_t col0, int64_t half, int tid) {
+    p = o.p;
+    ld = o.ld;
+    k_rows = o.k;
+    width = PAIR ? half + o.rows : o.rows;
+    const int k0 = tid / CH, cs = tid % CH;
+#pragma unroll
+    for (int i = 0; i < SL; ++i) {
+      const int k = k0 + i * KS;
+      const int c = (cs ^ swz(k)) * 8;
+      int64_t col;
+      bool in;
+      if constexpr (PAIR) {
+        const bool up = c >= R / 2;
+        const int64_t cc = col0 + (up ? c - R / 2 : c);
+        in = cc < o.rows;
+        col = up ? cc + half : cc;
+      } else {
+        col = col0 + c;
+        in = col < o.rows;
+      }
+      voff[i] = in ? static_cast<uint32_t>(k * ld + col) * 2u : kOobOff;
+    }
+  }
+  __device__ __forceinline__ void issue(uint32_t lds, int64_t k0, int64_t k_end, int wave) const {
+    const int64_t left = (k_rows < k_end ? k_rows : k_end) - k0;
+    const uint32_t bytes =
+        static_cast<uint32_t>(((left < kStepK ? left : kStepK) - 1) * ld + width) * 2u;
+    rsrc4 r = load_rsrc(p + k0 * ld, bytes);
+    settle_rsrc(r);
+#pragma unroll
+    for (int i = 0; i < SL; ++i) load_to_lds(r, voff[i], lds + (i * NT + wave * 64) * 16);
+  }
+};
+
+// ---- the tile ----
+
+// A_ROW, B_ROW: k is the memory row of that operand. PAIR: see LoadKRow
+// (B only); accumulator columns j < FN / 2 are then gate columns, the others
+// the up columns at the same place.
+template <bool BF16, bool A_ROW, bool B_ROW, bool PAIR, int BM, int BN, int WM, int WN, int STAGES>
+struct Tile {
+  static constexpr int NT = WM * WN * 64;
+  static constexpr int FM = BM / WM / 16, FN = BN / WN / 16;
+  static constexpr int A_BYTES = BM * kStepK * 2, B_BYTES = BN * kStepK * 2;
+  static constexpr int LDS_BYTES = STAGES * (A_BYTES + B_BYTES);
+  static_assert(FM >= 1 && FN >= 2 && FN % 2 == 0, "wave tile");
+  using LA = std::conditional_t<A_ROW, LoadKRow<BM, NT, false>, LoadKCol<BM, NT>>;
+  using LB = std::conditional_t<B_ROW, LoadKRow<BN, NT, PAIR>, LoadKCol<BN, NT>>;
+  static constexpr int LPT = LA::SL + LB::SL;  // loads per thread and step
+
+  // first column (in the tile) of accumulator column j of wave column wn
+  static __device__ __forceinline__ int ncol(int wn, int j) {
+    if constexpr (PAIR)
+      return j < FN / 2 ? wn * (BN / WN / 2) + j * 16
+                        : BN / 2 + wn * (BN / WN / 2) + (j - FN / 2) * 16;
+    else
+      return wn * (BN / WN) + j * 16;
+  }
+
+  template <int R, bool ROW>
+  static __device__ __forceinline__ half8 frag(const char* t, int row, int kk, int lane) {
+    const int g = lane >> 4, s = lane & 15;
+    if constexpr (!ROW) {
+      return *reinterpret_cast<const half8*>(
+          t + (row + s) * 128 + (((kk * 4 + g) ^ (s >> 1)) << 4));
+    } else {
+      // lane s of group g names k row 32 kk + 8 g + 4 half + s / 4, columns 4
+      // (s % 4) .. + 3 of the block; it receives column s of the 4 k rows
+      constexpr int CH = R / 8;
+      const int c = ((row >> 3) + ((s & 3) >> 1)) ^
+                    ((((s >> 2) | ((g & 1) << 2)) << 1) & (CH - 1));
+      const char* q = t + (kk * 32 + g * 8 + (s >> 2)) * (R * 2) + c * 16 + (s & 1) * 8;
+      const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)q);
+      const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(q + 4 * R * 2));
+      return __builtin_bit_cast(half8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    }
+  }
+
+  // acc[j][i]: n block j, m block i of the wave; k from k_begin (a multiple
+  // of 64) to k_end.
+  static __device__ __forceinline__ void run(const Operand& A, const Operand& B, int64_t half,
+                                             int64_t m0, int64_t n0, int64_t k_begin, int64_t k_end,
+                                             char* smem, float4v (&acc)[FN][FM]) {
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave / WN, wn = wave % WN;
+    LA la;
+    LB lb;
+    if constexpr (A_ROW) la.init(A, m0, 0, tid);
+    else la.init(A, m0, k_end, tid);
+    if constexpr (B_ROW) lb.init(B, n0, half, tid);
+    else lb.init(B, n0, k_end, tid);
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+#pragma unroll
+      for (int i = 0; i < FM; ++i) acc[j][i] = float4v{};
+
+    const int steps = static_cast<int>((k_end - k_begin + kStepK - 1) / kStepK);
+    auto issue = [&](int st, int buf) {
+      const uint32_t b = lds_addr(smem) + buf * (A_BYTES + B_BYTES);
+      const int64_t k0 = k_begin + static_cast<int64_t>(st) * kStepK;
+      la.issue(b, k0, k_end, wave);
+      lb.issue(b + A_BYTES, k0, k_end, wave);
+    };
+#pragma unroll
+    for (int st = 0; st < STAGES - 1; ++st)
+      if (st < steps) issue(st, st);
+
+    int buf = 0;
+    for (int st = 0; st < steps; ++st) {
+      // this step's loads are the oldest: all but the later steps' are waited
+      // for (and this wave's LDS reads of the last step), then every wave's
+      // through the barrier, after which the buffer that was read in the last
+      // step is overwritten
+      if (st + STAGES - 2 < steps) wait_loads<(STAGES - 2) * LPT>();
+      else wait_loads<0>();
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+      if (st + STAGES - 1 < steps) issue(st + STAGES - 1, buf == 0 ? STAGES - 1 : buf - 1);
+      const char* ta = smem + buf * (A_BYTES + B_BYTES);
+      const char* tb = ta + A_BYTES;
+#pragma unroll
+      for (int kk = 0; kk < kStepK / 32; ++kk) {
+        half8 fb[FN], fa[FM];
+#pragma unroll
+        for (int j = 0; j < FN; ++j) fb[j] = frag<BN, B_ROW>(tb, ncol(wn, j), kk, lane);
+#pragma unroll
+        for (int i = 0; i < FM; ++i) fa[i] = frag<BM, A_ROW>(ta, wm * (BM / WM) + i * 16, kk, lane);
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+          for (int j = 0; j < FN; ++j) acc[j][i] = mfma16<BF16>(fb[j], fa[i], acc[j][i]);
+      }
+      buf = buf + 1 == STAGES ? 0 : buf + 1;
+    }
+  }
+
+  template <int N>
+  static __device__ __forceinline__ void wait_loads() {
+    static_assert(N < 64, "vmcnt");
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
+  }
+};
+
+// Output tile of a workgroup: tiles are walked n first, and each XCD
+// (blockIdx % 8) takes a contiguous run of them, so that the n tiles which
+// read the same rows of A share that XCD's L2.
+struct TilePos {
+  int64_t m, n;
+};
+__device__ __forceinline__ TilePos tile_pos(int64_t m_tiles, int64_t n_tiles, int64_t bid) {
+  const int64_t total = m_tiles * n_tiles;
+  const int64_t q = total >> 3, r = total & 7, x = bid & 7, j = bid >> 3;
+  const int64_t t = x * q + (x < r ? x : r) + j;
+  return TilePos{t / n_tiles, t % n_tiles};
+}
+
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+inline int64_t round8(int64_t v) { return (v + 7) & ~int64_t{7}; }
+inline int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+}  // namespace
+}  // namespace submconv

@@ -1,0 +1,386 @@
+// Gated feed-forward block on site features, and its gradients:
+//
+//   [g | u] = x W_in + b_in      W_in [C][2F]: gate columns, then up columns
+//   h = act(g) u                 (elementwise)
+//   out = h W_out + b_out + residual
+//
+//   dh = dout W_out^T,  du = dh act(g),  dg = dh u act'(g)
+//   dx = [dg | du] W_in^T,  dW_in = x^T [dg | du],  dW_out = h^T dout
+//
+// Both projections, the activation and the product are one kernel: a
+// workgroup's tile holds the gate and up columns of the same hidden channels,
+// a wave both accumulators of each, so h is formed in registers and g and u
+// are written only where the gradient will need them. In the gradient, dg, du
+// and h are formed in the epilogue of dh, which is never stored. h, dg and du
+// are rounded to 16 bits, as operands of the products that follow have to be;
+// the bias gradient adds dg and du before that.
+#include <algorithm>
+
+#include "dense_common.h"
+#include "dense_tile.h"
+
+namespace submconv {
+namespace {
+
+// ---- forward: h = act(x W_g + b_g) (x W_u + b_u) ----
+
+struct GateEpi {
+  const float* bias;  // [2F] or null
+  uint16_t* h;        // [M][Fp], Fp = F rounded up to 8, the rest zeros
+  uint16_t* pre;      // [M][2F] or null
+  int64_t F, Fp;
+  int act;
+  bool vec_p;
+};
+
+template <bool BF16, int ACT, int BM, int FN, int FM>
+__device__ __forceinline__ void gate_epilogue(const GateEpi& e, int64_t M, int64_t m0, uint32_t mw,
+                                              uint32_t nb, int lane, float4v (&acc)[FN][FM]) {
+  constexpr int H = FN / 2;  // accumulator columns of the gate; then the up projection's
+  const int g = lane >> 4, s = lane & 15;
+  const RowsView h(e.h, e.Fp, m0, M, e.Fp, BM, true);
+  const RowsView pg(e.pre, 2 * e.F, m0, M, e.F, BM, e.vec_p);
+  const RowsView pu(e.pre ? e.pre + e.F : nullptr, 2 * e.F, m0, M, e.F, BM, e.vec_p);
+  const uint32_t bytes = e.bias ? static_cast<uint32_t>(e.F) * 4u : 0u;
+  const __amdgpu_buffer_rsrc_t bg = tile_rsrc(e.bias, bytes);
+  const __amdgpu_buffer_rsrc_t bu = tile_rsrc(e.bias ? e.bias + e.F : nullptr, bytes);
+#pragma unroll
+  for (int j = 0; j < H; j += 2) {
+    float4v b[2][2];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      b[0][q] = load_bias4(bg, nb + (j + q) * 16 + g * 4);
+      b[1][q] = load_bias4(bu, nb + (j + q) * 16 + g * 4);
+    }
+    const uint32_t n = nb + j * 16 + (g & 1) * 16 + (g >> 1) * 8;
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      const uint32_t m = mw + i * 16 + s;
+      float4v zg[2], zu[2], v[2];
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        zg[q] = acc[j + q][i] + b[0][q];
+        zu[q] = acc[H + j + q][i] + b[1][q];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) v[q][r] = act_value<ACT>(zg[q][r]) * zu[q][r];
+      }
+      if (e.pre) {
+        pg.store(m, n, join_quads(pack4<BF16>(zg[0]), pack4<BF16>(zg[1])));
+        pu.store(m, n, join_quads(pack4<BF16>(zu[0]), pack4<BF16>(zu[1])));
+      }
+      h.store(m, n, join_quads(pack4<BF16>(v[0]), pack4<BF16>(v[1])));
+    }
+  }
+}
+
+template <bool BF16, int BM, int BN, int WM, int WN, int STAGES>
+__global__ __launch_bounds__(WM* WN * 64) void k_gate(Operand A, Operand B, int64_t K, int64_t half,
+                                                      int64_t m_tiles, int64_t n_tiles, GateEpi e) {
+  using T = Tile<BF16, false, true, true, BM, BN, WM, WN, STAGES>;
+  __shared__ __attribute__((aligned(16))) char smem[T::LDS_BYTES];
+  const TilePos t = tile_pos(m_tiles, n_tiles, blockIdx.x);
+  const int64_t m0 = t.m * BM, n0 = t.n * (BN / 2);
+  float4v acc[T::FN][T::FM];
+  T::run(A, B, half, m0, n0, 0, K, smem, acc);
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t mw = (wave / WN) * (BM / WM);
+  const uint32_t nb = static_cast<uint32_t>(n0) + (wave % WN) * (BN / WN / 2);
+  with_act(e.act, [&](auto a) {
+    gate_epilogue<BF16, decltype(a)::value, BM>(e, A.rows, m0, mw, nb, lane, acc);
+  });
+}
+
+// ---- gradient: dh = dout W_out^T; dg, du, h in its epilogue ----
+
+struct GateGradEpi {
+  const uint16_t* pre;  // [M][2F]
+  uint16_t* dz;         // [M][2Fp]: dg, zeros up to Fp, du, zeros
+  uint16_t* h;          // [M][Fp]
+  float* sums;          // [m_tiles][2Fp] column sums of the tile's dg and du, or null
+  int64_t F, Fp;
+  int act;
+  bool vec_p;
+};
+
+template <bool BF16, int ACT, int BM, int BN, int WM, int FN, int FM>
+__device__ __forceinline__ void gate_grad_epilogue(const GateGradEpi& e, int64_t M, int64_t m_tile,
+                                                   int wave_m, uint32_t nt, uint32_t nb, int lane,
+                                                   float* red, float4v (&acc)[FN][FM]) {
+  const int g = lane >> 4, s = lane & 15;
+  const int64_t m0 = m_tile * BM;
+  const uint32_t mw = wave_m * (BM / WM);
+  const RowsView pg(e.pre, 2 * e.F, m0, M, e.F, BM, e.vec_p);
+  const RowsView pu(e.pre + e.F, 2 * e.F, m0, M, e.F, BM, e.vec_p);
+  const RowsView zg(e.dz, 2 * e.Fp, m0, M, e.Fp, BM, true);
+  const RowsView zu(e.dz + e.Fp, 2 * e.Fp, m0, M, e.Fp, BM, true);
+  const RowsView h(e.h, e.Fp, m0, M, e.Fp, BM, true);
+#pragma unroll
+  for (int j = 0; j < FN; j += 2) {
+    const uint32_t n = nb + j * 16 + (g & 1) * 16 + (g >> 1) * 8;
+    float4v sum[2][2] = {};
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      const uint32_t m = mw + i * 16 + s;
+      u32x2 rg[2], ru[2];
+      split_quads(pg.load(m, n), rg[0], rg[1]);
+      split_quads(pu.load(m, n), ru[0], ru[1]);
+      float4v dg[2], du[2], v[2];
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const float4v xg = unpack4<BF16>(rg[q]), xu = unpack4<BF16>(ru[q]);
+        const float4v dh = acc[j + q][i];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          float a, d;
+          act_both<ACT>(xg[r], a, d);
+          dg[q][r] = dh[r] * xu[r] * d;
+          du[q][r] = dh[r] * a;
+          v[q][r] = a * xu[r];
+        }
+        sum[0][q] += dg[q];
+        sum[1][q] += du[q];
+      }
+      zg.store(m, n, join_quads(pack4<BF16>(dg[0]), pack4<BF16>(dg[1])));
+      zu.store(m, n, join_quads(pack4<BF16>(du[0]), pack4<BF16>(du[1])));
+      h.store(m, n, join_quads(pack4<BF16>(v[0]), pack4<BF16>(v[1])));
+    }
+    if (e.sums) {
+      // rows past M add zeros: their dout is read as zeros
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const float x = lanes_sum<16>(sum[t][q][r]);
+            if (s == 0) red[(wave_m * 2 + t) * BN + (nb - nt) + (j + q) * 16 + g * 4 + r] = x;
+          }
+    }
+  }
+}
+
+template <bool BF16, int BM, int BN, int WM, int WN, int STAGES>
+__global__ __launch_bounds__(WM* WN * 64) void k_gate_grad(Operand A, Operand B, int64_t K,
+                                                           int64_t m_tiles, int64_t n_tiles,
+                                                           GateGradEpi e) {
+  using T = Tile<BF16, false, false, false, BM, BN, WM, WN, STAGES>;
+  __shared__ __attribute__((aligned(16))) char smem[T::LDS_BYTES];
+  const TilePos t = tile_pos(m_tiles, n_tiles, blockIdx.x);
+  const int64_t m0 = t.m * BM, n0 = t.n * BN;
+  float4v acc[T::FN][T::FM];
+  T::run(A, B, 0, m0, n0, 0, K, smem, acc);
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t nt = static_cast<uint32_t>(n0);
+  const uint32_t nb = nt + (wave % WN) * (BN / WN);
+  float* red = reinterpret_cast<float*>(smem);  // [WM][2][BN], once every wave is done with the tiles
+  __syncthreads();
+  with_act(e.act, [&](auto a) {
+    gate_grad_epilogue<BF16, decltype(a)::value, BM, BN, WM>(e, A.rows, t.m, wave / WN, nt, nb, lane,
+                                                             red, acc);
+  });
+  if (!e.sums) return;
+  __syncthreads();
+  for (int c = threadIdx.x; c < 2 * BN; c += WM * WN * 64) {
+    const int half = c / BN, n = c % BN;
+    float x = red[half * BN + n];
+#pragma unroll
+    for (int w = 1; w < WM; ++w) x += red[(w * 2 + half) * BN + n];
+    if (n0 + n < e.Fp) e.sums[(t.m * 2 + half) * e.Fp + n0 + n] = x;
+  }
+}
+
+constexpr int kGateTile = 128;
+
+int gate_forward(const Mat16& x, const Mat16& W, int64_t F, const float* bias, int act, bool bf16,
+                 uint16_t* h, uint16_t* pre, hipStream_t stream) {
+  const int64_t Fp = W.cols / 2;
+  const int64_t mt = div_up(x.rows, kGateTile), nt = div_up(Fp, kGateTile / 2);
+  if (mt * nt > INT32_MAX)
+    return set_error(SUBMCONV_ERR_UNSUPPORTED_SHAPE, "%lld output tiles", (long long)(mt * nt));
+  const GateEpi e{bias, h, pre, F, Fp, act, F % 8 == 0 && aligned16(pre)};
+  const Operand A{x.p, x.ld, x.rows, x.cols}, B{W.p, W.ld, Fp, W.rows};
+  const dim3 grid(static_cast<unsigned>(mt * nt));
+  if (bf16)
+    k_gate<true, kGateTile, kGateTile, 2, 2, 2><<<grid, 256, 0, stream>>>(A, B, x.cols, Fp, mt, nt, e);
+  else
+    k_gate<false, kGateTile, kGateTile, 2, 2, 2><<<grid, 256, 0, stream>>>(A, B, x.cols, Fp, mt, nt, e);
+  SUBMCONV_HIP_CHECK(hipGetLastError());
+  return SUBMCONV_OK;
+}
+
+int64_t gate_grad_tiles(int64_t rows) { return std::max<int64_t>(1, div_up(rows, kGateTile)); }
+
+// dy [M][C], W_out [F][C]
+int gate_grad(const Mat16& dy, const Mat16& W, int64_t Fp, const uint16_t* pre, int act, bool bf16,
+              uint16_t* dz, uint16_t* h, float* sums, hipStream_t stream) {
+  const int64_t F = W.rows;
+  const int64_t mt = gate_grad_tiles(dy.rows), nt = div_up(Fp, kGateTile);
+  if (mt * nt > INT32_MAX)
+    return set_error(SUBMCONV_ERR_UNSUPPORTED_SHAPE, "%lld output tiles", (long long)(mt * nt));
+  const GateGradEpi e{pre, dz, h, sums, F, Fp, act, F % 8 == 0 && aligned16(pre)};
+  const Operand A{dy.p, dy.ld, dy.rows, dy.cols}, B{W.p, W.ld, F, W.cols};
+  const dim3 grid(static_cast<unsigned>(mt * nt));
+  if (bf16)
+    k_gate_grad<true, kGateTile, kGateTile, 2, 2, 2><<<grid, 256, 0, stream>>>(A, B, dy.cols, mt, nt, e);
+  else
+    k_gate_grad<false, kGateTile, kGateTile, 2, 2, 2><<<grid, 256, 0, stream>>>(A, B, dy.cols, mt, nt, e);
+  SUBMCONV_HIP_CHECK(hipGetLastError());
+  return SUBMCONV_OK;
+}
+
+struct Ffn {
+  int64_t n, C, F, Co;
+  Mat16 x, W_in, W_out, dy;  // W_in [C][2F], W_out [F][Co]
+  int act;
+  bool bf16;
+};
+
+int ffn_forward(const Ffn& f, const float* b_in, const float* b_out, const uint16_t* residual,
+                int64_t ldr, uint16_t* out, uint16_t* pre, Arena& ws, hipStream_t stream) {
+  const int64_t Fp = round8(f.F);
+  Mat16 x, wi, wo;
+  SUBMCONV_TRY(readable(f.x, 1, ws, &x, stream));
+  SUBMCONV_TRY(readable(f.W_in, 2, ws, &wi, stream));
+  SUBMCONV_TRY(readable(f.W_out, 1, ws, &wo, stream));
+  uint16_t* h = static_cast<uint16_t*>(ws.take(f.n * Fp * 2));
+  if (ws.counting || f.n == 0) return SUBMCONV_OK;
+  SUBMCONV_TRY(gate_forward(x, wi, f.F, b_in, f.act, f.bf16, h, pre, stream));
+  return linear_forward(Mat16{h, f.n, Fp, Fp}, wo, b_out, kActNone, f.bf16, residual, ldr, out, f.Co,
+                        nullptr, f.Co, stream);
+}
+
+struct FfnGrads {
+  uint16_t *x, *W_in, *W_out;
+  float *b_in, *b_out;
+  bool all;  // count the workspace of every gradient
+};
+
+int ffn_backward(const Ffn& f, const uint16_t* pre, const FfnGrads& g, Arena& ws, hipStream_t stream) {
+  const bool run = !ws.counting;
+  const int64_t Fp = round8(f.F), Cp = round8(f.C), Op = round8(f.Co);
+  Mat16 dy, wo;
+  SUBMCONV_TRY(readable(f.dy, 1, ws, &dy, stream));
+  if (g.all || g.b_out) {
+    float* part = static_cast<float*>(ws.take(column_parts(f.n, f.Co) * Op * 4));
+    if (run) SUBMCONV_TRY(column_sums(f.dy, f.bf16, part, g.b_out, stream));
+  }
+  if (!(g.all || g.x || g.W_in || g.W_out || g.b_in)) return SUBMCONV_OK;
+  SUBMCONV_TRY(readable(f.W_out, 1, ws, &wo, stream));
+  uint16_t* h = static_cast<uint16_t*>(ws.take(f.n * Fp * 2));
+  uint16_t* dz = static_cast<uint16_t*>(ws.take(f.n * 2 * Fp * 2));
+  const int64_t tiles = gate_grad_tiles(f.n);
+  float* sums = g.all || g.b_in ? static_cast<float*>(ws.take(tiles * 2 * Fp * 4)) : nullptr;
+  const Mat16 hm{h, f.n, Fp, Fp}, zm{dz, f.n, 2 * Fp, 2 * Fp};
+  if (run) {
+    SUBMCONV_TRY(gate_grad(dy, wo, Fp, pre, f.act, f.bf16, dz, h, sums, stream));
+    if (g.b_in) SUBMCONV_TRY(sum_parts(sums, tiles, 2 * Fp, 2 * f.F, 2, g.b_in, stream));
+  }
+  if (g.all || g.x) {
+    Mat16 wi;
+    SUBMCONV_TRY(readable(f.W_in, 2, ws, &wi, stream));
+    if (run) SUBMCONV_TRY(product_nt(zm, wi, f.bf16, g.x, f.C, f.C, stream));
+  }
+  if (g.all || g.W_in || g.W_out) {
+    float* part = static_cast<float*>(ws.take(std::max(g.all || g.W_in ? product_tn_bytes(f.n, Cp, 2 * Fp) : 0,
+                                                       g.all || g.W_out ? product_tn_bytes(f.n, Fp, Op) : 0)));
+    if (g.all || g.W_in) {
+      Mat16 x;
+      SUBMCONV_TRY(readable(f.x, 1, ws, &x, stream));
+      if (run) SUBMCONV_TRY(product_tn(x, zm, f.bf16, part, g.W_in, f.C, 2 * f.F, 2, stream));
+    }
+    if (run && g.W_out) SUBMCONV_TRY(product_tn(hm, dy, f.bf16, part, g.W_out, f.F, f.Co, 1, stream));
+  }
+  return SUBMCONV_OK;
+}
+
+int ffn_shape(int64_t n, int32_t cin, int32_t hidden, int32_t cout) {
+  SUBMCONV_TRY(check_shape("x", n, cin));
+  if (hidden < 1 || hidden > (1 << 19))
+    return set_error(SUBMCONV_ERR_UNSUPPORTED_SHAPE, "hidden = %d", hidden);
+  return check_shape("out", n, cout);
+}
+
+}  // namespace
+}  // namespace submconv
+
+using namespace submconv;
+
+extern "C" int64_t submconv_gated_ffn_workspace_bytes(int64_t n, int32_t cin, int32_t hidden,
+                                                      int32_t cout, int32_t aligned) {
+  clear_error();
+  SUBMCONV_TRY(ffn_shape(n, cin, hidden, cout));
+  const Ffn f{n, cin, hidden, cout, shape_of(n, cin, aligned), shape_of(cin, 2 * hidden, aligned),
+              shape_of(hidden, cout, aligned), {}, kActSilu, false};
+  Arena ws;
+  SUBMCONV_TRY(ffn_forward(f, nullptr, nullptr, nullptr, 0, nullptr, nullptr, ws, nullptr));
+  return ws.used;
+}
+
+extern "C" int submconv_gated_ffn(const uint16_t* x, int64_t ldx, int64_t n, const uint16_t* W_in,
+                                  const float* b_in, const uint16_t* W_out, const float* b_out,
+                                  const uint16_t* residual, int64_t ldr, uint16_t* out,
+                                  uint16_t* pre, int32_t cin, int32_t hidden, int32_t cout,
+                                  int32_t act, int32_t dtype, void* workspace,
+                                  int64_t workspace_bytes, hipStream_t stream) {
+  clear_error();
+  SUBMCONV_TRY(check_kind(act, dtype));
+  SUBMCONV_TRY(ffn_shape(n, cin, hidden, cout));
+  SUBMCONV_TRY(check_matrix("x", x, n, cin, ldx));
+  SUBMCONV_TRY(check_matrix("W_in", W_in, cin, 2 * int64_t{hidden}, 2 * int64_t{hidden}));
+  SUBMCONV_TRY(check_matrix("W_out", W_out, hidden, cout, cout));
+  SUBMCONV_TRY(check_matrix("out", out, n, cout, cout));
+  if (residual) SUBMCONV_TRY(check_matrix("residual", residual, n, cout, ldr));
+  if (pre) SUBMCONV_TRY(check_matrix("pre", pre, n, 2 * int64_t{hidden}, 2 * int64_t{hidden}));
+  const Ffn f{n, cin, hidden, cout, Mat16{x, n, cin, n == 1 ? round8(cin) : ldx},
+              Mat16{W_in, cin, 2 * int64_t{hidden}, 2 * int64_t{hidden}},
+              Mat16{W_out, hidden, cout, cout}, {}, act, dtype == SUBMCONV_DTYPE_BF16};
+  const int64_t lr = n == 1 ? round8(cout) : ldr;
+  Arena count;
+  SUBMCONV_TRY(ffn_forward(f, b_in, b_out, residual, lr, out, pre, count, stream));
+  SUBMCONV_TRY(check_workspace(workspace, workspace_bytes, count.used));
+  Arena ws{false, static_cast<char*>(workspace)};
+  return ffn_forward(f, b_in, b_out, residual, lr, out, pre, ws, stream);
+}
+
+extern "C" int64_t submconv_gated_ffn_backward_workspace_bytes(int64_t n, int32_t cin,
+                                                               int32_t hidden, int32_t cout,
+                                                               int32_t aligned) {
+  clear_error();
+  SUBMCONV_TRY(ffn_shape(n, cin, hidden, cout));
+  const Ffn f{n, cin, hidden, cout, shape_of(n, cin, aligned), shape_of(cin, 2 * hidden, aligned),
+              shape_of(hidden, cout, aligned), shape_of(n, cout, aligned), kActSilu, false};
+  Arena ws;
+  SUBMCONV_TRY(ffn_backward(f, nullptr, {nullptr, nullptr, nullptr, nullptr, nullptr, true}, ws, nullptr));
+  return ws.used;
+}
+
+extern "C" int submconv_gated_ffn_backward(const uint16_t* grad_out, int64_t ldg, int64_t n,
+                                           const uint16_t* x, int64_t ldx, const uint16_t* W_in,
+                                           const uint16_t* W_out, const uint16_t* pre,
+                                           uint16_t* grad_x, uint16_t* grad_w_in, float* grad_b_in,
+                                           uint16_t* grad_w_out, float* grad_b_out, int32_t cin,
+                                           int32_t hidden, int32_t cout, int32_t act, int32_t dtype,
+                                           void* workspace, int64_t workspace_bytes,
+                                           hipStream_t stream) {
+  clear_error();
+  SUBMCONV_TRY(check_kind(act, dtype));
+  SUBMCONV_TRY(ffn_shape(n, cin, hidden, cout));
+  SUBMCONV_TRY(check_matrix("grad_out", grad_out, n, cout, ldg));
+  if (grad_w_in) SUBMCONV_TRY(check_matrix("x", x, n, cin, ldx));
+  if (grad_x) SUBMCONV_TRY(check_matrix("W_in", W_in, cin, 2 * int64_t{hidden}, 2 * int64_t{hidden}));
+  SUBMCONV_TRY(check_matrix("W_out", W_out, hidden, cout, cout));
+  SUBMCONV_TRY(check_matrix("pre", pre, n, 2 * int64_t{hidden}, 2 * int64_t{hidden}));
+  const Ffn f{n, cin, hidden, cout, Mat16{x, n, cin, n == 1 ? round8(cin) : ldx},
+              Mat16{W_in, cin, 2 * int64_t{hidden}, 2 * int64_t{hidden}},
+              Mat16{W_out, hidden, cout, cout},
+              Mat16{grad_out, n, cout, n == 1 ? round8(cout) : ldg}, act,
+              dtype == SUBMCONV_DTYPE_BF16};
+  const FfnGrads g{grad_x, grad_w_in, grad_w_out, grad_b_in, grad_b_out, false};
+  Arena count;
+  SUBMCONV_TRY(ffn_backward(f, pre, g, count, stream));
+  SUBMCONV_TRY(check_workspace(workspace, workspace_bytes, count.used));
+  Arena ws{false, static_cast<char*>(workspace)};
+  return ffn_backward(f, pre, g, ws, stream);
+}

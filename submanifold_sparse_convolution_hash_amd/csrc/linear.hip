@@ -1,0 +1,572 @@
+// Linear layer on site features with its epilogue fused, and its gradients:
+// the point-wise layers around a SubMConv3d (a 1x1x1 convolution is x W + b).
+//
+//   z = x W + b,  out = act(z) + residual
+//   dz = dout act'(z),  dx = dz W^T,  dW = x^T dz,  db = sum over rows of dz
+//
+// The products run on the MFMA tile of dense_tile.h with fp32 accumulation;
+// bias, activation and residual are applied to the fp32 accumulators and each
+// stored tensor is rounded once. dz is rounded to 16 bits before its two
+// products, as MFMA operands have to be; the bias gradient adds it unrounded.
+#include <algorithm>
+
+#include "dense_common.h"
+#include "dense_tile.h"
+
+namespace submconv {
+namespace {
+
+// ---- forward ----
+
+struct LinearEpi {
+  const float* bias;         // [N] or null
+  const uint16_t* residual;  // or null
+  int64_t ldr;
+  uint16_t* out;
+  int64_t ldo;
+  uint16_t* pre;  // [M][N] dense, or null
+  int act;
+  bool vec_r, vec_o, vec_p;
+};
+
+template <bool BF16, int ACT, int BM, int FN, int FM>
+__device__ __forceinline__ void linear_epilogue(const LinearEpi& e, int64_t M, int64_t N,
+                                                int64_t m0, uint32_t mw, uint32_t nb, int lane,
+                                                float4v (&acc)[FN][FM]) {
+  const int g = lane >> 4, s = lane & 15;
+  const RowsView out(e.out, e.ldo, m0, M, N, BM, e.vec_o);
+  const RowsView pre(e.pre, N, m0, M, N, BM, e.vec_p);
+  const RowsView res(e.residual, e.ldr, m0, M, N, BM, e.vec_r);
+  const __amdgpu_buffer_rsrc_t rb = tile_rsrc(e.bias, e.bias ? static_cast<uint32_t>(N) * 4u : 0u);
+#pragma unroll
+  for (int j = 0; j < FN; j += 2) {
+    const float4v b0 = load_bias4(rb, nb + j * 16 + g * 4);
+    const float4v b1 = load_bias4(rb, nb + j * 16 + 16 + g * 4);
+    const uint32_t n = nb + j * 16 + (g & 1) * 16 + (g >> 1) * 8;  // this lane's joined piece
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      const uint32_t m = mw + i * 16 + s;
+      float4v z[2] = {acc[j][i] + b0, acc[j + 1][i] + b1};
+      if (e.pre) pre.store(m, n, join_quads(pack4<BF16>(z[0]), pack4<BF16>(z[1])));
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) z[q][r] = act_value<ACT>(z[q][r]);
+      if (e.residual) {
+        u32x2 p, q;
+        split_quads(res.load(m, n), p, q);
+        z[0] += unpack4<BF16>(p);
+        z[1] += unpack4<BF16>(q);
+      }
+      out.store(m, n, join_quads(pack4<BF16>(z[0]), pack4<BF16>(z[1])));
+    }
+  }
+}
+
+// B_ROW: W [K][N] as stored (forward); else W [N][K] (input gradient).
+template <bool BF16, bool B_ROW, int BM, int BN, int WM, int WN, int STAGES>
+__global__ __launch_bounds__(WM* WN * 64) void k_linear(Operand A, Operand B, int64_t K, int64_t N,
+                                                        int64_t m_tiles, int64_t n_tiles,
+                                                        LinearEpi e) {
+  using T = Tile<BF16, false, B_ROW, false, BM, BN, WM, WN, STAGES>;
+  __shared__ __attribute__((aligned(16))) char smem[T::LDS_BYTES];
+  const TilePos t = tile_pos(m_tiles, n_tiles, blockIdx.x);
+  const int64_t m0 = t.m * BM, n0 = t.n * BN;
+  float4v acc[T::FN][T::FM];
+  T::run(A, B, 0, m0, n0, 0, K, smem, acc);
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t mw = (wave / WN) * (BM / WM);
+  const uint32_t nb = static_cast<uint32_t>(n0) + (wave % WN) * (BN / WN);
+  with_act(e.act, [&](auto a) {
+    linear_epilogue<BF16, decltype(a)::value, BM>(e, A.rows, N, m0, mw, nb, lane, acc);
+  });
+}
+
+template <bool B_ROW, int BM, int BN, int WM, int WN, int STAGES>
+int launch_linear(const Operand& A, const Operand& B, int64_t K, int64_t N, bool bf16,
+                  const LinearEpi& e, hipStream_t stream) {
+  const int64_t mt = div_up(A.rows, BM), nt = div_up(N, BN);
+  if (mt * nt > INT32_MAX)
+    return set_error(SUBMCONV_ERR_UNSUPPORTED_SHAPE, "%lld output tiles", (long long)(mt * nt));
+  const dim3 grid(static_cast<unsigned>(mt * nt));
+  if (bf16)
+    k_linear<true, B_ROW, BM, BN, WM, WN, STAGES><<<grid, WM * WN * 64, 0, stream>>>(A, B, K, N, mt, nt, e);
+  else
+    k_linear<false, B_ROW, BM, BN, WM, WN, STAGES><<<grid, WM * WN * 64, 0, stream>>>(A, B, K, N, mt, nt, e);
+  SUBMCONV_HIP_CHECK(hipGetLastError());
+  return SUBMCONV_OK;
+}
+
+template <bool B_ROW>
+int linear_product(const Operand& A, const Operand& B, int64_t K, int64_t N, bool bf16,
+                   const LinearEpi& e, hipStream_t stream) {
+  if (A.rows == 0 || N == 0) return SUBMCONV_OK;
+  return launch_linear<B_ROW, 128, 128, 2, 2, 2>(A, B, K, N, bf16, e, stream);
+}
+
+// ---- padded copies ----
+
+// thread: one 16-byte piece of the copy
+__global__ void k_pack16(const uint16_t* __restrict__ a, int64_t rows, int64_t cols, int64_t ld,
+                         int groups, int64_t gp, uint16_t* __restrict__ out) {
+  const int64_t gc = cols / groups;
+  const int64_t pr = groups * gp / 8;  // pieces per row
+  const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < rows * pr; i += step) {
+    const int64_t r = i / pr, c = (i - r * pr) * 8;
+    const int64_t q = c / gp, cc = c - q * gp;
+    const uint16_t* row = a + r * ld + q * gc;
+    reinterpret_cast<u32x4*>(out)[i] = load_piece(row, cc, gc, false);
+  }
+}
+
+// ---- dz and column sums ----
+
+constexpr int kSumThreads = 256;
+constexpr int kSumLanes = 32;                      // pieces (of 8 columns) a workgroup covers
+constexpr int kSumRows = kSumThreads / kSumLanes;  // rows per pass
+
+// dz = dy act'(z), rounded, into a matrix of pieces (columns past the width
+// are zeros), where dz is not null; and the unrounded column sums of this
+// workgroup's rows, where partial is not null. grid (column strips, row runs).
+template <bool BF16, int ACT>
+__device__ __forceinline__ void act_grad_rows(const uint16_t* dy, int64_t ldy, bool vec_y,
+                                              const uint16_t* z, bool vec_z, int64_t rows,
+                                              int64_t cols, int64_t run, uint16_t* dz, int64_t ldz,
+                                              float* partial, float (*sums)[kSumLanes * 8 + 1]) {
+  const int cl = threadIdx.x % kSumLanes, rl = threadIdx.x / kSumLanes;
+  const int64_t c = (static_cast<int64_t>(blockIdx.x) * kSumLanes + cl) * 8;
+  const int64_t r_end = min(rows, (static_cast<int64_t>(blockIdx.y) + 1) * run);
+  float s[8] = {};
+  if (c < cols) {
+    for (int64_t r = blockIdx.y * run + rl; r < r_end; r += kSumRows) {
+      const u32x4 v = load_piece(dy + r * ldy, c, cols, vec_y);
+      float d[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) d[e] = to_f32<BF16>(static_cast<uint16_t>(v[e >> 1] >> (16 * (e & 1))));
+      if constexpr (ACT != kActNone) {
+        const u32x4 w = load_piece(z + r * cols, c, cols, vec_z);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          float a, g;
+          act_both<ACT>(to_f32<BF16>(static_cast<uint16_t>(w[e >> 1] >> (16 * (e & 1)))), a, g);
+          d[e] *= g;
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s[e] += d[e];
+      if (dz) {
+        const u32x2 lo = pack4<BF16>(float4v{d[0], d[1], d[2], d[3]});
+        const u32x2 hi = pack4<BF16>(float4v{d[4], d[5], d[6], d[7]});
+        *reinterpret_cast<u32x4*>(dz + r * ldz + c) = u32x4{lo[0], lo[1], hi[0], hi[1]};
+      }
+    }
+  }
+  if (!partial) return;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) sums[rl][cl * 8 + e] = s[e];
+  __syncthreads();
+  const int64_t cc = static_cast<int64_t>(blockIdx.x) * (kSumLanes * 8) + threadIdx.x;
+  const int64_t cp = (cols + 7) & ~int64_t{7};
+  if (cc < cp) {
+    float t = 0.0f;
+#pragma unroll
+    for (int r = 0; r < kSumRows; ++r) t += sums[r][threadIdx.x];
+    partial[blockIdx.y * cp + cc] = t;
+  }
+}
+static_assert(kSumLanes * 8 == kSumThreads, "one thread per column of a strip");
+
+template <bool BF16>
+__global__ __launch_bounds__(kSumThreads) void k_act_grad(const uint16_t* dy, int64_t ldy,
+                                                          bool vec_y, const uint16_t* z, bool vec_z,
+                                                          int act, int64_t rows, int64_t cols,
+                                                          int64_t run, uint16_t* dz, int64_t ldz,
+                                                          float* partial) {
+  __shared__ float sums[kSumRows][kSumLanes * 8 + 1];
+  with_act(act, [&](auto a) {
+    act_grad_rows<BF16, decltype(a)::value>(dy, ldy, vec_y, z, vec_z, rows, cols, run, dz, ldz,
+                                            partial, sums);
+  });
+}
+
+// out[c] = sum of partial[0 .. parts)[c]: 16 columns a workgroup, thread (q, c)
+// adds the parts q, q + 64, ... in order, then the 64 sums are added pairwise
+__global__ __launch_bounds__(1024) void k_sum_parts(const float* __restrict__ partial, int64_t parts,
+                                                    int64_t ld, int64_t cols, int groups,
+                                                    float* __restrict__ out) {
+  __shared__ float sums[64][17];
+  const int cl = threadIdx.x & 15, q = threadIdx.x >> 4;
+  const int64_t c = static_cast<int64_t>(blockIdx.x) * 16 + cl;
+  float s = 0.0f;
+  if (c < cols) {
+    const int64_t gc = cols / groups, gp = ld / groups;
+    const int64_t at = c / gc * gp + c % gc;
+#pragma unroll 8
+    for (int64_t p = q; p < parts; p += 64) s += partial[p * ld + at];
+  }
+  sums[q][cl] = s;
+  __syncthreads();
+#pragma unroll
+  for (int w = 32; w > 0; w >>= 1) {
+    if (q < w) sums[q][cl] += sums[q + w][cl];
+    __syncthreads();
+  }
+  if (q == 0 && c < cols) out[c] = sums[0][cl];
+}
+
+int act_grad(const Mat16& dy, const uint16_t* z, int act, bool bf16, uint16_t* dz, int64_t ldz,
+             float* partial, hipStream_t stream) {
+  const int64_t strips = div_up(div_up(dy.cols, 8), kSumLanes);
+  const int64_t parts = column_parts(dy.rows, dy.cols);
+  const int64_t run = div_up(div_up(dy.rows, parts), kSumRows) * kSumRows;
+  const bool vec_y = pieces_fit(dy);
+  const bool vec_z = aligned16(z) && dy.cols % 8 == 0;
+  const dim3 grid(static_cast<unsigned>(strips), static_cast<unsigned>(parts));
+  if (bf16)
+    k_act_grad<true><<<grid, kSumThreads, 0, stream>>>(dy.p, dy.ld, vec_y, z, vec_z, act, dy.rows,
+                                                       dy.cols, run, dz, ldz, partial);
+  else
+    k_act_grad<false><<<grid, kSumThreads, 0, stream>>>(dy.p, dy.ld, vec_y, z, vec_z, act, dy.rows,
+                                                        dy.cols, run, dz, ldz, partial);
+  SUBMCONV_HIP_CHECK(hipGetLastError());
+  return SUBMCONV_OK;
+}
+
+// ---- weight gradient ----
+
+// One BM x BN tile of x^T dz over one run of rows, as fp32 partial sums.
+template <bool BF16, int BM, int BN, int WM, int WN, int STAGES>
+__global__ __launch_bounds__(WM* WN * 64) void k_weight_grad(Operand X, Operand Z, int64_t rows,
+                                                             int64_t run, int64_t m_tiles,
+                                                             int64_t n_tiles,
+                                                             float* __restrict__ partial) {
+  using T = Tile<BF16, true, true, false, BM, BN, WM, WN, STAGES>;
+  __shared__ __attribute__((aligned(16))) char smem[T::LDS_BYTES];
+  const TilePos t = tile_pos(gridDim.x / (m_tiles * n_tiles), m_tiles * n_tiles, blockIdx.x);
+  const int64_t m0 = t.n / n_tiles * BM, n0 = t.n % n_tiles * BN;
+  const int64_t kb = t.m * run, ke = min(rows, kb + run);
+  float4v acc[T::FN][T::FM];
+  T::run(X, Z, 0, m0, n0, kb, ke, smem, acc);
+  const int lane = threadIdx.x & 63, g = lane >> 4, s = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  float* out = partial + t.m * X.rows * Z.rows;
+#pragma unroll
+  for (int i = 0; i < T::FM; ++i) {
+    const int64_t m = m0 + (wave / WN) * (BM / WM) + i * 16 + s;
+    if (m >= X.rows) continue;
+#pragma unroll
+    for (int j = 0; j < T::FN; ++j) {
+      const int64_t n = n0 + (wave % WN) * (BN / WN) + j * 16 + g * 4;
+      if (n < Z.rows) *reinterpret_cast<float4v*>(out + m * Z.rows + n) = acc[j][i];
+    }
+  }
+}
+
+// out = the partial sums of the runs added in order, rounded once; columns of
+// `groups` padded groups are closed up
+template <bool BF16>
+__global__ __launch_bounds__(256) void k_weight_sum(const float* __restrict__ partial, int64_t runs,
+                                                    int64_t plane, int64_t ldp, int64_t rows,
+                                                    int64_t cols, int groups,
+                                                    uint16_t* __restrict__ out) {
+  __shared__ float4v sums[4][64];
+  const int cl = threadIdx.x & 63, q = threadIdx.x >> 6;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 64 + cl;  // float4 of a plane
+  const bool in = i * 4 < plane;
+  float4v s = {};
+  if (in) {
+    const int64_t per = (runs + 3) / 4, end = min(runs, (q + 1) * per);
+#pragma unroll 4
+    for (int64_t p = q * per; p < end; ++p)
+      s += *reinterpret_cast<const float4v*>(partial + p * plane + i * 4);
+  }
+  sums[q][cl] = s;
+  __syncthreads();
+  if (q != 0 || !in) return;
+  s = (sums[0][cl] + sums[1][cl]) + (sums[2][cl] + sums[3][cl]);
+  const int64_t r = i * 4 / ldp, c = i * 4 - r * ldp;
+  if (r >= rows) return;
+  const int64_t gp = ldp / groups, gc = cols / groups;
+  const int64_t grp = c / gp, cc = c - grp * gp;
+  uint16_t* o = out + r * cols + grp * gc + cc;
+  if (cc + 4 <= gc && (reinterpret_cast<uintptr_t>(o) & 7) == 0) {
+    *reinterpret_cast<u32x2*>(o) = pack4<BF16>(s);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (cc + e < gc) o[e] = to_16<BF16>(s[e]);
+  }
+}
+
+constexpr int kGradTile = 128;
+
+// Runs of rows of a weight gradient: enough workgroups for two per compute
+// unit, runs of at least 256 rows and a multiple of 64.
+int64_t grad_run(int64_t rows, int64_t cin, int64_t cols) {
+  const int64_t tiles = div_up(cin, kGradTile) * div_up(cols, kGradTile);
+  const int64_t runs = std::max<int64_t>(1, std::min(div_up(512, tiles), div_up(rows, 256)));
+  return std::max<int64_t>(kStepK, div_up(div_up(rows, runs), kStepK) * kStepK);
+}
+
+}  // namespace
+
+bool pieces_fit(const Mat16& a) { return aligned16(a.p) && a.ld % 8 == 0 && a.cols % 8 == 0; }
+
+int64_t packed_bytes(int64_t rows, int64_t cols, int groups) {
+  return rows * groups * round8(cols / groups) * 2;
+}
+
+int pack16(const Mat16& a, int groups, void* to, Mat16* out, hipStream_t stream) {
+  const int64_t gp = round8(a.cols / groups);
+  *out = Mat16{static_cast<const uint16_t*>(to), a.rows, groups * gp, groups * gp};
+  const int64_t pieces = a.rows * groups * gp / 8;
+  if (pieces == 0) return SUBMCONV_OK;
+  const unsigned blocks = static_cast<unsigned>(std::min<int64_t>(div_up(pieces, 256), 8192));
+  k_pack16<<<blocks, 256, 0, stream>>>(a.p, a.rows, a.cols, a.ld, groups, gp,
+                                       static_cast<uint16_t*>(to));
+  SUBMCONV_HIP_CHECK(hipGetLastError());
+  return SUBMCONV_OK;
+}
+
+int sum_parts(const float* partial, int64_t parts, int64_t ld, int64_t cols, int groups, float* out,
+              hipStream_t stream) {
+  k_sum_parts<<<static_cast<unsigned>(div_up(cols, 16)), 1024, 0, stream>>>(partial, parts, ld, cols,
+                                                                            groups, out);
+  SUBMCONV_HIP_CHECK(hipGetLastError());
+  return SUBMCONV_OK;
+}
+
+int64_t column_parts(int64_t rows, int64_t cols) {
+  const int64_t strips = div_up(div_up(cols, 8), kSumLanes);
+  return std::max<int64_t>(1, std::min(div_up(1024, strips), div_up(rows, 4 * kSumRows)));
+}
+
+int column_sums(const Mat16& a, bool bf16, float* partial, float* out, hipStream_t stream) {
+  const int st = act_grad(a, nullptr, kActNone, bf16, nullptr, 0, partial, stream);
+  if (st != SUBMCONV_OK) return st;
+  return sum_parts(partial, column_parts(a.rows, a.cols), round8(a.cols), a.cols, 1, out, stream);
+}
+
+int linear_forward(const Mat16& x, const Mat16& W, const float* bias, int act, bool bf16,
+                   const uint16_t* residual, int64_t ldr, uint16_t* out, int64_t ldo, uint16_t* pre,
+                   int64_t cols, hipStream_t stream) {
+  const LinearEpi e{bias, residual, ldr, out, ldo, pre, act,
+                    cols % 8 == 0 && ldr % 8 == 0 && aligned16(residual),
+                    cols % 8 == 0 && ldo % 8 == 0 && aligned16(out),
+                    cols % 8 == 0 && aligned16(pre)};
+  return linear_product<true>(Operand{x.p, x.ld, x.rows, x.cols}, Operand{W.p, W.ld, W.cols, W.rows}, x.cols, cols,
+                              bf16, e, stream);
+}
+
+int product_nt(const Mat16& dz, const Mat16& W, bool bf16, uint16_t* out, int64_t ldo,
+               int64_t cols, hipStream_t stream) {
+  const LinearEpi e{nullptr, nullptr, 0, out, ldo, nullptr, kActNone,
+                    false, cols % 8 == 0 && ldo % 8 == 0 && aligned16(out), false};
+  return linear_product<false>(Operand{dz.p, dz.ld, dz.rows, dz.cols}, Operand{W.p, W.ld, W.rows, W.cols}, dz.cols,
+                               cols, bf16, e, stream);
+}
+
+int64_t product_tn_bytes(int64_t rows, int64_t cin, int64_t cols) {
+  return std::max<int64_t>(1, div_up(rows, grad_run(rows, cin, cols))) * cin * cols * 4;
+}
+
+int product_tn(const Mat16& x, const Mat16& dz, bool bf16, float* partial, uint16_t* out,
+               int64_t cols_x, int64_t cols_z, int groups, hipStream_t stream) {
+  const int64_t run = grad_run(x.rows, x.cols, dz.cols);
+  const int64_t runs = std::max<int64_t>(1, div_up(x.rows, run));
+  const int64_t mt = div_up(x.cols, kGradTile), nt = div_up(dz.cols, kGradTile);
+  if (runs * mt * nt > INT32_MAX || div_up(x.cols * dz.cols, 256) > INT32_MAX)
+    return set_error(SUBMCONV_ERR_UNSUPPORTED_SHAPE, "weight gradient %lld x %lld",
+                     (long long)x.cols, (long long)dz.cols);
+  const Operand X{x.p, x.ld, x.cols, x.rows}, Z{dz.p, dz.ld, dz.cols, x.rows};
+  const dim3 grid(static_cast<unsigned>(runs * mt * nt));
+  if (bf16)
+    k_weight_grad<true, kGradTile, kGradTile, 2, 2, 2><<<grid, 256, 0, stream>>>(X, Z, x.rows, run, mt, nt, partial);
+  else
+    k_weight_grad<false, kGradTile, kGradTile, 2, 2, 2><<<grid, 256, 0, stream>>>(X, Z, x.rows, run, mt, nt, partial);
+  SUBMCONV_HIP_CHECK(hipGetLastError());
+  const int64_t plane = x.cols * dz.cols;
+  const dim3 rgrid(static_cast<unsigned>(div_up(plane, 256)));
+  if (bf16)
+    k_weight_sum<true><<<rgrid, 256, 0, stream>>>(partial, runs, plane, dz.cols, cols_x, cols_z, groups, out);
+  else
+    k_weight_sum<false><<<rgrid, 256, 0, stream>>>(partial, runs, plane, dz.cols, cols_x, cols_z, groups, out);
+  SUBMCONV_HIP_CHECK(hipGetLastError());
+  return SUBMCONV_OK;
+}
+
+int readable(const Mat16& a, int groups, Arena& ws, Mat16* out, hipStream_t stream) {
+  if (pieces_fit(a) && a.cols % (8 * groups) == 0) {
+    *out = a;
+    return SUBMCONV_OK;
+  }
+  void* to = ws.take(packed_bytes(a.rows, a.cols, groups));
+  if (ws.counting) return SUBMCONV_OK;
+  return pack16(a, groups, to, out, stream);
+}
+
+int check_shape(const char* name, int64_t rows, int64_t cols) {
+  if (cols < 1 || cols > (int64_t{1} << 20))
+    return set_error(SUBMCONV_ERR_UNSUPPORTED_SHAPE, "%s has %lld columns", name, (long long)cols);
+  if (rows < 0)
+    return set_error(SUBMCONV_ERR_INVALID_ARG, "%s has %lld rows", name, (long long)rows);
+  return SUBMCONV_OK;
+}
+
+int check_matrix(const char* name, const void* p, int64_t rows, int64_t cols, int64_t ld) {
+  SUBMCONV_TRY(check_shape(name, rows, cols));
+  if (rows > 0 && !p) return set_error(SUBMCONV_ERR_INVALID_ARG, "%s is NULL", name);
+  if (rows > 1 && ld < cols)
+    return set_error(SUBMCONV_ERR_INVALID_ARG, "%s: row stride %lld below %lld columns", name,
+                     (long long)ld, (long long)cols);
+  if (rows > 1 && ld > kMaxLd)
+    return set_error(SUBMCONV_ERR_UNSUPPORTED_SHAPE, "%s: row stride %lld above %lld", name,
+                     (long long)ld, (long long)kMaxLd);
+  if (reinterpret_cast<uintptr_t>(p) & 1)
+    return set_error(SUBMCONV_ERR_INVALID_ARG, "%s is not aligned to its elements", name);
+  return SUBMCONV_OK;
+}
+
+int check_workspace(const void* ws, int64_t have, int64_t need) {
+  if (need > 0 && (!ws || have < need))
+    return set_error(SUBMCONV_ERR_INVALID_ARG, "workspace of %lld bytes, %lld are needed",
+                     (long long)(ws ? have : 0), (long long)need);
+  if (!aligned16(ws)) return set_error(SUBMCONV_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
+  return SUBMCONV_OK;
+}
+
+int check_kind(int32_t act, int32_t dtype) {
+  if (act < kActNone || act > kActGeluTanh)
+    return set_error(SUBMCONV_ERR_INVALID_ARG, "act = %d", act);
+  if (dtype != SUBMCONV_DTYPE_F16 && dtype != SUBMCONV_DTYPE_BF16)
+    return set_error(SUBMCONV_ERR_INVALID_ARG, "dtype = %d", dtype);
+  return SUBMCONV_OK;
+}
+
+Mat16 shape_of(int64_t rows, int64_t cols, bool aligned) {
+  return Mat16{reinterpret_cast<const uint16_t*>(aligned ? 16 : 2), rows, cols, aligned ? round8(cols) : cols};
+}
+
+namespace {
+
+struct LinearWork {
+  Mat16 x, W;
+};
+int linear_work(const Mat16& x, const Mat16& W, Arena& ws, LinearWork* w, hipStream_t stream) {
+  SUBMCONV_TRY(readable(x, 1, ws, &w->x, stream));
+  return readable(W, 1, ws, &w->W, stream);
+}
+
+struct LinearGradNeeds {
+  bool x, w, b;
+};
+// The gradients' steps, or with an arena that counts, their workspace.
+int linear_grad(const Mat16& dy, const Mat16& x, const Mat16& W, const uint16_t* pre, int act,
+                bool bf16, uint16_t* gx, uint16_t* gw, float* gb, LinearGradNeeds need, Arena& ws,
+                hipStream_t stream) {
+  const bool run = !ws.counting;
+  const int64_t cp = round8(dy.cols);
+  const bool own_dz = act != kActNone || !pieces_fit(dy);
+  Mat16 dz = dy;
+  uint16_t* dz_to = nullptr;
+  if (own_dz) {
+    dz_to = static_cast<uint16_t*>(ws.take(dy.rows * cp * 2));
+    dz = Mat16{dz_to, dy.rows, cp, cp};
+  }
+  const int64_t parts = column_parts(dy.rows, dy.cols);
+  float* sums = need.b ? static_cast<float*>(ws.take(parts * cp * 4)) : nullptr;
+  if (run && (own_dz || need.b)) {
+    SUBMCONV_TRY(act_grad(dy, pre, act, bf16, dz_to, cp, sums, stream));
+    if (need.b) SUBMCONV_TRY(sum_parts(sums, parts, cp, dy.cols, 1, gb, stream));
+  }
+  if (need.x) {
+    Mat16 Wr;
+    SUBMCONV_TRY(readable(W, 1, ws, &Wr, stream));
+    if (run) SUBMCONV_TRY(product_nt(dz, Wr, bf16, gx, x.cols, x.cols, stream));
+  }
+  if (need.w) {
+    Mat16 xr;
+    SUBMCONV_TRY(readable(x, 1, ws, &xr, stream));
+    float* part = static_cast<float*>(ws.take(product_tn_bytes(x.rows, round8(x.cols), cp)));
+    if (run) SUBMCONV_TRY(product_tn(xr, dz, bf16, part, gw, x.cols, dy.cols, 1, stream));
+  }
+  return SUBMCONV_OK;
+}
+
+}  // namespace
+}  // namespace submconv
+
+using namespace submconv;
+
+extern "C" int64_t submconv_linear_workspace_bytes(int64_t n, int32_t cin, int32_t cout,
+                                                   int32_t aligned) {
+  clear_error();
+  SUBMCONV_TRY(check_shape("x", n, cin));
+  SUBMCONV_TRY(check_shape("W", cin, cout));
+  Arena ws;
+  LinearWork w;
+  SUBMCONV_TRY(linear_work(shape_of(n, cin, aligned), shape_of(cin, cout, aligned), ws, &w, nullptr));
+  return ws.used;
+}
+
+extern "C" int submconv_linear(const uint16_t* x, int64_t ldx, int64_t n, const uint16_t* W,
+                               const float* bias, const uint16_t* residual, int64_t ldr,
+                               uint16_t* out, uint16_t* pre, int32_t cin, int32_t cout, int32_t act,
+                               int32_t dtype, void* workspace, int64_t workspace_bytes,
+                               hipStream_t stream) {
+  clear_error();
+  SUBMCONV_TRY(check_kind(act, dtype));
+  SUBMCONV_TRY(check_matrix("x", x, n, cin, ldx));
+  SUBMCONV_TRY(check_matrix("W", W, cin, cout, cout));
+  SUBMCONV_TRY(check_matrix("out", out, n, cout, cout));
+  if (residual) SUBMCONV_TRY(check_matrix("residual", residual, n, cout, ldr));
+  if (pre) SUBMCONV_TRY(check_matrix("pre", pre, n, cout, cout));
+  if (n == 0) return SUBMCONV_OK;
+  const Mat16 xm{x, n, cin, n == 1 ? round8(cin) : ldx}, wm{W, cin, cout, cout};
+  Arena need;
+  LinearWork w;
+  SUBMCONV_TRY(linear_work(xm, wm, need, &w, stream));
+  SUBMCONV_TRY(check_workspace(workspace, workspace_bytes, need.used));
+  Arena ws{false, static_cast<char*>(workspace)};
+  if (need.used > 0) SUBMCONV_TRY(linear_work(xm, wm, ws, &w, stream));
+  return linear_forward(w.x, w.W, bias, act, dtype == SUBMCONV_DTYPE_BF16, residual,
+                        n == 1 ? round8(cout) : ldr, out, cout, pre, cout, stream);
+}
+
+extern "C" int64_t submconv_linear_backward_workspace_bytes(int64_t n, int32_t cin, int32_t cout,
+                                                            int32_t act, int32_t aligned) {
+  clear_error();
+  SUBMCONV_TRY(check_kind(act, SUBMCONV_DTYPE_F16));
+  SUBMCONV_TRY(check_shape("x", n, cin));
+  SUBMCONV_TRY(check_shape("W", cin, cout));
+  Arena ws;
+  SUBMCONV_TRY(linear_grad(shape_of(n, cout, aligned), shape_of(n, cin, aligned),
+                           shape_of(cin, cout, aligned), nullptr, act, false, nullptr, nullptr,
+                           nullptr, {true, true, true}, ws, nullptr));
+  return ws.used;
+}
+
+extern "C" int submconv_linear_backward(const uint16_t* grad_out, int64_t ldg, int64_t n,
+                                        const uint16_t* x, int64_t ldx, const uint16_t* W,
+                                        const uint16_t* pre, uint16_t* grad_x, uint16_t* grad_w,
+                                        float* grad_b, int32_t cin, int32_t cout, int32_t act,
+                                        int32_t dtype, void* workspace, int64_t workspace_bytes,
+                                        hipStream_t stream) {
+  clear_error();
+  SUBMCONV_TRY(check_kind(act, dtype));
+  SUBMCONV_TRY(check_matrix("grad_out", grad_out, n, cout, ldg));
+  if (grad_w) SUBMCONV_TRY(check_matrix("x", x, n, cin, ldx));
+  SUBMCONV_TRY(check_matrix("W", W, cin, cout, cout));
+  if (act != kActNone) SUBMCONV_TRY(check_matrix("pre", pre, n, cout, cout));
+  const Mat16 dy{grad_out, n, cout, n == 1 ? round8(cout) : ldg};
+  const Mat16 xm{x, n, cin, n == 1 ? round8(cin) : ldx}, wm{W, cin, cout, cout};
+  const LinearGradNeeds need{grad_x != nullptr, grad_w != nullptr, grad_b != nullptr};
+  Arena count;
+  const bool bf16 = dtype == SUBMCONV_DTYPE_BF16;
+  SUBMCONV_TRY(linear_grad(dy, xm, wm, pre, act, bf16, grad_x, grad_w, grad_b, need, count, stream));
+  SUBMCONV_TRY(check_workspace(workspace, workspace_bytes, count.used));
+  Arena ws{false, static_cast<char*>(workspace)};
+  return linear_grad(dy, xm, wm, pre, act, bf16, grad_x, grad_w, grad_b, need, ws, stream);
+}
