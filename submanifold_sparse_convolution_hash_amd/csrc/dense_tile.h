@@ -13,13 +13,14 @@
 // no operand is ever transposed in memory.
 //
 // v_mfma_f32_16x16x32 takes n as its row index and m as its column index, so
-// that a lane ends with 4 consecutive n of one m; v_permlane16_swap then pairs
-// two accumulators into 8 consecutive n, the 16 bytes of one store.
+// that a lane ends with 4 consecutive n of one m. The epilogue passes the fp32
+// accumulators through LDS once, so that each thread then holds 8 consecutive
+// columns of a row and neighbouring threads the row's next ones: bias,
+// activation, residual and every load and store work on whole memory lines.
 #pragma once
 
 #include <type_traits>
 
-#include "lane_ops.h"
 #include "submconv_internal.h"
 
 namespace submconv {
@@ -31,6 +32,7 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef short v4s __attribute__((ext_vector_type(4)));
 typedef float float4v __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) void lds_void;
 typedef __attribute__((address_space(3))) v4s lds_v4s;
@@ -71,14 +73,15 @@ __device__ __forceinline__ u32x2 pack4(float4v v) {
   }
 }
 template <bool BF16>
-__device__ __forceinline__ float4v unpack4(u32x2 v) {
-  float4v r;
+__device__ __forceinline__ u32x4 pack8(const float (&v)[8]) {
+  const u32x2 a = pack4<BF16>(float4v{v[0], v[1], v[2], v[3]});
+  const u32x2 b = pack4<BF16>(float4v{v[4], v[5], v[6], v[7]});
+  return u32x4{a[0], a[1], b[0], b[1]};
+}
+template <bool BF16>
+__device__ __forceinline__ void unpack8(u32x4 p, float (&v)[8]) {
 #pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    r[2 * e] = to_f32<BF16>(static_cast<uint16_t>(v[e]));
-    r[2 * e + 1] = to_f32<BF16>(static_cast<uint16_t>(v[e] >> 16));
-  }
-  return r;
+  for (int e = 0; e < 8; ++e) v[e] = to_f32<BF16>(static_cast<uint16_t>(p[e >> 1] >> (16 * (e & 1))));
 }
 
 template <bool BF16>
@@ -143,26 +146,13 @@ struct RowsView {
   }
 };
 
-// Four consecutive values of an fp32 vector of n_end, zeros past it.
-__device__ __forceinline__ float4v load_bias4(__amdgpu_buffer_rsrc_t r, uint32_t n) {
-  float4v v;
+// Eight consecutive values of an fp32 vector, zeros past its end (all of them
+// for a null vector, whose buffer holds nothing).
+__device__ __forceinline__ void load_bias8(const float* p, int64_t n_end, uint32_t n, float (&v)[8]) {
+  const __amdgpu_buffer_rsrc_t r = tile_rsrc(p, p ? static_cast<uint32_t>(n_end) * 4u : 0u);
 #pragma unroll
-  for (uint32_t e = 0; e < 4; ++e)
+  for (uint32_t e = 0; e < 8; ++e)
     v[e] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(r, (n + e) * 4u, 0, 0));
-  return v;
-}
-
-// Two accumulators' packed quads (n blocks j and j + 1; lane group g = lane /
-// 16 holds n = 4 g .. 4 g + 3) <-> 8 consecutive n: lane group g then holds n
-// block j + (g & 1), columns 8 (g >> 1) ... The exchange is its own inverse.
-__device__ __forceinline__ u32x4 join_quads(u32x2 p, u32x2 q) {
-  const u32x2 a = lane_rows_swap(p[0], q[0]), b = lane_rows_swap(p[1], q[1]);
-  return u32x4{a[0], b[0], a[1], b[1]};
-}
-__device__ __forceinline__ void split_quads(u32x4 v, u32x2& p, u32x2& q) {
-  const u32x2 a = lane_rows_swap(v[0], v[2]), b = lane_rows_swap(v[1], v[3]);
-  p = u32x2{a[0], b[0]};
-  q = u32x2{a[1], b[1]};
 }
 
 // ---- activations ----
@@ -443,6 +433,41 @@ struct Tile {
           for (int j = 0; j < FN; ++j) acc[j][i] = mfma16<BF16>(fb[j], fa[i], acc[j][i]);
       }
       buf = buf + 1 == STAGES ? 0 : buf + 1;
+    }
+  }
+
+  // ---- the accumulators as rows ----
+  //
+  // to_rows leaves the tile in LDS as fp32 rows, read8 takes 8 columns of one.
+  // The 16-byte piece p of row r sits at p ^ (r % 16) ^ (p / 16 % 2), which
+  // keeps the 16 rows of a write and the 16 pieces of a read apart.
+  static constexpr int PIECES = BN / 8;           // 8-column pieces per row
+  static constexpr int ROW_STEP = NT / PIECES;    // rows between a thread's pieces
+  static constexpr int ROW_PASSES = BM / ROW_STEP;
+  static_assert(BM * BN * 4 <= LDS_BYTES, "the rows fit the operand buffers");
+  static __device__ __forceinline__ int row_byte(int r, int p) {
+    return r * (BN * 4) + ((p ^ (r & 15) ^ (p >> 4 & 1)) << 4);
+  }
+  static __device__ __forceinline__ void to_rows(char* smem, const float4v (&acc)[FN][FM]) {
+    const int lane = threadIdx.x & 63, g = lane >> 4, s = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave / WN, wn = wave % WN;
+    __syncthreads();  // every wave has read its last operands
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; ++j)
+        *reinterpret_cast<float4v*>(smem + row_byte(wm * (BM / WM) + i * 16 + s, ncol(wn, j) / 4 + g)) =
+            acc[j][i];
+    __syncthreads();
+  }
+  static __device__ __forceinline__ void read8(const char* smem, int r, int piece, float (&v)[8]) {
+    const float4v a = *reinterpret_cast<const float4v*>(smem + row_byte(r, 2 * piece));
+    const float4v b = *reinterpret_cast<const float4v*>(smem + row_byte(r, 2 * piece + 1));
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      v[e] = a[e];
+      v[4 + e] = b[e];
     }
   }
 

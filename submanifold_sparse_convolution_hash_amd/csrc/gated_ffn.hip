@@ -33,43 +33,37 @@ struct GateEpi {
   bool vec_p;
 };
 
-template <bool BF16, int ACT, int BM, int FN, int FM>
-__device__ __forceinline__ void gate_epilogue(const GateEpi& e, int64_t M, int64_t m0, uint32_t mw,
-                                              uint32_t nb, int lane, float4v (&acc)[FN][FM]) {
-  constexpr int H = FN / 2;  // accumulator columns of the gate; then the up projection's
-  const int g = lane >> 4, s = lane & 15;
+template <bool BF16, int ACT, typename T, int BM>
+__device__ __forceinline__ void gate_epilogue(const GateEpi& e, int64_t M, int64_t m0, uint32_t n0,
+                                              const char* smem) {
+  // a row in LDS: the gate's columns, then the up projection's
+  constexpr int HP = T::PIECES / 2, STEP = T::NT / HP;
+  const int piece = threadIdx.x % HP, r0 = threadIdx.x / HP;
+  const uint32_t n = n0 + piece * 8;
   const RowsView h(e.h, e.Fp, m0, M, e.Fp, BM, true);
   const RowsView pg(e.pre, 2 * e.F, m0, M, e.F, BM, e.vec_p);
   const RowsView pu(e.pre ? e.pre + e.F : nullptr, 2 * e.F, m0, M, e.F, BM, e.vec_p);
-  const uint32_t bytes = e.bias ? static_cast<uint32_t>(e.F) * 4u : 0u;
-  const __amdgpu_buffer_rsrc_t bg = tile_rsrc(e.bias, bytes);
-  const __amdgpu_buffer_rsrc_t bu = tile_rsrc(e.bias ? e.bias + e.F : nullptr, bytes);
+  float bg[8], bu[8];
+  load_bias8(e.bias, e.F, n, bg);
+  load_bias8(e.bias ? e.bias + e.F : nullptr, e.F, n, bu);
 #pragma unroll
-  for (int j = 0; j < H; j += 2) {
-    float4v b[2][2];
+  for (int p = 0; p < BM / STEP; ++p) {
+    const int m = r0 + p * STEP;
+    float g[8], u[8];
+    T::read8(smem, m, piece, g);
+    T::read8(smem, m, HP + piece, u);
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      b[0][q] = load_bias4(bg, nb + (j + q) * 16 + g * 4);
-      b[1][q] = load_bias4(bu, nb + (j + q) * 16 + g * 4);
+    for (int q = 0; q < 8; ++q) {
+      g[q] += bg[q];
+      u[q] += bu[q];
     }
-    const uint32_t n = nb + j * 16 + (g & 1) * 16 + (g >> 1) * 8;
-#pragma unroll
-    for (int i = 0; i < FM; ++i) {
-      const uint32_t m = mw + i * 16 + s;
-      float4v zg[2], zu[2], v[2];
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        zg[q] = acc[j + q][i] + b[0][q];
-        zu[q] = acc[H + j + q][i] + b[1][q];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) v[q][r] = act_value<ACT>(zg[q][r]) * zu[q][r];
-      }
-      if (e.pre) {
-        pg.store(m, n, join_quads(pack4<BF16>(zg[0]), pack4<BF16>(zg[1])));
-        pu.store(m, n, join_quads(pack4<BF16>(zu[0]), pack4<BF16>(zu[1])));
-      }
-      h.store(m, n, join_quads(pack4<BF16>(v[0]), pack4<BF16>(v[1])));
+    if (e.pre) {
+      pg.store(m, n, pack8<BF16>(g));
+      pu.store(m, n, pack8<BF16>(u));
     }
+#pragma unroll
+    for (int q = 0; q < 8; ++q) g[q] = act_value<ACT>(g[q]) * u[q];
+    h.store(m, n, pack8<BF16>(g));
   }
 }
 
@@ -82,12 +76,9 @@ __global__ __launch_bounds__(WM* WN * 64) void k_gate(Operand A, Operand B, int6
   const int64_t m0 = t.m * BM, n0 = t.n * (BN / 2);
   float4v acc[T::FN][T::FM];
   T::run(A, B, half, m0, n0, 0, K, smem, acc);
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const uint32_t mw = (wave / WN) * (BM / WM);
-  const uint32_t nb = static_cast<uint32_t>(n0) + (wave % WN) * (BN / WN / 2);
+  T::to_rows(smem, acc);
   with_act(e.act, [&](auto a) {
-    gate_epilogue<BF16, decltype(a)::value, BM>(e, A.rows, m0, mw, nb, lane, acc);
+    gate_epilogue<BF16, decltype(a)::value, T, BM>(e, A.rows, m0, static_cast<uint32_t>(n0), smem);
   });
 }
 
@@ -103,60 +94,38 @@ struct GateGradEpi {
   bool vec_p;
 };
 
-template <bool BF16, int ACT, int BM, int BN, int WM, int FN, int FM>
-__device__ __forceinline__ void gate_grad_epilogue(const GateGradEpi& e, int64_t M, int64_t m_tile,
-                                                   int wave_m, uint32_t nt, uint32_t nb, int lane,
-                                                   float* red, float4v (&acc)[FN][FM]) {
-  const int g = lane >> 4, s = lane & 15;
-  const int64_t m0 = m_tile * BM;
-  const uint32_t mw = wave_m * (BM / WM);
+template <bool BF16, int ACT, typename T, int BM>
+__device__ __forceinline__ void gate_grad_epilogue(const GateGradEpi& e, int64_t M, int64_t m0,
+                                                   uint32_t n0, const char* smem, float (&sg)[8],
+                                                   float (&su)[8]) {
+  const int piece = threadIdx.x % T::PIECES, r0 = threadIdx.x / T::PIECES;
+  const uint32_t n = n0 + piece * 8;
   const RowsView pg(e.pre, 2 * e.F, m0, M, e.F, BM, e.vec_p);
   const RowsView pu(e.pre + e.F, 2 * e.F, m0, M, e.F, BM, e.vec_p);
   const RowsView zg(e.dz, 2 * e.Fp, m0, M, e.Fp, BM, true);
   const RowsView zu(e.dz + e.Fp, 2 * e.Fp, m0, M, e.Fp, BM, true);
   const RowsView h(e.h, e.Fp, m0, M, e.Fp, BM, true);
 #pragma unroll
-  for (int j = 0; j < FN; j += 2) {
-    const uint32_t n = nb + j * 16 + (g & 1) * 16 + (g >> 1) * 8;
-    float4v sum[2][2] = {};
+  for (int p = 0; p < T::ROW_PASSES; ++p) {
+    const int m = r0 + p * T::ROW_STEP;
+    float g[8], u[8], dh[8];
+    unpack8<BF16>(pg.load(m, n), g);
+    unpack8<BF16>(pu.load(m, n), u);
+    T::read8(smem, m, piece, dh);
+    float dg[8], du[8], v[8];
 #pragma unroll
-    for (int i = 0; i < FM; ++i) {
-      const uint32_t m = mw + i * 16 + s;
-      u32x2 rg[2], ru[2];
-      split_quads(pg.load(m, n), rg[0], rg[1]);
-      split_quads(pu.load(m, n), ru[0], ru[1]);
-      float4v dg[2], du[2], v[2];
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const float4v xg = unpack4<BF16>(rg[q]), xu = unpack4<BF16>(ru[q]);
-        const float4v dh = acc[j + q][i];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          float a, d;
-          act_both<ACT>(xg[r], a, d);
-          dg[q][r] = dh[r] * xu[r] * d;
-          du[q][r] = dh[r] * a;
-          v[q][r] = a * xu[r];
-        }
-        sum[0][q] += dg[q];
-        sum[1][q] += du[q];
-      }
-      zg.store(m, n, join_quads(pack4<BF16>(dg[0]), pack4<BF16>(dg[1])));
-      zu.store(m, n, join_quads(pack4<BF16>(du[0]), pack4<BF16>(du[1])));
-      h.store(m, n, join_quads(pack4<BF16>(v[0]), pack4<BF16>(v[1])));
+    for (int q = 0; q < 8; ++q) {
+      float a, d;
+      act_both<ACT>(g[q], a, d);
+      dg[q] = dh[q] * u[q] * d;
+      du[q] = dh[q] * a;
+      v[q] = a * u[q];
+      sg[q] += dg[q];  // rows past M add zeros: their dout is read as zeros
+      su[q] += du[q];
     }
-    if (e.sums) {
-      // rows past M add zeros: their dout is read as zeros
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int q = 0; q < 2; ++q)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const float x = lanes_sum<16>(sum[t][q][r]);
-            if (s == 0) red[(wave_m * 2 + t) * BN + (nb - nt) + (j + q) * 16 + g * 4 + r] = x;
-          }
-    }
+    zg.store(m, n, pack8<BF16>(dg));
+    zu.store(m, n, pack8<BF16>(du));
+    h.store(m, n, pack8<BF16>(v));
   }
 }
 
@@ -170,24 +139,28 @@ __global__ __launch_bounds__(WM* WN * 64) void k_gate_grad(Operand A, Operand B,
   const int64_t m0 = t.m * BM, n0 = t.n * BN;
   float4v acc[T::FN][T::FM];
   T::run(A, B, 0, m0, n0, 0, K, smem, acc);
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const uint32_t nt = static_cast<uint32_t>(n0);
-  const uint32_t nb = nt + (wave % WN) * (BN / WN);
-  float* red = reinterpret_cast<float*>(smem);  // [WM][2][BN], once every wave is done with the tiles
-  __syncthreads();
+  T::to_rows(smem, acc);
+  float sums[2][8] = {};
   with_act(e.act, [&](auto a) {
-    gate_grad_epilogue<BF16, decltype(a)::value, BM, BN, WM>(e, A.rows, t.m, wave / WN, nt, nb, lane,
-                                                             red, acc);
+    gate_grad_epilogue<BF16, decltype(a)::value, T, BM>(e, A.rows, m0, static_cast<uint32_t>(n0), smem,
+                                                        sums[0], sums[1]);
   });
   if (!e.sums) return;
+  // the threads that walked the same columns, in order
+  float* red = reinterpret_cast<float*>(smem);  // [ROW_STEP][2][BN]
+  const int piece = threadIdx.x % T::PIECES, r0 = threadIdx.x / T::PIECES;
   __syncthreads();
-  for (int c = threadIdx.x; c < 2 * BN; c += WM * WN * 64) {
-    const int half = c / BN, n = c % BN;
-    float x = red[half * BN + n];
 #pragma unroll
-    for (int w = 1; w < WM; ++w) x += red[(w * 2 + half) * BN + n];
-    if (n0 + n < e.Fp) e.sums[(t.m * 2 + half) * e.Fp + n0 + n] = x;
+  for (int t2 = 0; t2 < 2; ++t2)
+#pragma unroll
+    for (int q = 0; q < 8; ++q) red[(r0 * 2 + t2) * BN + piece * 8 + q] = sums[t2][q];
+  __syncthreads();
+  for (int c = threadIdx.x; c < 2 * BN; c += T::NT) {
+    float x = 0.0f;
+#pragma unroll
+    for (int r = 0; r < T::ROW_STEP; ++r) x += red[r * 2 * BN + c];
+    const int64_t n = n0 + c % BN;
+    if (n < e.Fp) e.sums[(t.m * 2 + c / BN) * e.Fp + n] = x;
   }
 }
 

@@ -29,37 +29,33 @@ struct LinearEpi {
   bool vec_r, vec_o, vec_p;
 };
 
-template <bool BF16, int ACT, int BM, int FN, int FM>
+template <bool BF16, int ACT, typename T, int BM>
 __device__ __forceinline__ void linear_epilogue(const LinearEpi& e, int64_t M, int64_t N,
-                                                int64_t m0, uint32_t mw, uint32_t nb, int lane,
-                                                float4v (&acc)[FN][FM]) {
-  const int g = lane >> 4, s = lane & 15;
+                                                int64_t m0, uint32_t n0, const char* smem) {
+  const int piece = threadIdx.x % T::PIECES, r0 = threadIdx.x / T::PIECES;
+  const uint32_t n = n0 + piece * 8;
   const RowsView out(e.out, e.ldo, m0, M, N, BM, e.vec_o);
   const RowsView pre(e.pre, N, m0, M, N, BM, e.vec_p);
   const RowsView res(e.residual, e.ldr, m0, M, N, BM, e.vec_r);
-  const __amdgpu_buffer_rsrc_t rb = tile_rsrc(e.bias, e.bias ? static_cast<uint32_t>(N) * 4u : 0u);
+  float b[8];
+  load_bias8(e.bias, N, n, b);
 #pragma unroll
-  for (int j = 0; j < FN; j += 2) {
-    const float4v b0 = load_bias4(rb, nb + j * 16 + g * 4);
-    const float4v b1 = load_bias4(rb, nb + j * 16 + 16 + g * 4);
-    const uint32_t n = nb + j * 16 + (g & 1) * 16 + (g >> 1) * 8;  // this lane's joined piece
+  for (int p = 0; p < T::ROW_PASSES; ++p) {
+    const int m = r0 + p * T::ROW_STEP;
+    float z[8];
+    T::read8(smem, m, piece, z);
 #pragma unroll
-    for (int i = 0; i < FM; ++i) {
-      const uint32_t m = mw + i * 16 + s;
-      float4v z[2] = {acc[j][i] + b0, acc[j + 1][i] + b1};
-      if (e.pre) pre.store(m, n, join_quads(pack4<BF16>(z[0]), pack4<BF16>(z[1])));
+    for (int q = 0; q < 8; ++q) z[q] += b[q];
+    if (e.pre) pre.store(m, n, pack8<BF16>(z));
 #pragma unroll
-      for (int q = 0; q < 2; ++q)
+    for (int q = 0; q < 8; ++q) z[q] = act_value<ACT>(z[q]);
+    if (e.residual) {
+      float v[8];
+      unpack8<BF16>(res.load(m, n), v);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) z[q][r] = act_value<ACT>(z[q][r]);
-      if (e.residual) {
-        u32x2 p, q;
-        split_quads(res.load(m, n), p, q);
-        z[0] += unpack4<BF16>(p);
-        z[1] += unpack4<BF16>(q);
-      }
-      out.store(m, n, join_quads(pack4<BF16>(z[0]), pack4<BF16>(z[1])));
+      for (int q = 0; q < 8; ++q) z[q] += v[q];
     }
+    out.store(m, n, pack8<BF16>(z));
   }
 }
 
@@ -74,12 +70,9 @@ __global__ __launch_bounds__(WM* WN * 64) void k_linear(Operand A, Operand B, in
   const int64_t m0 = t.m * BM, n0 = t.n * BN;
   float4v acc[T::FN][T::FM];
   T::run(A, B, 0, m0, n0, 0, K, smem, acc);
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const uint32_t mw = (wave / WN) * (BM / WM);
-  const uint32_t nb = static_cast<uint32_t>(n0) + (wave % WN) * (BN / WN);
+  T::to_rows(smem, acc);
   with_act(e.act, [&](auto a) {
-    linear_epilogue<BF16, decltype(a)::value, BM>(e, A.rows, N, m0, mw, nb, lane, acc);
+    linear_epilogue<BF16, decltype(a)::value, T, BM>(e, A.rows, N, m0, static_cast<uint32_t>(n0), smem);
   });
 }
 
@@ -141,26 +134,21 @@ __device__ __forceinline__ void act_grad_rows(const uint16_t* dy, int64_t ldy, b
   float s[8] = {};
   if (c < cols) {
     for (int64_t r = blockIdx.y * run + rl; r < r_end; r += kSumRows) {
-      const u32x4 v = load_piece(dy + r * ldy, c, cols, vec_y);
       float d[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) d[e] = to_f32<BF16>(static_cast<uint16_t>(v[e >> 1] >> (16 * (e & 1))));
+      unpack8<BF16>(load_piece(dy + r * ldy, c, cols, vec_y), d);
       if constexpr (ACT != kActNone) {
-        const u32x4 w = load_piece(z + r * cols, c, cols, vec_z);
+        float w[8];
+        unpack8<BF16>(load_piece(z + r * cols, c, cols, vec_z), w);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           float a, g;
-          act_both<ACT>(to_f32<BF16>(static_cast<uint16_t>(w[e >> 1] >> (16 * (e & 1)))), a, g);
+          act_both<ACT>(w[e], a, g);
           d[e] *= g;
         }
       }
 #pragma unroll
       for (int e = 0; e < 8; ++e) s[e] += d[e];
-      if (dz) {
-        const u32x2 lo = pack4<BF16>(float4v{d[0], d[1], d[2], d[3]});
-        const u32x2 hi = pack4<BF16>(float4v{d[4], d[5], d[6], d[7]});
-        *reinterpret_cast<u32x4*>(dz + r * ldz + c) = u32x4{lo[0], lo[1], hi[0], hi[1]};
-      }
+      if (dz) *reinterpret_cast<u32x4*>(dz + r * ldz + c) = pack8<BF16>(d);
     }
   }
   if (!partial) return;
