@@ -176,9 +176,9 @@ int gate_forward(const Mat16& x, const Mat16& W, int64_t F, const float* bias, i
   const Operand A{x.p, x.ld, x.rows, x.cols}, B{W.p, W.ld, Fp, W.rows};
   const dim3 grid(static_cast<unsigned>(mt * nt));
   if (bf16)
-    k_gate<true, kGateTile, kGateTile, 2, 2, 2><<<grid, 256, 0, stream>>>(A, B, x.cols, Fp, mt, nt, e);
+    k_gate<true, kGateTile, kGateTile, 2, 4, 2><<<grid, 512, 0, stream>>>(A, B, x.cols, Fp, mt, nt, e);
   else
-    k_gate<false, kGateTile, kGateTile, 2, 2, 2><<<grid, 256, 0, stream>>>(A, B, x.cols, Fp, mt, nt, e);
+    k_gate<false, kGateTile, kGateTile, 2, 4, 2><<<grid, 512, 0, stream>>>(A, B, x.cols, Fp, mt, nt, e);
   SUBMCONV_HIP_CHECK(hipGetLastError());
   return SUBMCONV_OK;
 }
@@ -196,9 +196,9 @@ int gate_grad(const Mat16& dy, const Mat16& W, int64_t Fp, const uint16_t* pre, 
   const Operand A{dy.p, dy.ld, dy.rows, dy.cols}, B{W.p, W.ld, F, W.cols};
   const dim3 grid(static_cast<unsigned>(mt * nt));
   if (bf16)
-    k_gate_grad<true, kGateTile, kGateTile, 2, 2, 2><<<grid, 256, 0, stream>>>(A, B, dy.cols, mt, nt, e);
+    k_gate_grad<true, kGateTile, kGateTile, 2, 4, 2><<<grid, 512, 0, stream>>>(A, B, dy.cols, mt, nt, e);
   else
-    k_gate_grad<false, kGateTile, kGateTile, 2, 2, 2><<<grid, 256, 0, stream>>>(A, B, dy.cols, mt, nt, e);
+    k_gate_grad<false, kGateTile, kGateTile, 2, 4, 2><<<grid, 512, 0, stream>>>(A, B, dy.cols, mt, nt, e);
   SUBMCONV_HIP_CHECK(hipGetLastError());
   return SUBMCONV_OK;
 }

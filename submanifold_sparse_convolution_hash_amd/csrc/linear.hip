@@ -95,7 +95,7 @@ template <bool B_ROW>
 int linear_product(const Operand& A, const Operand& B, int64_t K, int64_t N, bool bf16,
                    const LinearEpi& e, hipStream_t stream) {
   if (A.rows == 0 || N == 0) return SUBMCONV_OK;
-  return launch_linear<B_ROW, 128, 128, 2, 2, 2>(A, B, K, N, bf16, e, stream);
+  return launch_linear<B_ROW, 128, 128, 2, 4, 2>(A, B, K, N, bf16, e, stream);
 }
 
 // ---- padded copies ----
@@ -371,9 +371,9 @@ int product_tn(const Mat16& x, const Mat16& dz, bool bf16, float* partial, uint1
   const Operand X{x.p, x.ld, x.cols, x.rows}, Z{dz.p, dz.ld, dz.cols, x.rows};
   const dim3 grid(static_cast<unsigned>(runs * mt * nt));
   if (bf16)
-    k_weight_grad<true, kGradTile, kGradTile, 2, 2, 2><<<grid, 256, 0, stream>>>(X, Z, x.rows, run, mt, nt, partial);
+    k_weight_grad<true, kGradTile, kGradTile, 2, 4, 2><<<grid, 512, 0, stream>>>(X, Z, x.rows, run, mt, nt, partial);
   else
-    k_weight_grad<false, kGradTile, kGradTile, 2, 2, 2><<<grid, 256, 0, stream>>>(X, Z, x.rows, run, mt, nt, partial);
+    k_weight_grad<false, kGradTile, kGradTile, 2, 4, 2><<<grid, 512, 0, stream>>>(X, Z, x.rows, run, mt, nt, partial);
   SUBMCONV_HIP_CHECK(hipGetLastError());
   const int64_t plane = x.cols * dz.cols;
   const dim3 rgrid(static_cast<unsigned>(div_up(plane, 256)));
