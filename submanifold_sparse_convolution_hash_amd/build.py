@@ -26,7 +26,7 @@ VGPR_FORM = ["-mllvm", "-amdgpu-mfma-vgpr-form"]
 # sources whose MFMA accumulators stay in registers for a whole unit or tile
 # (64 to 128 per lane) are built without it: the accumulators take the AGPRs, the operands
 # the VGPRs
-AGPR_SOURCES = {"staged_wide.hip", "staged_bwd.hip", "linear.hip", "gated_ffn.hip"}
+AGPR_SOURCES = {"staged_wide.hip", "staged_bwd.hip"}
 
 
 def _compile(src, verbose):

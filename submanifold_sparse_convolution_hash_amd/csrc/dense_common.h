@@ -6,23 +6,27 @@
 
 namespace submconv {
 
-// A 16-bit matrix of `rows` rows, `cols` columns, `ld` elements between rows.
+// A 16-bit matrix of `rows` rows, `cols` columns, `ld` elements between rows;
+// or `blocked` (dense_tile.h), then `cols` is a multiple of 64.
 struct Mat16 {
   const uint16_t* p = nullptr;
   int64_t rows = 0, cols = 0, ld = 0;
+  bool blocked = false;
 };
+// A blocked matrix of the workspace and its bytes.
+inline Mat16 blocked16(const void* p, int64_t rows, int64_t cols) {
+  return Mat16{static_cast<const uint16_t*>(p), rows, cols, cols, true};
+}
+inline int64_t blocked_bytes(int64_t rows, int64_t cols) { return (rows + 127) / 128 * 128 * cols * 2; }
+
 
 // Whether a product can read the matrix as it is: 16-byte pieces that start
 // on 16 bytes and never straddle a row's end.
 bool pieces_fit(const Mat16& a);
 
-// Bytes of a packed copy: rows x groups x round8(cols / groups), 16-byte
-// aligned sizes.
-int64_t packed_bytes(int64_t rows, int64_t cols, int groups);
-
 // Copies `a` with each of its `groups` column groups padded with zeros to a
-// multiple of 8 columns, and returns the copy.
-int pack16(const Mat16& a, int groups, void* to, Mat16* out, hipStream_t stream);
+// multiple of `unit` columns, and returns the copy.
+int pack16(const Mat16& a, int groups, int unit, void* to, Mat16* out, hipStream_t stream);
 
 // out[c] = sum over `parts` rows of partial[part][ld], c < cols, in order;
 // columns of `groups` padded groups are closed up.
@@ -34,19 +38,21 @@ int sum_parts(const float* partial, int64_t parts, int64_t ld, int64_t cols, int
 int64_t column_parts(int64_t rows, int64_t cols);
 int column_sums(const Mat16& a, bool bf16, float* partial, float* out, hipStream_t stream);
 
-// dx[m][c] = sum_n dz[m][n] W[c][n] (both readable in pieces), rounded once.
+// dx[m][c] = sum_n dz[m][n] W[c][n] (both readable in pieces, or dz blocked),
+// rounded once.
 int product_nt(const Mat16& dz, const Mat16& W, bool bf16, uint16_t* out, int64_t ldo,
                int64_t cols, hipStream_t stream);
 
 // dW[c][n] = sum_m x[m][c] dz[m][n], rounded once; the rows are split over
 // workgroups, `partial` of product_tn_bytes holds their fp32 sums, added in
-// order. x and dz readable in pieces; out is [cols_x][cols_z] dense, dz's
-// columns in `groups` padded groups.
+// order. x and dz readable in pieces, one of them may be blocked; out is
+// [cols_x][cols_z] dense, dz's columns in `groups` padded groups.
 int64_t product_tn_bytes(int64_t rows, int64_t cin, int64_t cols);
 int product_tn(const Mat16& x, const Mat16& dz, bool bf16, float* partial, uint16_t* out,
                int64_t cols_x, int64_t cols_z, int groups, hipStream_t stream);
 
-// Linear layer: act(x W + bias) + residual, with operands readable in pieces.
+// Linear layer: act(x W + bias) + residual, with operands readable in pieces,
+// or x blocked.
 int linear_forward(const Mat16& x, const Mat16& W, const float* bias, int act, bool bf16,
                    const uint16_t* residual, int64_t ldr, uint16_t* out, int64_t ldo, uint16_t* pre,
                    int64_t cols, hipStream_t stream);
@@ -65,9 +71,11 @@ struct Arena {
   }
 };
 
-// The matrix itself where products can read it in pieces, else a padded copy
-// in the arena (which `out` describes unless the arena is counting).
-int readable(const Mat16& a, int groups, Arena& ws, Mat16* out, hipStream_t stream);
+// The matrix itself where products can read it in pieces and its column groups
+// are multiples of `unit` (8; 64 where its columns are the k of a blocked
+// matrix), else a padded copy in the arena (which `out` describes unless the
+// arena is counting).
+int readable(const Mat16& a, int groups, int unit, Arena& ws, Mat16* out, hipStream_t stream);
 
 // Argument checks shared by the entry points.
 int check_matrix(const char* name, const void* p, int64_t rows, int64_t cols, int64_t ld);

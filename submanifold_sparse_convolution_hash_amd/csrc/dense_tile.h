@@ -3,9 +3,10 @@
 //
 // A workgroup of WM x WN waves owns a BM x BN tile of the output and walks k
 // in steps of 64. Each step's two operand tiles go straight from memory into
-// LDS (buffer_load ... lds, 16 bytes a lane), STAGES buffers in turn, so
-// that the loads of the coming steps are in flight while the waves multiply
-// the current one; buffer bounds give zeros past the last row and the last k.
+// LDS (buffer_load ... lds, 16 bytes a lane): STAGES buffers in turn for A,
+// which comes from HBM, two for B, which stays in the caches; the loads of the
+// coming steps are in flight while the waves multiply the current one. Buffer
+// bounds give zeros past the last row and the last k.
 // An operand is read either with k contiguous in memory (x, and a weight
 // matrix under its transpose) by ds_read_b128, or with k as the row index (a
 // weight matrix as it is stored, both operands of a weight gradient) by
@@ -98,8 +99,8 @@ __device__ __forceinline__ float4v mfma16(half8 a, half8 b, float4v c) {
 // Row `row`'s columns n .. n + 7, zeros past n_end. `vec`: the matrix starts
 // on 16 bytes, its rows are 16-byte multiples apart and n_end is one of 8.
 __device__ __forceinline__ u32x4 load_piece(const uint16_t* row, int64_t n, int64_t n_end, bool vec) {
-  if (vec) return *reinterpret_cast<const u32x4*>(row + n);
   u32x4 r = {};
+  if (vec) return n < n_end ? *reinterpret_cast<const u32x4*>(row + n) : r;
 #pragma unroll
   for (int e = 0; e < 8; ++e)
     if (n + e < n_end) r[e >> 1] |= static_cast<uint32_t>(row[n + e]) << (16 * (e & 1));
@@ -213,6 +214,35 @@ __device__ __forceinline__ void with_act(int act, F&& f) {
   }
 }
 
+// ---- matrices between two kernels ----
+//
+// h, dg, du and dz live in the workspace only, between the kernel that forms
+// them and the products that read them, so they are laid out for those: blocks
+// of kBlockRows x 64 elements, each 16 KiB in one piece, a row of blocks after
+// the other. A product's tile of k = 64 is then contiguous memory, whichever
+// way it runs, instead of 128-byte pieces a row stride apart.
+constexpr int kBlockRows = 128;
+
+// Elements before element (row, col) of a blocked matrix with `blocks` = its
+// columns / 64.
+__host__ __device__ inline int64_t blocked_at(int64_t row, int64_t col, int64_t blocks) {
+  return ((row / kBlockRows * blocks + col / 64) * kBlockRows + row % kBlockRows) * 64 + col % 64;
+}
+// Stores 8 columns at tile row `m`, column n < n_end (a multiple of 64) of the
+// block row that starts at tile row 0.
+struct BlockView {
+  uint16_t* p;
+  uint32_t rows, n_end;
+  __device__ __forceinline__ BlockView(uint16_t* q, int64_t m0, int64_t M, int64_t N)
+      : p(q + m0 / kBlockRows * kBlockRows * N + m0 % kBlockRows * 64),
+        rows(static_cast<uint32_t>(M - m0 < kBlockRows ? M - m0 : kBlockRows)),
+        n_end(static_cast<uint32_t>(N)) {}
+  __device__ __forceinline__ void store(uint32_t m, uint32_t n, u32x4 v) const {
+    if (m < rows && n < n_end)
+      *reinterpret_cast<u32x4*>(p + static_cast<size_t>(n / 64) * (kBlockRows * 64) + m * 64 + n % 64) = v;
+  }
+};
+
 // ---- operand tiles ----
 
 typedef uint32_t rsrc4 __attribute__((ext_vector_type(4)));
@@ -243,7 +273,7 @@ __device__ __forceinline__ uint32_t lds_addr(const char* p) {
 // one are multiples of 8 elements, so a 16-byte piece is inside or outside.
 struct Operand {
   const uint16_t* p;
-  int64_t ld;
+  int64_t ld;    // columns, for a blocked matrix
   int64_t rows;  // m or n extent
   int64_t k;     // k extent; a product's k is the k-contiguous operand's, whose
                  // zeros may go up to 7 past the memory rows of a KRow one
@@ -252,7 +282,8 @@ struct Operand {
 // The k-contiguous form. LDS: row r is 128 bytes, its piece c (8 k) in slot c
 // ^ ((r / 2) % 8), so that the 16 rows a read pass takes fall on distinct
 // banks.
-template <int R, int NT>
+// TILED: a blocked matrix, R = kBlockRows of it.
+template <int R, int NT, bool TILED>
 struct LoadKCol {
   static constexpr int SL = R * 8 / NT;
   static_assert(R * 8 % NT == 0 && NT / 8 % 16 == 0, "slots");
@@ -262,22 +293,30 @@ struct LoadKCol {
   int kc;
   __device__ __forceinline__ void init(const Operand& o, int64_t row0, int64_t k_end, int tid) {
     const int64_t left = o.rows - row0;
-    base = o.p + row0 * o.ld;
-    bytes = left > 0 ? static_cast<uint32_t>(((left < R ? left : R) - 1) * o.ld + k_end) * 2u : 0u;
     const int r0 = tid >> 3;
     kc = ((tid & 7) ^ ((r0 >> 1) & 7)) * 8;
+    if constexpr (TILED) {
+      static_assert(R == kBlockRows, "one block row");
+      base = o.p + row0 * o.ld;
+      bytes = left > 0 ? static_cast<uint32_t>(left < R ? left : R) * 128u : 0u;
 #pragma unroll
-    for (int i = 0; i < SL; ++i)
-      voff[i] = static_cast<uint32_t>((r0 + i * (NT / 8)) * o.ld + kc) * 2u;
+      for (int i = 0; i < SL; ++i) voff[i] = static_cast<uint32_t>((r0 + i * (NT / 8)) * 64 + kc) * 2u;
+    } else {
+      base = o.p + row0 * o.ld;
+      bytes = left > 0 ? static_cast<uint32_t>(((left < R ? left : R) - 1) * o.ld + k_end) * 2u : 0u;
+#pragma unroll
+      for (int i = 0; i < SL; ++i)
+        voff[i] = static_cast<uint32_t>((r0 + i * (NT / 8)) * o.ld + kc) * 2u;
+    }
   }
   __device__ __forceinline__ void issue(uint32_t lds, int64_t k0, int64_t k_end, int wave) const {
-    rsrc4 r = load_rsrc(base, bytes);
+    rsrc4 r = load_rsrc(TILED ? base + k0 * R : base, bytes);
     settle_rsrc(r);
-    const bool in = k0 + kc < k_end;
+    const bool in = TILED || k0 + kc < k_end;  // a blocked matrix has whole steps
+    const uint32_t step = TILED ? 0u : static_cast<uint32_t>(k0) * 2u;
 #pragma unroll
     for (int i = 0; i < SL; ++i)
-      load_to_lds(r, in ? voff[i] + static_cast<uint32_t>(k0) * 2u : kOobOff,
-                  lds + (i * NT + wave * 64) * 16);
+      load_to_lds(r, in ? voff[i] + step : kOobOff, lds + (i * NT + wave * 64) * 16);
   }
 };
 
@@ -286,7 +325,8 @@ struct LoadKCol {
 // 8 k rows that a transposed read takes at a time fall on distinct banks.
 // PAIR: the tile's columns are R / 2 of the first half of the matrix (gate)
 // and the R / 2 at the same place of its second half (up, `half` further on).
-template <int R, int NT, bool PAIR>
+// TILED: a blocked matrix, whose rows past the last are not to be read.
+template <int R, int NT, bool PAIR, bool TILED>
 struct LoadKRow {
   static constexpr int CH = R / 8;  // pieces per k row
   static constexpr int SL = kStepK * CH / NT;
@@ -295,6 +335,7 @@ struct LoadKRow {
   const uint16_t* p;
   int64_t ld, width, k_rows;
   uint32_t voff[SL];
+  int k_thread;
   static __device__ __forceinline__ int swz(int k) {
     return (((k & 3) | ((k >> 3 & 1) << 2)) << 1) & (CH - 1);
   }
@@ -304,10 +345,17 @@ struct LoadKRow {
     k_rows = o.k;
     width = PAIR ? half + o.rows : o.rows;
     const int k0 = tid / CH, cs = tid % CH;
+    k_thread = k0;
+    if constexpr (TILED) p = o.p + col0 * kBlockRows;
 #pragma unroll
     for (int i = 0; i < SL; ++i) {
       const int k = k0 + i * KS;
       const int c = (cs ^ swz(k)) * 8;
+      if constexpr (TILED) {
+        voff[i] = col0 + c < o.rows
+                      ? static_cast<uint32_t>((c / 64 * kBlockRows + k) * 64 + c % 64) * 2u : kOobOff;
+        continue;
+      }
       int64_t col;
       bool in;
       if constexpr (PAIR) {
@@ -324,30 +372,42 @@ struct LoadKRow {
   }
   __device__ __forceinline__ void issue(uint32_t lds, int64_t k0, int64_t k_end, int wave) const {
     const int64_t left = (k_rows < k_end ? k_rows : k_end) - k0;
-    const uint32_t bytes =
-        static_cast<uint32_t>(((left < kStepK ? left : kStepK) - 1) * ld + width) * 2u;
-    rsrc4 r = load_rsrc(p + k0 * ld, bytes);
-    settle_rsrc(r);
+    if constexpr (TILED) {
+      // k0 starts one of a block's halves; the tile spans R / 64 blocks
+      rsrc4 r = load_rsrc(p + k0 / kBlockRows * kBlockRows * ld + k0 % kBlockRows * 64,
+                          R / 64 * kBlockRows * 128u);
+      settle_rsrc(r);
 #pragma unroll
-    for (int i = 0; i < SL; ++i) load_to_lds(r, voff[i], lds + (i * NT + wave * 64) * 16);
+      for (int i = 0; i < SL; ++i)
+        load_to_lds(r, k_thread + i * KS < left ? voff[i] : kOobOff, lds + (i * NT + wave * 64) * 16);
+    } else {
+      const uint32_t bytes =
+          static_cast<uint32_t>(((left < kStepK ? left : kStepK) - 1) * ld + width) * 2u;
+      rsrc4 r = load_rsrc(p + k0 * ld, bytes);
+      settle_rsrc(r);
+#pragma unroll
+      for (int i = 0; i < SL; ++i) load_to_lds(r, voff[i], lds + (i * NT + wave * 64) * 16);
+    }
   }
 };
 
 // ---- the tile ----
 
-// A_ROW, B_ROW: k is the memory row of that operand. PAIR: see LoadKRow
+// A_ROW, B_ROW: k is the memory row of that operand; A_TILED, B_TILED: it is
+// blocked (k as the row for B). PAIR: see LoadKRow
 // (B only); accumulator columns j < FN / 2 are then gate columns, the others
 // the up columns at the same place.
-template <bool BF16, bool A_ROW, bool B_ROW, bool PAIR, int BM, int BN, int WM, int WN, int STAGES>
+template <bool BF16, bool A_ROW, bool B_ROW, bool PAIR, int BM, int BN, int WM, int WN, int STAGES,
+          bool A_TILED = false, bool B_TILED = false>
 struct Tile {
   static constexpr int NT = WM * WN * 64;
   static constexpr int FM = BM / WM / 16, FN = BN / WN / 16;
   static constexpr int A_BYTES = BM * kStepK * 2, B_BYTES = BN * kStepK * 2;
-  static constexpr int LDS_BYTES = STAGES * (A_BYTES + B_BYTES);
-  static_assert(FM >= 1 && FN >= 2 && FN % 2 == 0, "wave tile");
-  using LA = std::conditional_t<A_ROW, LoadKRow<BM, NT, false>, LoadKCol<BM, NT>>;
-  using LB = std::conditional_t<B_ROW, LoadKRow<BN, NT, PAIR>, LoadKCol<BN, NT>>;
-  static constexpr int LPT = LA::SL + LB::SL;  // loads per thread and step
+  static constexpr int LDS_BYTES = STAGES * A_BYTES + 2 * B_BYTES;
+  static_assert(FM >= 1 && FN >= 1 && (!PAIR || FN % 2 == 0), "wave tile");
+  static_assert(STAGES == 2 || STAGES == 3, "buffers");
+  using LA = std::conditional_t<A_ROW, LoadKRow<BM, NT, false, A_TILED>, LoadKCol<BM, NT, A_TILED>>;
+  using LB = std::conditional_t<B_ROW, LoadKRow<BN, NT, PAIR, B_TILED>, LoadKCol<BN, NT, false>>;
 
   // first column (in the tile) of accumulator column j of wave column wn
   static __device__ __forceinline__ int ncol(int wn, int j) {
@@ -397,29 +457,32 @@ struct Tile {
       for (int i = 0; i < FM; ++i) acc[j][i] = float4v{};
 
     const int steps = static_cast<int>((k_end - k_begin + kStepK - 1) / kStepK);
-    auto issue = [&](int st, int buf) {
-      const uint32_t b = lds_addr(smem) + buf * (A_BYTES + B_BYTES);
-      const int64_t k0 = k_begin + static_cast<int64_t>(st) * kStepK;
-      la.issue(b, k0, k_end, wave);
-      lb.issue(b + A_BYTES, k0, k_end, wave);
+    const uint32_t lds = lds_addr(smem);
+    auto k_of = [&](int st) { return k_begin + static_cast<int64_t>(st) * kStepK; };
+    auto issue_a = [&](int st, int buf) { la.issue(lds + buf * A_BYTES, k_of(st), k_end, wave); };
+    auto issue_b = [&](int st) {
+      lb.issue(lds + STAGES * A_BYTES + (st & 1) * B_BYTES, k_of(st), k_end, wave);
     };
-#pragma unroll
-    for (int st = 0; st < STAGES - 1; ++st)
-      if (st < steps) issue(st, st);
+    if (steps > 0) {
+      issue_a(0, 0);
+      issue_b(0);
+    }
+    if (STAGES == 3 && steps > 1) issue_a(1, 1);
 
     int buf = 0;
     for (int st = 0; st < steps; ++st) {
-      // this step's loads are the oldest: all but the later steps' are waited
-      // for (and this wave's LDS reads of the last step), then every wave's
-      // through the barrier, after which the buffer that was read in the last
-      // step is overwritten
-      if (st + STAGES - 2 < steps) wait_loads<(STAGES - 2) * LPT>();
+      // this step's loads are the oldest: all but A's of the next step are
+      // waited for (and this wave's LDS reads of the last step), then every
+      // wave's through the barrier, after which the buffers that were read in
+      // the last step are overwritten
+      if (STAGES == 3 && st + 1 < steps) wait_loads<LA::SL>();
       else wait_loads<0>();
       __builtin_amdgcn_s_barrier();
       asm volatile("" ::: "memory");
-      if (st + STAGES - 1 < steps) issue(st + STAGES - 1, buf == 0 ? STAGES - 1 : buf - 1);
-      const char* ta = smem + buf * (A_BYTES + B_BYTES);
-      const char* tb = ta + A_BYTES;
+      if (st + 1 < steps) issue_b(st + 1);
+      if (st + STAGES - 1 < steps) issue_a(st + STAGES - 1, buf == 0 ? STAGES - 1 : buf - 1);
+      const char* ta = smem + buf * A_BYTES;
+      const char* tb = smem + STAGES * A_BYTES + (st & 1) * B_BYTES;
 #pragma unroll
       for (int kk = 0; kk < kStepK / 32; ++kk) {
         half8 fb[FN], fa[FM];
@@ -438,27 +501,32 @@ struct Tile {
 
   // ---- the accumulators as rows ----
   //
-  // to_rows leaves the tile in LDS as fp32 rows, read8 takes 8 columns of one.
-  // The 16-byte piece p of row r sits at p ^ (r % 16) ^ (p / 16 % 2), which
-  // keeps the 16 rows of a write and the 16 pieces of a read apart.
+  // to_rows leaves the rows of phase `ph` (as many as fit the operand buffers)
+  // in LDS in fp32, read8 takes 8 columns of one. The 16-byte piece p of row r
+  // sits at p ^ (r % 16) ^ (p / 16 % 2), which keeps the 16 rows of a write and
+  // the 16 pieces of a read apart.
+  static constexpr int PHASES = BM * BN * 4 <= LDS_BYTES ? 1 : WM;
+  static constexpr int PH_ROWS = BM / PHASES;     // rows of a phase
   static constexpr int PIECES = BN / 8;           // 8-column pieces per row
   static constexpr int ROW_STEP = NT / PIECES;    // rows between a thread's pieces
-  static constexpr int ROW_PASSES = BM / ROW_STEP;
-  static_assert(BM * BN * 4 <= LDS_BYTES, "the rows fit the operand buffers");
+  static constexpr int ROW_PASSES = PH_ROWS / ROW_STEP;
+  static_assert(PH_ROWS * BN * 4 <= LDS_BYTES, "a phase's rows fit the operand buffers");
   static __device__ __forceinline__ int row_byte(int r, int p) {
     return r * (BN * 4) + ((p ^ (r & 15) ^ (p >> 4 & 1)) << 4);
   }
-  static __device__ __forceinline__ void to_rows(char* smem, const float4v (&acc)[FN][FM]) {
+  static __device__ __forceinline__ void to_rows(char* smem, int ph, const float4v (&acc)[FN][FM]) {
     const int lane = threadIdx.x & 63, g = lane >> 4, s = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / WN, wn = wave % WN;
-    __syncthreads();  // every wave has read its last operands
+    __syncthreads();  // every wave has read its last operands, or the phase before
+    if (PHASES == 1 || wm == ph) {
+      const int r0 = PHASES == 1 ? wm * (BM / WM) : 0;
 #pragma unroll
-    for (int i = 0; i < FM; ++i)
+      for (int i = 0; i < FM; ++i)
 #pragma unroll
-      for (int j = 0; j < FN; ++j)
-        *reinterpret_cast<float4v*>(smem + row_byte(wm * (BM / WM) + i * 16 + s, ncol(wn, j) / 4 + g)) =
-            acc[j][i];
+        for (int j = 0; j < FN; ++j)
+          *reinterpret_cast<float4v*>(smem + row_byte(r0 + i * 16 + s, ncol(wn, j) / 4 + g)) = acc[j][i];
+    }
     __syncthreads();
   }
   static __device__ __forceinline__ void read8(const char* smem, int r, int piece, float (&v)[8]) {
@@ -478,21 +546,29 @@ struct Tile {
   }
 };
 
+// Waves per SIMD that the register budget leaves room for: two workgroups of
+// a 128 x 128 tile on a compute unit, one of a 256 x 256 tile (LDS allows no
+// more).
+constexpr int tile_waves(int bm, int bn) { return bm * bn > 128 * 128 ? 2 : 4; }
+
 // Output tile of a workgroup: tiles are walked n first, and each XCD
 // (blockIdx % 8) takes a contiguous run of them, so that the n tiles which
 // read the same rows of A share that XCD's L2.
 struct TilePos {
   int64_t m, n;
 };
-__device__ __forceinline__ TilePos tile_pos(int64_t m_tiles, int64_t n_tiles, int64_t bid) {
-  const int64_t total = m_tiles * n_tiles;
-  const int64_t q = total >> 3, r = total & 7, x = bid & 7, j = bid >> 3;
-  const int64_t t = x * q + (x < r ? x : r) + j;
-  return TilePos{t / n_tiles, t % n_tiles};
+__device__ __forceinline__ TilePos tile_pos(uint32_t m_tiles, uint32_t n_tiles, uint32_t bid) {
+  const uint32_t total = m_tiles * n_tiles;  // a grid's size: 31 bits
+  const uint32_t q = total >> 3, r = total & 7, x = bid & 7, j = bid >> 3;
+  const uint32_t t = x * q + (x < r ? x : r) + j;
+  const uint32_t m = t / n_tiles;
+  return TilePos{m, t - m * n_tiles};
 }
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
-inline int64_t round8(int64_t v) { return (v + 7) & ~int64_t{7}; }
+inline int64_t round_to(int64_t v, int64_t unit) { return (v + unit - 1) / unit * unit; }
+inline int64_t round8(int64_t v) { return round_to(v, 8); }
+inline int64_t round64(int64_t v) { return round_to(v, 64); }
 inline int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 }  // namespace

@@ -26,27 +26,28 @@ namespace {
 
 struct GateEpi {
   const float* bias;  // [2F] or null
-  uint16_t* h;        // [M][Fp], Fp = F rounded up to 8, the rest zeros
+  uint16_t* h;        // blocked [M][Fq], Fq = F rounded up to 64, the rest zeros
   uint16_t* pre;      // [M][2F] or null
-  int64_t F, Fp;
+  int64_t F, Fq;
   int act;
   bool vec_p;
 };
 
-template <bool BF16, int ACT, typename T, int BM>
+template <bool BF16, int ACT, typename T>
 __device__ __forceinline__ void gate_epilogue(const GateEpi& e, int64_t M, int64_t m0, uint32_t n0,
                                               const char* smem) {
+  constexpr int BM = T::PH_ROWS;
   // a row in LDS: the gate's columns, then the up projection's
   constexpr int HP = T::PIECES / 2, STEP = T::NT / HP;
   const int piece = threadIdx.x % HP, r0 = threadIdx.x / HP;
   const uint32_t n = n0 + piece * 8;
-  const RowsView h(e.h, e.Fp, m0, M, e.Fp, BM, true);
+  const BlockView h(e.h, m0, M, e.Fq);
   const RowsView pg(e.pre, 2 * e.F, m0, M, e.F, BM, e.vec_p);
   const RowsView pu(e.pre ? e.pre + e.F : nullptr, 2 * e.F, m0, M, e.F, BM, e.vec_p);
   float bg[8], bu[8];
   load_bias8(e.bias, e.F, n, bg);
   load_bias8(e.bias ? e.bias + e.F : nullptr, e.F, n, bu);
-#pragma unroll
+#pragma unroll 2
   for (int p = 0; p < BM / STEP; ++p) {
     const int m = r0 + p * STEP;
     float g[8], u[8];
@@ -68,44 +69,49 @@ __device__ __forceinline__ void gate_epilogue(const GateEpi& e, int64_t M, int64
 }
 
 template <bool BF16, int BM, int BN, int WM, int WN, int STAGES>
-__global__ __launch_bounds__(WM* WN * 64) void k_gate(Operand A, Operand B, int64_t K, int64_t half,
-                                                      int64_t m_tiles, int64_t n_tiles, GateEpi e) {
+__global__ __launch_bounds__(WM* WN * 64, tile_waves(BM, BN)) void k_gate(Operand A, Operand B, int64_t K, int64_t half,
+                                                      uint32_t m_tiles, uint32_t n_tiles, GateEpi e) {
   using T = Tile<BF16, false, true, true, BM, BN, WM, WN, STAGES>;
   __shared__ __attribute__((aligned(16))) char smem[T::LDS_BYTES];
   const TilePos t = tile_pos(m_tiles, n_tiles, blockIdx.x);
   const int64_t m0 = t.m * BM, n0 = t.n * (BN / 2);
   float4v acc[T::FN][T::FM];
   T::run(A, B, half, m0, n0, 0, K, smem, acc);
-  T::to_rows(smem, acc);
-  with_act(e.act, [&](auto a) {
-    gate_epilogue<BF16, decltype(a)::value, T, BM>(e, A.rows, m0, static_cast<uint32_t>(n0), smem);
-  });
+#pragma unroll 1
+  for (int ph = 0; ph < T::PHASES; ++ph) {
+    T::to_rows(smem, ph, acc);
+    with_act(e.act, [&](auto a) {
+      gate_epilogue<BF16, decltype(a)::value, T>(e, A.rows, m0 + ph * T::PH_ROWS,
+                                                 static_cast<uint32_t>(n0), smem);
+    });
+  }
 }
 
 // ---- gradient: dh = dout W_out^T; dg, du, h in its epilogue ----
 
 struct GateGradEpi {
   const uint16_t* pre;  // [M][2F]
-  uint16_t* dz;         // [M][2Fp]: dg, zeros up to Fp, du, zeros
-  uint16_t* h;          // [M][Fp]
-  float* sums;          // [m_tiles][2Fp] column sums of the tile's dg and du, or null
-  int64_t F, Fp;
+  uint16_t* dz;         // blocked [M][2Fq]: dg, zeros up to Fq, du, zeros
+  uint16_t* h;          // blocked [M][Fq]
+  float* sums;          // [m_tiles][2Fq] column sums of the tile's dg and du, or null
+  int64_t F, Fq;
   int act;
   bool vec_p;
 };
 
-template <bool BF16, int ACT, typename T, int BM>
+template <bool BF16, int ACT, typename T>
 __device__ __forceinline__ void gate_grad_epilogue(const GateGradEpi& e, int64_t M, int64_t m0,
                                                    uint32_t n0, const char* smem, float (&sg)[8],
                                                    float (&su)[8]) {
+  constexpr int BM = T::PH_ROWS;
   const int piece = threadIdx.x % T::PIECES, r0 = threadIdx.x / T::PIECES;
   const uint32_t n = n0 + piece * 8;
   const RowsView pg(e.pre, 2 * e.F, m0, M, e.F, BM, e.vec_p);
   const RowsView pu(e.pre + e.F, 2 * e.F, m0, M, e.F, BM, e.vec_p);
-  const RowsView zg(e.dz, 2 * e.Fp, m0, M, e.Fp, BM, true);
-  const RowsView zu(e.dz + e.Fp, 2 * e.Fp, m0, M, e.Fp, BM, true);
-  const RowsView h(e.h, e.Fp, m0, M, e.Fp, BM, true);
-#pragma unroll
+  const BlockView z(e.dz, m0, M, 2 * e.Fq);
+  const uint32_t Fq = static_cast<uint32_t>(e.Fq);
+  const BlockView h(e.h, m0, M, e.Fq);
+#pragma unroll 2
   for (int p = 0; p < T::ROW_PASSES; ++p) {
     const int m = r0 + p * T::ROW_STEP;
     float g[8], u[8], dh[8];
@@ -123,15 +129,17 @@ __device__ __forceinline__ void gate_grad_epilogue(const GateGradEpi& e, int64_t
       sg[q] += dg[q];  // rows past M add zeros: their dout is read as zeros
       su[q] += du[q];
     }
-    zg.store(m, n, pack8<BF16>(dg));
-    zu.store(m, n, pack8<BF16>(du));
-    h.store(m, n, pack8<BF16>(v));
+    if (n < Fq) {
+      z.store(m, n, pack8<BF16>(dg));
+      z.store(m, Fq + n, pack8<BF16>(du));
+      h.store(m, n, pack8<BF16>(v));
+    }
   }
 }
 
 template <bool BF16, int BM, int BN, int WM, int WN, int STAGES>
-__global__ __launch_bounds__(WM* WN * 64) void k_gate_grad(Operand A, Operand B, int64_t K,
-                                                           int64_t m_tiles, int64_t n_tiles,
+__global__ __launch_bounds__(WM* WN * 64, tile_waves(BM, BN)) void k_gate_grad(Operand A, Operand B, int64_t K,
+                                                           uint32_t m_tiles, uint32_t n_tiles,
                                                            GateGradEpi e) {
   using T = Tile<BF16, false, false, false, BM, BN, WM, WN, STAGES>;
   __shared__ __attribute__((aligned(16))) char smem[T::LDS_BYTES];
@@ -139,12 +147,15 @@ __global__ __launch_bounds__(WM* WN * 64) void k_gate_grad(Operand A, Operand B,
   const int64_t m0 = t.m * BM, n0 = t.n * BN;
   float4v acc[T::FN][T::FM];
   T::run(A, B, 0, m0, n0, 0, K, smem, acc);
-  T::to_rows(smem, acc);
   float sums[2][8] = {};
-  with_act(e.act, [&](auto a) {
-    gate_grad_epilogue<BF16, decltype(a)::value, T, BM>(e, A.rows, m0, static_cast<uint32_t>(n0), smem,
-                                                        sums[0], sums[1]);
-  });
+#pragma unroll 1
+  for (int ph = 0; ph < T::PHASES; ++ph) {
+    T::to_rows(smem, ph, acc);
+    with_act(e.act, [&](auto a) {
+      gate_grad_epilogue<BF16, decltype(a)::value, T>(e, A.rows, m0 + ph * T::PH_ROWS,
+                                                      static_cast<uint32_t>(n0), smem, sums[0], sums[1]);
+    });
+  }
   if (!e.sums) return;
   // the threads that walked the same columns, in order
   float* red = reinterpret_cast<float*>(smem);  // [ROW_STEP][2][BN]
@@ -160,7 +171,7 @@ __global__ __launch_bounds__(WM* WN * 64) void k_gate_grad(Operand A, Operand B,
 #pragma unroll
     for (int r = 0; r < T::ROW_STEP; ++r) x += red[r * 2 * BN + c];
     const int64_t n = n0 + c % BN;
-    if (n < e.Fp) e.sums[(t.m * 2 + c / BN) * e.Fp + n] = x;
+    if (n < e.Fq) e.sums[(t.m * 2 + c / BN) * e.Fq + n] = x;
   }
 }
 
@@ -168,11 +179,11 @@ constexpr int kGateTile = 128;
 
 int gate_forward(const Mat16& x, const Mat16& W, int64_t F, const float* bias, int act, bool bf16,
                  uint16_t* h, uint16_t* pre, hipStream_t stream) {
-  const int64_t Fp = W.cols / 2;
-  const int64_t mt = div_up(x.rows, kGateTile), nt = div_up(Fp, kGateTile / 2);
+  const int64_t Fp = W.cols / 2, Fq = round64(F);
+  const int64_t mt = div_up(x.rows, kGateTile), nt = div_up(Fq, kGateTile / 2);
   if (mt * nt > INT32_MAX)
     return set_error(SUBMCONV_ERR_UNSUPPORTED_SHAPE, "%lld output tiles", (long long)(mt * nt));
-  const GateEpi e{bias, h, pre, F, Fp, act, F % 8 == 0 && aligned16(pre)};
+  const GateEpi e{bias, h, pre, F, Fq, act, F % 8 == 0 && aligned16(pre)};
   const Operand A{x.p, x.ld, x.rows, x.cols}, B{W.p, W.ld, Fp, W.rows};
   const dim3 grid(static_cast<unsigned>(mt * nt));
   if (bf16)
@@ -186,13 +197,13 @@ int gate_forward(const Mat16& x, const Mat16& W, int64_t F, const float* bias, i
 int64_t gate_grad_tiles(int64_t rows) { return std::max<int64_t>(1, div_up(rows, kGateTile)); }
 
 // dy [M][C], W_out [F][C]
-int gate_grad(const Mat16& dy, const Mat16& W, int64_t Fp, const uint16_t* pre, int act, bool bf16,
+int gate_grad(const Mat16& dy, const Mat16& W, int64_t Fq, const uint16_t* pre, int act, bool bf16,
               uint16_t* dz, uint16_t* h, float* sums, hipStream_t stream) {
   const int64_t F = W.rows;
-  const int64_t mt = gate_grad_tiles(dy.rows), nt = div_up(Fp, kGateTile);
+  const int64_t mt = gate_grad_tiles(dy.rows), nt = div_up(Fq, kGateTile);
   if (mt * nt > INT32_MAX)
     return set_error(SUBMCONV_ERR_UNSUPPORTED_SHAPE, "%lld output tiles", (long long)(mt * nt));
-  const GateGradEpi e{pre, dz, h, sums, F, Fp, act, F % 8 == 0 && aligned16(pre)};
+  const GateGradEpi e{pre, dz, h, sums, F, Fq, act, F % 8 == 0 && aligned16(pre)};
   const Operand A{dy.p, dy.ld, dy.rows, dy.cols}, B{W.p, W.ld, F, W.cols};
   const dim3 grid(static_cast<unsigned>(mt * nt));
   if (bf16)
@@ -212,15 +223,15 @@ struct Ffn {
 
 int ffn_forward(const Ffn& f, const float* b_in, const float* b_out, const uint16_t* residual,
                 int64_t ldr, uint16_t* out, uint16_t* pre, Arena& ws, hipStream_t stream) {
-  const int64_t Fp = round8(f.F);
+  const int64_t Fq = round64(f.F);
   Mat16 x, wi, wo;
-  SUBMCONV_TRY(readable(f.x, 1, ws, &x, stream));
-  SUBMCONV_TRY(readable(f.W_in, 2, ws, &wi, stream));
-  SUBMCONV_TRY(readable(f.W_out, 1, ws, &wo, stream));
-  uint16_t* h = static_cast<uint16_t*>(ws.take(f.n * Fp * 2));
+  SUBMCONV_TRY(readable(f.x, 1, 8, ws, &x, stream));
+  SUBMCONV_TRY(readable(f.W_in, 2, 8, ws, &wi, stream));
+  SUBMCONV_TRY(readable(f.W_out, 1, 8, ws, &wo, stream));
+  uint16_t* h = static_cast<uint16_t*>(ws.take(blocked_bytes(f.n, Fq)));
   if (ws.counting || f.n == 0) return SUBMCONV_OK;
   SUBMCONV_TRY(gate_forward(x, wi, f.F, b_in, f.act, f.bf16, h, pre, stream));
-  return linear_forward(Mat16{h, f.n, Fp, Fp}, wo, b_out, kActNone, f.bf16, residual, ldr, out, f.Co,
+  return linear_forward(blocked16(h, f.n, Fq), wo, b_out, kActNone, f.bf16, residual, ldr, out, f.Co,
                         nullptr, f.Co, stream);
 }
 
@@ -232,35 +243,35 @@ struct FfnGrads {
 
 int ffn_backward(const Ffn& f, const uint16_t* pre, const FfnGrads& g, Arena& ws, hipStream_t stream) {
   const bool run = !ws.counting;
-  const int64_t Fp = round8(f.F), Cp = round8(f.C), Op = round8(f.Co);
+  const int64_t Fq = round64(f.F), Cp = round8(f.C), Op = round8(f.Co);
   Mat16 dy, wo;
-  SUBMCONV_TRY(readable(f.dy, 1, ws, &dy, stream));
+  SUBMCONV_TRY(readable(f.dy, 1, 8, ws, &dy, stream));
   if (g.all || g.b_out) {
     float* part = static_cast<float*>(ws.take(column_parts(f.n, f.Co) * Op * 4));
     if (run) SUBMCONV_TRY(column_sums(f.dy, f.bf16, part, g.b_out, stream));
   }
   if (!(g.all || g.x || g.W_in || g.W_out || g.b_in)) return SUBMCONV_OK;
-  SUBMCONV_TRY(readable(f.W_out, 1, ws, &wo, stream));
-  uint16_t* h = static_cast<uint16_t*>(ws.take(f.n * Fp * 2));
-  uint16_t* dz = static_cast<uint16_t*>(ws.take(f.n * 2 * Fp * 2));
+  SUBMCONV_TRY(readable(f.W_out, 1, 8, ws, &wo, stream));
+  uint16_t* h = static_cast<uint16_t*>(ws.take(blocked_bytes(f.n, Fq)));
+  uint16_t* dz = static_cast<uint16_t*>(ws.take(blocked_bytes(f.n, 2 * Fq)));
   const int64_t tiles = gate_grad_tiles(f.n);
-  float* sums = g.all || g.b_in ? static_cast<float*>(ws.take(tiles * 2 * Fp * 4)) : nullptr;
-  const Mat16 hm{h, f.n, Fp, Fp}, zm{dz, f.n, 2 * Fp, 2 * Fp};
+  float* sums = g.all || g.b_in ? static_cast<float*>(ws.take(tiles * 2 * Fq * 4)) : nullptr;
+  const Mat16 hm = blocked16(h, f.n, Fq), zm = blocked16(dz, f.n, 2 * Fq);
   if (run) {
-    SUBMCONV_TRY(gate_grad(dy, wo, Fp, pre, f.act, f.bf16, dz, h, sums, stream));
-    if (g.b_in) SUBMCONV_TRY(sum_parts(sums, tiles, 2 * Fp, 2 * f.F, 2, g.b_in, stream));
+    SUBMCONV_TRY(gate_grad(dy, wo, Fq, pre, f.act, f.bf16, dz, h, sums, stream));
+    if (g.b_in) SUBMCONV_TRY(sum_parts(sums, tiles, 2 * Fq, 2 * f.F, 2, g.b_in, stream));
   }
   if (g.all || g.x) {
     Mat16 wi;
-    SUBMCONV_TRY(readable(f.W_in, 2, ws, &wi, stream));
+    SUBMCONV_TRY(readable(f.W_in, 2, 64, ws, &wi, stream));
     if (run) SUBMCONV_TRY(product_nt(zm, wi, f.bf16, g.x, f.C, f.C, stream));
   }
   if (g.all || g.W_in || g.W_out) {
-    float* part = static_cast<float*>(ws.take(std::max(g.all || g.W_in ? product_tn_bytes(f.n, Cp, 2 * Fp) : 0,
-                                                       g.all || g.W_out ? product_tn_bytes(f.n, Fp, Op) : 0)));
+    float* part = static_cast<float*>(ws.take(std::max(g.all || g.W_in ? product_tn_bytes(f.n, Cp, 2 * Fq) : 0,
+                                                       g.all || g.W_out ? product_tn_bytes(f.n, Fq, Op) : 0)));
     if (g.all || g.W_in) {
       Mat16 x;
-      SUBMCONV_TRY(readable(f.x, 1, ws, &x, stream));
+      SUBMCONV_TRY(readable(f.x, 1, 8, ws, &x, stream));
       if (run) SUBMCONV_TRY(product_tn(x, zm, f.bf16, part, g.W_in, f.C, 2 * f.F, 2, stream));
     }
     if (run && g.W_out) SUBMCONV_TRY(product_tn(hm, dy, f.bf16, part, g.W_out, f.F, f.Co, 1, stream));

@@ -29,9 +29,10 @@ struct LinearEpi {
   bool vec_r, vec_o, vec_p;
 };
 
-template <bool BF16, int ACT, typename T, int BM>
+template <bool BF16, int ACT, typename T>
 __device__ __forceinline__ void linear_epilogue(const LinearEpi& e, int64_t M, int64_t N,
                                                 int64_t m0, uint32_t n0, const char* smem) {
+  constexpr int BM = T::PH_ROWS;
   const int piece = threadIdx.x % T::PIECES, r0 = threadIdx.x / T::PIECES;
   const uint32_t n = n0 + piece * 8;
   const RowsView out(e.out, e.ldo, m0, M, N, BM, e.vec_o);
@@ -39,7 +40,7 @@ __device__ __forceinline__ void linear_epilogue(const LinearEpi& e, int64_t M, i
   const RowsView res(e.residual, e.ldr, m0, M, N, BM, e.vec_r);
   float b[8];
   load_bias8(e.bias, N, n, b);
-#pragma unroll
+#pragma unroll 2
   for (int p = 0; p < T::ROW_PASSES; ++p) {
     const int m = r0 + p * T::ROW_STEP;
     float z[8];
@@ -60,23 +61,27 @@ __device__ __forceinline__ void linear_epilogue(const LinearEpi& e, int64_t M, i
 }
 
 // B_ROW: W [K][N] as stored (forward); else W [N][K] (input gradient).
-template <bool BF16, bool B_ROW, int BM, int BN, int WM, int WN, int STAGES>
-__global__ __launch_bounds__(WM* WN * 64) void k_linear(Operand A, Operand B, int64_t K, int64_t N,
-                                                        int64_t m_tiles, int64_t n_tiles,
+template <bool BF16, bool B_ROW, bool A_TILED, int BM, int BN, int WM, int WN, int STAGES>
+__global__ __launch_bounds__(WM* WN * 64, tile_waves(BM, BN)) void k_linear(Operand A, Operand B, int64_t K, int64_t N,
+                                                        uint32_t m_tiles, uint32_t n_tiles,
                                                         LinearEpi e) {
-  using T = Tile<BF16, false, B_ROW, false, BM, BN, WM, WN, STAGES>;
+  using T = Tile<BF16, false, B_ROW, false, BM, BN, WM, WN, STAGES, A_TILED>;
   __shared__ __attribute__((aligned(16))) char smem[T::LDS_BYTES];
   const TilePos t = tile_pos(m_tiles, n_tiles, blockIdx.x);
   const int64_t m0 = t.m * BM, n0 = t.n * BN;
   float4v acc[T::FN][T::FM];
   T::run(A, B, 0, m0, n0, 0, K, smem, acc);
-  T::to_rows(smem, acc);
-  with_act(e.act, [&](auto a) {
-    linear_epilogue<BF16, decltype(a)::value, T, BM>(e, A.rows, N, m0, static_cast<uint32_t>(n0), smem);
-  });
+#pragma unroll 1
+  for (int ph = 0; ph < T::PHASES; ++ph) {
+    T::to_rows(smem, ph, acc);
+    with_act(e.act, [&](auto a) {
+      linear_epilogue<BF16, decltype(a)::value, T>(e, A.rows, N, m0 + ph * T::PH_ROWS,
+                                                   static_cast<uint32_t>(n0), smem);
+    });
+  }
 }
 
-template <bool B_ROW, int BM, int BN, int WM, int WN, int STAGES>
+template <bool B_ROW, bool A_TILED, int BM, int BN, int WM, int WN, int STAGES>
 int launch_linear(const Operand& A, const Operand& B, int64_t K, int64_t N, bool bf16,
                   const LinearEpi& e, hipStream_t stream) {
   const int64_t mt = div_up(A.rows, BM), nt = div_up(N, BN);
@@ -84,18 +89,21 @@ int launch_linear(const Operand& A, const Operand& B, int64_t K, int64_t N, bool
     return set_error(SUBMCONV_ERR_UNSUPPORTED_SHAPE, "%lld output tiles", (long long)(mt * nt));
   const dim3 grid(static_cast<unsigned>(mt * nt));
   if (bf16)
-    k_linear<true, B_ROW, BM, BN, WM, WN, STAGES><<<grid, WM * WN * 64, 0, stream>>>(A, B, K, N, mt, nt, e);
+    k_linear<true, B_ROW, A_TILED, BM, BN, WM, WN, STAGES><<<grid, WM * WN * 64, 0, stream>>>(A, B, K, N, mt, nt, e);
   else
-    k_linear<false, B_ROW, BM, BN, WM, WN, STAGES><<<grid, WM * WN * 64, 0, stream>>>(A, B, K, N, mt, nt, e);
+    k_linear<false, B_ROW, A_TILED, BM, BN, WM, WN, STAGES><<<grid, WM * WN * 64, 0, stream>>>(A, B, K, N, mt, nt, e);
   SUBMCONV_HIP_CHECK(hipGetLastError());
   return SUBMCONV_OK;
 }
 
+// a [M][K], and B [K][N] (B_ROW) or [N][K]
 template <bool B_ROW>
-int linear_product(const Operand& A, const Operand& B, int64_t K, int64_t N, bool bf16,
-                   const LinearEpi& e, hipStream_t stream) {
-  if (A.rows == 0 || N == 0) return SUBMCONV_OK;
-  return launch_linear<B_ROW, 128, 128, 2, 4, 2>(A, B, K, N, bf16, e, stream);
+int linear_product(const Mat16& a, const Operand& B, int64_t N, bool bf16, const LinearEpi& e,
+                   hipStream_t stream) {
+  if (a.rows == 0 || N == 0) return SUBMCONV_OK;
+  const Operand A{a.p, a.ld, a.rows, a.cols};
+  return a.blocked ? launch_linear<B_ROW, true, 128, 128, 2, 4, 3>(A, B, a.cols, N, bf16, e, stream)
+                   : launch_linear<B_ROW, false, 128, 128, 2, 4, 3>(A, B, a.cols, N, bf16, e, stream);
 }
 
 // ---- padded copies ----
@@ -120,19 +128,19 @@ constexpr int kSumThreads = 256;
 constexpr int kSumLanes = 32;                      // pieces (of 8 columns) a workgroup covers
 constexpr int kSumRows = kSumThreads / kSumLanes;  // rows per pass
 
-// dz = dy act'(z), rounded, into a matrix of pieces (columns past the width
-// are zeros), where dz is not null; and the unrounded column sums of this
+// dz = dy act'(z), rounded, into a blocked matrix of `blocks` x 64 columns
+// (zeros past the width), where dz is not null; and the unrounded column sums of this
 // workgroup's rows, where partial is not null. grid (column strips, row runs).
 template <bool BF16, int ACT>
 __device__ __forceinline__ void act_grad_rows(const uint16_t* dy, int64_t ldy, bool vec_y,
                                               const uint16_t* z, bool vec_z, int64_t rows,
-                                              int64_t cols, int64_t run, uint16_t* dz, int64_t ldz,
+                                              int64_t cols, int64_t run, uint16_t* dz, int64_t blocks,
                                               float* partial, float (*sums)[kSumLanes * 8 + 1]) {
   const int cl = threadIdx.x % kSumLanes, rl = threadIdx.x / kSumLanes;
   const int64_t c = (static_cast<int64_t>(blockIdx.x) * kSumLanes + cl) * 8;
   const int64_t r_end = min(rows, (static_cast<int64_t>(blockIdx.y) + 1) * run);
   float s[8] = {};
-  if (c < cols) {
+  if (c < (dz ? blocks * 64 : cols)) {
     for (int64_t r = blockIdx.y * run + rl; r < r_end; r += kSumRows) {
       float d[8];
       unpack8<BF16>(load_piece(dy + r * ldy, c, cols, vec_y), d);
@@ -148,7 +156,7 @@ __device__ __forceinline__ void act_grad_rows(const uint16_t* dy, int64_t ldy, b
       }
 #pragma unroll
       for (int e = 0; e < 8; ++e) s[e] += d[e];
-      if (dz) *reinterpret_cast<u32x4*>(dz + r * ldz + c) = pack8<BF16>(d);
+      if (dz) *reinterpret_cast<u32x4*>(dz + blocked_at(r, c, blocks)) = pack8<BF16>(d);
     }
   }
   if (!partial) return;
@@ -170,11 +178,11 @@ template <bool BF16>
 __global__ __launch_bounds__(kSumThreads) void k_act_grad(const uint16_t* dy, int64_t ldy,
                                                           bool vec_y, const uint16_t* z, bool vec_z,
                                                           int act, int64_t rows, int64_t cols,
-                                                          int64_t run, uint16_t* dz, int64_t ldz,
+                                                          int64_t run, uint16_t* dz, int64_t blocks,
                                                           float* partial) {
   __shared__ float sums[kSumRows][kSumLanes * 8 + 1];
   with_act(act, [&](auto a) {
-    act_grad_rows<BF16, decltype(a)::value>(dy, ldy, vec_y, z, vec_z, rows, cols, run, dz, ldz,
+    act_grad_rows<BF16, decltype(a)::value>(dy, ldy, vec_y, z, vec_z, rows, cols, run, dz, blocks,
                                             partial, sums);
   });
 }
@@ -204,9 +212,10 @@ __global__ __launch_bounds__(1024) void k_sum_parts(const float* __restrict__ pa
   if (q == 0 && c < cols) out[c] = sums[0][cl];
 }
 
-int act_grad(const Mat16& dy, const uint16_t* z, int act, bool bf16, uint16_t* dz, int64_t ldz,
-             float* partial, hipStream_t stream) {
-  const int64_t strips = div_up(div_up(dy.cols, 8), kSumLanes);
+int act_grad(const Mat16& dy, const uint16_t* z, int act, bool bf16, uint16_t* dz, float* partial,
+             hipStream_t stream) {
+  const int64_t blocks = div_up(dy.cols, 64);
+  const int64_t strips = div_up(dz ? blocks * 8 : div_up(dy.cols, 8), kSumLanes);
   const int64_t parts = column_parts(dy.rows, dy.cols);
   const int64_t run = div_up(div_up(dy.rows, parts), kSumRows) * kSumRows;
   const bool vec_y = pieces_fit(dy);
@@ -214,10 +223,10 @@ int act_grad(const Mat16& dy, const uint16_t* z, int act, bool bf16, uint16_t* d
   const dim3 grid(static_cast<unsigned>(strips), static_cast<unsigned>(parts));
   if (bf16)
     k_act_grad<true><<<grid, kSumThreads, 0, stream>>>(dy.p, dy.ld, vec_y, z, vec_z, act, dy.rows,
-                                                       dy.cols, run, dz, ldz, partial);
+                                                       dy.cols, run, dz, blocks, partial);
   else
     k_act_grad<false><<<grid, kSumThreads, 0, stream>>>(dy.p, dy.ld, vec_y, z, vec_z, act, dy.rows,
-                                                        dy.cols, run, dz, ldz, partial);
+                                                        dy.cols, run, dz, blocks, partial);
   SUBMCONV_HIP_CHECK(hipGetLastError());
   return SUBMCONV_OK;
 }
@@ -225,12 +234,12 @@ int act_grad(const Mat16& dy, const uint16_t* z, int act, bool bf16, uint16_t* d
 // ---- weight gradient ----
 
 // One BM x BN tile of x^T dz over one run of rows, as fp32 partial sums.
-template <bool BF16, int BM, int BN, int WM, int WN, int STAGES>
-__global__ __launch_bounds__(WM* WN * 64) void k_weight_grad(Operand X, Operand Z, int64_t rows,
-                                                             int64_t run, int64_t m_tiles,
-                                                             int64_t n_tiles,
+template <bool BF16, bool X_TILED, bool Z_TILED, int BM, int BN, int WM, int WN, int STAGES>
+__global__ __launch_bounds__(WM* WN * 64, tile_waves(BM, BN)) void k_weight_grad(Operand X, Operand Z, int64_t rows,
+                                                             int64_t run, uint32_t m_tiles,
+                                                             uint32_t n_tiles,
                                                              float* __restrict__ partial) {
-  using T = Tile<BF16, true, true, false, BM, BN, WM, WN, STAGES>;
+  using T = Tile<BF16, true, true, false, BM, BN, WM, WN, STAGES, X_TILED, Z_TILED>;
   __shared__ __attribute__((aligned(16))) char smem[T::LDS_BYTES];
   const TilePos t = tile_pos(gridDim.x / (m_tiles * n_tiles), m_tiles * n_tiles, blockIdx.x);
   const int64_t m0 = t.n / n_tiles * BM, n0 = t.n % n_tiles * BN;
@@ -288,13 +297,13 @@ __global__ __launch_bounds__(256) void k_weight_sum(const float* __restrict__ pa
   }
 }
 
-constexpr int kGradTile = 128;
+constexpr int kGradTile = 256;
 
 // Runs of rows of a weight gradient: enough workgroups for two per compute
 // unit, runs of at least 256 rows and a multiple of 64.
 int64_t grad_run(int64_t rows, int64_t cin, int64_t cols) {
   const int64_t tiles = div_up(cin, kGradTile) * div_up(cols, kGradTile);
-  const int64_t runs = std::max<int64_t>(1, std::min(div_up(512, tiles), div_up(rows, 256)));
+  const int64_t runs = std::max<int64_t>(1, std::min(div_up(256, tiles), div_up(rows, 256)));
   return std::max<int64_t>(kStepK, div_up(div_up(rows, runs), kStepK) * kStepK);
 }
 
@@ -302,12 +311,8 @@ int64_t grad_run(int64_t rows, int64_t cin, int64_t cols) {
 
 bool pieces_fit(const Mat16& a) { return aligned16(a.p) && a.ld % 8 == 0 && a.cols % 8 == 0; }
 
-int64_t packed_bytes(int64_t rows, int64_t cols, int groups) {
-  return rows * groups * round8(cols / groups) * 2;
-}
-
-int pack16(const Mat16& a, int groups, void* to, Mat16* out, hipStream_t stream) {
-  const int64_t gp = round8(a.cols / groups);
+int pack16(const Mat16& a, int groups, int unit, void* to, Mat16* out, hipStream_t stream) {
+  const int64_t gp = round_to(a.cols / groups, unit);
   *out = Mat16{static_cast<const uint16_t*>(to), a.rows, groups * gp, groups * gp};
   const int64_t pieces = a.rows * groups * gp / 8;
   if (pieces == 0) return SUBMCONV_OK;
@@ -332,7 +337,7 @@ int64_t column_parts(int64_t rows, int64_t cols) {
 }
 
 int column_sums(const Mat16& a, bool bf16, float* partial, float* out, hipStream_t stream) {
-  const int st = act_grad(a, nullptr, kActNone, bf16, nullptr, 0, partial, stream);
+  const int st = act_grad(a, nullptr, kActNone, bf16, nullptr, partial, stream);
   if (st != SUBMCONV_OK) return st;
   return sum_parts(partial, column_parts(a.rows, a.cols), round8(a.cols), a.cols, 1, out, stream);
 }
@@ -344,16 +349,14 @@ int linear_forward(const Mat16& x, const Mat16& W, const float* bias, int act, b
                     cols % 8 == 0 && ldr % 8 == 0 && aligned16(residual),
                     cols % 8 == 0 && ldo % 8 == 0 && aligned16(out),
                     cols % 8 == 0 && aligned16(pre)};
-  return linear_product<true>(Operand{x.p, x.ld, x.rows, x.cols}, Operand{W.p, W.ld, W.cols, W.rows}, x.cols, cols,
-                              bf16, e, stream);
+  return linear_product<true>(x, Operand{W.p, W.ld, W.cols, W.rows}, cols, bf16, e, stream);
 }
 
 int product_nt(const Mat16& dz, const Mat16& W, bool bf16, uint16_t* out, int64_t ldo,
                int64_t cols, hipStream_t stream) {
   const LinearEpi e{nullptr, nullptr, 0, out, ldo, nullptr, kActNone,
                     false, cols % 8 == 0 && ldo % 8 == 0 && aligned16(out), false};
-  return linear_product<false>(Operand{dz.p, dz.ld, dz.rows, dz.cols}, Operand{W.p, W.ld, W.rows, W.cols}, dz.cols,
-                               cols, bf16, e, stream);
+  return linear_product<false>(dz, Operand{W.p, W.ld, W.rows, W.cols}, cols, bf16, e, stream);
 }
 
 int64_t product_tn_bytes(int64_t rows, int64_t cin, int64_t cols) {
@@ -370,10 +373,15 @@ int product_tn(const Mat16& x, const Mat16& dz, bool bf16, float* partial, uint1
                      (long long)x.cols, (long long)dz.cols);
   const Operand X{x.p, x.ld, x.cols, x.rows}, Z{dz.p, dz.ld, dz.cols, x.rows};
   const dim3 grid(static_cast<unsigned>(runs * mt * nt));
-  if (bf16)
-    k_weight_grad<true, kGradTile, kGradTile, 2, 4, 2><<<grid, 512, 0, stream>>>(X, Z, x.rows, run, mt, nt, partial);
-  else
-    k_weight_grad<false, kGradTile, kGradTile, 2, 4, 2><<<grid, 512, 0, stream>>>(X, Z, x.rows, run, mt, nt, partial);
+  auto launch = [&](auto xt, auto zt) {
+    if (bf16)
+      k_weight_grad<true, xt, zt, kGradTile, kGradTile, 2, 4, 3><<<grid, 512, 0, stream>>>(X, Z, x.rows, run, mt, nt, partial);
+    else
+      k_weight_grad<false, xt, zt, kGradTile, kGradTile, 2, 4, 3><<<grid, 512, 0, stream>>>(X, Z, x.rows, run, mt, nt, partial);
+  };
+  if (x.blocked) launch(std::true_type{}, std::false_type{});
+  else if (dz.blocked) launch(std::false_type{}, std::true_type{});
+  else launch(std::false_type{}, std::false_type{});
   SUBMCONV_HIP_CHECK(hipGetLastError());
   const int64_t plane = x.cols * dz.cols;
   const dim3 rgrid(static_cast<unsigned>(div_up(plane, 256)));
@@ -385,14 +393,14 @@ int product_tn(const Mat16& x, const Mat16& dz, bool bf16, float* partial, uint1
   return SUBMCONV_OK;
 }
 
-int readable(const Mat16& a, int groups, Arena& ws, Mat16* out, hipStream_t stream) {
-  if (pieces_fit(a) && a.cols % (8 * groups) == 0) {
+int readable(const Mat16& a, int groups, int unit, Arena& ws, Mat16* out, hipStream_t stream) {
+  if (pieces_fit(a) && a.cols % (unit * groups) == 0) {
     *out = a;
     return SUBMCONV_OK;
   }
-  void* to = ws.take(packed_bytes(a.rows, a.cols, groups));
+  void* to = ws.take(a.rows * groups * round_to(a.cols / groups, unit) * 2);
   if (ws.counting) return SUBMCONV_OK;
-  return pack16(a, groups, to, out, stream);
+  return pack16(a, groups, unit, to, out, stream);
 }
 
 int check_shape(const char* name, int64_t rows, int64_t cols) {
@@ -443,8 +451,8 @@ struct LinearWork {
   Mat16 x, W;
 };
 int linear_work(const Mat16& x, const Mat16& W, Arena& ws, LinearWork* w, hipStream_t stream) {
-  SUBMCONV_TRY(readable(x, 1, ws, &w->x, stream));
-  return readable(W, 1, ws, &w->W, stream);
+  SUBMCONV_TRY(readable(x, 1, 8, ws, &w->x, stream));
+  return readable(W, 1, 8, ws, &w->W, stream);
 }
 
 struct LinearGradNeeds {
@@ -456,28 +464,29 @@ int linear_grad(const Mat16& dy, const Mat16& x, const Mat16& W, const uint16_t*
                 hipStream_t stream) {
   const bool run = !ws.counting;
   const int64_t cp = round8(dy.cols);
-  const bool own_dz = act != kActNone || !pieces_fit(dy);
+  const bool own_dz = (act != kActNone || !pieces_fit(dy)) && (need.x || need.w);
   Mat16 dz = dy;
   uint16_t* dz_to = nullptr;
   if (own_dz) {
-    dz_to = static_cast<uint16_t*>(ws.take(dy.rows * cp * 2));
-    dz = Mat16{dz_to, dy.rows, cp, cp};
+    const int64_t cq = round64(dy.cols);
+    dz_to = static_cast<uint16_t*>(ws.take(blocked_bytes(dy.rows, cq)));
+    dz = blocked16(dz_to, dy.rows, cq);
   }
   const int64_t parts = column_parts(dy.rows, dy.cols);
   float* sums = need.b ? static_cast<float*>(ws.take(parts * cp * 4)) : nullptr;
   if (run && (own_dz || need.b)) {
-    SUBMCONV_TRY(act_grad(dy, pre, act, bf16, dz_to, cp, sums, stream));
+    SUBMCONV_TRY(act_grad(dy, pre, act, bf16, dz_to, sums, stream));
     if (need.b) SUBMCONV_TRY(sum_parts(sums, parts, cp, dy.cols, 1, gb, stream));
   }
   if (need.x) {
     Mat16 Wr;
-    SUBMCONV_TRY(readable(W, 1, ws, &Wr, stream));
+    SUBMCONV_TRY(readable(W, 1, own_dz ? 64 : 8, ws, &Wr, stream));
     if (run) SUBMCONV_TRY(product_nt(dz, Wr, bf16, gx, x.cols, x.cols, stream));
   }
   if (need.w) {
     Mat16 xr;
-    SUBMCONV_TRY(readable(x, 1, ws, &xr, stream));
-    float* part = static_cast<float*>(ws.take(product_tn_bytes(x.rows, round8(x.cols), cp)));
+    SUBMCONV_TRY(readable(x, 1, 8, ws, &xr, stream));
+    float* part = static_cast<float*>(ws.take(product_tn_bytes(x.rows, round8(x.cols), dz.cols)));
     if (run) SUBMCONV_TRY(product_tn(xr, dz, bf16, part, gw, x.cols, dy.cols, 1, stream));
   }
   return SUBMCONV_OK;
