@@ -57,6 +57,18 @@ int linear_forward(const Mat16& x, const Mat16& W, const float* bias, int act, b
                    const uint16_t* residual, int64_t ldr, uint16_t* out, int64_t ldo, uint16_t* pre,
                    int64_t cols, hipStream_t stream);
 
+// Forward products of 1 .. kFewRows rows, which read any matrix as it is
+// (few_rows.hip): the linear layer, the gated block's hidden rows in fp32
+// [rows][W_in.cols / 2], and its output from those.
+constexpr int kFewRows = 8;
+int few_linear(const Mat16& x, const Mat16& W, const float* bias, int act, bool bf16,
+               const uint16_t* residual, int64_t ldr, uint16_t* out, uint16_t* pre,
+               hipStream_t stream);
+int few_gate(const Mat16& x, const Mat16& W, const float* bias, int act, bool bf16, float* h,
+             uint16_t* pre, hipStream_t stream);
+int few_out(const float* h, int64_t rows, const Mat16& W, const float* bias, bool bf16,
+            const uint16_t* residual, int64_t ldr, uint16_t* out, hipStream_t stream);
+
 // Cuts a caller's workspace into 256-byte aligned pieces, or, counting, only
 // adds up what they take: the steps of an operator go through one function,
 // which enqueues nothing while it counts.

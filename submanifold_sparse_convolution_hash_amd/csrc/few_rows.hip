@@ -1,0 +1,162 @@
+// Forward products of a few rows (at most kFewRows) with a weight matrix: one
+// conditioning vector, one timestep, a handful of sites. A product reads its
+// whole weight matrix for 2 flops per row and element, so it is bound by the
+// weights' way to the compute units and, at the usual sizes, by its latency:
+// one launch, no join between workgroups, no LDS tiles.
+//
+// A workgroup owns a strip of LPR x 8 columns for all rows. Each thread walks
+// every (512 / LPR)-th row of W, 16 bytes at a time, straight from memory into
+// fp32 products with the rows of x (held in LDS as fp32); the threads' sums
+// are joined by lane exchanges, then through LDS, in one fixed order. Strips
+// are narrow (32 bytes, 64 or 128) while the matrix has few columns, so that
+// enough compute units pull on it.
+//
+// At 1 x 256 -> 1024 and 1 x 512 -> 2048 -> 512 (gated) the MFMA tile kernels
+// take longer than these: their 128 rows are mostly empty, and a workgroup
+// walks all of k in latency-bound steps.
+#include <algorithm>
+
+#include "dense_common.h"
+#include "dense_tile.h"
+
+namespace submconv {
+namespace {
+
+constexpr int kFewThreads = 512;
+constexpr int kFewChunk = 1024;  // k of x in LDS at a time
+
+struct FewEpi {
+  const float* bias;
+  const uint16_t* residual;
+  int64_t ldr;
+  uint16_t* out;   // 16-bit result, or
+  float* out32;    // fp32 result (the hidden rows between two products)
+  uint16_t* pre;   // or null; GATED: [rows][2 N]
+  int act;
+};
+
+template <bool BF16, typename X>
+__device__ __forceinline__ float few_x(X v) {
+  if constexpr (std::is_same_v<X, float>) return v;
+  else return to_f32<BF16>(v);
+}
+
+// out[m][n] = epilogue(sum_k x[m][k] W[k][n]), m < M; GATED: the gate's N
+// columns of W, then the up projection's, out = act(gate) up.
+template <bool BF16, typename X, int M, int LPR, bool GATED>
+__global__ __launch_bounds__(kFewThreads) void k_few(const X* __restrict__ x, int64_t ldx, int rows,
+                                                     const uint16_t* __restrict__ W, int64_t ldw,
+                                                     bool vec, int64_t K, int64_t N, FewEpi e) {
+  constexpr int H = GATED ? 2 : 1;
+  constexpr int SLICES = kFewThreads / LPR, COLS = LPR * 8, WAVES = kFewThreads / 64;
+  __shared__ float xs[M][kFewChunk];
+  __shared__ float sums[WAVES][H][M][COLS];
+  const int l = threadIdx.x % LPR, slice = threadIdx.x / LPR;
+  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * COLS, n = n0 + l * 8;
+  float acc[H][M][8] = {};
+  for (int64_t c0 = 0; c0 < K; c0 += kFewChunk) {
+    const int len = static_cast<int>(K - c0 < kFewChunk ? K - c0 : kFewChunk);
+    __syncthreads();
+    for (int i = threadIdx.x; i < M * kFewChunk; i += kFewThreads) {
+      const int m = i / kFewChunk, k = i % kFewChunk;
+      if (k < len) xs[m][k] = m < rows ? few_x<BF16>(x[m * ldx + c0 + k]) : 0.0f;
+    }
+    __syncthreads();
+#pragma unroll 4
+    for (int k = slice; k < len; k += SLICES) {
+#pragma unroll
+      for (int h = 0; h < H; ++h) {
+        float w[8];
+        unpack8<BF16>(load_piece(W + (c0 + k) * ldw + h * N, n, N, vec), w);
+#pragma unroll
+        for (int m = 0; m < M; ++m) {
+          const float v = xs[m][k];
+#pragma unroll
+          for (int q = 0; q < 8; ++q) acc[h][m][q] += v * w[q];
+        }
+      }
+    }
+  }
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+  for (int h = 0; h < H; ++h)
+#pragma unroll
+    for (int m = 0; m < M; ++m)
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        float v = acc[h][m][q];
+#pragma unroll
+        for (int o = LPR; o < 64; o <<= 1) v += __shfl_xor(v, o, 64);
+        if (lane < LPR) sums[wave][h][m][l * 8 + q] = v;
+      }
+  __syncthreads();
+  for (int i = threadIdx.x; i < M * COLS; i += kFewThreads) {
+    const int m = i / COLS, c = i % COLS;
+    const int64_t col = n0 + c;
+    if (m >= rows || col >= N) continue;
+    float z[H];
+#pragma unroll
+    for (int h = 0; h < H; ++h) {
+      z[h] = e.bias ? e.bias[h * N + col] : 0.0f;
+#pragma unroll
+      for (int w = 0; w < WAVES; ++w) z[h] += sums[w][h][m][c];
+      if (e.pre) e.pre[(m * H + h) * N + col] = to_16<BF16>(z[h]);
+    }
+    float v = 0.0f;
+    with_act(e.act, [&](auto a) { v = act_value<decltype(a)::value>(z[0]); });
+    if constexpr (GATED) v *= z[H - 1];
+    if (e.residual) v += to_f32<BF16>(e.residual[m * e.ldr + col]);
+    if (e.out32) e.out32[m * N + col] = v;
+    else e.out[m * N + col] = to_16<BF16>(v);
+  }
+}
+
+template <bool BF16, typename X, bool GATED>
+int launch_few(const X* x, int64_t ldx, int rows, const Mat16& W, int64_t N, const FewEpi& e,
+               hipStream_t stream) {
+  const bool vec = aligned16(W.p) && W.ld % 8 == 0 && N % 8 == 0;
+  auto go = [&](auto m, auto lpr) {
+    const dim3 grid(static_cast<unsigned>(div_up(N, lpr * 8)));
+    k_few<BF16, X, m, lpr, GATED><<<grid, kFewThreads, 0, stream>>>(x, ldx, rows, W.p, W.ld, vec,
+                                                                   W.rows, N, e);
+  };
+  auto by_rows = [&](auto lpr) {
+    if (rows <= 1) go(std::integral_constant<int, 1>{}, lpr);
+    else if (rows <= 2) go(std::integral_constant<int, 2>{}, lpr);
+    else if (rows <= 4) go(std::integral_constant<int, 4>{}, lpr);
+    else go(std::integral_constant<int, kFewRows>{}, lpr);
+  };
+  if (N <= 2048) by_rows(std::integral_constant<int, 2>{});
+  else if (N <= 8192) by_rows(std::integral_constant<int, 4>{});
+  else by_rows(std::integral_constant<int, 8>{});
+  SUBMCONV_HIP_CHECK(hipGetLastError());
+  return SUBMCONV_OK;
+}
+
+}  // namespace
+
+int few_linear(const Mat16& x, const Mat16& W, const float* bias, int act, bool bf16,
+               const uint16_t* residual, int64_t ldr, uint16_t* out, uint16_t* pre,
+               hipStream_t stream) {
+  const FewEpi e{bias, residual, ldr, out, nullptr, pre, act};
+  const int rows = static_cast<int>(x.rows);
+  return bf16 ? launch_few<true, uint16_t, false>(x.p, x.ld, rows, W, W.cols, e, stream)
+              : launch_few<false, uint16_t, false>(x.p, x.ld, rows, W, W.cols, e, stream);
+}
+
+int few_gate(const Mat16& x, const Mat16& W, const float* bias, int act, bool bf16, float* h,
+             uint16_t* pre, hipStream_t stream) {
+  const FewEpi e{bias, nullptr, 0, nullptr, h, pre, act};
+  const int rows = static_cast<int>(x.rows);
+  return bf16 ? launch_few<true, uint16_t, true>(x.p, x.ld, rows, W, W.cols / 2, e, stream)
+              : launch_few<false, uint16_t, true>(x.p, x.ld, rows, W, W.cols / 2, e, stream);
+}
+
+int few_out(const float* h, int64_t rows, const Mat16& W, const float* bias, bool bf16,
+            const uint16_t* residual, int64_t ldr, uint16_t* out, hipStream_t stream) {
+  const FewEpi e{bias, residual, ldr, out, nullptr, nullptr, kActNone};
+  return bf16 ? launch_few<true, float, false>(h, W.rows, static_cast<int>(rows), W, W.cols, e, stream)
+              : launch_few<false, float, false>(h, W.rows, static_cast<int>(rows), W, W.cols, e, stream);
+}
+
+}  // namespace submconv

@@ -223,6 +223,12 @@ struct Ffn {
 
 int ffn_forward(const Ffn& f, const float* b_in, const float* b_out, const uint16_t* residual,
                 int64_t ldr, uint16_t* out, uint16_t* pre, Arena& ws, hipStream_t stream) {
+  if (f.n <= kFewRows) {
+    float* h = static_cast<float*>(ws.take(f.n * f.F * 4));
+    if (ws.counting || f.n == 0) return SUBMCONV_OK;
+    SUBMCONV_TRY(few_gate(f.x, f.W_in, b_in, f.act, f.bf16, h, pre, stream));
+    return few_out(h, f.n, f.W_out, b_out, f.bf16, residual, ldr, out, stream);
+  }
   const int64_t Fq = round64(f.F);
   Mat16 x, wi, wo;
   SUBMCONV_TRY(readable(f.x, 1, 8, ws, &x, stream));

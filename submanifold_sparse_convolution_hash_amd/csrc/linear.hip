@@ -451,6 +451,10 @@ struct LinearWork {
   Mat16 x, W;
 };
 int linear_work(const Mat16& x, const Mat16& W, Arena& ws, LinearWork* w, hipStream_t stream) {
+  if (x.rows <= kFewRows) {  // read in place
+    *w = LinearWork{x, W};
+    return SUBMCONV_OK;
+  }
   SUBMCONV_TRY(readable(x, 1, 8, ws, &w->x, stream));
   return readable(W, 1, 8, ws, &w->W, stream);
 }
@@ -528,8 +532,10 @@ extern "C" int submconv_linear(const uint16_t* x, int64_t ldx, int64_t n, const 
   SUBMCONV_TRY(check_workspace(workspace, workspace_bytes, need.used));
   Arena ws{false, static_cast<char*>(workspace)};
   if (need.used > 0) SUBMCONV_TRY(linear_work(xm, wm, ws, &w, stream));
-  return linear_forward(w.x, w.W, bias, act, dtype == SUBMCONV_DTYPE_BF16, residual,
-                        n == 1 ? round8(cout) : ldr, out, cout, pre, cout, stream);
+  if (n <= kFewRows)
+    return few_linear(w.x, w.W, bias, act, dtype == SUBMCONV_DTYPE_BF16, residual, ldr, out, pre, stream);
+  return linear_forward(w.x, w.W, bias, act, dtype == SUBMCONV_DTYPE_BF16, residual, ldr, out, cout, pre,
+                        cout, stream);
 }
 
 extern "C" int64_t submconv_linear_backward_workspace_bytes(int64_t n, int32_t cin, int32_t cout,

@@ -17,7 +17,7 @@ from typing import Optional, Tuple
 
 import torch
 
-from . import _DTYPES, _check, _ptr, _stream, load_library
+from . import _DTYPES, _check, load_library
 
 __all__ = [
     "layer_norm", "layer_norm_backward", "linear", "linear_backward", "gated_ffn", "gated_ffn_backward",
@@ -29,6 +29,14 @@ __all__ = [
 ACTIVATIONS = {"none": 0, None: 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 _NORM_DTYPES = {**_DTYPES, torch.float32: 2}
 _HERE = contextlib.nullcontext()
+
+
+def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
+    return None if t is None else t.data_ptr()
+
+
+def _stream(device: torch.device) -> int:
+    return torch.cuda.current_stream(device).cuda_stream
 
 
 def _on(device: torch.device):

@@ -163,7 +163,8 @@ def test_layer_norm_differences(dev):
 # linear
 # ---------------------------------------------------------------------------
 
-LINEAR_SHAPES = [(1, 256, 1024, 0), (1, 1, 1, 0), (0, 16, 8, 0), (2, 8, 8, 0), (7, 72, 40, 0), (5, 33, 130, 1),
+LINEAR_SHAPES = [(1, 256, 1024, 0), (8, 40, 24, 1), (9, 40, 24, 1), (3, 2500, 40, 0), (4, 16, 8200, 0), (6, 24, 3000, 3),
+                  (1, 1, 1, 0), (0, 16, 8, 0), (2, 8, 8, 0), (7, 72, 40, 0), (5, 33, 130, 1),
                  (16, 64, 64, 8), (127, 64, 128, 0), (128, 128, 128, 0), (129, 136, 264, 0), (300, 195, 77, 5),
                  (1000, 64, 512, 0), (513, 1000, 24, 0), (260, 512, 520, 4), (33, 2048, 96, 0)]
 
@@ -280,7 +281,7 @@ def test_linear_writes_nothing_else(dev):
 # gated feed-forward
 # ---------------------------------------------------------------------------
 
-FFN_SHAPES = [(1, 64, 128, 64, 0), (1, 512, 2048, 512, 0), (0, 32, 64, 16, 0), (2, 16, 8, 8, 0), (3, 9, 5, 3, 1),
+FFN_SHAPES = [(1, 64, 128, 64, 0), (8, 33, 1100, 17, 2), (5, 16, 3000, 24, 0), (1, 512, 2048, 512, 0), (0, 32, 64, 16, 0), (2, 16, 8, 8, 0), (3, 9, 5, 3, 1),
               (9, 40, 100, 24, 0), (64, 64, 64, 64, 0), (130, 128, 512, 128, 0), (129, 100, 267, 100, 0),
               (300, 72, 136, 200, 8), (1000, 64, 256, 64, 3), (257, 256, 72, 136, 0)]
 
@@ -509,8 +510,9 @@ def test_refusals(dev):
     assert call(_0=None) == -1 and call(_3=None) == -1 and call(_7=None) == -1
     assert call(_1=7) == -1 and call(_1=1 << 40) == -4
     assert call(_9=0) == -4 and call(_11=9) == -1 and call(_12=2) == -1 and call(_2=-1) == -1
-    odd = torch.zeros(65, **h)[1:]
-    assert call(_0=p(odd)) == -1  # needs a copy: workspace missing
+    odd, outs = torch.zeros(9 * 8 + 1, **h)[1:], torch.zeros((9, 16), **h)
+    assert call(_0=p(odd)) == 0   # few rows are read as they are
+    assert call(_0=p(odd), _2=9, _7=p(outs)) == -1  # more need a copy: workspace missing
     assert b"workspace" in lib.submconv_last_error()
     assert lib.submconv_linear_workspace_bytes(4, 0, 16, 0) == -4
     assert lib.submconv_gated_ffn_workspace_bytes(-1, 8, 16, 8, 0) == -1
