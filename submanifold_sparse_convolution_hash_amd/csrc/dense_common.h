@@ -24,9 +24,19 @@ inline int64_t blocked_bytes(int64_t rows, int64_t cols) { return (rows + 127) /
 // on 16 bytes and never straddle a row's end.
 bool pieces_fit(const Mat16& a);
 
-// Copies `a` with each of its `groups` column groups padded with zeros to a
-// multiple of `unit` columns, and returns the copy.
-int pack16(const Mat16& a, int groups, int unit, void* to, Mat16* out, hipStream_t stream);
+// A copy of a matrix whose column groups of `from_cols` are padded with zeros
+// to `to_cols`, a multiple of 8.
+struct PackJob {
+  const uint16_t* from;
+  int64_t rows, ld, from_cols, to_cols, row_pieces;
+  uint16_t* to;
+};
+constexpr int kPacks = 4;
+struct PackList {
+  PackJob job[kPacks];
+  int count = 0;
+};
+int run_packs(const PackList& list, hipStream_t stream);
 
 // out[c] = sum over `parts` rows of partial[part][ld], c < cols, in order;
 // columns of `groups` padded groups are closed up.
@@ -85,9 +95,8 @@ struct Arena {
 
 // The matrix itself where products can read it in pieces and its column groups
 // are multiples of `unit` (8; 64 where its columns are the k of a blocked
-// matrix), else a padded copy in the arena (which `out` describes unless the
-// arena is counting).
-int readable(const Mat16& a, int groups, int unit, Arena& ws, Mat16* out, hipStream_t stream);
+// matrix), else its padded copy in the arena, which is then on the list.
+Mat16 readable(const Mat16& a, int groups, int unit, Arena& ws, PackList* list);
 
 // Argument checks shared by the entry points.
 int check_matrix(const char* name, const void* p, int64_t rows, int64_t cols, int64_t ld);

@@ -18,12 +18,12 @@
 
 #include "dense_common.h"
 #include "dense_tile.h"
+#include "lane_ops.h"
 
 namespace submconv {
 namespace {
 
 constexpr int kFewThreads = 512;
-constexpr int kFewChunk = 1024;  // k of x in LDS at a time
 
 struct FewEpi {
   const float* bias;
@@ -49,32 +49,23 @@ __global__ __launch_bounds__(kFewThreads) void k_few(const X* __restrict__ x, in
                                                      bool vec, int64_t K, int64_t N, FewEpi e) {
   constexpr int H = GATED ? 2 : 1;
   constexpr int SLICES = kFewThreads / LPR, COLS = LPR * 8, WAVES = kFewThreads / 64;
-  __shared__ float xs[M][kFewChunk];
   __shared__ float sums[WAVES][H][M][COLS];
   const int l = threadIdx.x % LPR, slice = threadIdx.x / LPR;
   const int64_t n0 = static_cast<int64_t>(blockIdx.x) * COLS, n = n0 + l * 8;
   float acc[H][M][8] = {};
-  for (int64_t c0 = 0; c0 < K; c0 += kFewChunk) {
-    const int len = static_cast<int>(K - c0 < kFewChunk ? K - c0 : kFewChunk);
-    __syncthreads();
-    for (int i = threadIdx.x; i < M * kFewChunk; i += kFewThreads) {
-      const int m = i / kFewChunk, k = i % kFewChunk;
-      if (k < len) xs[m][k] = m < rows ? few_x<BF16>(x[m * ldx + c0 + k]) : 0.0f;
-    }
-    __syncthreads();
 #pragma unroll 4
-    for (int k = slice; k < len; k += SLICES) {
+  for (int64_t k = slice; k < K; k += SLICES) {
+    float v[M];
 #pragma unroll
-      for (int h = 0; h < H; ++h) {
-        float w[8];
-        unpack8<BF16>(load_piece(W + (c0 + k) * ldw + h * N, n, N, vec), w);
+    for (int m = 0; m < M; ++m) v[m] = few_x<BF16>(x[(m < rows ? m : 0) * ldx + k]);
 #pragma unroll
-        for (int m = 0; m < M; ++m) {
-          const float v = xs[m][k];
+    for (int h = 0; h < H; ++h) {
+      float w[8];
+      unpack8<BF16>(load_piece(W + k * ldw + h * N, n, N, vec), w);
 #pragma unroll
-          for (int q = 0; q < 8; ++q) acc[h][m][q] += v * w[q];
-        }
-      }
+      for (int m = 0; m < M; ++m)
+#pragma unroll
+        for (int q = 0; q < 8; ++q) acc[h][m][q] += v[m] * w[q];
     }
   }
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -84,9 +75,7 @@ __global__ __launch_bounds__(kFewThreads) void k_few(const X* __restrict__ x, in
     for (int m = 0; m < M; ++m)
 #pragma unroll
       for (int q = 0; q < 8; ++q) {
-        float v = acc[h][m][q];
-#pragma unroll
-        for (int o = LPR; o < 64; o <<= 1) v += __shfl_xor(v, o, 64);
+        const float v = lanes_sum_over<LPR>(acc[h][m][q]);
         if (lane < LPR) sums[wave][h][m][l * 8 + q] = v;
       }
   __syncthreads();

@@ -230,12 +230,12 @@ int ffn_forward(const Ffn& f, const float* b_in, const float* b_out, const uint1
     return few_out(h, f.n, f.W_out, b_out, f.bf16, residual, ldr, out, stream);
   }
   const int64_t Fq = round64(f.F);
-  Mat16 x, wi, wo;
-  SUBMCONV_TRY(readable(f.x, 1, 8, ws, &x, stream));
-  SUBMCONV_TRY(readable(f.W_in, 2, 8, ws, &wi, stream));
-  SUBMCONV_TRY(readable(f.W_out, 1, 8, ws, &wo, stream));
+  PackList packs;
+  const Mat16 x = readable(f.x, 1, 8, ws, &packs), wi = readable(f.W_in, 2, 8, ws, &packs);
+  const Mat16 wo = readable(f.W_out, 1, 8, ws, &packs);
   uint16_t* h = static_cast<uint16_t*>(ws.take(blocked_bytes(f.n, Fq)));
   if (ws.counting || f.n == 0) return SUBMCONV_OK;
+  SUBMCONV_TRY(run_packs(packs, stream));
   SUBMCONV_TRY(gate_forward(x, wi, f.F, b_in, f.act, f.bf16, h, pre, stream));
   return linear_forward(blocked16(h, f.n, Fq), wo, b_out, kActNone, f.bf16, residual, ldr, out, f.Co,
                         nullptr, f.Co, stream);
@@ -248,40 +248,38 @@ struct FfnGrads {
 };
 
 int ffn_backward(const Ffn& f, const uint16_t* pre, const FfnGrads& g, Arena& ws, hipStream_t stream) {
-  const bool run = !ws.counting;
   const int64_t Fq = round64(f.F), Cp = round8(f.C), Op = round8(f.Co);
-  Mat16 dy, wo;
-  SUBMCONV_TRY(readable(f.dy, 1, 8, ws, &dy, stream));
-  if (g.all || g.b_out) {
-    float* part = static_cast<float*>(ws.take(column_parts(f.n, f.Co) * Op * 4));
-    if (run) SUBMCONV_TRY(column_sums(f.dy, f.bf16, part, g.b_out, stream));
+  const bool need_x = g.all || g.x, need_wi = g.all || g.W_in, need_wo = g.all || g.W_out;
+  const bool need_bi = g.all || g.b_in, need_bo = g.all || g.b_out;
+  const bool hidden = need_x || need_wi || need_wo || need_bi;
+  PackList packs;
+  Mat16 dy, x, wi, wo;
+  if (hidden) {
+    dy = readable(f.dy, 1, 8, ws, &packs);
+    wo = readable(f.W_out, 1, 8, ws, &packs);
   }
-  if (!(g.all || g.x || g.W_in || g.W_out || g.b_in)) return SUBMCONV_OK;
-  SUBMCONV_TRY(readable(f.W_out, 1, 8, ws, &wo, stream));
-  uint16_t* h = static_cast<uint16_t*>(ws.take(blocked_bytes(f.n, Fq)));
-  uint16_t* dz = static_cast<uint16_t*>(ws.take(blocked_bytes(f.n, 2 * Fq)));
+  if (need_x) wi = readable(f.W_in, 2, 64, ws, &packs);
+  if (need_wi) x = readable(f.x, 1, 8, ws, &packs);
+  float* dy_sums = need_bo ? static_cast<float*>(ws.take(column_parts(f.n, f.Co) * Op * 4)) : nullptr;
   const int64_t tiles = gate_grad_tiles(f.n);
-  float* sums = g.all || g.b_in ? static_cast<float*>(ws.take(tiles * 2 * Fq * 4)) : nullptr;
+  uint16_t* h = hidden ? static_cast<uint16_t*>(ws.take(blocked_bytes(f.n, Fq))) : nullptr;
+  uint16_t* dz = hidden ? static_cast<uint16_t*>(ws.take(blocked_bytes(f.n, 2 * Fq))) : nullptr;
+  float* sums = need_bi ? static_cast<float*>(ws.take(tiles * 2 * Fq * 4)) : nullptr;
+  float* part = nullptr;
+  if (need_wi || need_wo)
+    part = static_cast<float*>(ws.take(std::max(need_wi ? product_tn_bytes(f.n, Cp, 2 * Fq) : 0,
+                                                need_wo ? product_tn_bytes(f.n, Fq, Op) : 0)));
+  if (ws.counting) return SUBMCONV_OK;
+
+  SUBMCONV_TRY(run_packs(packs, stream));
+  if (need_bo) SUBMCONV_TRY(column_sums(f.dy, f.bf16, dy_sums, g.b_out, stream));
+  if (!hidden) return SUBMCONV_OK;
   const Mat16 hm = blocked16(h, f.n, Fq), zm = blocked16(dz, f.n, 2 * Fq);
-  if (run) {
-    SUBMCONV_TRY(gate_grad(dy, wo, Fq, pre, f.act, f.bf16, dz, h, sums, stream));
-    if (g.b_in) SUBMCONV_TRY(sum_parts(sums, tiles, 2 * Fq, 2 * f.F, 2, g.b_in, stream));
-  }
-  if (g.all || g.x) {
-    Mat16 wi;
-    SUBMCONV_TRY(readable(f.W_in, 2, 64, ws, &wi, stream));
-    if (run) SUBMCONV_TRY(product_nt(zm, wi, f.bf16, g.x, f.C, f.C, stream));
-  }
-  if (g.all || g.W_in || g.W_out) {
-    float* part = static_cast<float*>(ws.take(std::max(g.all || g.W_in ? product_tn_bytes(f.n, Cp, 2 * Fq) : 0,
-                                                       g.all || g.W_out ? product_tn_bytes(f.n, Fq, Op) : 0)));
-    if (g.all || g.W_in) {
-      Mat16 x;
-      SUBMCONV_TRY(readable(f.x, 1, 8, ws, &x, stream));
-      if (run) SUBMCONV_TRY(product_tn(x, zm, f.bf16, part, g.W_in, f.C, 2 * f.F, 2, stream));
-    }
-    if (run && g.W_out) SUBMCONV_TRY(product_tn(hm, dy, f.bf16, part, g.W_out, f.F, f.Co, 1, stream));
-  }
+  SUBMCONV_TRY(gate_grad(dy, wo, Fq, pre, f.act, f.bf16, dz, h, sums, stream));
+  if (need_bi) SUBMCONV_TRY(sum_parts(sums, tiles, 2 * Fq, 2 * f.F, 2, g.b_in, stream));
+  if (need_x) SUBMCONV_TRY(product_nt(zm, wi, f.bf16, g.x, f.C, f.C, stream));
+  if (need_wi) SUBMCONV_TRY(product_tn(x, zm, f.bf16, part, g.W_in, f.C, 2 * f.F, 2, stream));
+  if (need_wo) SUBMCONV_TRY(product_tn(hm, dy, f.bf16, part, g.W_out, f.F, f.Co, 1, stream));
   return SUBMCONV_OK;
 }
 

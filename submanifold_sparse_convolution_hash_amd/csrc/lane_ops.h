@@ -52,5 +52,18 @@ __device__ __forceinline__ float lanes_sum(float x) {
   return x;
 }
 
+// Sum over the lanes that are equal modulo L (2, 4 or 8), in all of them.
+template <int L>
+__device__ __forceinline__ float lanes_sum_over(float x) {
+  static_assert(L == 2 || L == 4 || L == 8, "lanes");
+  if constexpr (L <= 2) x += dpp<0x4E>(x);   // lanes 2 3 0 1 of each four
+  if constexpr (L <= 4) x += dpp<0x124>(x);  // each sixteen turned by four
+  x += dpp<0x128>(x);                        // and by eight
+  const uint32_t v = __builtin_bit_cast(uint32_t, x);
+  x = swap_sum(lane_rows_swap(v, v));
+  const uint32_t u = __builtin_bit_cast(uint32_t, x);
+  return swap_sum(lane_halves_swap(u, u));
+}
+
 }  // namespace
 }  // namespace submconv

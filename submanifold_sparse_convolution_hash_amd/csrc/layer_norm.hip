@@ -50,6 +50,25 @@ __device__ __forceinline__ void store_vec(T* p, const float (&v)[VEC]) {
   }
 }
 
+// VEC weights from column c of [C] (zeros past it, or from a null vector),
+// without a branch.
+template <int VEC>
+__device__ __forceinline__ void load_weights(const float* w, int C, int c, float (&v)[VEC]) {
+  const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<float*>(w), static_cast<short>(0), w ? C * 4 : 0, 0x00020000);
+  if constexpr (VEC >= 4) {
+    typedef float float4v __attribute__((ext_vector_type(4)));
+#pragma unroll
+    for (int e = 0; e < VEC; e += 4) {
+      const float4v t = __builtin_bit_cast(float4v, __builtin_amdgcn_raw_buffer_load_b128(r, (c + e) * 4, 0, 0));
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v[e + q] = t[q];
+    }
+  } else {
+    v[0] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(r, c * 4, 0, 0));
+  }
+}
+
 // ---- sums over the G lanes of a row, the same in each of them ----
 
 // G = 256: the four waves' sums through LDS (`slot`: a place per use, so that
@@ -78,13 +97,10 @@ __global__ __launch_bounds__(kNormThreads) void k_layer_norm(
   const bool lead = l == 0;
   float wv[V][VEC], bv[V][VEC];
 #pragma unroll
-  for (int i = 0; i < V; ++i)
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      const int c = (i * G + l) * VEC + e;
-      wv[i][e] = w && c < C ? w[c] : 1.0f;
-      bv[i][e] = b && c < C ? b[c] : 0.0f;
-    }
+  for (int i = 0; i < V; ++i) {
+    load_weights<VEC>(w, C, (i * G + l) * VEC, wv[i]);
+    load_weights<VEC>(b, C, (i * G + l) * VEC, bv[i]);
+  }
   int turn = 0;
   for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * RPB; r0 < n;
        r0 += static_cast<int64_t>(gridDim.x) * RPB, turn ^= 1) {
@@ -118,7 +134,7 @@ __global__ __launch_bounds__(kNormThreads) void k_layer_norm(
     for (int i = 0; i < V; ++i) {
       const int c = (i * G + l) * VEC;
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) v[i][e] = v[i][e] * rs * wv[i][e] + bv[i][e];
+      for (int e = 0; e < VEC; ++e) v[i][e] = v[i][e] * rs * (w ? wv[i][e] : 1.0f) + bv[i][e];
       if (c < C) store_vec<T, VEC>(y + r * C + c, v[i]);
     }
     if (lead) {
@@ -141,12 +157,11 @@ __global__ __launch_bounds__(kNormThreads) void k_layer_norm_grad(
   const int l = threadIdx.x % G;
   float wv[V][VEC], sw[V][VEC] = {}, sb[V][VEC] = {};
 #pragma unroll
-  for (int i = 0; i < V; ++i)
+  for (int i = 0; i < V; ++i) {
+    load_weights<VEC>(w, C, (i * G + l) * VEC, wv[i]);
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      const int c = (i * G + l) * VEC + e;
-      wv[i][e] = w && c < C ? w[c] : 1.0f;
-    }
+    for (int e = 0; e < VEC; ++e) wv[i][e] = w ? wv[i][e] : 1.0f;
+  }
   int turn = 0;
   for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * RPB; r0 < n;
        r0 += static_cast<int64_t>(gridDim.x) * RPB, turn ^= 1) {

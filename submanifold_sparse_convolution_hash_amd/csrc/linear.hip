@@ -108,17 +108,22 @@ int linear_product(const Mat16& a, const Operand& B, int64_t N, bool bf16, const
 
 // ---- padded copies ----
 
-// thread: one 16-byte piece of the copy
-__global__ void k_pack16(const uint16_t* __restrict__ a, int64_t rows, int64_t cols, int64_t ld,
-                         int groups, int64_t gp, uint16_t* __restrict__ out) {
-  const int64_t gc = cols / groups;
-  const int64_t pr = groups * gp / 8;  // pieces per row
-  const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < rows * pr; i += step) {
-    const int64_t r = i / pr, c = (i - r * pr) * 8;
-    const int64_t q = c / gp, cc = c - q * gp;
-    const uint16_t* row = a + r * ld + q * gc;
-    reinterpret_cast<u32x4*>(out)[i] = load_piece(row, cc, gc, false);
+// Up to kPacks copies in one launch, one grid row each: thread i of a copy
+// writes its 16-byte piece i. I: 32-bit indices where a copy has fewer pieces
+// (a division of 64 bits costs more than the rest of the loop).
+struct Packs {
+  PackJob job[kPacks];
+};
+template <typename I>
+__global__ __launch_bounds__(256) void k_pack16(Packs p) {
+  const PackJob& a = p.job[blockIdx.y];
+  const I row_pieces = static_cast<I>(a.row_pieces), to_cols = static_cast<I>(a.to_cols);
+  const I pieces = static_cast<I>(a.rows) * row_pieces, step = gridDim.x * blockDim.x;
+  for (I i = blockIdx.x * blockDim.x + threadIdx.x; i < pieces; i += step) {
+    const I r = i / row_pieces, c = (i - r * row_pieces) * 8;
+    const I grp = c / to_cols, cc = c - grp * to_cols;
+    reinterpret_cast<u32x4*>(a.to)[i] =
+        load_piece(a.from + static_cast<int64_t>(r) * a.ld + grp * a.from_cols, cc, a.from_cols, false);
   }
 }
 
@@ -311,14 +316,18 @@ int64_t grad_run(int64_t rows, int64_t cin, int64_t cols) {
 
 bool pieces_fit(const Mat16& a) { return aligned16(a.p) && a.ld % 8 == 0 && a.cols % 8 == 0; }
 
-int pack16(const Mat16& a, int groups, int unit, void* to, Mat16* out, hipStream_t stream) {
-  const int64_t gp = round_to(a.cols / groups, unit);
-  *out = Mat16{static_cast<const uint16_t*>(to), a.rows, groups * gp, groups * gp};
-  const int64_t pieces = a.rows * groups * gp / 8;
-  if (pieces == 0) return SUBMCONV_OK;
-  const unsigned blocks = static_cast<unsigned>(std::min<int64_t>(div_up(pieces, 256), 8192));
-  k_pack16<<<blocks, 256, 0, stream>>>(a.p, a.rows, a.cols, a.ld, groups, gp,
-                                       static_cast<uint16_t*>(to));
+int run_packs(const PackList& list, hipStream_t stream) {
+  int64_t most = 0;
+  Packs p{};
+  for (int q = 0; q < list.count; ++q) {
+    p.job[q] = list.job[q];
+    most = std::max(most, list.job[q].rows * list.job[q].row_pieces);
+  }
+  if (most == 0) return SUBMCONV_OK;
+  const dim3 grid(static_cast<unsigned>(std::min<int64_t>(div_up(most, 256), 8192)),
+                  static_cast<unsigned>(list.count));
+  if (most < INT32_MAX / 2) k_pack16<uint32_t><<<grid, 256, 0, stream>>>(p);
+  else k_pack16<int64_t><<<grid, 256, 0, stream>>>(p);
   SUBMCONV_HIP_CHECK(hipGetLastError());
   return SUBMCONV_OK;
 }
@@ -393,14 +402,12 @@ int product_tn(const Mat16& x, const Mat16& dz, bool bf16, float* partial, uint1
   return SUBMCONV_OK;
 }
 
-int readable(const Mat16& a, int groups, int unit, Arena& ws, Mat16* out, hipStream_t stream) {
-  if (pieces_fit(a) && a.cols % (unit * groups) == 0) {
-    *out = a;
-    return SUBMCONV_OK;
-  }
-  void* to = ws.take(a.rows * groups * round_to(a.cols / groups, unit) * 2);
-  if (ws.counting) return SUBMCONV_OK;
-  return pack16(a, groups, unit, to, out, stream);
+Mat16 readable(const Mat16& a, int groups, int unit, Arena& ws, PackList* list) {
+  if (pieces_fit(a) && a.cols % (unit * groups) == 0) return a;
+  const int64_t from = a.cols / groups, to = round_to(from, unit);
+  uint16_t* p = static_cast<uint16_t*>(ws.take(a.rows * groups * to * 2));
+  list->job[list->count++] = PackJob{a.p, a.rows, a.ld, from, to, groups * to / 8, p};
+  return Mat16{p, a.rows, groups * to, groups * to};
 }
 
 int check_shape(const char* name, int64_t rows, int64_t cols) {
@@ -447,18 +454,6 @@ Mat16 shape_of(int64_t rows, int64_t cols, bool aligned) {
 
 namespace {
 
-struct LinearWork {
-  Mat16 x, W;
-};
-int linear_work(const Mat16& x, const Mat16& W, Arena& ws, LinearWork* w, hipStream_t stream) {
-  if (x.rows <= kFewRows) {  // read in place
-    *w = LinearWork{x, W};
-    return SUBMCONV_OK;
-  }
-  SUBMCONV_TRY(readable(x, 1, 8, ws, &w->x, stream));
-  return readable(W, 1, 8, ws, &w->W, stream);
-}
-
 struct LinearGradNeeds {
   bool x, w, b;
 };
@@ -469,30 +464,25 @@ int linear_grad(const Mat16& dy, const Mat16& x, const Mat16& W, const uint16_t*
   const bool run = !ws.counting;
   const int64_t cp = round8(dy.cols);
   const bool own_dz = (act != kActNone || !pieces_fit(dy)) && (need.x || need.w);
-  Mat16 dz = dy;
+  PackList packs;
+  Mat16 dz = dy, Wr, xr;
   uint16_t* dz_to = nullptr;
   if (own_dz) {
     const int64_t cq = round64(dy.cols);
     dz_to = static_cast<uint16_t*>(ws.take(blocked_bytes(dy.rows, cq)));
     dz = blocked16(dz_to, dy.rows, cq);
   }
+  if (need.x) Wr = readable(W, 1, own_dz ? 64 : 8, ws, &packs);
+  if (need.w) xr = readable(x, 1, 8, ws, &packs);
   const int64_t parts = column_parts(dy.rows, dy.cols);
   float* sums = need.b ? static_cast<float*>(ws.take(parts * cp * 4)) : nullptr;
-  if (run && (own_dz || need.b)) {
-    SUBMCONV_TRY(act_grad(dy, pre, act, bf16, dz_to, sums, stream));
-    if (need.b) SUBMCONV_TRY(sum_parts(sums, parts, cp, dy.cols, 1, gb, stream));
-  }
-  if (need.x) {
-    Mat16 Wr;
-    SUBMCONV_TRY(readable(W, 1, own_dz ? 64 : 8, ws, &Wr, stream));
-    if (run) SUBMCONV_TRY(product_nt(dz, Wr, bf16, gx, x.cols, x.cols, stream));
-  }
-  if (need.w) {
-    Mat16 xr;
-    SUBMCONV_TRY(readable(x, 1, 8, ws, &xr, stream));
-    float* part = static_cast<float*>(ws.take(product_tn_bytes(x.rows, round8(x.cols), dz.cols)));
-    if (run) SUBMCONV_TRY(product_tn(xr, dz, bf16, part, gw, x.cols, dy.cols, 1, stream));
-  }
+  float* part = need.w ? static_cast<float*>(ws.take(product_tn_bytes(x.rows, round8(x.cols), dz.cols))) : nullptr;
+  if (!run) return SUBMCONV_OK;
+  SUBMCONV_TRY(run_packs(packs, stream));
+  if (own_dz || need.b) SUBMCONV_TRY(act_grad(dy, pre, act, bf16, dz_to, sums, stream));
+  if (need.b) SUBMCONV_TRY(sum_parts(sums, parts, cp, dy.cols, 1, gb, stream));
+  if (need.x) SUBMCONV_TRY(product_nt(dz, Wr, bf16, gx, x.cols, x.cols, stream));
+  if (need.w) SUBMCONV_TRY(product_tn(xr, dz, bf16, part, gw, x.cols, dy.cols, 1, stream));
   return SUBMCONV_OK;
 }
 
@@ -507,8 +497,11 @@ extern "C" int64_t submconv_linear_workspace_bytes(int64_t n, int32_t cin, int32
   SUBMCONV_TRY(check_shape("x", n, cin));
   SUBMCONV_TRY(check_shape("W", cin, cout));
   Arena ws;
-  LinearWork w;
-  SUBMCONV_TRY(linear_work(shape_of(n, cin, aligned), shape_of(cin, cout, aligned), ws, &w, nullptr));
+  PackList packs;
+  if (n > kFewRows) {
+    readable(shape_of(n, cin, aligned), 1, 8, ws, &packs);
+    readable(shape_of(cin, cout, aligned), 1, 8, ws, &packs);
+  }
   return ws.used;
 }
 
@@ -525,17 +518,15 @@ extern "C" int submconv_linear(const uint16_t* x, int64_t ldx, int64_t n, const 
   if (residual) SUBMCONV_TRY(check_matrix("residual", residual, n, cout, ldr));
   if (pre) SUBMCONV_TRY(check_matrix("pre", pre, n, cout, cout));
   if (n == 0) return SUBMCONV_OK;
-  const Mat16 xm{x, n, cin, n == 1 ? round8(cin) : ldx}, wm{W, cin, cout, cout};
-  Arena need;
-  LinearWork w;
-  SUBMCONV_TRY(linear_work(xm, wm, need, &w, stream));
-  SUBMCONV_TRY(check_workspace(workspace, workspace_bytes, need.used));
+  const Mat16 xm{x, n, cin, ldx}, wm{W, cin, cout, cout};
+  const bool bf16 = dtype == SUBMCONV_DTYPE_BF16;
+  if (n <= kFewRows) return few_linear(xm, wm, bias, act, bf16, residual, ldr, out, pre, stream);
   Arena ws{false, static_cast<char*>(workspace)};
-  if (need.used > 0) SUBMCONV_TRY(linear_work(xm, wm, ws, &w, stream));
-  if (n <= kFewRows)
-    return few_linear(w.x, w.W, bias, act, dtype == SUBMCONV_DTYPE_BF16, residual, ldr, out, pre, stream);
-  return linear_forward(w.x, w.W, bias, act, dtype == SUBMCONV_DTYPE_BF16, residual, ldr, out, cout, pre,
-                        cout, stream);
+  PackList packs;
+  const Mat16 xr = readable(xm, 1, 8, ws, &packs), wr = readable(wm, 1, 8, ws, &packs);
+  SUBMCONV_TRY(check_workspace(workspace, workspace_bytes, ws.used));
+  SUBMCONV_TRY(run_packs(packs, stream));
+  return linear_forward(xr, wr, bias, act, bf16, residual, ldr, out, cout, pre, cout, stream);
 }
 
 extern "C" int64_t submconv_linear_backward_workspace_bytes(int64_t n, int32_t cin, int32_t cout,

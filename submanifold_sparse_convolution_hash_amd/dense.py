@@ -11,7 +11,6 @@ and the modules are the autograd form.
 """
 from __future__ import annotations
 
-import contextlib
 import functools
 from typing import Optional, Tuple
 
@@ -28,20 +27,25 @@ __all__ = [
 #: names of the activations, as SUBMCONV_ACT_*
 ACTIVATIONS = {"none": 0, None: 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 _NORM_DTYPES = {**_DTYPES, torch.float32: 2}
-_HERE = contextlib.nullcontext()
 
 
 def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
 
-def _stream(device: torch.device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
+_current_stream = torch._C._cuda_getCurrentRawStream  # torch.cuda.current_stream(i).cuda_stream
 
 
-def _on(device: torch.device):
-    """The device guard, only where another device is current."""
-    return _HERE if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+def _call(device: torch.device, name: str, *args) -> None:
+    """Calls an entry point on the device's current stream, its last argument."""
+    fn = getattr(load_library(), name)
+    if device.index == torch.cuda.current_device():
+        status = fn(*args, _current_stream(device.index))
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, _current_stream(device.index))
+    if status:
+        _check(status)
 
 
 def _act(act) -> int:
@@ -119,10 +123,10 @@ def _workspace_bytes(query: str, *sizes: int) -> int:
     return v
 
 
-def _workspace(query: str, device, *sizes: int):
+def _workspace(query: str, x: torch.Tensor, *sizes: int):
     """(tensor or None, bytes) of an operator's workspace."""
     need = _workspace_bytes(query, *sizes)
-    return (torch.empty(need, dtype=torch.uint8, device=device) if need else None), need
+    return (x.new_empty((need,), dtype=torch.uint8) if need else None), need
 
 
 # ---------------------------------------------------------------------------
@@ -141,14 +145,12 @@ def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
     dev = x.device
     _optional(weight, "weight", torch.float32, (c,), dev)
     _optional(bias, "bias", torch.float32, (c,), dev)
-    y = torch.empty((n, c), dtype=x.dtype, device=dev)
+    y = x.new_empty((n, c))
     mean = rstd = None
     if return_stats:
-        mean = torch.empty((n,), dtype=torch.float32, device=dev)
-        rstd = torch.empty((n,), dtype=torch.float32, device=dev)
-    with _on(dev):
-        _check(load_library().submconv_layer_norm(_ptr(x), ld, n, c, _ptr(weight), _ptr(bias), eps, _ptr(y),
-                                                  _ptr(mean), _ptr(rstd), _NORM_DTYPES[x.dtype], _stream(dev)))
+        mean = x.new_empty((n,), dtype=torch.float32)
+        rstd = x.new_empty((n,), dtype=torch.float32)
+    _call(dev, "submconv_layer_norm", _ptr(x), ld, n, c, _ptr(weight), _ptr(bias), eps, _ptr(y), _ptr(mean), _ptr(rstd), _NORM_DTYPES[x.dtype])
     return (y, mean, rstd) if return_stats else y
 
 
@@ -163,16 +165,13 @@ def layer_norm_backward(grad_out: torch.Tensor, x: torch.Tensor, mean: torch.Ten
     _dense(mean, "mean", torch.float32, (n,), dev)
     _dense(rstd, "rstd", torch.float32, (n,), dev)
     _optional(weight, "weight", torch.float32, (c,), dev)
-    gx = torch.empty((n, c), dtype=x.dtype, device=dev) if needs[0] else None
-    gw = torch.empty((c,), dtype=torch.float32, device=dev) if needs[1] else None
-    gb = torch.empty((c,), dtype=torch.float32, device=dev) if needs[2] else None
+    gx = x.new_empty((n, c)) if needs[0] else None
+    gw = x.new_empty((c,), dtype=torch.float32) if needs[1] else None
+    gb = x.new_empty((c,), dtype=torch.float32) if needs[2] else None
     ws, nb = None, 0
     if needs[1] or needs[2]:
-        ws, nb = _workspace("submconv_layer_norm_backward_workspace_bytes", dev, n, c)
-    with _on(dev):
-        _check(load_library().submconv_layer_norm_backward(
-            _ptr(grad_out), ldg, _ptr(x), ldx, n, c, _ptr(mean), _ptr(rstd), _ptr(weight), _ptr(gx), _ptr(gw),
-            _ptr(gb), _NORM_DTYPES[x.dtype], _ptr(ws), nb, _stream(dev)))
+        ws, nb = _workspace("submconv_layer_norm_backward_workspace_bytes", x, n, c)
+    _call(dev, "submconv_layer_norm_backward", _ptr(grad_out), ldg, _ptr(x), ldx, n, c, _ptr(mean), _ptr(rstd), _ptr(weight), _ptr(gx), _ptr(gw), _ptr(gb), _NORM_DTYPES[x.dtype], _ptr(ws), nb)
     return gx, gw, gb
 
 
@@ -196,13 +195,10 @@ def linear(x: torch.Tensor, W: torch.Tensor, bias: Optional[torch.Tensor] = None
     _optional(bias, "bias", torch.float32, (cout,), dev)
     a = _act(act)
     ldr = _rows(residual, "residual", (x.dtype,), cout, x) if residual is not None else 0
-    out = torch.empty((n, cout), dtype=x.dtype, device=dev)
-    pre = torch.empty((n, cout), dtype=x.dtype, device=dev) if return_pre else None
-    ws, nb = _workspace("submconv_linear_workspace_bytes", dev, n, cin, cout, _aligned((x, ldx), (W, cout)))
-    with _on(dev):
-        _check(load_library().submconv_linear(_ptr(x), ldx, n, _ptr(W), _ptr(bias), _ptr(residual), ldr, _ptr(out),
-                                              _ptr(pre), cin, cout, a, _DTYPES[x.dtype], _ptr(ws), nb,
-                                              _stream(dev)))
+    out = x.new_empty((n, cout))
+    pre = x.new_empty((n, cout)) if return_pre else None
+    ws, nb = _workspace("submconv_linear_workspace_bytes", x, n, cin, cout, _aligned((x, ldx), (W, cout)))
+    _call(dev, "submconv_linear", _ptr(x), ldx, n, _ptr(W), _ptr(bias), _ptr(residual), ldr, _ptr(out), _ptr(pre), cin, cout, a, _DTYPES[x.dtype], _ptr(ws), nb)
     return (out, pre) if return_pre else out
 
 
@@ -222,15 +218,12 @@ def linear_backward(grad_out: torch.Tensor, x: torch.Tensor, W: torch.Tensor, pr
     a = _act(act)
     if a:
         _dense(pre, "pre", x.dtype, (n, cout), dev)
-    gx = torch.empty((n, cin), dtype=x.dtype, device=dev) if needs[0] else None
-    gw = torch.empty((cin, cout), dtype=x.dtype, device=dev) if needs[1] else None
-    gb = torch.empty((cout,), dtype=torch.float32, device=dev) if needs[2] else None
-    ws, nb = _workspace("submconv_linear_backward_workspace_bytes", dev, n, cin, cout, a,
+    gx = x.new_empty((n, cin)) if needs[0] else None
+    gw = x.new_empty((cin, cout)) if needs[1] else None
+    gb = x.new_empty((cout,), dtype=torch.float32) if needs[2] else None
+    ws, nb = _workspace("submconv_linear_backward_workspace_bytes", x, n, cin, cout, a,
                         _aligned((x, ldx), (W, cout), (grad_out, ldg)))
-    with _on(dev):
-        _check(load_library().submconv_linear_backward(
-            _ptr(grad_out), ldg, n, _ptr(x), ldx, _ptr(W), _ptr(pre) if a else None, _ptr(gx), _ptr(gw), _ptr(gb),
-            cin, cout, a, _DTYPES[x.dtype], _ptr(ws), nb, _stream(dev)))
+    _call(dev, "submconv_linear_backward", _ptr(grad_out), ldg, n, _ptr(x), ldx, _ptr(W), _ptr(pre) if a else None, _ptr(gx), _ptr(gw), _ptr(gb), cin, cout, a, _DTYPES[x.dtype], _ptr(ws), nb)
     return gx, gw, gb
 
 
@@ -264,14 +257,11 @@ def gated_ffn(x: torch.Tensor, W_in: torch.Tensor, b_in: Optional[torch.Tensor],
     _optional(b_out, "b_out", torch.float32, (cout,), dev)
     a = _act(act)
     ldr = _rows(residual, "residual", (x.dtype,), cout, x) if residual is not None else 0
-    out = torch.empty((n, cout), dtype=x.dtype, device=dev)
-    pre = torch.empty((n, 2 * hidden), dtype=x.dtype, device=dev) if return_pre else None
-    ws, nb = _workspace("submconv_gated_ffn_workspace_bytes", dev, n, cin, hidden, cout,
+    out = x.new_empty((n, cout))
+    pre = x.new_empty((n, 2 * hidden)) if return_pre else None
+    ws, nb = _workspace("submconv_gated_ffn_workspace_bytes", x, n, cin, hidden, cout,
                         _aligned((x, ldx), (W_in, 2 * hidden), (W_out, cout)))
-    with _on(dev):
-        _check(load_library().submconv_gated_ffn(
-            _ptr(x), ldx, n, _ptr(W_in), _ptr(b_in), _ptr(W_out), _ptr(b_out), _ptr(residual), ldr, _ptr(out),
-            _ptr(pre), cin, hidden, cout, a, _DTYPES[x.dtype], _ptr(ws), nb, _stream(dev)))
+    _call(dev, "submconv_gated_ffn", _ptr(x), ldx, n, _ptr(W_in), _ptr(b_in), _ptr(W_out), _ptr(b_out), _ptr(residual), ldr, _ptr(out), _ptr(pre), cin, hidden, cout, a, _DTYPES[x.dtype], _ptr(ws), nb)
     return (out, pre) if return_pre else out
 
 
@@ -290,13 +280,10 @@ def gated_ffn_backward(grad_out: torch.Tensor, x: torch.Tensor, W_in: torch.Tens
     a = _act(act)
     shapes = [((n, cin), x.dtype), ((cin, 2 * hidden), x.dtype), ((2 * hidden,), torch.float32),
               ((hidden, cout), x.dtype), ((cout,), torch.float32)]
-    g = [torch.empty(s, dtype=d, device=dev) if need else None for (s, d), need in zip(shapes, needs)]
-    ws, nb = _workspace("submconv_gated_ffn_backward_workspace_bytes", dev, n, cin, hidden, cout,
+    g = [x.new_empty(s, dtype=d) if need else None for (s, d), need in zip(shapes, needs)]
+    ws, nb = _workspace("submconv_gated_ffn_backward_workspace_bytes", x, n, cin, hidden, cout,
                         _aligned((x, ldx), (W_in, 2 * hidden), (W_out, cout), (grad_out, ldg)))
-    with _on(dev):
-        _check(load_library().submconv_gated_ffn_backward(
-            _ptr(grad_out), ldg, n, _ptr(x), ldx, _ptr(W_in), _ptr(W_out), _ptr(pre), _ptr(g[0]), _ptr(g[1]),
-            _ptr(g[2]), _ptr(g[3]), _ptr(g[4]), cin, hidden, cout, a, _DTYPES[x.dtype], _ptr(ws), nb, _stream(dev)))
+    _call(dev, "submconv_gated_ffn_backward", _ptr(grad_out), ldg, n, _ptr(x), ldx, _ptr(W_in), _ptr(W_out), _ptr(pre), _ptr(g[0]), _ptr(g[1]), _ptr(g[2]), _ptr(g[3]), _ptr(g[4]), cin, hidden, cout, a, _DTYPES[x.dtype], _ptr(ws), nb)
     return tuple(g)
 
 
