@@ -13,7 +13,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libsubmconv.so")
 SOURCES = ["map_build.hip", "forward.hip", "backward.hip", "coord_ops.hip", "masked.hip",
-           "staged.hip", "staged_wide.hip", "staged_bwd.hip", "linear.hip", "gated_ffn.hip",
+           "staged.hip", "staged_wide.hip", "staged_bwd.hip", "linear.hip", "gated_ffn.hip", "gated_fused.hip",
            "few_rows.hip", "layer_norm.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

@@ -79,6 +79,13 @@ int few_gate(const Mat16& x, const Mat16& W, const float* bias, int act, bool bf
 int few_out(const float* h, int64_t rows, const Mat16& W, const float* bias, bool bf16,
             const uint16_t* residual, int64_t ldr, uint16_t* out, hipStream_t stream);
 
+// The gated block in one kernel, which keeps the hidden rows to itself
+// (gated_fused.hip); operands readable in pieces, W_in in two groups.
+bool fused_ffn_takes(int64_t rows, int64_t cin, int64_t cout);
+int fused_ffn(const Mat16& x, const Mat16& W_in, int64_t F, const float* b_in, const Mat16& W_out,
+              const float* b_out, int act, bool bf16, const uint16_t* residual, int64_t ldr,
+              uint16_t* out, int64_t cout, hipStream_t stream);
+
 // Cuts a caller's workspace into 256-byte aligned pieces, or, counting, only
 // adds up what they take: the steps of an operator go through one function,
 // which enqueues nothing while it counts.

@@ -391,6 +391,39 @@ struct LoadKRow {
   }
 };
 
+// Waits until at most N of this wave's loads to LDS are in flight, and for its
+// LDS reads.
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  static_assert(N < 64, "vmcnt");
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
+}
+
+// ---- accumulators as rows ----
+
+// ROWS rows of BN fp32 columns in LDS, 8 columns of a row per thread and turn.
+// The 16-byte piece p of row r sits at p ^ (r % 16) ^ (p / 16 % 2), which keeps
+// the 16 rows of an accumulator's write and the 16 pieces of a read apart.
+template <int ROWS, int BN, int NT>
+struct LdsRows {
+  static constexpr int PH_ROWS = ROWS;
+  static constexpr int PIECES = BN / 8;          // 8-column pieces per row
+  static constexpr int ROW_STEP = NT / PIECES;   // rows between a thread's pieces
+  static constexpr int ROW_PASSES = ROWS / ROW_STEP;
+  static __device__ __forceinline__ int row_byte(int r, int p) {
+    return r * (BN * 4) + ((p ^ (r & 15) ^ (p >> 4 & 1)) << 4);
+  }
+  static __device__ __forceinline__ void read8(const char* smem, int r, int piece, float (&v)[8]) {
+    const float4v a = *reinterpret_cast<const float4v*>(smem + row_byte(r, 2 * piece));
+    const float4v b = *reinterpret_cast<const float4v*>(smem + row_byte(r, 2 * piece + 1));
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      v[e] = a[e];
+      v[4 + e] = b[e];
+    }
+  }
+};
+
 // ---- the tile ----
 
 // A_ROW, B_ROW: k is the memory row of that operand; A_TILED, B_TILED: it is
@@ -502,18 +535,10 @@ struct Tile {
   // ---- the accumulators as rows ----
   //
   // to_rows leaves the rows of phase `ph` (as many as fit the operand buffers)
-  // in LDS in fp32, read8 takes 8 columns of one. The 16-byte piece p of row r
-  // sits at p ^ (r % 16) ^ (p / 16 % 2), which keeps the 16 rows of a write and
-  // the 16 pieces of a read apart.
+  // in LDS.
   static constexpr int PHASES = BM * BN * 4 <= LDS_BYTES ? 1 : WM;
-  static constexpr int PH_ROWS = BM / PHASES;     // rows of a phase
-  static constexpr int PIECES = BN / 8;           // 8-column pieces per row
-  static constexpr int ROW_STEP = NT / PIECES;    // rows between a thread's pieces
-  static constexpr int ROW_PASSES = PH_ROWS / ROW_STEP;
-  static_assert(PH_ROWS * BN * 4 <= LDS_BYTES, "a phase's rows fit the operand buffers");
-  static __device__ __forceinline__ int row_byte(int r, int p) {
-    return r * (BN * 4) + ((p ^ (r & 15) ^ (p >> 4 & 1)) << 4);
-  }
+  using Rows = LdsRows<BM / PHASES, BN, NT>;
+  static_assert(Rows::PH_ROWS * BN * 4 <= LDS_BYTES, "a phase's rows fit the operand buffers");
   static __device__ __forceinline__ void to_rows(char* smem, int ph, const float4v (&acc)[FN][FM]) {
     const int lane = threadIdx.x & 63, g = lane >> 4, s = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -525,24 +550,9 @@ struct Tile {
       for (int i = 0; i < FM; ++i)
 #pragma unroll
         for (int j = 0; j < FN; ++j)
-          *reinterpret_cast<float4v*>(smem + row_byte(r0 + i * 16 + s, ncol(wn, j) / 4 + g)) = acc[j][i];
+          *reinterpret_cast<float4v*>(smem + Rows::row_byte(r0 + i * 16 + s, ncol(wn, j) / 4 + g)) = acc[j][i];
     }
     __syncthreads();
-  }
-  static __device__ __forceinline__ void read8(const char* smem, int r, int piece, float (&v)[8]) {
-    const float4v a = *reinterpret_cast<const float4v*>(smem + row_byte(r, 2 * piece));
-    const float4v b = *reinterpret_cast<const float4v*>(smem + row_byte(r, 2 * piece + 1));
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      v[e] = a[e];
-      v[4 + e] = b[e];
-    }
-  }
-
-  template <int N>
-  static __device__ __forceinline__ void wait_loads() {
-    static_assert(N < 64, "vmcnt");
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
   }
 };
 

@@ -33,12 +33,12 @@ struct GateEpi {
   bool vec_p;
 };
 
-template <bool BF16, int ACT, typename T>
+template <bool BF16, int ACT, typename R, int NT>
 __device__ __forceinline__ void gate_epilogue(const GateEpi& e, int64_t M, int64_t m0, uint32_t n0,
                                               const char* smem) {
-  constexpr int BM = T::PH_ROWS;
+  constexpr int BM = R::PH_ROWS;
   // a row in LDS: the gate's columns, then the up projection's
-  constexpr int HP = T::PIECES / 2, STEP = T::NT / HP;
+  constexpr int HP = R::PIECES / 2, STEP = NT / HP;
   const int piece = threadIdx.x % HP, r0 = threadIdx.x / HP;
   const uint32_t n = n0 + piece * 8;
   const BlockView h(e.h, m0, M, e.Fq);
@@ -51,8 +51,8 @@ __device__ __forceinline__ void gate_epilogue(const GateEpi& e, int64_t M, int64
   for (int p = 0; p < BM / STEP; ++p) {
     const int m = r0 + p * STEP;
     float g[8], u[8];
-    T::read8(smem, m, piece, g);
-    T::read8(smem, m, HP + piece, u);
+    R::read8(smem, m, piece, g);
+    R::read8(smem, m, HP + piece, u);
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
       g[q] += bg[q];
@@ -81,7 +81,7 @@ __global__ __launch_bounds__(WM* WN * 64, tile_waves(BM, BN)) void k_gate(Operan
   for (int ph = 0; ph < T::PHASES; ++ph) {
     T::to_rows(smem, ph, acc);
     with_act(e.act, [&](auto a) {
-      gate_epilogue<BF16, decltype(a)::value, T>(e, A.rows, m0 + ph * T::PH_ROWS,
+      gate_epilogue<BF16, decltype(a)::value, typename T::Rows, T::NT>(e, A.rows, m0 + ph * T::Rows::PH_ROWS,
                                                  static_cast<uint32_t>(n0), smem);
     });
   }
@@ -99,12 +99,12 @@ struct GateGradEpi {
   bool vec_p;
 };
 
-template <bool BF16, int ACT, typename T>
+template <bool BF16, int ACT, typename R>
 __device__ __forceinline__ void gate_grad_epilogue(const GateGradEpi& e, int64_t M, int64_t m0,
                                                    uint32_t n0, const char* smem, float (&sg)[8],
                                                    float (&su)[8]) {
-  constexpr int BM = T::PH_ROWS;
-  const int piece = threadIdx.x % T::PIECES, r0 = threadIdx.x / T::PIECES;
+  constexpr int BM = R::PH_ROWS;
+  const int piece = threadIdx.x % R::PIECES, r0 = threadIdx.x / R::PIECES;
   const uint32_t n = n0 + piece * 8;
   const RowsView pg(e.pre, 2 * e.F, m0, M, e.F, BM, e.vec_p);
   const RowsView pu(e.pre + e.F, 2 * e.F, m0, M, e.F, BM, e.vec_p);
@@ -112,12 +112,12 @@ __device__ __forceinline__ void gate_grad_epilogue(const GateGradEpi& e, int64_t
   const uint32_t Fq = static_cast<uint32_t>(e.Fq);
   const BlockView h(e.h, m0, M, e.Fq);
 #pragma unroll 2
-  for (int p = 0; p < T::ROW_PASSES; ++p) {
-    const int m = r0 + p * T::ROW_STEP;
+  for (int p = 0; p < R::ROW_PASSES; ++p) {
+    const int m = r0 + p * R::ROW_STEP;
     float g[8], u[8], dh[8];
     unpack8<BF16>(pg.load(m, n), g);
     unpack8<BF16>(pu.load(m, n), u);
-    T::read8(smem, m, piece, dh);
+    R::read8(smem, m, piece, dh);
     float dg[8], du[8], v[8];
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
@@ -152,14 +152,14 @@ __global__ __launch_bounds__(WM* WN * 64, tile_waves(BM, BN)) void k_gate_grad(O
   for (int ph = 0; ph < T::PHASES; ++ph) {
     T::to_rows(smem, ph, acc);
     with_act(e.act, [&](auto a) {
-      gate_grad_epilogue<BF16, decltype(a)::value, T>(e, A.rows, m0 + ph * T::PH_ROWS,
+      gate_grad_epilogue<BF16, decltype(a)::value, typename T::Rows>(e, A.rows, m0 + ph * T::Rows::PH_ROWS,
                                                       static_cast<uint32_t>(n0), smem, sums[0], sums[1]);
     });
   }
   if (!e.sums) return;
   // the threads that walked the same columns, in order
   float* red = reinterpret_cast<float*>(smem);  // [ROW_STEP][2][BN]
-  const int piece = threadIdx.x % T::PIECES, r0 = threadIdx.x / T::PIECES;
+  const int piece = threadIdx.x % T::Rows::PIECES, r0 = threadIdx.x / T::Rows::PIECES;
   __syncthreads();
 #pragma unroll
   for (int t2 = 0; t2 < 2; ++t2)
@@ -169,7 +169,7 @@ __global__ __launch_bounds__(WM* WN * 64, tile_waves(BM, BN)) void k_gate_grad(O
   for (int c = threadIdx.x; c < 2 * BN; c += T::NT) {
     float x = 0.0f;
 #pragma unroll
-    for (int r = 0; r < T::ROW_STEP; ++r) x += red[r * 2 * BN + c];
+    for (int r = 0; r < T::Rows::ROW_STEP; ++r) x += red[r * 2 * BN + c];
     const int64_t n = n0 + c % BN;
     if (n < e.Fq) e.sums[(t.m * 2 + c / BN) * e.Fq + n] = x;
   }
@@ -233,6 +233,11 @@ int ffn_forward(const Ffn& f, const float* b_in, const float* b_out, const uint1
   PackList packs;
   const Mat16 x = readable(f.x, 1, 8, ws, &packs), wi = readable(f.W_in, 2, 8, ws, &packs);
   const Mat16 wo = readable(f.W_out, 1, 8, ws, &packs);
+  // (a query does not know whether pre is asked for: it counts h)
+  if (!ws.counting && !pre && fused_ffn_takes(f.n, f.C, f.Co)) {
+    SUBMCONV_TRY(run_packs(packs, stream));
+    return fused_ffn(x, wi, f.F, b_in, wo, b_out, f.act, f.bf16, residual, ldr, out, f.Co, stream);
+  }
   uint16_t* h = static_cast<uint16_t*>(ws.take(blocked_bytes(f.n, Fq)));
   if (ws.counting || f.n == 0) return SUBMCONV_OK;
   SUBMCONV_TRY(run_packs(packs, stream));

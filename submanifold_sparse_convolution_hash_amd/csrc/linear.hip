@@ -12,53 +12,12 @@
 
 #include "dense_common.h"
 #include "dense_tile.h"
+#include "linear_epilogue.h"
 
 namespace submconv {
 namespace {
 
 // ---- forward ----
-
-struct LinearEpi {
-  const float* bias;         // [N] or null
-  const uint16_t* residual;  // or null
-  int64_t ldr;
-  uint16_t* out;
-  int64_t ldo;
-  uint16_t* pre;  // [M][N] dense, or null
-  int act;
-  bool vec_r, vec_o, vec_p;
-};
-
-template <bool BF16, int ACT, typename T>
-__device__ __forceinline__ void linear_epilogue(const LinearEpi& e, int64_t M, int64_t N,
-                                                int64_t m0, uint32_t n0, const char* smem) {
-  constexpr int BM = T::PH_ROWS;
-  const int piece = threadIdx.x % T::PIECES, r0 = threadIdx.x / T::PIECES;
-  const uint32_t n = n0 + piece * 8;
-  const RowsView out(e.out, e.ldo, m0, M, N, BM, e.vec_o);
-  const RowsView pre(e.pre, N, m0, M, N, BM, e.vec_p);
-  const RowsView res(e.residual, e.ldr, m0, M, N, BM, e.vec_r);
-  float b[8];
-  load_bias8(e.bias, N, n, b);
-#pragma unroll 2
-  for (int p = 0; p < T::ROW_PASSES; ++p) {
-    const int m = r0 + p * T::ROW_STEP;
-    float z[8];
-    T::read8(smem, m, piece, z);
-#pragma unroll
-    for (int q = 0; q < 8; ++q) z[q] += b[q];
-    if (e.pre) pre.store(m, n, pack8<BF16>(z));
-#pragma unroll
-    for (int q = 0; q < 8; ++q) z[q] = act_value<ACT>(z[q]);
-    if (e.residual) {
-      float v[8];
-      unpack8<BF16>(res.load(m, n), v);
-#pragma unroll
-      for (int q = 0; q < 8; ++q) z[q] += v[q];
-    }
-    out.store(m, n, pack8<BF16>(z));
-  }
-}
 
 // B_ROW: W [K][N] as stored (forward); else W [N][K] (input gradient).
 template <bool BF16, bool B_ROW, bool A_TILED, int BM, int BN, int WM, int WN, int STAGES>
@@ -75,7 +34,7 @@ __global__ __launch_bounds__(WM* WN * 64, tile_waves(BM, BN)) void k_linear(Oper
   for (int ph = 0; ph < T::PHASES; ++ph) {
     T::to_rows(smem, ph, acc);
     with_act(e.act, [&](auto a) {
-      linear_epilogue<BF16, decltype(a)::value, T>(e, A.rows, N, m0 + ph * T::PH_ROWS,
+      linear_epilogue<BF16, decltype(a)::value, typename T::Rows>(e, A.rows, N, m0 + ph * T::Rows::PH_ROWS,
                                                    static_cast<uint32_t>(n0), smem);
     });
   }

@@ -281,7 +281,8 @@ def test_linear_writes_nothing_else(dev):
 # gated feed-forward
 # ---------------------------------------------------------------------------
 
-FFN_SHAPES = [(1, 64, 128, 64, 0), (8, 33, 1100, 17, 2), (5, 16, 3000, 24, 0), (1, 512, 2048, 512, 0), (0, 32, 64, 16, 0), (2, 16, 8, 8, 0), (3, 9, 5, 3, 1),
+FFN_SHAPES = [(257, 65, 65, 128, 0), (600, 128, 200, 9, 1), (300, 16, 130, 64, 0), (520, 120, 33, 127, 0),
+              (1, 64, 128, 64, 0), (8, 33, 1100, 17, 2), (5, 16, 3000, 24, 0), (1, 512, 2048, 512, 0), (0, 32, 64, 16, 0), (2, 16, 8, 8, 0), (3, 9, 5, 3, 1),
               (9, 40, 100, 24, 0), (64, 64, 64, 64, 0), (130, 128, 512, 128, 0), (129, 100, 267, 100, 0),
               (300, 72, 136, 200, 8), (1000, 64, 256, 64, 3), (257, 256, 72, 136, 0)]
 
@@ -299,8 +300,10 @@ def test_gated_ffn(dev, shape, dtype):
     res = mk.rows(n, cout, dtype, pad) if n % 2 else None
     u, tiny = U[dtype], TINY[dtype]
     out, pre = sc.gated_ffn(x, Wi, bi, Wo, bo, act=act, residual=res, return_pre=True)
-    same = sc.gated_ffn(x, Wi, bi, Wo, bo, act=act, residual=res)
-    assert torch.equal(out.view(torch.int16), same.view(torch.int16))
+    # without pre-activations to write, narrow layers take another kernel
+    alone = sc.gated_ffn(x, Wi, bi, Wo, bo, act=act, residual=res)
+    again = sc.gated_ffn(x, Wi, bi, Wo, bo, act=act, residual=res)
+    assert torch.equal(alone.view(torch.int16), again.view(torch.int16))
     xn, Win, Won = _np(x), _np(Wi), _np(Wo)
     bin_, bon = (None, None) if bi is None else (_np(bi), _np(bo))
     rn = None if res is None else _np(res)
@@ -315,6 +318,7 @@ def test_gated_ffn(dev, shape, dtype):
     tol = eh @ aWo + (F + 4) * V * (np.abs(h) @ aWo + (0 if bon is None else np.abs(bon))) \
         + (0 if rn is None else 2 * V * np.abs(rn)) + u * np.abs(ro) + tiny
     _check(out, ro, tol, "out")
+    _check(alone, ro, tol, "out without pre")
     # gradients, for the pre-activations that the forward wrote
     dy = mk.rows(n, cout, dtype, pad)
     grads = sc.gated_ffn_backward(dy, x, Wi, Wo, pre, act=act)
