@@ -81,7 +81,7 @@ int few_out(const float* h, int64_t rows, const Mat16& W, const float* bias, boo
 
 // The gated block in one kernel, which keeps the hidden rows to itself
 // (gated_fused.hip); operands readable in pieces, W_in in two groups.
-bool fused_ffn_takes(int64_t rows, int64_t cin, int64_t cout);
+bool fused_ffn_takes(int64_t rows, int64_t cin, int64_t hidden, int64_t cout);
 int fused_ffn(const Mat16& x, const Mat16& W_in, int64_t F, const float* b_in, const Mat16& W_out,
               const float* b_out, int act, bool bf16, const uint16_t* residual, int64_t ldr,
               uint16_t* out, int64_t cout, hipStream_t stream);

@@ -282,7 +282,7 @@ struct Operand {
 // The k-contiguous form. LDS: row r is 128 bytes, its piece c (8 k) in slot c
 // ^ ((r / 2) % 8), so that the 16 rows a read pass takes fall on distinct
 // banks.
-// TILED: a blocked matrix, R = kBlockRows of it.
+// TILED: a blocked matrix.
 template <int R, int NT, bool TILED>
 struct LoadKCol {
   static constexpr int SL = R * 8 / NT;
@@ -296,11 +296,16 @@ struct LoadKCol {
     const int r0 = tid >> 3;
     kc = ((tid & 7) ^ ((r0 >> 1) & 7)) * 8;
     if constexpr (TILED) {
-      static_assert(R == kBlockRows, "one block row");
+      // R / kBlockRows blocks of 16 KiB, a row of blocks apart
+      static_assert(R % kBlockRows == 0, "whole blocks");
       base = o.p + row0 * o.ld;
-      bytes = left > 0 ? static_cast<uint32_t>(left < R ? left : R) * 128u : 0u;
+      bytes = static_cast<uint32_t>((R / kBlockRows - 1) * kBlockRows * o.ld + kBlockRows * 64) * 2u;
 #pragma unroll
-      for (int i = 0; i < SL; ++i) voff[i] = static_cast<uint32_t>((r0 + i * (NT / 8)) * 64 + kc) * 2u;
+      for (int i = 0; i < SL; ++i) {
+        const int r = r0 + i * (NT / 8);
+        voff[i] = r < left ? static_cast<uint32_t>(r / kBlockRows * kBlockRows * o.ld + r % kBlockRows * 64 + kc) * 2u
+                           : kOobOff;
+      }
     } else {
       base = o.p + row0 * o.ld;
       bytes = left > 0 ? static_cast<uint32_t>(((left < R ? left : R) - 1) * o.ld + k_end) * 2u : 0u;
@@ -310,7 +315,7 @@ struct LoadKCol {
     }
   }
   __device__ __forceinline__ void issue(uint32_t lds, int64_t k0, int64_t k_end, int wave) const {
-    rsrc4 r = load_rsrc(TILED ? base + k0 * R : base, bytes);
+    rsrc4 r = load_rsrc(TILED ? base + k0 * kBlockRows : base, bytes);
     settle_rsrc(r);
     const bool in = TILED || k0 + kc < k_end;  // a blocked matrix has whole steps
     const uint32_t step = TILED ? 0u : static_cast<uint32_t>(k0) * 2u;
@@ -322,7 +327,13 @@ struct LoadKCol {
 
 // The form with k as the memory row. LDS: k row r is 2 R bytes; its 32-byte
 // pair of pieces p sits at p ^ f(r), f(r) = r % 4 + 4 (r / 8 % 2), so that the
-// 8 k rows that a transposed read takes at a time fall on distinct banks.
+// 8 k rows that a transposed read takes at a time fall on distinct banks. At
+// R = 64 two rows share the banks' width and f(r) = r / 2 % 2 + 2 (r / 8 % 2).
+template <int CH>
+__device__ __forceinline__ int krow_swizzle(int k) {
+  if constexpr (CH == 8) return ((k >> 1 & 1) | ((k >> 3 & 1) << 1)) << 1;
+  else return ((k & 3) | ((k >> 3 & 1) << 2)) << 1;
+}
 // PAIR: the tile's columns are R / 2 of the first half of the matrix (gate)
 // and the R / 2 at the same place of its second half (up, `half` further on).
 // TILED: a blocked matrix, whose rows past the last are not to be read.
@@ -336,9 +347,8 @@ struct LoadKRow {
   int64_t ld, width, k_rows;
   uint32_t voff[SL];
   int k_thread;
-  static __device__ __forceinline__ int swz(int k) {
-    return (((k & 3) | ((k >> 3 & 1) << 2)) << 1) & (CH - 1);
-  }
+  int64_t pair_col;
+  static __device__ __forceinline__ int swz(int k) { return krow_swizzle<CH>(k); }
   __device__ __forceinline__ void init(const Operand& o, int64_t col0, int64_t half, int tid) {
     p = o.p;
     ld = o.ld;
@@ -369,6 +379,18 @@ struct LoadKRow {
       }
       voff[i] = in ? static_cast<uint32_t>(k * ld + col) * 2u : kOobOff;
     }
+    if constexpr (PAIR) {
+      const int c = (cs ^ swz(k0)) * 8;
+      pair_col = col0 + (c >= R / 2 ? c - R / 2 : c);
+    }
+  }
+  // PAIR: the tile `step` columns further on. (A thread's slots share their
+  // column: swz repeats every 16 k rows, which KS is a multiple of.)
+  __device__ __forceinline__ void next(int step, int64_t cols) {
+    static_assert(!PAIR || KS % 16 == 0, "one column per thread");
+    pair_col += step;
+#pragma unroll
+    for (int i = 0; i < SL; ++i) voff[i] = pair_col < cols ? voff[i] + step * 2u : kOobOff;
   }
   __device__ __forceinline__ void issue(uint32_t lds, int64_t k0, int64_t k_end, int wave) const {
     const int64_t left = (k_rows < k_end ? k_rows : k_end) - k0;
@@ -382,7 +404,7 @@ struct LoadKRow {
         load_to_lds(r, k_thread + i * KS < left ? voff[i] : kOobOff, lds + (i * NT + wave * 64) * 16);
     } else {
       const uint32_t bytes =
-          static_cast<uint32_t>(((left < kStepK ? left : kStepK) - 1) * ld + width) * 2u;
+          left > 0 ? static_cast<uint32_t>(((left < kStepK ? left : kStepK) - 1) * ld + width) * 2u : 0u;
       rsrc4 r = load_rsrc(p + k0 * ld, bytes);
       settle_rsrc(r);
 #pragma unroll
@@ -461,8 +483,7 @@ struct Tile {
       // lane s of group g names k row 32 kk + 8 g + 4 half + s / 4, columns 4
       // (s % 4) .. + 3 of the block; it receives column s of the 4 k rows
       constexpr int CH = R / 8;
-      const int c = ((row >> 3) + ((s & 3) >> 1)) ^
-                    ((((s >> 2) | ((g & 1) << 2)) << 1) & (CH - 1));
+      const int c = ((row >> 3) + ((s & 3) >> 1)) ^ krow_swizzle<CH>(g * 8 + (s >> 2));
       const char* q = t + (kk * 32 + g * 8 + (s >> 2)) * (R * 2) + c * 16 + (s & 1) * 8;
       const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)q);
       const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(q + 4 * R * 2));

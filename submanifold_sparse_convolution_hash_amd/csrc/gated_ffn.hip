@@ -234,7 +234,7 @@ int ffn_forward(const Ffn& f, const float* b_in, const float* b_out, const uint1
   const Mat16 x = readable(f.x, 1, 8, ws, &packs), wi = readable(f.W_in, 2, 8, ws, &packs);
   const Mat16 wo = readable(f.W_out, 1, 8, ws, &packs);
   // (a query does not know whether pre is asked for: it counts h)
-  if (!ws.counting && !pre && fused_ffn_takes(f.n, f.C, f.Co)) {
+  if (!ws.counting && !pre && fused_ffn_takes(f.n, f.C, f.F, f.Co)) {
     SUBMCONV_TRY(run_packs(packs, stream));
     return fused_ffn(x, wi, f.F, b_in, wo, b_out, f.act, f.bf16, residual, ldr, out, f.Co, stream);
   }
