@@ -39,9 +39,10 @@ struct PackList {
 int run_packs(const PackList& list, hipStream_t stream);
 
 // out[c] = sum over `parts` rows of partial[part][ld], c < cols, in order;
-// columns of `groups` padded groups are closed up.
+// columns of `groups` padded groups are closed up, and those from `split` on go
+// to out2.
 int sum_parts(const float* partial, int64_t parts, int64_t ld, int64_t cols, int groups, float* out,
-              hipStream_t stream);
+              hipStream_t stream, int64_t split = INT64_MAX, float* out2 = nullptr);
 
 // Column sums of a matrix in fp32 (bias gradients), with `partial` of
 // column_parts(rows, cols) x round8(cols) floats.

@@ -96,11 +96,12 @@ __device__ __forceinline__ float4v mfma16(half8 a, half8 b, float4v c) {
 
 // ---- 8 columns of a 16-bit matrix row ----
 
-// Row `row`'s columns n .. n + 7, zeros past n_end. `vec`: the matrix starts
-// on 16 bytes, its rows are 16-byte multiples apart and n_end is one of 8.
-__device__ __forceinline__ u32x4 load_piece(const uint16_t* row, int64_t n, int64_t n_end, bool vec) {
+// Row `row`'s columns n .. n + 7, zeros past n_end (16 bytes at any element's
+// address: the memory system takes an access that is not aligned to its size).
+__device__ __forceinline__ u32x4 load_piece(const uint16_t* row, int64_t n, int64_t n_end) {
+  typedef uint32_t loose __attribute__((ext_vector_type(4), aligned(2)));
+  if (n + 8 <= n_end) return *reinterpret_cast<const loose*>(row + n);
   u32x4 r = {};
-  if (vec) return n < n_end ? *reinterpret_cast<const u32x4*>(row + n) : r;
 #pragma unroll
   for (int e = 0; e < 8; ++e)
     if (n + e < n_end) r[e >> 1] |= static_cast<uint32_t>(row[n + e]) << (16 * (e & 1));

@@ -46,7 +46,7 @@ __device__ __forceinline__ float few_x(X v) {
 template <bool BF16, typename X, int M, int LPR, bool GATED>
 __global__ __launch_bounds__(kFewThreads) void k_few(const X* __restrict__ x, int64_t ldx, int rows,
                                                      const uint16_t* __restrict__ W, int64_t ldw,
-                                                     bool vec, int64_t K, int64_t N, FewEpi e) {
+                                                     int64_t K, int64_t N, FewEpi e) {
   constexpr int H = GATED ? 2 : 1;
   constexpr int SLICES = kFewThreads / LPR, COLS = LPR * 8, WAVES = kFewThreads / 64;
   __shared__ float sums[WAVES][H][M][COLS];
@@ -61,7 +61,7 @@ __global__ __launch_bounds__(kFewThreads) void k_few(const X* __restrict__ x, in
 #pragma unroll
     for (int h = 0; h < H; ++h) {
       float w[8];
-      unpack8<BF16>(load_piece(W + k * ldw + h * N, n, N, vec), w);
+      unpack8<BF16>(load_piece(W + k * ldw + h * N, n, N), w);
 #pragma unroll
       for (int m = 0; m < M; ++m)
 #pragma unroll
@@ -103,10 +103,9 @@ __global__ __launch_bounds__(kFewThreads) void k_few(const X* __restrict__ x, in
 template <bool BF16, typename X, bool GATED>
 int launch_few(const X* x, int64_t ldx, int rows, const Mat16& W, int64_t N, const FewEpi& e,
                hipStream_t stream) {
-  const bool vec = aligned16(W.p) && W.ld % 8 == 0 && N % 8 == 0;
   auto go = [&](auto m, auto lpr) {
     const dim3 grid(static_cast<unsigned>(div_up(N, lpr * 8)));
-    k_few<BF16, X, m, lpr, GATED><<<grid, kFewThreads, 0, stream>>>(x, ldx, rows, W.p, W.ld, vec,
+    k_few<BF16, X, m, lpr, GATED><<<grid, kFewThreads, 0, stream>>>(x, ldx, rows, W.p, W.ld,
                                                                    W.rows, N, e);
   };
   auto by_rows = [&](auto lpr) {

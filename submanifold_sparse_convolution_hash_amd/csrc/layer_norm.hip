@@ -26,27 +26,33 @@ constexpr int64_t kMaxChannels = 8192;  // 256 lanes of 32 values
 
 // ---- elements ----
 
+// Columns c .. c + VEC - 1 of a row, zeros past C (16 bytes at any element's
+// address: the memory system takes an access that is not aligned to its size,
+// at the cost of the lines it straddles).
 template <typename T, int VEC>
-__device__ __forceinline__ void load_vec(const T* p, float (&v)[VEC]) {
-  typedef T vec __attribute__((ext_vector_type(VEC)));
-  if constexpr (VEC == 1) {
-    v[0] = static_cast<float>(*p);
-  } else {
-    const vec t = *reinterpret_cast<const vec*>(p);
+__device__ __forceinline__ void load_piece(const T* row, int c, int C, float (&v)[VEC]) {
+  typedef T vec __attribute__((ext_vector_type(VEC), aligned(sizeof(T))));
+  if (c + VEC <= C) {
+    const vec t = *reinterpret_cast<const vec*>(row + c);
 #pragma unroll
     for (int e = 0; e < VEC; ++e) v[e] = static_cast<float>(t[e]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) v[e] = c + e < C ? static_cast<float>(row[c + e]) : 0.0f;
   }
 }
 template <typename T, int VEC>
-__device__ __forceinline__ void store_vec(T* p, const float (&v)[VEC]) {
-  typedef T vec __attribute__((ext_vector_type(VEC)));
-  if constexpr (VEC == 1) {
-    *p = static_cast<T>(v[0]);
-  } else {
+__device__ __forceinline__ void store_piece(T* row, int c, int C, const float (&v)[VEC]) {
+  typedef T vec __attribute__((ext_vector_type(VEC), aligned(sizeof(T))));
+  if (c + VEC <= C) {
     vec t;
 #pragma unroll
     for (int e = 0; e < VEC; ++e) t[e] = static_cast<T>(v[e]);  // round to nearest even
-    *reinterpret_cast<vec*>(p) = t;
+    *reinterpret_cast<vec*>(row + c) = t;
+  } else {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e)
+      if (c + e < C) row[c + e] = static_cast<T>(v[e]);
   }
 }
 
@@ -56,16 +62,12 @@ template <int VEC>
 __device__ __forceinline__ void load_weights(const float* w, int C, int c, float (&v)[VEC]) {
   const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
       const_cast<float*>(w), static_cast<short>(0), w ? C * 4 : 0, 0x00020000);
-  if constexpr (VEC >= 4) {
-    typedef float float4v __attribute__((ext_vector_type(4)));
+  typedef float float4v __attribute__((ext_vector_type(4)));
 #pragma unroll
-    for (int e = 0; e < VEC; e += 4) {
-      const float4v t = __builtin_bit_cast(float4v, __builtin_amdgcn_raw_buffer_load_b128(r, (c + e) * 4, 0, 0));
+  for (int e = 0; e < VEC; e += 4) {
+    const float4v t = __builtin_bit_cast(float4v, __builtin_amdgcn_raw_buffer_load_b128(r, (c + e) * 4, 0, 0));
 #pragma unroll
-      for (int q = 0; q < 4; ++q) v[e + q] = t[q];
-    }
-  } else {
-    v[0] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(r, c * 4, 0, 0));
+    for (int q = 0; q < 4; ++q) v[e + q] = t[q];
   }
 }
 
@@ -113,7 +115,7 @@ __global__ __launch_bounds__(kNormThreads) void k_layer_norm(
       const int c = (i * G + l) * VEC;
 #pragma unroll
       for (int e = 0; e < VEC; ++e) v[i][e] = 0.0f;
-      if (live && c < C) load_vec<T, VEC>(x + r * ldx + c, v[i]);
+      if (live) load_piece<T, VEC>(x + r * ldx, c, C, v[i]);
 #pragma unroll
       for (int e = 0; e < VEC; ++e) s += v[i][e];
     }
@@ -121,11 +123,11 @@ __global__ __launch_bounds__(kNormThreads) void k_layer_norm(
     float q = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const bool in = (i * G + l) * VEC < C;
+      const int c = (i * G + l) * VEC;
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
         v[i][e] -= m;
-        q += in ? v[i][e] * v[i][e] : 0.0f;
+        q += c + e < C ? v[i][e] * v[i][e] : 0.0f;
       }
     }
     const float rs = 1.0f / sqrtf(row_sum<G>(q, slots[turn][1]) * inv_c + eps);
@@ -135,7 +137,7 @@ __global__ __launch_bounds__(kNormThreads) void k_layer_norm(
       const int c = (i * G + l) * VEC;
 #pragma unroll
       for (int e = 0; e < VEC; ++e) v[i][e] = v[i][e] * rs * (w ? wv[i][e] : 1.0f) + bv[i][e];
-      if (c < C) store_vec<T, VEC>(y + r * C + c, v[i]);
+      store_piece<T, VEC>(y + r * C, c, C, v[i]);
     }
     if (lead) {
       if (mean) mean[r] = m;
@@ -175,17 +177,17 @@ __global__ __launch_bounds__(kNormThreads) void k_layer_norm_grad(
       const int c = (i * G + l) * VEC;
 #pragma unroll
       for (int e = 0; e < VEC; ++e) d[i][e] = xh[i][e] = 0.0f;
-      if (live && c < C) {
-        load_vec<T, VEC>(dy + r * ldg + c, d[i]);
-        load_vec<T, VEC>(x + r * ldx + c, xh[i]);
+      if (live) {
+        load_piece<T, VEC>(dy + r * ldg, c, C, d[i]);
+        load_piece<T, VEC>(x + r * ldx, c, C, xh[i]);
       }
     }
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const bool in = live && (i * G + l) * VEC < C;
+      const int c = (i * G + l) * VEC;
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
-        xh[i][e] = in ? (xh[i][e] - m) * rs : 0.0f;
+        xh[i][e] = live && c + e < C ? (xh[i][e] - m) * rs : 0.0f;
         sw[i][e] += d[i][e] * xh[i][e];
         sb[i][e] += d[i][e];
         d[i][e] *= wv[i][e];
@@ -202,7 +204,7 @@ __global__ __launch_bounds__(kNormThreads) void k_layer_norm_grad(
       const int c = (i * G + l) * VEC;
 #pragma unroll
       for (int e = 0; e < VEC; ++e) d[i][e] = rs * (d[i][e] - s1 - xh[i][e] * s2);
-      if (c < C) store_vec<T, VEC>(dx + r * C + c, d[i]);
+      store_piece<T, VEC>(dx + r * C, c, C, d[i]);
     }
   }
   if (!partial) return;
@@ -245,63 +247,40 @@ __global__ __launch_bounds__(kNormThreads) void k_layer_norm_grad(
   }
 }
 
-// ---- dispatch: lanes and values per row by the width and the alignment ----
+// ---- dispatch: lanes and values per row by the width ----
 
 // Workgroups: eight a compute unit for the forward (its loop keeps the
 // weights), four for the gradient, whose column sums cost 8 C bytes each.
 constexpr int64_t kNormBlocks = 2048, kNormGradBlocks = 1024;
 
-template <typename F>
-int by_width(int64_t C, int vec, F&& f) {
+template <int VEC, typename F>
+int by_width(int64_t C, F&& f) {
   using std::integral_constant;
-#define SUBMCONV_NORM(VEC, G, V) \
-  return f(integral_constant<int, VEC>{}, integral_constant<int, G>{}, integral_constant<int, V>{})
-#define SUBMCONV_NORM_VEC(VEC, VMID, VTOP)               \
-  do {                                                   \
-    if (C <= 8 * VEC) SUBMCONV_NORM(VEC, 8, 1);          \
-    if (C <= 16 * VEC) SUBMCONV_NORM(VEC, 16, 1);        \
-    if (C <= 32 * VEC) SUBMCONV_NORM(VEC, 32, 1);        \
-    if (C <= 64 * VEC) SUBMCONV_NORM(VEC, 64, 1);        \
-    if (C <= 128 * VEC) SUBMCONV_NORM(VEC, 64, 2);       \
-    if (C <= 64 * VMID * VEC) SUBMCONV_NORM(VEC, 64, VMID); \
-    if (C <= 64 * VTOP * VEC) SUBMCONV_NORM(VEC, 64, VTOP); \
-    SUBMCONV_NORM(VEC, 256, VTOP);                       \
-  } while (0)
-  if (vec == 8) SUBMCONV_NORM_VEC(8, 2, 4);
-  if (vec == 4) SUBMCONV_NORM_VEC(4, 4, 8);
-  if (C <= 32) SUBMCONV_NORM(1, 32, 1);
-  if (C <= 64) SUBMCONV_NORM(1, 64, 1);
-  if (C <= 128) SUBMCONV_NORM(1, 64, 2);
-  if (C <= 256) SUBMCONV_NORM(1, 64, 4);
-  if (C <= 512) SUBMCONV_NORM(1, 64, 8);
-  if (C <= 1024) SUBMCONV_NORM(1, 64, 16);
-  if (C <= 2048) SUBMCONV_NORM(1, 64, 32);
-  SUBMCONV_NORM(1, 256, 32);
-#undef SUBMCONV_NORM_VEC
+  auto go = [&](auto g, auto v) { return f(g, v); };
+#define SUBMCONV_NORM(G, V) return go(integral_constant<int, G>{}, integral_constant<int, V>{})
+  if (C <= 8 * VEC) SUBMCONV_NORM(8, 1);
+  if (C <= 16 * VEC) SUBMCONV_NORM(16, 1);
+  if (C <= 32 * VEC) SUBMCONV_NORM(32, 1);
+  if (C <= 64 * VEC) SUBMCONV_NORM(64, 1);
+  if (C <= 128 * VEC) SUBMCONV_NORM(64, 2);
+  if (C <= 256 * VEC) SUBMCONV_NORM(64, 4);
+  if constexpr (VEC == 4)
+    if (C <= 512 * VEC) SUBMCONV_NORM(64, 8);
+  SUBMCONV_NORM(256, 32 / VEC);
 #undef SUBMCONV_NORM
-}
-
-bool on16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
-
-template <typename T>
-int vec_of(int64_t C, int64_t ld1, int64_t ld2, const void* a, const void* b, const void* c) {
-  constexpr int v = 16 / sizeof(T);
-  return C % v == 0 && ld1 % v == 0 && ld2 % v == 0 && on16(a) && on16(b) && on16(c) ? v : 1;
 }
 
 template <typename T>
 int norm_forward(const void* x, int64_t ldx, int64_t n, int C, const float* w, const float* b,
                  float eps, void* y, float* mean, float* rstd, hipStream_t stream) {
-  const int vec = vec_of<T>(C, ldx, ldx, x, y, y);
-  return by_width(C, vec, [&](auto ve, auto g, auto v) {
-    if constexpr (ve == 1 || ve == 16 / sizeof(T)) {
-      const int64_t rpb = kNormThreads / g;
-      const int64_t blocks = std::min((n + rpb - 1) / rpb, kNormBlocks);
-      k_layer_norm<T, ve, g, v><<<static_cast<unsigned>(blocks), kNormThreads, 0, stream>>>(
-          static_cast<const T*>(x), ldx, n, C, w, b, eps, 1.0f / static_cast<float>(C),
-          static_cast<T*>(y), mean, rstd);
-      SUBMCONV_HIP_CHECK(hipGetLastError());
-    }
+  constexpr int VEC = 16 / sizeof(T);
+  return by_width<VEC>(C, [&](auto g, auto v) {
+    const int64_t rpb = kNormThreads / g;
+    const int64_t blocks = std::min((n + rpb - 1) / rpb, kNormBlocks);
+    k_layer_norm<T, VEC, g, v><<<static_cast<unsigned>(blocks), kNormThreads, 0, stream>>>(
+        static_cast<const T*>(x), ldx, n, C, w, b, eps, 1.0f / static_cast<float>(C),
+        static_cast<T*>(y), mean, rstd);
+    SUBMCONV_HIP_CHECK(hipGetLastError());
     return SUBMCONV_OK;
   });
 }
@@ -310,17 +289,15 @@ template <typename T>
 int norm_backward(const void* dy, int64_t ldg, const void* x, int64_t ldx, int64_t n, int C,
                   const float* mean, const float* rstd, const float* w, void* dx, float* partial,
                   int64_t* parts, hipStream_t stream) {
-  const int vec = vec_of<T>(C, ldg, ldx, dy, x, dx);
-  return by_width(C, vec, [&](auto ve, auto g, auto v) {
-    if constexpr (ve == 1 || ve == 16 / sizeof(T)) {
-      const int64_t rpb = kNormThreads / g;
-      const int64_t blocks = std::max<int64_t>(1, std::min((n + rpb - 1) / rpb, kNormGradBlocks));
-      *parts = blocks;
-      k_layer_norm_grad<T, ve, g, v><<<static_cast<unsigned>(blocks), kNormThreads, 0, stream>>>(
-          static_cast<const T*>(dy), ldg, static_cast<const T*>(x), ldx, n, C, mean, rstd, w,
-          1.0f / static_cast<float>(C), static_cast<T*>(dx), partial);
-      SUBMCONV_HIP_CHECK(hipGetLastError());
-    }
+  constexpr int VEC = 16 / sizeof(T);
+  return by_width<VEC>(C, [&](auto g, auto v) {
+    const int64_t rpb = kNormThreads / g;
+    const int64_t blocks = std::max<int64_t>(1, std::min((n + rpb - 1) / rpb, kNormGradBlocks));
+    *parts = blocks;
+    k_layer_norm_grad<T, VEC, g, v><<<static_cast<unsigned>(blocks), kNormThreads, 0, stream>>>(
+        static_cast<const T*>(dy), ldg, static_cast<const T*>(x), ldx, n, C, mean, rstd, w,
+        1.0f / static_cast<float>(C), static_cast<T*>(dx), partial);
+    SUBMCONV_HIP_CHECK(hipGetLastError());
     return SUBMCONV_OK;
   });
 }
@@ -404,6 +381,8 @@ extern "C" int submconv_layer_norm_backward(const void* grad_out, int64_t ldg, c
   else
     SUBMCONV_TRY(norm_backward<float>(grad_out, lg, x, lx, n, cdim, mean, rstd, weight, grad_x,
                                       partial, &parts, stream));
+  if (grad_weight && grad_bias)
+    return sum_parts(partial, parts, 2 * cdim, 2 * cdim, 1, grad_weight, stream, cdim, grad_bias);
   if (grad_weight) SUBMCONV_TRY(sum_parts(partial, parts, 2 * cdim, cdim, 1, grad_weight, stream));
   if (grad_bias) SUBMCONV_TRY(sum_parts(partial + cdim, parts, 2 * cdim, cdim, 1, grad_bias, stream));
   return SUBMCONV_OK;

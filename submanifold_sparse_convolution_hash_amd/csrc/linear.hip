@@ -55,12 +55,27 @@ int launch_linear(const Operand& A, const Operand& B, int64_t K, int64_t N, bool
   return SUBMCONV_OK;
 }
 
+// The tile of a product: 256 x 256 reads half as much LDS and cache per product
+// as 128 x 128, but is alone on its compute unit, where nothing covers its
+// epilogue or its wait for memory. It is taken where a product has many
+// products per element moved (K N / (K + N)) and enough tiles for every unit.
+// Measured, 128 against 256: 209715 x 2048 -> 256 (228) 284 against 287 us,
+// 65536 x 1024 -> 1024 (512) 154 against 140, 8192^3 1229 against 920;
+// 209715 x 1024 -> 256 (205) 150 against 156, 100003 x 1024 -> 256 67.5 against
+// 72, 209715 x 512 -> 128 (102) 51 against 80.
+bool wide_tile(int64_t M, int64_t K, int64_t N) {
+  return N >= 256 && K * N / (K + N) >= 240 && div_up(M, 256) * div_up(N, 256) >= 256;
+}
+
 // a [M][K], and B [K][N] (B_ROW) or [N][K]
 template <bool B_ROW>
 int linear_product(const Mat16& a, const Operand& B, int64_t N, bool bf16, const LinearEpi& e,
                    hipStream_t stream) {
   if (a.rows == 0 || N == 0) return SUBMCONV_OK;
   const Operand A{a.p, a.ld, a.rows, a.cols};
+  if (wide_tile(a.rows, a.cols, N))
+    return a.blocked ? launch_linear<B_ROW, true, 256, 256, 2, 4, 2>(A, B, a.cols, N, bf16, e, stream)
+                     : launch_linear<B_ROW, false, 256, 256, 2, 4, 2>(A, B, a.cols, N, bf16, e, stream);
   return a.blocked ? launch_linear<B_ROW, true, 128, 128, 2, 4, 3>(A, B, a.cols, N, bf16, e, stream)
                    : launch_linear<B_ROW, false, 128, 128, 2, 4, 3>(A, B, a.cols, N, bf16, e, stream);
 }
@@ -82,7 +97,7 @@ __global__ __launch_bounds__(256) void k_pack16(Packs p) {
     const I r = i / row_pieces, c = (i - r * row_pieces) * 8;
     const I grp = c / to_cols, cc = c - grp * to_cols;
     reinterpret_cast<u32x4*>(a.to)[i] =
-        load_piece(a.from + static_cast<int64_t>(r) * a.ld + grp * a.from_cols, cc, a.from_cols, false);
+        load_piece(a.from + static_cast<int64_t>(r) * a.ld + grp * a.from_cols, cc, a.from_cols);
   }
 }
 
@@ -96,9 +111,9 @@ constexpr int kSumRows = kSumThreads / kSumLanes;  // rows per pass
 // (zeros past the width), where dz is not null; and the unrounded column sums of this
 // workgroup's rows, where partial is not null. grid (column strips, row runs).
 template <bool BF16, int ACT>
-__device__ __forceinline__ void act_grad_rows(const uint16_t* dy, int64_t ldy, bool vec_y,
-                                              const uint16_t* z, bool vec_z, int64_t rows,
-                                              int64_t cols, int64_t run, uint16_t* dz, int64_t blocks,
+__device__ __forceinline__ void act_grad_rows(const uint16_t* dy, int64_t ldy,
+                                              const uint16_t* z, int64_t rows, int64_t cols,
+                                              int64_t run, uint16_t* dz, int64_t blocks,
                                               float* partial, float (*sums)[kSumLanes * 8 + 1]) {
   const int cl = threadIdx.x % kSumLanes, rl = threadIdx.x / kSumLanes;
   const int64_t c = (static_cast<int64_t>(blockIdx.x) * kSumLanes + cl) * 8;
@@ -107,10 +122,10 @@ __device__ __forceinline__ void act_grad_rows(const uint16_t* dy, int64_t ldy, b
   if (c < (dz ? blocks * 64 : cols)) {
     for (int64_t r = blockIdx.y * run + rl; r < r_end; r += kSumRows) {
       float d[8];
-      unpack8<BF16>(load_piece(dy + r * ldy, c, cols, vec_y), d);
+      unpack8<BF16>(load_piece(dy + r * ldy, c, cols), d);
       if constexpr (ACT != kActNone) {
         float w[8];
-        unpack8<BF16>(load_piece(z + r * cols, c, cols, vec_z), w);
+        unpack8<BF16>(load_piece(z + r * cols, c, cols), w);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           float a, g;
@@ -140,13 +155,12 @@ static_assert(kSumLanes * 8 == kSumThreads, "one thread per column of a strip");
 
 template <bool BF16>
 __global__ __launch_bounds__(kSumThreads) void k_act_grad(const uint16_t* dy, int64_t ldy,
-                                                          bool vec_y, const uint16_t* z, bool vec_z,
-                                                          int act, int64_t rows, int64_t cols,
+                                                          const uint16_t* z, int act, int64_t rows, int64_t cols,
                                                           int64_t run, uint16_t* dz, int64_t blocks,
                                                           float* partial) {
   __shared__ float sums[kSumRows][kSumLanes * 8 + 1];
   with_act(act, [&](auto a) {
-    act_grad_rows<BF16, decltype(a)::value>(dy, ldy, vec_y, z, vec_z, rows, cols, run, dz, blocks,
+    act_grad_rows<BF16, decltype(a)::value>(dy, ldy, z, rows, cols, run, dz, blocks,
                                             partial, sums);
   });
 }
@@ -155,7 +169,8 @@ __global__ __launch_bounds__(kSumThreads) void k_act_grad(const uint16_t* dy, in
 // adds the parts q, q + 64, ... in order, then the 64 sums are added pairwise
 __global__ __launch_bounds__(1024) void k_sum_parts(const float* __restrict__ partial, int64_t parts,
                                                     int64_t ld, int64_t cols, int groups,
-                                                    float* __restrict__ out) {
+                                                    float* __restrict__ out, int64_t split,
+                                                    float* __restrict__ out2) {
   __shared__ float sums[64][17];
   const int cl = threadIdx.x & 15, q = threadIdx.x >> 4;
   const int64_t c = static_cast<int64_t>(blockIdx.x) * 16 + cl;
@@ -173,7 +188,9 @@ __global__ __launch_bounds__(1024) void k_sum_parts(const float* __restrict__ pa
     if (q < w) sums[q][cl] += sums[q + w][cl];
     __syncthreads();
   }
-  if (q == 0 && c < cols) out[c] = sums[0][cl];
+  if (q != 0 || c >= cols) return;
+  if (c < split) out[c] = sums[0][cl];
+  else out2[c - split] = sums[0][cl];
 }
 
 int act_grad(const Mat16& dy, const uint16_t* z, int act, bool bf16, uint16_t* dz, float* partial,
@@ -182,14 +199,12 @@ int act_grad(const Mat16& dy, const uint16_t* z, int act, bool bf16, uint16_t* d
   const int64_t strips = div_up(dz ? blocks * 8 : div_up(dy.cols, 8), kSumLanes);
   const int64_t parts = column_parts(dy.rows, dy.cols);
   const int64_t run = div_up(div_up(dy.rows, parts), kSumRows) * kSumRows;
-  const bool vec_y = pieces_fit(dy);
-  const bool vec_z = aligned16(z) && dy.cols % 8 == 0;
   const dim3 grid(static_cast<unsigned>(strips), static_cast<unsigned>(parts));
   if (bf16)
-    k_act_grad<true><<<grid, kSumThreads, 0, stream>>>(dy.p, dy.ld, vec_y, z, vec_z, act, dy.rows,
+    k_act_grad<true><<<grid, kSumThreads, 0, stream>>>(dy.p, dy.ld, z, act, dy.rows,
                                                        dy.cols, run, dz, blocks, partial);
   else
-    k_act_grad<false><<<grid, kSumThreads, 0, stream>>>(dy.p, dy.ld, vec_y, z, vec_z, act, dy.rows,
+    k_act_grad<false><<<grid, kSumThreads, 0, stream>>>(dy.p, dy.ld, z, act, dy.rows,
                                                         dy.cols, run, dz, blocks, partial);
   SUBMCONV_HIP_CHECK(hipGetLastError());
   return SUBMCONV_OK;
@@ -261,13 +276,17 @@ __global__ __launch_bounds__(256) void k_weight_sum(const float* __restrict__ pa
   }
 }
 
-constexpr int kGradTile = 256;
+// A weight gradient's tile: 256 x 256 (one workgroup a compute unit), or 128 x
+// 128 (two) where the weights are no larger than that and three quarters or
+// more of the wide tile would be empty.
+int64_t grad_tile(int64_t cin, int64_t cols) { return cin <= 128 && cols <= 128 ? 128 : 256; }
 
-// Runs of rows of a weight gradient: enough workgroups for two per compute
-// unit, runs of at least 256 rows and a multiple of 64.
+// Runs of rows of a weight gradient: a workgroup for every place, runs of at
+// least 256 rows and a multiple of 64.
 int64_t grad_run(int64_t rows, int64_t cin, int64_t cols) {
-  const int64_t tiles = div_up(cin, kGradTile) * div_up(cols, kGradTile);
-  const int64_t runs = std::max<int64_t>(1, std::min(div_up(256, tiles), div_up(rows, 256)));
+  const int64_t tile = grad_tile(cin, cols), places = tile == 256 ? 256 : 512;
+  const int64_t tiles = div_up(cin, tile) * div_up(cols, tile);
+  const int64_t runs = std::max<int64_t>(1, std::min(div_up(places, tiles), div_up(rows, 256)));
   return std::max<int64_t>(kStepK, div_up(div_up(rows, runs), kStepK) * kStepK);
 }
 
@@ -292,9 +311,9 @@ int run_packs(const PackList& list, hipStream_t stream) {
 }
 
 int sum_parts(const float* partial, int64_t parts, int64_t ld, int64_t cols, int groups, float* out,
-              hipStream_t stream) {
+              hipStream_t stream, int64_t split, float* out2) {
   k_sum_parts<<<static_cast<unsigned>(div_up(cols, 16)), 1024, 0, stream>>>(partial, parts, ld, cols,
-                                                                            groups, out);
+                                                                            groups, out, split, out2);
   SUBMCONV_HIP_CHECK(hipGetLastError());
   return SUBMCONV_OK;
 }
@@ -335,17 +354,22 @@ int product_tn(const Mat16& x, const Mat16& dz, bool bf16, float* partial, uint1
                int64_t cols_x, int64_t cols_z, int groups, hipStream_t stream) {
   const int64_t run = grad_run(x.rows, x.cols, dz.cols);
   const int64_t runs = std::max<int64_t>(1, div_up(x.rows, run));
-  const int64_t mt = div_up(x.cols, kGradTile), nt = div_up(dz.cols, kGradTile);
+  const int64_t tile = grad_tile(x.cols, dz.cols);
+  const int64_t mt = div_up(x.cols, tile), nt = div_up(dz.cols, tile);
   if (runs * mt * nt > INT32_MAX || div_up(x.cols * dz.cols, 256) > INT32_MAX)
     return set_error(SUBMCONV_ERR_UNSUPPORTED_SHAPE, "weight gradient %lld x %lld",
                      (long long)x.cols, (long long)dz.cols);
   const Operand X{x.p, x.ld, x.cols, x.rows}, Z{dz.p, dz.ld, dz.cols, x.rows};
   const dim3 grid(static_cast<unsigned>(runs * mt * nt));
   auto launch = [&](auto xt, auto zt) {
-    if (bf16)
-      k_weight_grad<true, xt, zt, kGradTile, kGradTile, 2, 4, 3><<<grid, 512, 0, stream>>>(X, Z, x.rows, run, mt, nt, partial);
-    else
-      k_weight_grad<false, xt, zt, kGradTile, kGradTile, 2, 4, 3><<<grid, 512, 0, stream>>>(X, Z, x.rows, run, mt, nt, partial);
+    auto go = [&](auto t) {
+      if (bf16)
+        k_weight_grad<true, xt, zt, t, t, 2, 4, 3><<<grid, 512, 0, stream>>>(X, Z, x.rows, run, mt, nt, partial);
+      else
+        k_weight_grad<false, xt, zt, t, t, 2, 4, 3><<<grid, 512, 0, stream>>>(X, Z, x.rows, run, mt, nt, partial);
+    };
+    if (tile == 256) go(std::integral_constant<int, 256>{});
+    else go(std::integral_constant<int, 128>{});
   };
   if (x.blocked) launch(std::true_type{}, std::false_type{});
   else if (dz.blocked) launch(std::false_type{}, std::true_type{});

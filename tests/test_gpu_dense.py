@@ -214,6 +214,39 @@ def test_linear(dev, shape, dtype):
 
 
 @gpu
+def test_wide_tiles(dev):
+    """Products large enough for the 256 x 256 tile, in both orders of the weight,
+    of plain and of blocked rows, against torch in fp64 on some rows of the
+    result (rows at both ends and inside, all columns)."""
+    sc = _sc()
+    n, cin, cout = 66001, 512, 520
+    mk = Maker(dev, 2)
+    x, W, dy = mk.rows(n, cin, torch.bfloat16), mk.mat(cin, cout, torch.bfloat16), mk.rows(n, cout, torch.bfloat16)
+    b = mk.vec(cout)
+    out, pre = sc.linear(x, W, b, act="silu", return_pre=True)
+    at = torch.tensor([0, 1, 127, 128, 255, 256, 33000, n - 130, n - 2, n - 1], device=dev)
+    z = x[at].double() @ W.double() + b.double()
+    s = x[at].double().abs() @ W.double().abs() + b.double().abs()
+    ez = (cin + 4) * V * s
+    u = U[torch.bfloat16]
+    _check(pre[at], z.cpu().numpy(), (ez + u * z.abs()).cpu().numpy() + 1e-30, "pre")
+    r = torch.nn.functional.silu(z)
+    _check(out[at], r.cpu().numpy(), (1.2 * ez + 32 * V * (1 + z.abs()) + u * r.abs()).cpu().numpy(), "out")
+    for act, p in ((None, None), ("silu", pre)):
+        gx = sc.linear_backward(dy, x, W, p, act=act, needs=(True, False, False))[0]
+        dz = dy[at].double()
+        ed = torch.zeros_like(dz)
+        if act:
+            v, d = od.act(pre[at].double().cpu().numpy(), act)
+            ed = dz.abs() * 32 * V * (1 + pre[at].double().abs())
+            dz = dz * torch.from_numpy(d).to(dev)
+            ed = ed + u * dz.abs()
+        rx, sx = dz @ W.double().t(), dz.abs() @ W.double().abs().t()
+        tol = ed @ W.double().abs().t() + (cout + 4) * V * sx + u * rx.abs() + 1e-30
+        _check(gx[at], rx.cpu().numpy(), tol.cpu().numpy(), f"grad_x {act}")
+
+
+@gpu
 @pytest.mark.parametrize("act", od.ACTS)
 def test_linear_every_activation(dev, act):
     """Every activation's value and slope over pre-activations from -30 to 30
