@@ -29,7 +29,7 @@ __all__ = [
     "abi_version", "release_scratch", "FLAG_MORTON", "downsample", "subdivide", "MaskedPlan", "masked_plan",
     "forward_masked", "layer_norm", "layer_norm_backward", "linear", "linear_backward", "gated_ffn",
     "gated_ffn_backward", "LayerNormFunction", "LinearFunction", "GatedFeedForwardFunction", "LayerNorm",
-    "Linear", "GatedFeedForward",
+    "Linear", "GatedFeedForward", "SparseConvBlock",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -654,3 +654,4 @@ class SubMConv3d(torch.nn.Module):
 from .dense import (  # noqa: E402  (dense.py uses this module's helpers)
     GatedFeedForward, GatedFeedForwardFunction, LayerNorm, LayerNormFunction, Linear, LinearFunction, gated_ffn,
     gated_ffn_backward, layer_norm, layer_norm_backward, linear, linear_backward)
+from .blocks import SparseConvBlock  # noqa: E402

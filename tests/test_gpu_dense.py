@@ -430,7 +430,7 @@ def test_modules_train_like_torch(dev):
              (ffn.w_out.grad, wo.grad), (ffn.b_out.grad, bo.grad)]
     for i, (a, b) in enumerate(pairs):
         assert a.dtype in (torch.float16, torch.float32)
-        err = float((a.double() - b).norm() / b.norm())
+        err = float((a.detach().double() - b.detach()).norm() / b.detach().norm())
         assert err < 1e-2, (i, err)
 
 
@@ -442,6 +442,60 @@ def test_gradients_of_expanded_and_scaled_losses(dev):
     x = torch.randn(40, 16, device=dev).half().requires_grad_()
     ffn(x).sum().backward()
     assert torch.equal(ffn.b_out.grad, torch.full((16,), 40.0, device=dev))
+
+
+@gpu
+def test_block_equals_torch(dev):
+    """A residual block (projection, convolution, norm, gated feed-forward, skip
+    connection) and all its gradients against torch in fp64 over the exported
+    neighbour map: relative 2-norm error within 1 % (as for the modules: a chain
+    of fp16 roundings of 2^-11, here eight)."""
+    sc = _sc()
+    torch.manual_seed(4)
+    G, c, f = 12, 32, 72
+    lin = torch.randperm(G ** 3)[:500].sort().values
+    coords = torch.stack([0 * lin, lin // (G * G), lin // G % G, lin % G], 1).int().to(dev)
+    kmap = sc.build_map(coords, (G, G, G), 1)
+    block = sc.SparseConvBlock(c, f, cin=16, device=dev)
+    x = torch.randn(500, 16, device=dev).half().requires_grad_()
+    out = block(kmap, x)
+    dy = torch.randn_like(out)
+    (out * dy).sum().backward()
+    with torch.no_grad():
+        assert float((block(kmap, x) - out).abs().max()) <= 2 * 2.0 ** -11 * float(out.abs().max())
+
+    p = {k: v.detach().double().requires_grad_() for k, v in block.named_parameters()}
+    rx = x.detach().double().requires_grad_()
+    F = torch.nn.functional
+    h = F.silu(rx @ p["proj.weight"] + p["proj.bias"])
+    nbr = kmap.export().long()
+    rows = torch.cat([h, h.new_zeros(1, c)])[torch.where(nbr < 0, 500, nbr)]  # [N,27,C]
+    conv = rows.reshape(500, 27 * c) @ p["conv_weight"].reshape(27 * c, c) + p["conv_bias"]
+    z = F.layer_norm(conv, (c,), p["norm.weight"], p["norm.bias"], 1e-5) @ p["ffn.w_in"] + p["ffn.b_in"]
+    ref = (F.silu(z[:, :f]) * z[:, f:]) @ p["ffn.w_out"] + p["ffn.b_out"] + h
+    (ref * dy.double()).sum().backward()
+    pairs = [("out", out, ref), ("x", x.grad, rx.grad)]
+    pairs += [(k, v.grad, p[k].grad) for k, v in block.named_parameters()]
+    for name, a, b in pairs:
+        err = float((a.detach().double() - b.detach()).norm() / b.detach().norm())
+        assert err < 1e-2, (name, err)
+    kmap.free()
+
+
+@gpu
+def test_example_runs(dev):
+    """The training example: every loss is finite and the last is the smallest
+    of the first and last; the block runs without gradients afterwards."""
+    import importlib.util
+    import os
+
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "train_block.py")
+    spec = importlib.util.spec_from_file_location("train_block", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    losses, final = mod.train(grid=24, channels=32, steps=10)
+    assert all(np.isfinite(losses)) and np.isfinite(final)
+    assert losses[-1] < losses[0]
 
 
 @gpu
