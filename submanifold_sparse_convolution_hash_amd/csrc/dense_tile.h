@@ -116,38 +116,41 @@ __device__ __forceinline__ u32x4 load_piece(const uint16_t* row, int64_t n, int6
 constexpr int kStream = 2;  // the instructions' nt bit
 struct RowsView {
   __amdgpu_buffer_rsrc_t r;
-  uint32_t ld2, n_end;
+  const uint16_t* p;
+  int64_t ld;
+  uint32_t ld2, n_end, rows;
   bool vec;
-  __device__ __forceinline__ RowsView(const uint16_t* p, int64_t ld, int64_t m0, int64_t M,
+  __device__ __forceinline__ RowsView(const uint16_t* q, int64_t ld_, int64_t m0, int64_t M,
                                       int64_t N, int tile_rows, bool vec_)
-      : ld2(static_cast<uint32_t>(ld) * 2u), n_end(static_cast<uint32_t>(N)), vec(vec_) {
+      : p(q ? q + m0 * ld_ : nullptr), ld(ld_), ld2(static_cast<uint32_t>(ld_) * 2u),
+        n_end(static_cast<uint32_t>(N)), vec(vec_) {
     const int64_t left = M - m0 < tile_rows ? M - m0 : tile_rows;
-    r = tile_rsrc(p ? p + m0 * ld : nullptr,
-                  p && left > 0 ? static_cast<uint32_t>((left - 1) * ld + N) * 2u : 0u);
+    rows = q && left > 0 ? static_cast<uint32_t>(left) : 0u;
+    r = tile_rsrc(p, rows ? static_cast<uint32_t>((left - 1) * ld_ + N) * 2u : 0u);
   }
   __device__ __forceinline__ u32x4 load(uint32_t m, uint32_t n) const {
-    const uint32_t off = m * ld2 + n * 2u;
     if (vec)
-      return __builtin_bit_cast(u32x4,
-                                __builtin_amdgcn_raw_buffer_load_b128(r, n < n_end ? off : kOobOff, 0, 0));
+      return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                           r, n < n_end ? m * ld2 + n * 2u : kOobOff, 0, 0));
     u32x4 v = {};
-#pragma unroll
-    for (uint32_t e = 0; e < 8; ++e)
-      v[e >> 1] |= static_cast<uint32_t>(static_cast<uint16_t>(__builtin_amdgcn_raw_buffer_load_b16(
-                       r, n + e < n_end ? off + 2u * e : kOobOff, 0, 0)))
-                   << (16 * (e & 1));
+    if (m < rows) v = load_piece(p + m * ld, n, n_end);
     return v;
   }
   __device__ __forceinline__ void store(uint32_t m, uint32_t n, u32x4 v) const {
-    const uint32_t off = m * ld2 + n * 2u;
     if (vec) {
-      __builtin_amdgcn_raw_buffer_store_b128(v, r, n < n_end ? off : kOobOff, 0, kStream);
+      __builtin_amdgcn_raw_buffer_store_b128(v, r, n < n_end ? m * ld2 + n * 2u : kOobOff, 0, kStream);
+      return;
+    }
+    if (m >= rows) return;
+    typedef uint32_t loose __attribute__((ext_vector_type(4), aligned(2)));
+    uint16_t* row = const_cast<uint16_t*>(p) + m * ld;
+    if (n + 8 <= n_end) {
+      *reinterpret_cast<loose*>(row + n) = v;
       return;
     }
 #pragma unroll
     for (uint32_t e = 0; e < 8; ++e)
-      __builtin_amdgcn_raw_buffer_store_b16(static_cast<uint16_t>(v[e >> 1] >> (16 * (e & 1))), r,
-                                            n + e < n_end ? off + 2u * e : kOobOff, 0, 0);
+      if (n + e < n_end) row[n + e] = static_cast<uint16_t>(v[e >> 1] >> (16 * (e & 1)));
   }
 };
 
@@ -459,12 +462,14 @@ struct LdsRows {
 template <bool BF16, bool A_ROW, bool B_ROW, bool PAIR, int BM, int BN, int WM, int WN, int STAGES,
           bool A_TILED = false, bool B_TILED = false>
 struct Tile {
+  static constexpr bool DEEP = STAGES > 3;  // as many buffers for B as for A
   static constexpr int NT = WM * WN * 64;
   static constexpr int FM = BM / WM / 16, FN = BN / WN / 16;
   static constexpr int A_BYTES = BM * kStepK * 2, B_BYTES = BN * kStepK * 2;
-  static constexpr int LDS_BYTES = STAGES * A_BYTES + 2 * B_BYTES;
+  static constexpr int B_STAGES = DEEP ? STAGES : 2;
+  static constexpr int LDS_BYTES = STAGES * A_BYTES + B_STAGES * B_BYTES;
   static_assert(FM >= 1 && FN >= 1 && (!PAIR || FN % 2 == 0), "wave tile");
-  static_assert(STAGES == 2 || STAGES == 3, "buffers");
+  static_assert(STAGES >= 2 && STAGES <= 4, "buffers");
   using LA = std::conditional_t<A_ROW, LoadKRow<BM, NT, false, A_TILED>, LoadKCol<BM, NT, A_TILED>>;
   using LB = std::conditional_t<B_ROW, LoadKRow<BN, NT, PAIR, B_TILED>, LoadKCol<BN, NT, false>>;
 
@@ -518,29 +523,40 @@ struct Tile {
     const uint32_t lds = lds_addr(smem);
     auto k_of = [&](int st) { return k_begin + static_cast<int64_t>(st) * kStepK; };
     auto issue_a = [&](int st, int buf) { la.issue(lds + buf * A_BYTES, k_of(st), k_end, wave); };
-    auto issue_b = [&](int st) {
-      lb.issue(lds + STAGES * A_BYTES + (st & 1) * B_BYTES, k_of(st), k_end, wave);
+    auto issue_b = [&](int st, int buf) {
+      lb.issue(lds + STAGES * A_BYTES + buf * B_BYTES, k_of(st), k_end, wave);
     };
-    if (steps > 0) {
-      issue_a(0, 0);
-      issue_b(0);
-    }
-    if (STAGES == 3 && steps > 1) issue_a(1, 1);
+#pragma unroll
+    for (int st = 0; st < STAGES - 1; ++st)
+      if (st < steps) {
+        issue_a(st, st);
+        if (st < B_STAGES - 1) issue_b(st, st);
+      }
 
     int buf = 0;
     for (int st = 0; st < steps; ++st) {
-      // this step's loads are the oldest: all but A's of the next step are
-      // waited for (and this wave's LDS reads of the last step), then every
-      // wave's through the barrier, after which the buffers that were read in
-      // the last step are overwritten
-      if (STAGES == 3 && st + 1 < steps) wait_loads<LA::SL>();
-      else wait_loads<0>();
+      // this step's loads are the oldest: all but those of the later steps
+      // (A's only, unless DEEP) are waited for (and this wave's LDS reads of
+      // the last step), then every wave's through the barrier, after which the
+      // buffers that were read in the last step are overwritten
+      if constexpr (DEEP) {
+        static_assert(STAGES == 4, "waits");
+        if (st + 2 < steps) wait_loads<2 * (LA::SL + LB::SL)>();
+        else if (st + 1 < steps) wait_loads<LA::SL + LB::SL>();
+        else wait_loads<0>();
+      } else if (STAGES == 3 && st + 1 < steps) {
+        wait_loads<LA::SL>();
+      } else {
+        wait_loads<0>();
+      }
       __builtin_amdgcn_s_barrier();
       asm volatile("" ::: "memory");
-      if (st + 1 < steps) issue_b(st + 1);
-      if (st + STAGES - 1 < steps) issue_a(st + STAGES - 1, buf == 0 ? STAGES - 1 : buf - 1);
+      const int last = buf == 0 ? STAGES - 1 : buf - 1;
+      if (DEEP ? st + STAGES - 1 < steps : st + 1 < steps)
+        issue_b(DEEP ? st + STAGES - 1 : st + 1, DEEP ? last : (st + 1) & 1);
+      if (st + STAGES - 1 < steps) issue_a(st + STAGES - 1, last);
       const char* ta = smem + buf * A_BYTES;
-      const char* tb = smem + STAGES * A_BYTES + (st & 1) * B_BYTES;
+      const char* tb = smem + STAGES * A_BYTES + (DEEP ? buf : st & 1) * B_BYTES;
 #pragma unroll
       for (int kk = 0; kk < kStepK / 32; ++kk) {
         half8 fb[FN], fa[FM];
@@ -581,10 +597,19 @@ struct Tile {
   }
 };
 
+// Products of at most one 128 x 128 tile a compute unit take four buffers of
+// both operands: their time is the latency of their steps' loads, and the LDS
+// of a second workgroup is free.
+inline bool few_tiles(int64_t rows, int64_t cols) {
+  return (rows + 127) / 128 * ((cols + 127) / 128) <= 256;
+}
+
 // Waves per SIMD that the register budget leaves room for: two workgroups of
-// a 128 x 128 tile on a compute unit, one of a 256 x 256 tile (LDS allows no
+// a 128 x 128 tile on a compute unit, one of a larger or deeper one (LDS allows no
 // more).
-constexpr int tile_waves(int bm, int bn) { return bm * bn > 128 * 128 ? 2 : 4; }
+constexpr int tile_waves(int bm, int bn, int stages) {
+  return bm * bn > 128 * 128 || stages > 3 ? 2 : 4;
+}
 
 // Output tile of a workgroup: tiles are walked n first, and each XCD
 // (blockIdx % 8) takes a contiguous run of them, so that the n tiles which

@@ -69,7 +69,7 @@ __device__ __forceinline__ void gate_epilogue(const GateEpi& e, int64_t M, int64
 }
 
 template <bool BF16, int BM, int BN, int WM, int WN, int STAGES>
-__global__ __launch_bounds__(WM* WN * 64, tile_waves(BM, BN)) void k_gate(Operand A, Operand B, int64_t K, int64_t half,
+__global__ __launch_bounds__(WM* WN * 64, tile_waves(BM, BN, STAGES)) void k_gate(Operand A, Operand B, int64_t K, int64_t half,
                                                       uint32_t m_tiles, uint32_t n_tiles, GateEpi e) {
   using T = Tile<BF16, false, true, true, BM, BN, WM, WN, STAGES>;
   __shared__ __attribute__((aligned(16))) char smem[T::LDS_BYTES];
@@ -138,7 +138,7 @@ __device__ __forceinline__ void gate_grad_epilogue(const GateGradEpi& e, int64_t
 }
 
 template <bool BF16, int BM, int BN, int WM, int WN, int STAGES>
-__global__ __launch_bounds__(WM* WN * 64, tile_waves(BM, BN)) void k_gate_grad(Operand A, Operand B, int64_t K,
+__global__ __launch_bounds__(WM* WN * 64, tile_waves(BM, BN, STAGES)) void k_gate_grad(Operand A, Operand B, int64_t K,
                                                            uint32_t m_tiles, uint32_t n_tiles,
                                                            GateGradEpi e) {
   using T = Tile<BF16, false, false, false, BM, BN, WM, WN, STAGES>;
@@ -186,10 +186,12 @@ int gate_forward(const Mat16& x, const Mat16& W, int64_t F, const float* bias, i
   const GateEpi e{bias, h, pre, F, Fq, act, F % 8 == 0 && aligned16(pre)};
   const Operand A{x.p, x.ld, x.rows, x.cols}, B{W.p, W.ld, Fp, W.rows};
   const dim3 grid(static_cast<unsigned>(mt * nt));
-  if (bf16)
-    k_gate<true, kGateTile, kGateTile, 2, 4, 2><<<grid, 512, 0, stream>>>(A, B, x.cols, Fp, mt, nt, e);
-  else
-    k_gate<false, kGateTile, kGateTile, 2, 4, 2><<<grid, 512, 0, stream>>>(A, B, x.cols, Fp, mt, nt, e);
+  auto go = [&](auto st) {
+    if (bf16) k_gate<true, kGateTile, kGateTile, 2, 4, st><<<grid, 512, 0, stream>>>(A, B, x.cols, Fp, mt, nt, e);
+    else k_gate<false, kGateTile, kGateTile, 2, 4, st><<<grid, 512, 0, stream>>>(A, B, x.cols, Fp, mt, nt, e);
+  };
+  if (mt * nt <= 256) go(std::integral_constant<int, 4>{});
+  else go(std::integral_constant<int, 2>{});
   SUBMCONV_HIP_CHECK(hipGetLastError());
   return SUBMCONV_OK;
 }
@@ -206,10 +208,12 @@ int gate_grad(const Mat16& dy, const Mat16& W, int64_t Fq, const uint16_t* pre, 
   const GateGradEpi e{pre, dz, h, sums, F, Fq, act, F % 8 == 0 && aligned16(pre)};
   const Operand A{dy.p, dy.ld, dy.rows, dy.cols}, B{W.p, W.ld, F, W.cols};
   const dim3 grid(static_cast<unsigned>(mt * nt));
-  if (bf16)
-    k_gate_grad<true, kGateTile, kGateTile, 2, 4, 2><<<grid, 512, 0, stream>>>(A, B, dy.cols, mt, nt, e);
-  else
-    k_gate_grad<false, kGateTile, kGateTile, 2, 4, 2><<<grid, 512, 0, stream>>>(A, B, dy.cols, mt, nt, e);
+  auto go = [&](auto st) {
+    if (bf16) k_gate_grad<true, kGateTile, kGateTile, 2, 4, st><<<grid, 512, 0, stream>>>(A, B, dy.cols, mt, nt, e);
+    else k_gate_grad<false, kGateTile, kGateTile, 2, 4, st><<<grid, 512, 0, stream>>>(A, B, dy.cols, mt, nt, e);
+  };
+  if (mt * nt <= 256) go(std::integral_constant<int, 4>{});
+  else go(std::integral_constant<int, 2>{});
   SUBMCONV_HIP_CHECK(hipGetLastError());
   return SUBMCONV_OK;
 }

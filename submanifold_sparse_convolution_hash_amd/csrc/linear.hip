@@ -21,7 +21,7 @@ namespace {
 
 // B_ROW: W [K][N] as stored (forward); else W [N][K] (input gradient).
 template <bool BF16, bool B_ROW, bool A_TILED, int BM, int BN, int WM, int WN, int STAGES>
-__global__ __launch_bounds__(WM* WN * 64, tile_waves(BM, BN)) void k_linear(Operand A, Operand B, int64_t K, int64_t N,
+__global__ __launch_bounds__(WM* WN * 64, tile_waves(BM, BN, STAGES)) void k_linear(Operand A, Operand B, int64_t K, int64_t N,
                                                         uint32_t m_tiles, uint32_t n_tiles,
                                                         LinearEpi e) {
   using T = Tile<BF16, false, B_ROW, false, BM, BN, WM, WN, STAGES, A_TILED>;
@@ -76,6 +76,9 @@ int linear_product(const Mat16& a, const Operand& B, int64_t N, bool bf16, const
   if (wide_tile(a.rows, a.cols, N))
     return a.blocked ? launch_linear<B_ROW, true, 256, 256, 2, 4, 2>(A, B, a.cols, N, bf16, e, stream)
                      : launch_linear<B_ROW, false, 256, 256, 2, 4, 2>(A, B, a.cols, N, bf16, e, stream);
+  if (few_tiles(a.rows, N))
+    return a.blocked ? launch_linear<B_ROW, true, 128, 128, 2, 4, 4>(A, B, a.cols, N, bf16, e, stream)
+                     : launch_linear<B_ROW, false, 128, 128, 2, 4, 4>(A, B, a.cols, N, bf16, e, stream);
   return a.blocked ? launch_linear<B_ROW, true, 128, 128, 2, 4, 3>(A, B, a.cols, N, bf16, e, stream)
                    : launch_linear<B_ROW, false, 128, 128, 2, 4, 3>(A, B, a.cols, N, bf16, e, stream);
 }
@@ -214,7 +217,7 @@ int act_grad(const Mat16& dy, const uint16_t* z, int act, bool bf16, uint16_t* d
 
 // One BM x BN tile of x^T dz over one run of rows, as fp32 partial sums.
 template <bool BF16, bool X_TILED, bool Z_TILED, int BM, int BN, int WM, int WN, int STAGES>
-__global__ __launch_bounds__(WM* WN * 64, tile_waves(BM, BN)) void k_weight_grad(Operand X, Operand Z, int64_t rows,
+__global__ __launch_bounds__(WM* WN * 64, tile_waves(BM, BN, STAGES)) void k_weight_grad(Operand X, Operand Z, int64_t rows,
                                                              int64_t run, uint32_t m_tiles,
                                                              uint32_t n_tiles,
                                                              float* __restrict__ partial) {
