@@ -50,8 +50,10 @@ int64_t column_parts(int64_t rows, int64_t cols);
 int column_sums(const Mat16& a, bool bf16, float* partial, float* out, hipStream_t stream);
 
 // dx[m][c] = sum_n dz[m][n] W[c][n] (both readable in pieces, or dz blocked),
-// rounded once.
-int product_nt(const Mat16& dz, const Mat16& W, bool bf16, uint16_t* out, int64_t ldo,
+// rounded once, dense. Small products are split over runs of n; `partial` of
+// product_nt_bytes holds the runs' fp32 sums, added in order.
+int64_t product_nt_bytes(int64_t rows, int64_t k, int64_t cols);
+int product_nt(const Mat16& dz, const Mat16& W, bool bf16, float* partial, uint16_t* out,
                int64_t cols, hipStream_t stream);
 
 // dW[c][n] = sum_m x[m][c] dz[m][n], rounded once; the rows are split over

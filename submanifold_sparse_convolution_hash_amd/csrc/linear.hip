@@ -215,6 +215,25 @@ int act_grad(const Mat16& dy, const uint16_t* z, int act, bool bf16, uint16_t* d
 
 // ---- weight gradient ----
 
+// A wave's accumulators into a plane of fp32 partial sums [rows][cols], cols a
+// multiple of 8.
+template <typename T, int BM, int BN, int WM, int WN>
+__device__ __forceinline__ void store_partial(float* plane, int64_t rows, int64_t cols, int64_t m0,
+                                              int64_t n0, const float4v (&acc)[T::FN][T::FM]) {
+  const int lane = threadIdx.x & 63, g = lane >> 4, s = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+#pragma unroll
+  for (int i = 0; i < T::FM; ++i) {
+    const int64_t m = m0 + (wave / WN) * (BM / WM) + i * 16 + s;
+    if (m >= rows) continue;
+#pragma unroll
+    for (int j = 0; j < T::FN; ++j) {
+      const int64_t n = n0 + (wave % WN) * (BN / WN) + j * 16 + g * 4;
+      if (n < cols) *reinterpret_cast<float4v*>(plane + m * cols + n) = acc[j][i];
+    }
+  }
+}
+
 // One BM x BN tile of x^T dz over one run of rows, as fp32 partial sums.
 template <bool BF16, bool X_TILED, bool Z_TILED, int BM, int BN, int WM, int WN, int STAGES>
 __global__ __launch_bounds__(WM* WN * 64, tile_waves(BM, BN, STAGES)) void k_weight_grad(Operand X, Operand Z, int64_t rows,
@@ -228,19 +247,23 @@ __global__ __launch_bounds__(WM* WN * 64, tile_waves(BM, BN, STAGES)) void k_wei
   const int64_t kb = t.m * run, ke = min(rows, kb + run);
   float4v acc[T::FN][T::FM];
   T::run(X, Z, 0, m0, n0, kb, ke, smem, acc);
-  const int lane = threadIdx.x & 63, g = lane >> 4, s = lane & 15;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  float* out = partial + t.m * X.rows * Z.rows;
-#pragma unroll
-  for (int i = 0; i < T::FM; ++i) {
-    const int64_t m = m0 + (wave / WN) * (BM / WM) + i * 16 + s;
-    if (m >= X.rows) continue;
-#pragma unroll
-    for (int j = 0; j < T::FN; ++j) {
-      const int64_t n = n0 + (wave % WN) * (BN / WN) + j * 16 + g * 4;
-      if (n < Z.rows) *reinterpret_cast<float4v*>(out + m * Z.rows + n) = acc[j][i];
-    }
-  }
+  store_partial<T, BM, BN, WM, WN>(partial + t.m * X.rows * Z.rows, X.rows, Z.rows, m0, n0, acc);
+}
+
+// One tile of an input gradient over one run of k, as fp32 partial sums: for a
+// product of few tiles and many steps, whose time is the steps' latency.
+template <bool BF16, bool A_TILED>
+__global__ __launch_bounds__(512, 2) void k_product_part(Operand A, Operand B, int64_t K, int64_t run,
+                                                         int64_t cols, uint32_t m_tiles,
+                                                         uint32_t n_tiles, float* __restrict__ partial) {
+  using T = Tile<BF16, false, false, false, 128, 128, 2, 4, 4, A_TILED>;
+  __shared__ __attribute__((aligned(16))) char smem[T::LDS_BYTES];
+  const TilePos t = tile_pos(gridDim.x / (m_tiles * n_tiles), m_tiles * n_tiles, blockIdx.x);
+  const int64_t m0 = t.n / n_tiles * 128, n0 = t.n % n_tiles * 128;
+  const int64_t kb = t.m * run, ke = min(K, kb + run);
+  float4v acc[T::FN][T::FM];
+  T::run(A, B, 0, m0, n0, kb, ke, smem, acc);
+  store_partial<T, 128, 128, 2, 4>(partial + t.m * A.rows * cols, A.rows, cols, m0, n0, acc);
 }
 
 // out = the partial sums of the runs added in order, rounded once; columns of
@@ -280,17 +303,42 @@ __global__ __launch_bounds__(256) void k_weight_sum(const float* __restrict__ pa
 }
 
 // A weight gradient's tile: 256 x 256 (one workgroup a compute unit), or 128 x
-// 128 (two) where the weights are no larger than that and three quarters or
-// more of the wide tile would be empty.
-int64_t grad_tile(int64_t cin, int64_t cols) { return cin <= 128 && cols <= 128 ? 128 : 256; }
+// 128 (two) where the weights are no larger than that, so that three quarters
+// or more of the wide tile would be empty, or where the wide tiles of all runs
+// of 256 rows would leave half of the units idle (a tile's 256 KiB of partial
+// sums then take longer to write than its products: 300 rows of 256 x 2048 15 us).
+int64_t grad_tile(int64_t rows, int64_t cin, int64_t cols) {
+  if (cin <= 128 && cols <= 128) return 128;
+  return div_up(cin, 256) * div_up(cols, 256) * div_up(rows, 256) < 128 ? 128 : 256;
+}
 
 // Runs of rows of a weight gradient: a workgroup for every place, runs of at
 // least 256 rows and a multiple of 64.
 int64_t grad_run(int64_t rows, int64_t cin, int64_t cols) {
-  const int64_t tile = grad_tile(cin, cols), places = tile == 256 ? 256 : 512;
+  const int64_t tile = grad_tile(rows, cin, cols), places = tile == 256 ? 256 : 512;
   const int64_t tiles = div_up(cin, tile) * div_up(cols, tile);
   const int64_t runs = std::max<int64_t>(1, std::min(div_up(places, tiles), div_up(rows, 256)));
   return std::max<int64_t>(kStepK, div_up(div_up(rows, runs), kStepK) * kStepK);
+}
+
+// Runs of k of an input gradient (1: not split): at most a quarter of the
+// units have a tile and a tile at least eight steps; runs of at least four.
+int64_t split_k(int64_t M, int64_t K, int64_t N) {
+  const int64_t tiles = div_up(M, 128) * div_up(N, 128), steps = div_up(K, kStepK);
+  if (tiles == 0 || tiles > 64 || steps < 8) return 1;
+  const int64_t runs = std::min(256 / tiles, steps / 4), per = div_up(steps, runs);
+  return div_up(steps, per);
+}
+
+int sum_planes(const float* partial, int64_t runs, int64_t plane, int64_t ldp, int64_t rows,
+               int64_t cols, int groups, bool bf16, uint16_t* out, hipStream_t stream) {
+  const dim3 grid(static_cast<unsigned>(div_up(plane, 256)));
+  if (bf16)
+    k_weight_sum<true><<<grid, 256, 0, stream>>>(partial, runs, plane, ldp, rows, cols, groups, out);
+  else
+    k_weight_sum<false><<<grid, 256, 0, stream>>>(partial, runs, plane, ldp, rows, cols, groups, out);
+  SUBMCONV_HIP_CHECK(hipGetLastError());
+  return SUBMCONV_OK;
 }
 
 }  // namespace
@@ -342,10 +390,31 @@ int linear_forward(const Mat16& x, const Mat16& W, const float* bias, int act, b
   return linear_product<true>(x, Operand{W.p, W.ld, W.cols, W.rows}, cols, bf16, e, stream);
 }
 
-int product_nt(const Mat16& dz, const Mat16& W, bool bf16, uint16_t* out, int64_t ldo,
+int64_t product_nt_bytes(int64_t rows, int64_t k, int64_t cols) {
+  const int64_t runs = split_k(rows, k, cols);
+  return runs > 1 ? runs * rows * round8(cols) * 4 : 0;
+}
+
+int product_nt(const Mat16& dz, const Mat16& W, bool bf16, float* partial, uint16_t* out,
                int64_t cols, hipStream_t stream) {
-  const LinearEpi e{nullptr, nullptr, 0, out, ldo, nullptr, kActNone,
-                    false, cols % 8 == 0 && ldo % 8 == 0 && aligned16(out), false};
+  const int64_t runs = split_k(dz.rows, dz.cols, cols);
+  if (runs > 1) {
+    const int64_t mt = div_up(dz.rows, 128), nt = div_up(cols, 128), cp = round8(cols);
+    const int64_t run = div_up(div_up(dz.cols, kStepK), runs) * kStepK;
+    const Operand A{dz.p, dz.ld, dz.rows, dz.cols}, B{W.p, W.ld, W.rows, W.cols};
+    const dim3 grid(static_cast<unsigned>(runs * mt * nt));
+    auto go = [&](auto bf, auto blocked) {
+      k_product_part<bf, blocked><<<grid, 512, 0, stream>>>(A, B, dz.cols, run, cp, mt, nt, partial);
+    };
+    if (bf16 && dz.blocked) go(std::true_type{}, std::true_type{});
+    else if (bf16) go(std::true_type{}, std::false_type{});
+    else if (dz.blocked) go(std::false_type{}, std::true_type{});
+    else go(std::false_type{}, std::false_type{});
+    SUBMCONV_HIP_CHECK(hipGetLastError());
+    return sum_planes(partial, runs, dz.rows * cp, cp, dz.rows, cols, 1, bf16, out, stream);
+  }
+  const LinearEpi e{nullptr, nullptr, 0, out, cols, nullptr, kActNone,
+                    false, cols % 8 == 0 && aligned16(out), false};
   return linear_product<false>(dz, Operand{W.p, W.ld, W.rows, W.cols}, cols, bf16, e, stream);
 }
 
@@ -357,7 +426,7 @@ int product_tn(const Mat16& x, const Mat16& dz, bool bf16, float* partial, uint1
                int64_t cols_x, int64_t cols_z, int groups, hipStream_t stream) {
   const int64_t run = grad_run(x.rows, x.cols, dz.cols);
   const int64_t runs = std::max<int64_t>(1, div_up(x.rows, run));
-  const int64_t tile = grad_tile(x.cols, dz.cols);
+  const int64_t tile = grad_tile(x.rows, x.cols, dz.cols);
   const int64_t mt = div_up(x.cols, tile), nt = div_up(dz.cols, tile);
   if (runs * mt * nt > INT32_MAX || div_up(x.cols * dz.cols, 256) > INT32_MAX)
     return set_error(SUBMCONV_ERR_UNSUPPORTED_SHAPE, "weight gradient %lld x %lld",
@@ -378,14 +447,7 @@ int product_tn(const Mat16& x, const Mat16& dz, bool bf16, float* partial, uint1
   else if (dz.blocked) launch(std::false_type{}, std::true_type{});
   else launch(std::false_type{}, std::false_type{});
   SUBMCONV_HIP_CHECK(hipGetLastError());
-  const int64_t plane = x.cols * dz.cols;
-  const dim3 rgrid(static_cast<unsigned>(div_up(plane, 256)));
-  if (bf16)
-    k_weight_sum<true><<<rgrid, 256, 0, stream>>>(partial, runs, plane, dz.cols, cols_x, cols_z, groups, out);
-  else
-    k_weight_sum<false><<<rgrid, 256, 0, stream>>>(partial, runs, plane, dz.cols, cols_x, cols_z, groups, out);
-  SUBMCONV_HIP_CHECK(hipGetLastError());
-  return SUBMCONV_OK;
+  return sum_planes(partial, runs, x.cols * dz.cols, dz.cols, cols_x, cols_z, groups, bf16, out, stream);
 }
 
 Mat16 readable(const Mat16& a, int groups, int unit, Arena& ws, PackList* list) {
@@ -462,12 +524,14 @@ int linear_grad(const Mat16& dy, const Mat16& x, const Mat16& W, const uint16_t*
   if (need.w) xr = readable(x, 1, 8, ws, &packs);
   const int64_t parts = column_parts(dy.rows, dy.cols);
   float* sums = need.b ? static_cast<float*>(ws.take(parts * cp * 4)) : nullptr;
-  float* part = need.w ? static_cast<float*>(ws.take(product_tn_bytes(x.rows, round8(x.cols), dz.cols))) : nullptr;
+  const int64_t part_bytes = std::max(need.x ? product_nt_bytes(dz.rows, dz.cols, x.cols) : 0,
+                                      need.w ? product_tn_bytes(x.rows, round8(x.cols), dz.cols) : 0);
+  float* part = static_cast<float*>(ws.take(part_bytes));
   if (!run) return SUBMCONV_OK;
   SUBMCONV_TRY(run_packs(packs, stream));
   if (own_dz || need.b) SUBMCONV_TRY(act_grad(dy, pre, act, bf16, dz_to, sums, stream));
   if (need.b) SUBMCONV_TRY(sum_parts(sums, parts, cp, dy.cols, 1, gb, stream));
-  if (need.x) SUBMCONV_TRY(product_nt(dz, Wr, bf16, gx, x.cols, x.cols, stream));
+  if (need.x) SUBMCONV_TRY(product_nt(dz, Wr, bf16, part, gx, x.cols, stream));
   if (need.w) SUBMCONV_TRY(product_tn(xr, dz, bf16, part, gw, x.cols, dy.cols, 1, stream));
   return SUBMCONV_OK;
 }
