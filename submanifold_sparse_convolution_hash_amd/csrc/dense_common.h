@@ -40,29 +40,58 @@ int run_packs(const PackList& list, hipStream_t stream);
 
 // out[c] = sum over `parts` rows of partial[part][ld], c < cols, in order;
 // columns of `groups` padded groups are closed up, and those from `split` on go
-// to out2.
-int sum_parts(const float* partial, int64_t parts, int64_t ld, int64_t cols, int groups, float* out,
-              hipStream_t stream, int64_t split = INT64_MAX, float* out2 = nullptr);
+// to out2. Up to kSums of them in one launch.
+struct SumJob {
+  const float* partial;
+  int64_t parts, ld, cols;
+  int32_t groups;
+  float* out;
+  int64_t split = INT64_MAX;
+  float* out2 = nullptr;
+};
+constexpr int kSums = 2;
+struct SumList {
+  SumJob job[kSums];
+  int count = 0;
+};
+int run_sums(const SumList& list, hipStream_t stream);
+
+// out[r][c] = sum over the `runs` planes [.. >= rows][ldp] of partial sums, in
+// order, rounded once; columns of `groups` padded groups are closed up. Up to
+// kPlanes of them in one launch.
+struct PlaneJob {
+  const float* partial;
+  int64_t runs, plane, ldp, rows, cols;
+  int32_t groups;
+  uint16_t* out;
+};
+constexpr int kPlanes = 3;
+struct PlaneList {
+  PlaneJob job[kPlanes];
+  int count = 0;
+};
+int run_planes(const PlaneList& list, bool bf16, hipStream_t stream);
 
 // Column sums of a matrix in fp32 (bias gradients), with `partial` of
-// column_parts(rows, cols) x round8(cols) floats.
+// column_parts(rows, cols) x round8(cols) floats; the last sum goes on the list.
 int64_t column_parts(int64_t rows, int64_t cols);
-int column_sums(const Mat16& a, bool bf16, float* partial, float* out, hipStream_t stream);
+int column_sums(const Mat16& a, bool bf16, float* partial, float* out, SumList* list,
+                hipStream_t stream);
 
 // dx[m][c] = sum_n dz[m][n] W[c][n] (both readable in pieces, or dz blocked),
 // rounded once, dense. Small products are split over runs of n; `partial` of
-// product_nt_bytes holds the runs' fp32 sums, added in order.
+// product_nt_bytes holds the runs' fp32 sums, whose addition goes on the list.
 int64_t product_nt_bytes(int64_t rows, int64_t k, int64_t cols);
 int product_nt(const Mat16& dz, const Mat16& W, bool bf16, float* partial, uint16_t* out,
-               int64_t cols, hipStream_t stream);
+               int64_t cols, PlaneList* list, hipStream_t stream);
 
 // dW[c][n] = sum_m x[m][c] dz[m][n], rounded once; the rows are split over
-// workgroups, `partial` of product_tn_bytes holds their fp32 sums, added in
-// order. x and dz readable in pieces, one of them may be blocked; out is
+// workgroups, `partial` of product_tn_bytes holds their fp32 sums, whose
+// addition goes on the list. x and dz readable in pieces, one of them may be blocked; out is
 // [cols_x][cols_z] dense, dz's columns in `groups` padded groups.
 int64_t product_tn_bytes(int64_t rows, int64_t cin, int64_t cols);
 int product_tn(const Mat16& x, const Mat16& dz, bool bf16, float* partial, uint16_t* out,
-               int64_t cols_x, int64_t cols_z, int groups, hipStream_t stream);
+               int64_t cols_x, int64_t cols_z, int groups, PlaneList* list, hipStream_t stream);
 
 // Linear layer: act(x W + bias) + residual, with operands readable in pieces,
 // or x blocked.

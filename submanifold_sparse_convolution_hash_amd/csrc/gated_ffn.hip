@@ -274,21 +274,25 @@ int ffn_backward(const Ffn& f, const uint16_t* pre, const FfnGrads& g, Arena& ws
   uint16_t* h = hidden ? static_cast<uint16_t*>(ws.take(blocked_bytes(f.n, Fq))) : nullptr;
   uint16_t* dz = hidden ? static_cast<uint16_t*>(ws.take(blocked_bytes(f.n, 2 * Fq))) : nullptr;
   float* sums = need_bi ? static_cast<float*>(ws.take(tiles * 2 * Fq * 4)) : nullptr;
-  float* part = static_cast<float*>(ws.take(std::max({need_x ? product_nt_bytes(f.n, 2 * Fq, f.C) : 0,
-                                                      need_wi ? product_tn_bytes(f.n, Cp, 2 * Fq) : 0,
-                                                      need_wo ? product_tn_bytes(f.n, Fq, Op) : 0})));
+  float* part_x = need_x ? static_cast<float*>(ws.take(product_nt_bytes(f.n, 2 * Fq, f.C))) : nullptr;
+  float* part_wi = need_wi ? static_cast<float*>(ws.take(product_tn_bytes(f.n, Cp, 2 * Fq))) : nullptr;
+  float* part_wo = need_wo ? static_cast<float*>(ws.take(product_tn_bytes(f.n, Fq, Op))) : nullptr;
   if (ws.counting) return SUBMCONV_OK;
 
+  PlaneList planes;
+  SumList columns;
   SUBMCONV_TRY(run_packs(packs, stream));
-  if (need_bo) SUBMCONV_TRY(column_sums(f.dy, f.bf16, dy_sums, g.b_out, stream));
-  if (!hidden) return SUBMCONV_OK;
-  const Mat16 hm = blocked16(h, f.n, Fq), zm = blocked16(dz, f.n, 2 * Fq);
-  SUBMCONV_TRY(gate_grad(dy, wo, Fq, pre, f.act, f.bf16, dz, h, sums, stream));
-  if (need_bi) SUBMCONV_TRY(sum_parts(sums, tiles, 2 * Fq, 2 * f.F, 2, g.b_in, stream));
-  if (need_x) SUBMCONV_TRY(product_nt(zm, wi, f.bf16, part, g.x, f.C, stream));
-  if (need_wi) SUBMCONV_TRY(product_tn(x, zm, f.bf16, part, g.W_in, f.C, 2 * f.F, 2, stream));
-  if (need_wo) SUBMCONV_TRY(product_tn(hm, dy, f.bf16, part, g.W_out, f.F, f.Co, 1, stream));
-  return SUBMCONV_OK;
+  if (need_bo) SUBMCONV_TRY(column_sums(f.dy, f.bf16, dy_sums, g.b_out, &columns, stream));
+  if (hidden) {
+    const Mat16 hm = blocked16(h, f.n, Fq), zm = blocked16(dz, f.n, 2 * Fq);
+    SUBMCONV_TRY(gate_grad(dy, wo, Fq, pre, f.act, f.bf16, dz, h, sums, stream));
+    if (need_bi) columns.job[columns.count++] = SumJob{sums, tiles, 2 * Fq, 2 * f.F, 2, g.b_in};
+    if (need_x) SUBMCONV_TRY(product_nt(zm, wi, f.bf16, part_x, g.x, f.C, &planes, stream));
+    if (need_wi) SUBMCONV_TRY(product_tn(x, zm, f.bf16, part_wi, g.W_in, f.C, 2 * f.F, 2, &planes, stream));
+    if (need_wo) SUBMCONV_TRY(product_tn(hm, dy, f.bf16, part_wo, g.W_out, f.F, f.Co, 1, &planes, stream));
+  }
+  SUBMCONV_TRY(run_planes(planes, f.bf16, stream));
+  return run_sums(columns, stream);
 }
 
 int ffn_shape(int64_t n, int32_t cin, int32_t hidden, int32_t cout) {

@@ -381,9 +381,12 @@ extern "C" int submconv_layer_norm_backward(const void* grad_out, int64_t ldg, c
   else
     SUBMCONV_TRY(norm_backward<float>(grad_out, lg, x, lx, n, cdim, mean, rstd, weight, grad_x,
                                       partial, &parts, stream));
+  SumList sums;
   if (grad_weight && grad_bias)
-    return sum_parts(partial, parts, 2 * cdim, 2 * cdim, 1, grad_weight, stream, cdim, grad_bias);
-  if (grad_weight) SUBMCONV_TRY(sum_parts(partial, parts, 2 * cdim, cdim, 1, grad_weight, stream));
-  if (grad_bias) SUBMCONV_TRY(sum_parts(partial + cdim, parts, 2 * cdim, cdim, 1, grad_bias, stream));
-  return SUBMCONV_OK;
+    sums.job[sums.count++] = SumJob{partial, parts, 2 * cdim, 2 * cdim, 1, grad_weight, cdim, grad_bias};
+  else if (grad_weight)
+    sums.job[sums.count++] = SumJob{partial, parts, 2 * cdim, cdim, 1, grad_weight};
+  else if (grad_bias)
+    sums.job[sums.count++] = SumJob{partial + cdim, parts, 2 * cdim, cdim, 1, grad_bias};
+  return run_sums(sums, stream);
 }

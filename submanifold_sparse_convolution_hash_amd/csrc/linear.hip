@@ -170,10 +170,13 @@ __global__ __launch_bounds__(kSumThreads) void k_act_grad(const uint16_t* dy, in
 
 // out[c] = sum of partial[0 .. parts)[c]: 16 columns a workgroup, thread (q, c)
 // adds the parts q, q + 64, ... in order, then the 64 sums are added pairwise
-__global__ __launch_bounds__(1024) void k_sum_parts(const float* __restrict__ partial, int64_t parts,
-                                                    int64_t ld, int64_t cols, int groups,
-                                                    float* __restrict__ out, int64_t split,
-                                                    float* __restrict__ out2) {
+struct Sums {
+  SumJob job[kSums];
+};
+__global__ __launch_bounds__(1024) void k_sum_parts(Sums list) {
+  const SumJob& a = list.job[blockIdx.y];
+  const float* __restrict__ partial = a.partial;
+  const int64_t parts = a.parts, ld = a.ld, cols = a.cols, groups = a.groups;
   __shared__ float sums[64][17];
   const int cl = threadIdx.x & 15, q = threadIdx.x >> 4;
   const int64_t c = static_cast<int64_t>(blockIdx.x) * 16 + cl;
@@ -192,8 +195,8 @@ __global__ __launch_bounds__(1024) void k_sum_parts(const float* __restrict__ pa
     __syncthreads();
   }
   if (q != 0 || c >= cols) return;
-  if (c < split) out[c] = sums[0][cl];
-  else out2[c - split] = sums[0][cl];
+  if (c < a.split) a.out[c] = sums[0][cl];
+  else a.out2[c - a.split] = sums[0][cl];
 }
 
 int act_grad(const Mat16& dy, const uint16_t* z, int act, bool bf16, uint16_t* dz, float* partial,
@@ -268,11 +271,16 @@ __global__ __launch_bounds__(512, 2) void k_product_part(Operand A, Operand B, i
 
 // out = the partial sums of the runs added in order, rounded once; columns of
 // `groups` padded groups are closed up
+struct Planes {
+  PlaneJob job[kPlanes];
+};
 template <bool BF16>
-__global__ __launch_bounds__(256) void k_weight_sum(const float* __restrict__ partial, int64_t runs,
-                                                    int64_t plane, int64_t ldp, int64_t rows,
-                                                    int64_t cols, int groups,
-                                                    uint16_t* __restrict__ out) {
+__global__ __launch_bounds__(256) void k_weight_sum(Planes list) {
+  const PlaneJob& a = list.job[blockIdx.y];
+  const float* __restrict__ partial = a.partial;
+  uint16_t* __restrict__ out = a.out;
+  const int64_t runs = a.runs, plane = a.plane, ldp = a.ldp, rows = a.rows, cols = a.cols;
+  const int64_t groups = a.groups;
   __shared__ float4v sums[4][64];
   const int cl = threadIdx.x & 63, q = threadIdx.x >> 6;
   const int64_t i = static_cast<int64_t>(blockIdx.x) * 64 + cl;  // float4 of a plane
@@ -330,17 +338,6 @@ int64_t split_k(int64_t M, int64_t K, int64_t N) {
   return div_up(steps, per);
 }
 
-int sum_planes(const float* partial, int64_t runs, int64_t plane, int64_t ldp, int64_t rows,
-               int64_t cols, int groups, bool bf16, uint16_t* out, hipStream_t stream) {
-  const dim3 grid(static_cast<unsigned>(div_up(plane, 256)));
-  if (bf16)
-    k_weight_sum<true><<<grid, 256, 0, stream>>>(partial, runs, plane, ldp, rows, cols, groups, out);
-  else
-    k_weight_sum<false><<<grid, 256, 0, stream>>>(partial, runs, plane, ldp, rows, cols, groups, out);
-  SUBMCONV_HIP_CHECK(hipGetLastError());
-  return SUBMCONV_OK;
-}
-
 }  // namespace
 
 bool pieces_fit(const Mat16& a) { return aligned16(a.p) && a.ld % 8 == 0 && a.cols % 8 == 0; }
@@ -361,10 +358,31 @@ int run_packs(const PackList& list, hipStream_t stream) {
   return SUBMCONV_OK;
 }
 
-int sum_parts(const float* partial, int64_t parts, int64_t ld, int64_t cols, int groups, float* out,
-              hipStream_t stream, int64_t split, float* out2) {
-  k_sum_parts<<<static_cast<unsigned>(div_up(cols, 16)), 1024, 0, stream>>>(partial, parts, ld, cols,
-                                                                            groups, out, split, out2);
+int run_sums(const SumList& list, hipStream_t stream) {
+  int64_t most = 0;
+  Sums sums{};
+  for (int q = 0; q < list.count; ++q) {
+    sums.job[q] = list.job[q];
+    most = std::max(most, list.job[q].cols);
+  }
+  if (most == 0) return SUBMCONV_OK;
+  const dim3 grid(static_cast<unsigned>(div_up(most, 16)), static_cast<unsigned>(list.count));
+  k_sum_parts<<<grid, 1024, 0, stream>>>(sums);
+  SUBMCONV_HIP_CHECK(hipGetLastError());
+  return SUBMCONV_OK;
+}
+
+int run_planes(const PlaneList& list, bool bf16, hipStream_t stream) {
+  int64_t most = 0;
+  Planes planes{};
+  for (int q = 0; q < list.count; ++q) {
+    planes.job[q] = list.job[q];
+    most = std::max(most, list.job[q].plane);
+  }
+  if (most == 0) return SUBMCONV_OK;
+  const dim3 grid(static_cast<unsigned>(div_up(most, 256)), static_cast<unsigned>(list.count));
+  if (bf16) k_weight_sum<true><<<grid, 256, 0, stream>>>(planes);
+  else k_weight_sum<false><<<grid, 256, 0, stream>>>(planes);
   SUBMCONV_HIP_CHECK(hipGetLastError());
   return SUBMCONV_OK;
 }
@@ -374,10 +392,10 @@ int64_t column_parts(int64_t rows, int64_t cols) {
   return std::max<int64_t>(1, std::min(div_up(1024, strips), div_up(rows, 4 * kSumRows)));
 }
 
-int column_sums(const Mat16& a, bool bf16, float* partial, float* out, hipStream_t stream) {
-  const int st = act_grad(a, nullptr, kActNone, bf16, nullptr, partial, stream);
-  if (st != SUBMCONV_OK) return st;
-  return sum_parts(partial, column_parts(a.rows, a.cols), round8(a.cols), a.cols, 1, out, stream);
+int column_sums(const Mat16& a, bool bf16, float* partial, float* out, SumList* list,
+                hipStream_t stream) {
+  list->job[list->count++] = SumJob{partial, column_parts(a.rows, a.cols), round8(a.cols), a.cols, 1, out};
+  return act_grad(a, nullptr, kActNone, bf16, nullptr, partial, stream);
 }
 
 int linear_forward(const Mat16& x, const Mat16& W, const float* bias, int act, bool bf16,
@@ -396,7 +414,7 @@ int64_t product_nt_bytes(int64_t rows, int64_t k, int64_t cols) {
 }
 
 int product_nt(const Mat16& dz, const Mat16& W, bool bf16, float* partial, uint16_t* out,
-               int64_t cols, hipStream_t stream) {
+               int64_t cols, PlaneList* list, hipStream_t stream) {
   const int64_t runs = split_k(dz.rows, dz.cols, cols);
   if (runs > 1) {
     const int64_t mt = div_up(dz.rows, 128), nt = div_up(cols, 128), cp = round8(cols);
@@ -411,7 +429,8 @@ int product_nt(const Mat16& dz, const Mat16& W, bool bf16, float* partial, uint1
     else if (dz.blocked) go(std::false_type{}, std::true_type{});
     else go(std::false_type{}, std::false_type{});
     SUBMCONV_HIP_CHECK(hipGetLastError());
-    return sum_planes(partial, runs, dz.rows * cp, cp, dz.rows, cols, 1, bf16, out, stream);
+    list->job[list->count++] = PlaneJob{partial, runs, dz.rows * cp, cp, dz.rows, cols, 1, out};
+    return SUBMCONV_OK;
   }
   const LinearEpi e{nullptr, nullptr, 0, out, cols, nullptr, kActNone,
                     false, cols % 8 == 0 && aligned16(out), false};
@@ -423,7 +442,7 @@ int64_t product_tn_bytes(int64_t rows, int64_t cin, int64_t cols) {
 }
 
 int product_tn(const Mat16& x, const Mat16& dz, bool bf16, float* partial, uint16_t* out,
-               int64_t cols_x, int64_t cols_z, int groups, hipStream_t stream) {
+               int64_t cols_x, int64_t cols_z, int groups, PlaneList* list, hipStream_t stream) {
   const int64_t run = grad_run(x.rows, x.cols, dz.cols);
   const int64_t runs = std::max<int64_t>(1, div_up(x.rows, run));
   const int64_t tile = grad_tile(x.rows, x.cols, dz.cols);
@@ -447,7 +466,8 @@ int product_tn(const Mat16& x, const Mat16& dz, bool bf16, float* partial, uint1
   else if (dz.blocked) launch(std::false_type{}, std::true_type{});
   else launch(std::false_type{}, std::false_type{});
   SUBMCONV_HIP_CHECK(hipGetLastError());
-  return sum_planes(partial, runs, x.cols * dz.cols, dz.cols, cols_x, cols_z, groups, bf16, out, stream);
+  list->job[list->count++] = PlaneJob{partial, runs, x.cols * dz.cols, dz.cols, cols_x, cols_z, groups, out};
+  return SUBMCONV_OK;
 }
 
 Mat16 readable(const Mat16& a, int groups, int unit, Arena& ws, PackList* list) {
@@ -524,16 +544,18 @@ int linear_grad(const Mat16& dy, const Mat16& x, const Mat16& W, const uint16_t*
   if (need.w) xr = readable(x, 1, 8, ws, &packs);
   const int64_t parts = column_parts(dy.rows, dy.cols);
   float* sums = need.b ? static_cast<float*>(ws.take(parts * cp * 4)) : nullptr;
-  const int64_t part_bytes = std::max(need.x ? product_nt_bytes(dz.rows, dz.cols, x.cols) : 0,
-                                      need.w ? product_tn_bytes(x.rows, round8(x.cols), dz.cols) : 0);
-  float* part = static_cast<float*>(ws.take(part_bytes));
+  float* part_x = need.x ? static_cast<float*>(ws.take(product_nt_bytes(dz.rows, dz.cols, x.cols))) : nullptr;
+  float* part_w = need.w ? static_cast<float*>(ws.take(product_tn_bytes(x.rows, round8(x.cols), dz.cols))) : nullptr;
   if (!run) return SUBMCONV_OK;
+  PlaneList planes;
+  SumList columns;
   SUBMCONV_TRY(run_packs(packs, stream));
   if (own_dz || need.b) SUBMCONV_TRY(act_grad(dy, pre, act, bf16, dz_to, sums, stream));
-  if (need.b) SUBMCONV_TRY(sum_parts(sums, parts, cp, dy.cols, 1, gb, stream));
-  if (need.x) SUBMCONV_TRY(product_nt(dz, Wr, bf16, part, gx, x.cols, stream));
-  if (need.w) SUBMCONV_TRY(product_tn(xr, dz, bf16, part, gw, x.cols, dy.cols, 1, stream));
-  return SUBMCONV_OK;
+  if (need.x) SUBMCONV_TRY(product_nt(dz, Wr, bf16, part_x, gx, x.cols, &planes, stream));
+  if (need.w) SUBMCONV_TRY(product_tn(xr, dz, bf16, part_w, gw, x.cols, dy.cols, 1, &planes, stream));
+  SUBMCONV_TRY(run_planes(planes, bf16, stream));
+  if (need.b) columns.job[columns.count++] = SumJob{sums, parts, cp, dy.cols, 1, gb};
+  return run_sums(columns, stream);
 }
 
 }  // namespace
