@@ -15,6 +15,7 @@ import functools
 from typing import Optional, Tuple
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _DTYPES, _check, load_library
 
@@ -150,7 +151,8 @@ def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
     if return_stats:
         mean = x.new_empty((n,), dtype=torch.float32)
         rstd = x.new_empty((n,), dtype=torch.float32)
-    _call(dev, "submconv_layer_norm", _ptr(x), ld, n, c, _ptr(weight), _ptr(bias), eps, _ptr(y), _ptr(mean), _ptr(rstd), _NORM_DTYPES[x.dtype])
+    _call(dev, "submconv_layer_norm", _ptr(x), ld, n, c, _ptr(weight), _ptr(bias), eps, _ptr(y), _ptr(mean),
+          _ptr(rstd), _NORM_DTYPES[x.dtype])
     return (y, mean, rstd) if return_stats else y
 
 
@@ -171,7 +173,8 @@ def layer_norm_backward(grad_out: torch.Tensor, x: torch.Tensor, mean: torch.Ten
     ws, nb = None, 0
     if needs[1] or needs[2]:
         ws, nb = _workspace("submconv_layer_norm_backward_workspace_bytes", x, n, c)
-    _call(dev, "submconv_layer_norm_backward", _ptr(grad_out), ldg, _ptr(x), ldx, n, c, _ptr(mean), _ptr(rstd), _ptr(weight), _ptr(gx), _ptr(gw), _ptr(gb), _NORM_DTYPES[x.dtype], _ptr(ws), nb)
+    _call(dev, "submconv_layer_norm_backward", _ptr(grad_out), ldg, _ptr(x), ldx, n, c, _ptr(mean),
+          _ptr(rstd), _ptr(weight), _ptr(gx), _ptr(gw), _ptr(gb), _NORM_DTYPES[x.dtype], _ptr(ws), nb)
     return gx, gw, gb
 
 
@@ -198,7 +201,8 @@ def linear(x: torch.Tensor, W: torch.Tensor, bias: Optional[torch.Tensor] = None
     out = x.new_empty((n, cout))
     pre = x.new_empty((n, cout)) if return_pre else None
     ws, nb = _workspace("submconv_linear_workspace_bytes", x, n, cin, cout, _aligned((x, ldx), (W, cout)))
-    _call(dev, "submconv_linear", _ptr(x), ldx, n, _ptr(W), _ptr(bias), _ptr(residual), ldr, _ptr(out), _ptr(pre), cin, cout, a, _DTYPES[x.dtype], _ptr(ws), nb)
+    _call(dev, "submconv_linear", _ptr(x), ldx, n, _ptr(W), _ptr(bias), _ptr(residual), ldr, _ptr(out),
+          _ptr(pre), cin, cout, a, _DTYPES[x.dtype], _ptr(ws), nb)
     return (out, pre) if return_pre else out
 
 
@@ -223,7 +227,8 @@ def linear_backward(grad_out: torch.Tensor, x: torch.Tensor, W: torch.Tensor, pr
     gb = x.new_empty((cout,), dtype=torch.float32) if needs[2] else None
     ws, nb = _workspace("submconv_linear_backward_workspace_bytes", x, n, cin, cout, a,
                         _aligned((x, ldx), (W, cout), (grad_out, ldg)))
-    _call(dev, "submconv_linear_backward", _ptr(grad_out), ldg, n, _ptr(x), ldx, _ptr(W), _ptr(pre) if a else None, _ptr(gx), _ptr(gw), _ptr(gb), cin, cout, a, _DTYPES[x.dtype], _ptr(ws), nb)
+    _call(dev, "submconv_linear_backward", _ptr(grad_out), ldg, n, _ptr(x), ldx, _ptr(W), _ptr(pre) if a else
+          None, _ptr(gx), _ptr(gw), _ptr(gb), cin, cout, a, _DTYPES[x.dtype], _ptr(ws), nb)
     return gx, gw, gb
 
 
@@ -261,7 +266,8 @@ def gated_ffn(x: torch.Tensor, W_in: torch.Tensor, b_in: Optional[torch.Tensor],
     pre = x.new_empty((n, 2 * hidden)) if return_pre else None
     ws, nb = _workspace("submconv_gated_ffn_workspace_bytes", x, n, cin, hidden, cout,
                         _aligned((x, ldx), (W_in, 2 * hidden), (W_out, cout)))
-    _call(dev, "submconv_gated_ffn", _ptr(x), ldx, n, _ptr(W_in), _ptr(b_in), _ptr(W_out), _ptr(b_out), _ptr(residual), ldr, _ptr(out), _ptr(pre), cin, hidden, cout, a, _DTYPES[x.dtype], _ptr(ws), nb)
+    _call(dev, "submconv_gated_ffn", _ptr(x), ldx, n, _ptr(W_in), _ptr(b_in), _ptr(W_out), _ptr(b_out),
+          _ptr(residual), ldr, _ptr(out), _ptr(pre), cin, hidden, cout, a, _DTYPES[x.dtype], _ptr(ws), nb)
     return (out, pre) if return_pre else out
 
 
@@ -283,7 +289,9 @@ def gated_ffn_backward(grad_out: torch.Tensor, x: torch.Tensor, W_in: torch.Tens
     g = [x.new_empty(s, dtype=d) if need else None for (s, d), need in zip(shapes, needs)]
     ws, nb = _workspace("submconv_gated_ffn_backward_workspace_bytes", x, n, cin, hidden, cout,
                         _aligned((x, ldx), (W_in, 2 * hidden), (W_out, cout), (grad_out, ldg)))
-    _call(dev, "submconv_gated_ffn_backward", _ptr(grad_out), ldg, n, _ptr(x), ldx, _ptr(W_in), _ptr(W_out), _ptr(pre), _ptr(g[0]), _ptr(g[1]), _ptr(g[2]), _ptr(g[3]), _ptr(g[4]), cin, hidden, cout, a, _DTYPES[x.dtype], _ptr(ws), nb)
+    _call(dev, "submconv_gated_ffn_backward", _ptr(grad_out), ldg, n, _ptr(x), ldx, _ptr(W_in), _ptr(W_out),
+          _ptr(pre), _ptr(g[0]), _ptr(g[1]), _ptr(g[2]), _ptr(g[3]), _ptr(g[4]), cin, hidden, cout, a,
+          _DTYPES[x.dtype], _ptr(ws), nb)
     return tuple(g)
 
 
@@ -302,6 +310,7 @@ class LayerNormFunction(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, grad_out):
         x, weight, mean, rstd = ctx.saved_tensors
         gx, gw, gb = layer_norm_backward(grad_out.contiguous(), x, mean, rstd, weight, ctx.needs_input_grad[:3])
@@ -324,6 +333,7 @@ class LinearFunction(torch.autograd.Function):
         return out
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, grad_out):
         x, W, pre = ctx.saved_tensors
         g = grad_out.contiguous()
@@ -342,6 +352,7 @@ class GatedFeedForwardFunction(torch.autograd.Function):
         return out
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, grad_out):
         x, W_in, W_out, pre = ctx.saved_tensors
         g = grad_out.contiguous()
