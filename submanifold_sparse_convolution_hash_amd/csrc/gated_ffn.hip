@@ -23,6 +23,9 @@ namespace submconv {
 namespace {
 
 // ---- forward: h = act(x W_g + b_g) (x W_u + b_u) ----
+//
+// Bound by its per-tile work at few channels (209715 x 128 / 512 fp16 155 us: a
+// tile of 128 rows has two steps of k, then exp and reciprocal of 64 columns).
 
 struct GateEpi {
   const float* bias;  // [2F] or null
@@ -88,6 +91,9 @@ __global__ __launch_bounds__(WM* WN * 64, tile_waves(BM, BN, STAGES)) void k_gat
 }
 
 // ---- gradient: dh = dout W_out^T; dg, du, h in its epilogue ----
+//
+// Memory-bound: 209715 x 256 / 1024 bf16 reads pre and dout once and writes dg,
+// du and h, 2.3 GB in 450-470 us (5.0 TB/s).
 
 struct GateGradEpi {
   const uint16_t* pre;  // [M][2F]

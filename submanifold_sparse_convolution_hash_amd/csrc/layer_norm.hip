@@ -86,6 +86,7 @@ __device__ __forceinline__ float row_sum(float x, float* slot) {
   return x;
 }
 
+// 209715 x 128 fp16 19 us (107 MB), 1 x 1024 2.4 us.
 // Lane l of a row's G holds V pieces of VEC columns, piece i at column
 // (i G + l) VEC.
 template <typename T, int VEC, int G, int V>
@@ -146,7 +147,9 @@ __global__ __launch_bounds__(kNormThreads) void k_layer_norm(
   }
 }
 
-// PARAMS: also this workgroup's sums of dy xh and dy, [2][C] of partial.
+// dx, and where partial is not null this workgroup's sums of dy xh and dy,
+// [2][C] of it. 209715 x 128 bf16 28 us (161 MB), 20011 x 515 fp32 24 us
+// (124 MB): a copy's rate.
 template <typename T, int VEC, int G, int V>
 __global__ __launch_bounds__(kNormThreads) void k_layer_norm_grad(
     const T* __restrict__ dy, int64_t ldg, const T* __restrict__ x, int64_t ldx, int64_t n, int C,

@@ -247,6 +247,66 @@ def test_wide_tiles(dev):
 
 
 @gpu
+def test_offsets_past_32_bits(dev):
+    """17 million sites: pre-activations, dz and norm rows of more than 2^31
+    elements. Rows at both ends and around element 2^31 against the oracle on
+    those rows alone; a NaN tail row would show reads past the end."""
+    sc = _sc()
+    n, c, f = 17_000_000, 16, 64
+    g = torch.Generator(device=dev).manual_seed(1)
+    half = torch.float16
+    x = torch.randn((n, c), generator=g, device=dev).to(half)
+    Wi = (torch.randn((c, 2 * f), generator=g, device=dev) * c ** -0.5).to(half)
+    Wo = (torch.randn((f, c), generator=g, device=dev) * f ** -0.5).to(half)
+    edge = 2 ** 31 // (2 * f)
+    at = torch.tensor([0, 1, edge - 1, edge, edge + 1, n - 129, n - 2, n - 1], device=dev)
+    u, tiny = U[half], TINY[half]
+    out, pre = sc.gated_ffn(x, Wi, None, Wo, act="silu", return_pre=True)
+    xn, wi, wo = _np(x[at]), _np(Wi), _np(Wo)
+    ro, rz, h = od.gated_ffn(xn, wi, None, wo, None, "silu", None)
+    ez = (c + 4) * V * (np.abs(xn) @ np.abs(wi))
+    _check(pre[at], rz, ez + u * np.abs(rz) + tiny, "pre")
+    eh = (1.2 * ez[:, :f] + 32 * V * (1 + np.abs(rz[:, :f]))) * (np.abs(rz[:, f:]) + ez[:, f:]) \
+        + np.abs(rz[:, :f]) * ez[:, f:] + (4 * V + u) * np.abs(h) + tiny
+    _check(out[at], ro, eh @ np.abs(wo) + (f + 4) * V * (np.abs(h) @ np.abs(wo)) + u * np.abs(ro) + tiny, "out")
+    gx, _, _, gwo, gb = sc.gated_ffn_backward(out, x, Wi, Wo, pre, act="silu")
+    dyn, zn = _np(out[at]), _np(pre[at])
+    rx, _, _, _, _, dz, _ = od.gated_ffn_backward(dyn, xn, wi, wo, zn, "silu")
+    adh = np.abs(dyn) @ np.abs(wo).T
+    a, d = od.act(zn[:, :f], "silu")
+    eact = 32 * V * (1 + np.abs(zn[:, :f]))
+    edh = (c + 4) * V * adh
+    ed = np.concatenate([(edh * np.abs(d) + adh * eact) * np.abs(zn[:, f:]), edh * np.abs(a) + adh * eact], 1)
+    er = ed + (4 * V + u) * np.abs(dz) + tiny
+    _check(gx[at], rx, er @ np.abs(wi).T + (2 * f + 4) * V * (np.abs(dz) @ np.abs(wi).T) + u * np.abs(rx) + tiny, "grad_x")
+    # the weight gradient's sums of 17 million terms, against torch in fp64;
+    # many are past fp16's largest number, which has to give infinities
+    p64, u64 = pre[:, :f].double(), pre[:, f:].double()
+    h64, dy64 = torch.nn.functional.silu(p64) * u64, out.double()
+    ref = h64.t() @ dy64
+    eh = (u + 4 * V) * h64.abs() + 32 * V * (1 + p64.abs()) * u64.abs() + tiny
+    tol = eh.t() @ dy64.abs() + (n / 256 + 260) * V * (h64.abs().t() @ dy64.abs()) + u * ref.abs()
+    del p64, u64, h64, dy64, eh
+    inside, beyond = ref.abs() + tol < 65504, ref.abs() - tol > 65520
+    assert bool((((gwo.double() - ref).abs() <= tol) | ~inside).all())
+    assert bool(((gwo.double() == torch.sign(ref) * float("inf")) | ~beyond).all())
+    # the column sum: n terms in fp32, against torch in fp64
+    ref = out.double().sum(0)
+    tol = (n / 1024 + 2000) * V * out.double().abs().sum(0)  # 1024 runs, then their sums
+    assert bool(((gb.double() - ref).abs() <= tol).all())
+    del gx, gwo, dz
+    y, mean, rstd = sc.layer_norm(pre, return_stats=True)
+    ry, _, rr = od.layer_norm(zn, None, None, 1e-5)
+    _check(y[at], ry, 64 * (2 * f + 8) * V * (1 + np.abs(ry)) + u * np.abs(ry) + tiny, "norm")
+    del y
+    gx, _, _ = sc.layer_norm_backward(pre, pre, mean, rstd)
+    rx, _, _ = od.layer_norm_backward(zn, zn, _np(mean[at]), _np(rstd[at]), None)
+    # d - mean(d) - xh mean(d xh) of d = x cancels to eps: the terms' size counts
+    _check(gx[at], rx, 64 * (2 * f + 8) * V * (1 + np.abs(zn)) * rr[:, None] ** 2 * (1 + np.abs(zn)) ** 2 + u * np.abs(rx) + tiny,
+           "norm grad")
+
+
+@gpu
 @pytest.mark.parametrize("act", od.ACTS)
 def test_linear_every_activation(dev, act):
     """Every activation's value and slope over pre-activations from -30 to 30
