@@ -5,22 +5,23 @@
 //
 // At these widths the hidden rows are the traffic: at 209715 x 128 / 512 they
 // are 215 MB written and read between two kernels, four times x and out. Here
-// they never leave the registers. A wave owns 32 rows: their x is read once
-// into MFMA operands, their out stays in accumulators, and the hidden channels
-// pass by in chunks of 32. A chunk's columns of W_in and rows of W_out go
+// they never leave the registers. A wave owns 32 rows (16 where
+// there are few): their x is read once into MFMA operands, their out stays in
+// accumulators, and the hidden channels pass by in chunks of 32. A chunk's columns of W_in and rows of W_out go
 // through LDS, shared by the workgroup's waves; the chunk's g and u accumulate
 // on b_in, and h, rounded to 16 bits, is at once the operand of the second
 // product: an accumulator holds 4 consecutive hidden channels of one row per
 // lane, two of them the 8 values of k of one operand, and W_out is read from
 // LDS in that same order of k.
 //
-// 209715 x 128 / 512 with silu and a residual: 126 us, 650 TFLOP/s (two kernels:
-// 207 us). The matrix units are busy 27 % and the vector units, with exp and
-// reciprocal at a quarter of their rate, 35 % of the time; two waves a SIMD
+// 209715 x 128 / 512 with silu and a residual: 126-131 us, 640 TFLOP/s (two
+// kernels: 207 us). The matrix units are busy 27 % and the vector units, with exp
+// and reciprocal at a quarter of their rate, 35 % of the time; two waves a SIMD
 // (the registers allow no more) overlap them only in part, and the last of 3.2
-// rounds of workgroups is mostly empty. Chunks of 64, one or two buffers,
-// eight waves, and reads or activations interleaved by hand measured the same
-// or slower (126 to 144 us).
+// rounds of workgroups is mostly empty (given to a launch of its own with half
+// the rows a wave, it cost as much again: 131 -> 135 us on new rows). Chunks of
+// 64, one buffer, eight waves, and reads or activations interleaved by hand
+// measured the same or slower (126 to 144 us).
 #include <algorithm>
 
 #include "dense_common.h"
@@ -32,7 +33,6 @@ namespace {
 
 constexpr int kHidden = 32;      // hidden channels of a chunk
 constexpr int kWaves = 4;        // of a workgroup; two workgroups fit a compute unit
-constexpr int kWaveRows = 32;
 constexpr int kFusedHidden = 2048;  // most hidden channels (their biases sit in LDS)
 
 // A chunk's k rows of W_out, OC columns: the transposed reads take k rows 4 g ..
@@ -73,11 +73,11 @@ struct LoadOut {
 
 // x [M][<= KC], W_in [C][2 F] as a pair operand, W_out [F][<= OC], out as in
 // LinearEpi.
-template <bool BF16, int KC, int OC>
+template <bool BF16, int KC, int OC, int FM>
 __global__ __launch_bounds__(kWaves * 64, 2) void k_gated_ffn(Operand X, Operand Wi, Operand Wo,
                                                           int64_t half, const float* __restrict__ b_in,
                                                           int64_t F, int64_t cout, int act, LinearEpi e) {
-  constexpr int NT = kWaves * 64, FM = kWaveRows / 16, KS = KC / 32, OB = OC / 16;
+  constexpr int NT = kWaves * 64, kWaveRows = 16 * FM, KS = KC / 32, OB = OC / 16;
   using LI = LoadKRow<2 * kHidden, NT, true, false>;
   using LO = LoadOut<OC, NT>;
   using T = Tile<BF16, false, true, true, 128, 2 * kHidden, 1, 1, 2>;  // its operand reads
@@ -208,10 +208,10 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_gated_ffn(Operand X, Operand
 }  // namespace
 
 // At 64 channels the two kernels are never faster (64 / 256: 1000 rows 11.2 us
-// against 11.0 here, 20000 rows 16.4 against 11.9, 209715 rows 87.7 against
-// 44.1). At 128 a workgroup walks the hidden channels longer than a few rows'
-// tiles take (128 / 512: 3000 rows 14.6 us against 23.2 here, 20000 rows 27.6
-// against 24.8, 209715 rows 207 against 127).
+// against 8.8 here, 20000 rows 16.4 against 10.4, 209715 rows 87.7 against 43).
+// At 128 a workgroup walks the hidden channels longer than a few rows' tiles
+// take (128 / 512: 3000 rows 14.6 us against 23.2 here, 20000 rows 27.6 against
+// 22.2, 209715 rows 207 against 127).
 bool fused_ffn_takes(int64_t rows, int64_t cin, int64_t hidden, int64_t cout) {
   if (hidden > kFusedHidden) return false;
   return (cin <= 64 && cout <= 64) || (cin <= 128 && cout <= 128 && rows >= 16384);
@@ -220,23 +220,29 @@ bool fused_ffn_takes(int64_t rows, int64_t cin, int64_t hidden, int64_t cout) {
 int fused_ffn(const Mat16& x, const Mat16& W_in, int64_t F, const float* b_in, const Mat16& W_out,
               const float* b_out, int act, bool bf16, const uint16_t* residual, int64_t ldr,
               uint16_t* out, int64_t cout, hipStream_t stream) {
-  const LinearEpi e{b_out, residual, ldr, out, cout, nullptr, kActNone,
-                    cout % 8 == 0 && ldr % 8 == 0 && aligned16(residual),
-                    cout % 8 == 0 && aligned16(out), false};
   const int64_t half = W_in.cols / 2;
   const Operand X{x.p, x.ld, x.rows, x.cols}, Wi{W_in.p, W_in.ld, half, W_in.rows};
   const Operand Wo{W_out.p, W_out.ld, W_out.cols, W_out.rows};
-  const dim3 grid(static_cast<unsigned>(div_up(x.rows, kWaves * kWaveRows)));
-  auto go = [&](auto kc, auto oc) {
+  const LinearEpi e{b_out, residual, ldr, out, cout, nullptr, kActNone,
+                    cout % 8 == 0 && ldr % 8 == 0 && aligned16(residual),
+                    cout % 8 == 0 && aligned16(out), false};
+  auto go = [&](auto width, auto fm) {
+    const dim3 grid(static_cast<unsigned>(div_up(x.rows, kWaves * 16 * fm)));
     if (bf16)
-      k_gated_ffn<true, kc, oc><<<grid, kWaves * 64, 0, stream>>>(X, Wi, Wo, half, b_in, F, cout, act, e);
+      k_gated_ffn<true, width, width, fm><<<grid, kWaves * 64, 0, stream>>>(X, Wi, Wo, half, b_in, F, cout, act, e);
     else
-      k_gated_ffn<false, kc, oc><<<grid, kWaves * 64, 0, stream>>>(X, Wi, Wo, half, b_in, F, cout, act, e);
+      k_gated_ffn<false, width, width, fm><<<grid, kWaves * 64, 0, stream>>>(X, Wi, Wo, half, b_in, F, cout, act, e);
   };
-  using C64 = std::integral_constant<int, 64>;
-  using C128 = std::integral_constant<int, 128>;
-  if (x.cols <= 64 && cout <= 64) go(C64{}, C64{});
-  else go(C128{}, C128{});
+  auto by_rows = [&](auto width) {
+    // 16 rows a wave where those fill at most every place once (two workgroups
+    // a compute unit), else 32, which read the weights half as often. 32 against
+    // 16: 128 / 512, 20000 rows 27.1 us against 22.2, 30000 rows 27.6 against 24.5;
+    // 64 / 256, 1000 rows 11.2 against 8.8, 20000 rows 11.9 against 10.4.
+    if (x.rows <= 512 * kWaves * 16) go(width, std::integral_constant<int, 1>{});
+    else go(width, std::integral_constant<int, 2>{});
+  };
+  if (x.cols <= 64 && cout <= 64) by_rows(std::integral_constant<int, 64>{});
+  else by_rows(std::integral_constant<int, 128>{});
   SUBMCONV_HIP_CHECK(hipGetLastError());
   return SUBMCONV_OK;
 }

@@ -438,6 +438,35 @@ def test_gated_ffn(dev, shape, dtype):
 
 
 @gpu
+def test_gated_ffn_full_and_partial_rounds(dev):
+    """The one-kernel block over a whole round of workgroups (65536 rows) and a
+    part of the next, short and long: rows around the seam and at both ends
+    against the oracle, the rows past it against the call on those alone, which
+    gives a wave half as many rows (two roundings of h and one of out apart at
+    most: 4 u of the largest)."""
+    sc = _sc()
+    for n, c, f in ((65536 + 77, 64, 96), (65536 + 40000, 48, 40), (65536, 128, 72)):
+        mk = Maker(dev, n)
+        x, Wi, Wo = mk.rows(n, c, torch.float16, 3), mk.mat(c, 2 * f, torch.float16), mk.mat(f, c, torch.float16)
+        bi, bo = mk.vec(2 * f), mk.vec(c)
+        out = sc.gated_ffn(x, Wi, bi, Wo, bo, act="gelu", residual=x)
+        at = torch.tensor([i for i in (0, 1, 65534, 65535, 65536, 65537, n - 2, n - 1) if i < n], device=dev)
+        xn, wi, wo, b1, b2 = _np(x[at]), _np(Wi), _np(Wo), _np(bi), _np(bo)
+        ro, rz, h = od.gated_ffn(xn, wi, b1, wo, b2, "gelu", xn)
+        u, tiny = U[torch.float16], TINY[torch.float16]
+        ez = (c + 4) * V * (np.abs(xn) @ np.abs(wi) + np.abs(b1))
+        g, up = rz[:, :f], rz[:, f:]
+        eh = (1.2 * ez[:, :f] + 32 * V * (1 + np.abs(g))) * (np.abs(up) + ez[:, f:]) + np.abs(g) * ez[:, f:] \
+            + (4 * V + u) * np.abs(h) + tiny
+        tol = eh @ np.abs(wo) + (f + 4) * V * (np.abs(h) @ np.abs(wo) + np.abs(b2)) + 2 * V * np.abs(xn) \
+            + u * np.abs(ro) + tiny
+        _check(out[at], ro, tol, f"out {n}")
+        tail = sc.gated_ffn(x[65536 - 64:], Wi, bi, Wo, bo, act="gelu", residual=x[65536 - 64:])
+        err = float((out[65536 - 64:].float() - tail.float()).abs().max())
+        assert err <= 4 * u * float(tail.float().abs().max()), (n, err)
+
+
+@gpu
 def test_gated_ffn_leaves_gradients_out(dev):
     sc = _sc()
     mk = Maker(dev, 31)
