@@ -14,7 +14,7 @@
 // lane, two of them the 8 values of k of one operand, and W_out is read from
 // LDS in that same order of k.
 //
-// 209715 x 128 / 512 with silu and a residual: 126-131 us, 640 TFLOP/s (two
+// 209715 x 128 / 512 with silu and a residual: 123-131 us, 650 TFLOP/s (two
 // kernels: 207 us). The matrix units are busy 27 % and the vector units, with exp
 // and reciprocal at a quarter of their rate, 35 % of the time; two waves a SIMD
 // (the registers allow no more) overlap them only in part, and the last of 3.2

@@ -28,7 +28,7 @@ __device__ __forceinline__ void linear_epilogue(const LinearEpi& e, int64_t M, i
   const RowsView res(e.residual, e.ldr, m0, M, N, BM, e.vec_r);
   float b[8];
   load_bias8(e.bias, N, n, b);
-#pragma unroll 2
+#pragma unroll 4
   for (int p = 0; p < R::ROW_PASSES; ++p) {
     const int m = r0 + p * R::ROW_STEP;
     float z[8];
