@@ -28,6 +28,8 @@ __device__ __forceinline__ void linear_epilogue(const LinearEpi& e, int64_t M, i
   const RowsView res(e.residual, e.ldr, m0, M, N, BM, e.vec_r);
   float b[8];
   load_bias8(e.bias, N, n, b);
+  // four rows' loads of the residual in flight (209715 rows of 128 / 512 in the
+  // gated block 130 -> 123 us; linear 128 -> 512 98 -> 95 us)
 #pragma unroll 4
   for (int p = 0; p < R::ROW_PASSES; ++p) {
     const int m = r0 + p * R::ROW_STEP;
