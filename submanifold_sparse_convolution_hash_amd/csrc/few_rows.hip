@@ -6,14 +6,13 @@
 //
 // A workgroup owns a strip of LPR x 8 columns for all rows. Each thread walks
 // every (512 / LPR)-th row of W, 16 bytes at a time, straight from memory into
-// fp32 products with the rows of x (held in LDS as fp32); the threads' sums
-// are joined by lane exchanges, then through LDS, in one fixed order. Strips
-// are narrow (32 bytes, 64 or 128) while the matrix has few columns, so that
-// enough compute units pull on it.
+// fp32 products with the rows of x, read beside it; the threads' sums are joined
+// by lane exchanges, then through LDS, in one fixed order.
 //
-// At 1 x 256 -> 1024 it takes 3.2 us, at 1 x 512 / 2048 (gated) 4.6 + 4.3; the
-// MFMA tile kernels take 7 to 9 us each there: their 128 rows are mostly empty
-// and a workgroup walks all of k in steps of a memory latency each.
+// At 1 x 256 -> 1024 it takes 3.2 us, at 1 x 512 / 2048 (gated) 4.6 + 4.4, or
+// 5.2 + 6.6 with weights that no L2 holds. The MFMA tile kernels' rows are mostly empty and a workgroup walks all of k in
+// steps of a memory latency each: 8 rows here against 9 there take 6.9 and 6.4
+// us at 256 -> 1024, 8.4 and 13.0 at 1024 -> 1024, 17.0 and 39.7 at 4096 -> 1024.
 #include <algorithm>
 
 #include "dense_common.h"
@@ -108,15 +107,31 @@ int launch_few(const X* x, int64_t ldx, int rows, const Mat16& W, int64_t N, con
     k_few<BF16, X, m, lpr, GATED><<<grid, kFewThreads, 0, stream>>>(x, ldx, rows, W.p, W.ld,
                                                                    W.rows, N, e);
   };
-  auto by_rows = [&](auto lpr) {
-    if (rows <= 1) go(std::integral_constant<int, 1>{}, lpr);
-    else if (rows <= 2) go(std::integral_constant<int, 2>{}, lpr);
-    else if (rows <= 4) go(std::integral_constant<int, 4>{}, lpr);
-    else go(std::integral_constant<int, kFewRows>{}, lpr);
-  };
-  if (N <= 2048) by_rows(std::integral_constant<int, 2>{});
-  else if (N <= 8192) by_rows(std::integral_constant<int, 4>{});
-  else by_rows(std::integral_constant<int, 8>{});
+  // Strips of 128 bytes take whole memory lines; more rows hold too many sums a
+  // thread for them until there are strips for every compute unit, and a narrow
+  // matrix has too few strips. With strips of 32 / 64 / 128 bytes, in us:
+  // 1 row of 300 -> 77 5.9 / 6.5 / 7.9, 256 -> 1024 3.4 / 3.4 / 3.2, 1024 -> 4096
+  // 7.6 / 5.5 / 4.8, 4096 -> 8192 43 / 21 / 12; 8 rows of 1024 -> 1024 8.4 / 8.4
+  // / 10.8, 1024 -> 4096 11.2 / 9.3 / 11.1, 512 -> 16384 27 / 15 / 8.7.
+  constexpr std::integral_constant<int, 1> one;
+  constexpr std::integral_constant<int, 2> two;
+  constexpr std::integral_constant<int, 4> four;
+  constexpr std::integral_constant<int, 8> eight;
+  static_assert(kFewRows == 8);
+  if (N <= 256) {
+    if (rows <= 1) go(one, two);
+    else if (rows <= 2) go(two, two);
+    else if (rows <= 4) go(four, two);
+    else go(eight, two);
+  } else if (rows <= 2 || N >= 8192) {
+    if (rows <= 1) go(one, eight);
+    else if (rows <= 2) go(two, eight);
+    else if (rows <= 4) go(four, eight);
+    else go(eight, eight);
+  } else {
+    if (rows <= 4) go(four, four);
+    else go(eight, four);
+  }
   SUBMCONV_HIP_CHECK(hipGetLastError());
   return SUBMCONV_OK;
 }

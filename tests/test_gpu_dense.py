@@ -214,6 +214,23 @@ def test_linear(dev, shape, dtype):
 
 
 @gpu
+@pytest.mark.parametrize("rows", [1, 2, 3, 5, 8])
+@pytest.mark.parametrize("cout", [255, 257, 1030, 8191, 8193])
+def test_linear_few_rows(dev, rows, cout):
+    """Every width of strip for every count of rows, with a k that no strip's
+    threads divide and rows of W that start anywhere."""
+    sc = _sc()
+    cin = 131
+    mk = Maker(dev, rows * 7 + cout)
+    for dtype in (torch.float16, torch.bfloat16):
+        x, W, bias = mk.rows(rows, cin, dtype, 3), mk.mat(cin, cout, dtype), mk.vec(cout)
+        out = sc.linear(x, W, bias, act="silu")
+        xn, Wn, bn = _np(x), _np(W), _np(bias)
+        ro, rz = od.linear(xn, Wn, bn, "silu", None)
+        _check(out, ro, _linear_tol(xn, Wn, bn, rz, ro, U[dtype], TINY[dtype])[0], "out")
+
+
+@gpu
 def test_wide_tiles(dev):
     """Products large enough for the 256 x 256 tile, in both orders of the weight,
     of plain and of blocked rows, against torch in fp64 on some rows of the
