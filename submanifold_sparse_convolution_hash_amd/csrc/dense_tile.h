@@ -167,7 +167,6 @@ __device__ __forceinline__ void load_bias8(const float* p, int64_t n_end, uint32
 
 enum Act : int { kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3, kActGeluTanh = 4 };
 
-constexpr float kSqrtHalf = 0.70710678118654752f;
 constexpr float kInvSqrt2Pi = 0.39894228040143268f;
 constexpr float kTwoSqrt2OverPi = 1.5957691216057308f;  // 2 sqrt(2 / pi)
 
@@ -178,11 +177,31 @@ __device__ __forceinline__ float logistic(float z) {
 __device__ __forceinline__ float tanh_arg(float z) {
   return kTwoSqrt2OverPi * (z + 0.044715f * z * z * z);
 }
+// gelu = z Phi(z). Phi(-a) = erfc(a / sqrt 2) / 2 = exp(-a^2 / 2) s P(s), s = 1 /
+// (1 + 0.305 a), a >= 0: P is a least-squares polynomial, reweighted towards its
+// largest relative error, 1.1e-7 for a up to 15; with the roundings Phi is within
+// 2^-22 for z > 0 and, relative to itself, 1.3e-6 down to z = -6 and 4.1e-6 down to
+// -13 (the exponent's own rounding). 1 + erf loses all digits by z = -5.5, which
+// bf16 results show. `e`: exp(-z^2 / 2), which the slope needs as well. 209715 x
+// 128 -> 512 with pre-activations takes 118 us (with the library's erff 137, erfcf 172).
+__device__ __forceinline__ float normal_cdf(float z, float e) {
+  const float s = __builtin_amdgcn_rcpf(1.0f + 0.305f * fabsf(z));
+  float p = 0.0364274792f;
+  p = p * s - 0.151897117f;
+  p = p * s + 0.183906615f;
+  p = p * s - 0.036374446f;
+  p = p * s + 0.120207421f;
+  p = p * s + 0.103657544f;
+  p = p * s + 0.122430496f;
+  p = p * s + 0.121642001f;
+  const float q = p * s * e;
+  return z < 0.0f ? q : 1.0f - q;
+}
 template <int ACT>
 __device__ __forceinline__ float act_value(float z) {
   if constexpr (ACT == kActRelu) return z < 0.0f ? 0.0f : z;  // a NaN stays one
   else if constexpr (ACT == kActSilu) return z * logistic(z);
-  else if constexpr (ACT == kActGelu) return 0.5f * z * (1.0f + erff(z * kSqrtHalf));
+  else if constexpr (ACT == kActGelu) return z * normal_cdf(z, __expf(-0.5f * z * z));
   else if constexpr (ACT == kActGeluTanh) return z * logistic(tanh_arg(z));
   else return z;
 }
@@ -197,9 +216,9 @@ __device__ __forceinline__ void act_both(float z, float& a, float& d) {
     a = z * p;
     d = p + a * (1.0f - p);
   } else if constexpr (ACT == kActGelu) {
-    const float c = 0.5f * (1.0f + erff(z * kSqrtHalf));
+    const float e = __expf(-0.5f * z * z), c = normal_cdf(z, e);
     a = z * c;
-    d = c + z * kInvSqrt2Pi * __expf(-0.5f * z * z);
+    d = c + z * kInvSqrt2Pi * e;
   } else if constexpr (ACT == kActGeluTanh) {
     const float p = logistic(tanh_arg(z));
     a = z * p;

@@ -1,0 +1,71 @@
+"""Values of the dense layers where fp32 formulas lose digits or range: the
+negative tail of the erf form of gelu, in bf16 which can hold it."""
+import numpy as np
+import pytest
+import torch
+from scipy.special import ndtr
+
+gpu = pytest.mark.gpu
+V = 2.0 ** -24
+UB = 2.0 ** -8  # unit roundoff of bf16
+
+
+def _sc():
+    import submanifold_sparse_convolution_hash_amd as sc
+    sc.load_library()
+    return sc
+
+
+@pytest.fixture(scope="module")
+def dev():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    return torch.device("cuda:0")
+
+
+def _np(t):
+    return t.detach().float().cpu().numpy().astype(np.float64)
+
+
+def _eye(c, dev):
+    return torch.eye(c, dtype=torch.bfloat16, device=dev)
+
+
+def _check(got, ref, tol, what):
+    err = np.abs(_np(got) - ref)
+    assert (err <= tol).all(), (what, float(np.nanmax(err / tol)), int((~(err <= tol)).sum()))
+
+
+@gpu
+@pytest.mark.parametrize("n", [8, 200])
+def test_gelu_tail(dev, n):
+    """gelu = z Phi(z) and its slope Phi(z) + z phi(z) for z from 0 to -12, to a
+    bf16's own rounding. An identity weight hands z on exactly. Phi is half of
+    erfc(-z / sqrt 2), whose argument is off by 2 v: (z^2 + 1) 2 v of its value, next
+    to erfc's own 16 ulps (32 v) and three products; phi is exp of an argument off
+    by 1.5 v z^2 and a few ulps more."""
+    sc = _sc()
+    c = 32
+    x = torch.linspace(-12, 0, n * c).reshape(n, c).to(torch.bfloat16).to(dev)
+    z = _np(x)
+    big, pdf = ndtr(z), np.exp(-0.5 * z * z) / np.sqrt(2 * np.pi)
+    rel = V * (2 * z * z + 40)
+    value, slope = z * big, big + z * pdf
+    tol_v = (rel + UB) * np.abs(value) + 1e-38
+    tol_s = rel * (big + np.abs(z) * pdf) + UB * np.abs(slope) + 1e-38
+    eye = _eye(c, dev)
+    _check(sc.linear(x, eye, act="gelu"), value, tol_v, "linear")
+    # the gated block with u = 1 on its gate's side
+    Wi = torch.cat([eye, torch.zeros_like(eye)], 1).contiguous()
+    bi = torch.cat([torch.zeros(c), torch.ones(c)]).to(dev)
+    _check(sc.gated_ffn(x, Wi, bi, eye, act="gelu"), value, tol_v, "gated")
+    out, pre = sc.gated_ffn(x, Wi, bi, eye, act="gelu", return_pre=True)
+    _check(out, value, tol_v, "gated with pre")
+    one = torch.ones_like(x)
+    _check(sc.linear_backward(one, x, eye, x, act="gelu")[0], slope, tol_s, "slope")
+    _check(sc.gated_ffn_backward(one, x, Wi, eye, pre, act="gelu")[0], slope, tol_s, "gated slope")
+    # h, formed again from pre, against one row of ones at a time
+    dy = torch.zeros((n, c), dtype=torch.bfloat16, device=dev)
+    dy[n // 2] = 1
+    gw = sc.gated_ffn_backward(dy, x, Wi, eye, pre, act="gelu")[3]
+    _check(gw, np.repeat(value[n // 2][:, None], c, 1), np.repeat(tol_v[n // 2][:, None], c, 1), "h of the gradient")
