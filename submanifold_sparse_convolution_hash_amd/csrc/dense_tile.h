@@ -222,7 +222,8 @@ __device__ __forceinline__ void act_both(float z, float& a, float& d) {
   } else if constexpr (ACT == kActGeluTanh) {
     const float p = logistic(tanh_arg(z));
     a = z * p;
-    d = p + a * (1.0f - p) * kTwoSqrt2OverPi * (1.0f + 0.134145f * z * z);
+    // (p is 0 or 1 long before z^2 reaches the bound, and z^2 infinite would make 0 inf of it)
+    d = p + a * (1.0f - p) * kTwoSqrt2OverPi * (1.0f + 0.134145f * fminf(z * z, 1e30f));
   } else {
     a = z;
     d = 1.0f;

@@ -1,5 +1,6 @@
 """Values of the dense layers where fp32 formulas lose digits or range: the
-negative tail of the erf form of gelu, in bf16 which can hold it."""
+negative tail of the erf form of gelu, in bf16 which can hold it, and bf16's
+largest numbers."""
 import numpy as np
 import pytest
 import torch
@@ -69,3 +70,24 @@ def test_gelu_tail(dev, n):
     dy[n // 2] = 1
     gw = sc.gated_ffn_backward(dy, x, Wi, eye, pre, act="gelu")[3]
     _check(gw, np.repeat(value[n // 2][:, None], c, 1), np.repeat(tol_v[n // 2][:, None], c, 1), "h of the gradient")
+
+
+@gpu
+@pytest.mark.parametrize("act", ["none", "relu", "silu", "gelu", "gelu_tanh"])
+@pytest.mark.parametrize("n", [8, 64])
+def test_activations_of_huge_values(dev, n, act):
+    """Up to bf16's largest numbers the value is z or 0 and the slope 1 or 0."""
+    sc = _sc()
+    c = 16
+    big = torch.tensor([1e9, 1e13, 2e19, 1e25, 1e30, 3e38])
+    x = torch.cat([big, -big]).repeat(n * c // 12 + 1)[:n * c].reshape(n, c).to(torch.bfloat16).to(dev)
+    eye = _eye(c, dev)
+    ref, on = (x, torch.ones_like(x)) if act == "none" else (x.clamp(min=0), (x > 0).to(x.dtype))
+    assert torch.equal(sc.linear(x, eye, act=act), ref)
+    one = torch.ones_like(x)
+    gx, _, gb = sc.linear_backward(one, x, eye, x, act=act)
+    assert torch.equal(gx, on)
+    assert torch.equal(gb, on.float().sum(0))
+    pre = torch.cat([x, one], 1).contiguous()
+    Wi = torch.cat([eye, torch.zeros_like(eye)], 1).contiguous()
+    assert torch.equal(sc.gated_ffn_backward(one, x, Wi, eye, pre, act=act)[0], on)
