@@ -28,6 +28,7 @@ __all__ = [
 #: names of the activations, as SUBMCONV_ACT_*
 ACTIVATIONS = {"none": 0, None: 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 _NORM_DTYPES = {**_DTYPES, torch.float32: 2}
+_INT32_MAX = 2 ** 31 - 1  # widths cross the C ABI as int32, which would cut larger ones
 
 
 def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
@@ -67,6 +68,8 @@ def _rows(t, name: str, dtypes, cols: Optional[int] = None, like=None) -> int:
     if t.dim() != 2:
         raise ValueError(f"{name} must have 2 dims, got {tuple(t.shape)}")
     n, c = t.shape
+    if c > _INT32_MAX:
+        raise ValueError(f"{name} has {c} columns")
     if cols is not None and c != cols:
         raise ValueError(f"{name} must have {cols} columns, got {tuple(t.shape)}")
     if like is not None:
@@ -106,6 +109,8 @@ def _matrix(t, name: str, x) -> Tuple[int, int]:
     if t.dim() != 2:
         raise ValueError(f"{name} must have 2 dims, got {tuple(t.shape)}")
     shape = tuple(t.shape)
+    if max(shape) > _INT32_MAX:
+        raise ValueError(f"{name} is {shape}")
     _dense(t, name, x.dtype, shape, x.device)
     return shape
 

@@ -1,6 +1,6 @@
 """Values of the dense layers where fp32 formulas lose digits or range: the
-negative tail of the erf form of gelu, in bf16 which can hold it, and bf16's
-largest numbers."""
+negative tail of the erf form of gelu, in bf16 which can hold it, bf16's
+largest numbers, and widths that 32 bits do not hold."""
 import numpy as np
 import pytest
 import torch
@@ -91,3 +91,20 @@ def test_activations_of_huge_values(dev, n, act):
     pre = torch.cat([x, one], 1).contiguous()
     Wi = torch.cat([eye, torch.zeros_like(eye)], 1).contiguous()
     assert torch.equal(sc.gated_ffn_backward(one, x, Wi, eye, pre, act=act)[0], on)
+
+
+@gpu
+def test_more_columns_than_32_bits_are_refused(dev):
+    """Sizes past 2^31 do not reach the library cut to 32 bits."""
+    sc = _sc()
+    many = 2 ** 32 + 8
+    h = dict(dtype=torch.float16, device=dev)
+    wide, tall = torch.empty((1, many), **h), torch.empty((many, 1), **h)
+    one = torch.zeros((1, 1), **h)
+    stat = torch.zeros(1, device=dev)
+    for call in (lambda: sc.layer_norm(wide), lambda: sc.layer_norm_backward(wide, wide, stat, stat),
+                 lambda: sc.linear(wide, tall), lambda: sc.linear(one, wide),
+                 lambda: sc.linear_backward(wide, one, wide),
+                 lambda: sc.gated_ffn(one, torch.empty((1, 2 * many), **h), None, tall)):
+        with pytest.raises(ValueError):
+            call()
