@@ -35,7 +35,12 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
 
-_current_stream = torch._C._cuda_getCurrentRawStream  # torch.cuda.current_stream(i).cuda_stream
+try:
+    from torch._C import _cuda_getCurrentRawStream as _current_stream
+except ImportError:  # a torch without it: the same through the public object
+
+    def _current_stream(index: int) -> int:
+        return torch.cuda.current_stream(index).cuda_stream
 
 
 def _call(device: torch.device, name: str, *args) -> None:
