@@ -370,6 +370,12 @@ class GatedFeedForwardFunction(torch.autograd.Function):
         return (*grads, g if ctx.needs_input_grad[5] else None, None)
 
 
+def _recorded(*tensors: Optional[torch.Tensor]) -> bool:
+    """Whether autograd will ask for a gradient of any of them: only then do the
+    modules take the functions that keep what the backward pass reads."""
+    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
+
+
 class LayerNorm(torch.nn.Module):
     """Layer norm over ``channels`` with fp32 weight and bias."""
 
@@ -380,7 +386,7 @@ class LayerNorm(torch.nn.Module):
         self.bias = torch.nn.Parameter(torch.zeros(channels, device=device))
 
     def forward(self, x: torch.Tensor) -> torch.Tensor:
-        if torch.is_grad_enabled():
+        if _recorded(x, self.weight, self.bias):
             return LayerNormFunction.apply(x, self.weight, self.bias, self.eps)
         return layer_norm(x, self.weight, self.bias, self.eps)
 
@@ -402,7 +408,7 @@ class Linear(torch.nn.Module):
         self.bias = torch.nn.Parameter(torch.zeros(cout, device=device)) if bias else None
 
     def forward(self, x: torch.Tensor, residual: Optional[torch.Tensor] = None) -> torch.Tensor:
-        if torch.is_grad_enabled():
+        if _recorded(x, self.weight, self.bias, residual):
             return LinearFunction.apply(x, self.weight, self.bias, residual, self.act)
         return linear(x, self.weight, self.bias, self.act, residual)
 
@@ -421,6 +427,6 @@ class GatedFeedForward(torch.nn.Module):
         self.b_out = torch.nn.Parameter(torch.zeros(channels, device=device)) if bias else None
 
     def forward(self, x: torch.Tensor, residual: Optional[torch.Tensor] = None) -> torch.Tensor:
-        if torch.is_grad_enabled():
+        if _recorded(x, self.w_in, self.b_in, self.w_out, self.b_out, residual):
             return GatedFeedForwardFunction.apply(x, self.w_in, self.b_in, self.w_out, self.b_out, residual, self.act)
         return gated_ffn(x, self.w_in, self.b_in, self.w_out, self.b_out, self.act, residual)

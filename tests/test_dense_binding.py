@@ -3,6 +3,9 @@ import os
 import subprocess
 import sys
 
+import pytest
+import torch
+
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
@@ -14,3 +17,30 @@ def test_package_imports_on_a_torch_without_gpu_support():
             "assert callable(sc.linear)\n")
     r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
     assert r.returncode == 0, r.stderr
+
+
+@pytest.mark.parametrize("kind", ["LayerNorm", "Linear", "GatedFeedForward"])
+def test_modules_record_only_where_something_requires_a_gradient(kind, monkeypatch):
+    """A frozen module keeps nothing for a backward pass that cannot come (the
+    gated block would write its pre-activations and take slower kernels)."""
+    from submanifold_sparse_convolution_hash_amd import dense
+
+    name = {"LayerNorm": "layer_norm", "Linear": "linear", "GatedFeedForward": "gated_ffn"}[kind]
+    monkeypatch.setattr(dense, name, lambda *a: "plain")
+    monkeypatch.setattr(getattr(dense, kind + "Function"), "apply", lambda *a: "recorded")
+    sizes = {"LayerNorm": (8,), "Linear": (8, 4), "GatedFeedForward": (8, 4)}[kind]
+    m = getattr(dense, kind)(*sizes)
+    x = torch.zeros(2, 8, dtype=torch.float16)
+    assert m(x) == "recorded"
+    with torch.no_grad():
+        assert m(x) == "plain"
+    m.requires_grad_(False)
+    assert m(x) == "plain"
+    for p in m.parameters():  # any one of them is enough
+        p.requires_grad_(True)
+        assert m(x) == "recorded"
+        p.requires_grad_(False)
+    y = x.clone().requires_grad_()
+    assert m(y) == "recorded"
+    if kind != "LayerNorm":
+        assert m(x, x) == "plain" and m(x, y) == "recorded"
