@@ -602,9 +602,13 @@ int submconv_linear_backward(const uint16_t* grad_out, int64_t ldg, int64_t n, c
                              int32_t act, int32_t dtype, void* workspace, int64_t workspace_bytes,
                              hipStream_t stream);
 
-/* Workspace of submconv_gated_ffn (the hidden rows h among it). */
+/* Workspace of submconv_gated_ffn with pre (the hidden rows h among it), and
+ * without: layers of up to 128 channels may then keep h in registers, and up to
+ * all of the workspace falls away. The first is enough for either call. */
 int64_t submconv_gated_ffn_workspace_bytes(int64_t n, int32_t cin, int32_t hidden, int32_t cout,
                                            int32_t aligned);
+int64_t submconv_gated_ffn_inference_workspace_bytes(int64_t n, int32_t cin, int32_t hidden,
+                                                     int32_t cout, int32_t aligned);
 
 /*
  * submconv_gated_ffn -- [g | u] = x W_in + b_in, h = act(g) u, out = h W_out +

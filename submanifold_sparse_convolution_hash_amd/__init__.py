@@ -111,6 +111,7 @@ def load_library():
         "submconv_linear_backward": ([P, I64, I64, P, I64, P, P, P, P, P, I32, I32, I32, I32, P, I64, P],
                                      ctypes.c_int),
         "submconv_gated_ffn_workspace_bytes": ([I64, I32, I32, I32, I32], I64),
+        "submconv_gated_ffn_inference_workspace_bytes": ([I64, I32, I32, I32, I32], I64),
         "submconv_gated_ffn": ([P, I64, I64, P, P, P, P, P, I64, P, P, I32, I32, I32, I32, I32, P, I64, P],
                                ctypes.c_int),
         "submconv_gated_ffn_backward_workspace_bytes": ([I64, I32, I32, I32, I32], I64),

@@ -231,8 +231,10 @@ struct Ffn {
   bool bf16;
 };
 
-int ffn_forward(const Ffn& f, const float* b_in, const float* b_out, const uint16_t* residual,
-                int64_t ldr, uint16_t* out, uint16_t* pre, Arena& ws, hipStream_t stream) {
+// `keeps`: pre is asked for (it may be null while the arena counts).
+int ffn_forward(const Ffn& f, bool keeps, const float* b_in, const float* b_out,
+                const uint16_t* residual, int64_t ldr, uint16_t* out, uint16_t* pre, Arena& ws,
+                hipStream_t stream) {
   if (f.n <= kFewRows) {
     float* h = static_cast<float*>(ws.take(f.n * f.F * 4));
     if (ws.counting || f.n == 0) return SUBMCONV_OK;
@@ -243,13 +245,13 @@ int ffn_forward(const Ffn& f, const float* b_in, const float* b_out, const uint1
   PackList packs;
   const Mat16 x = readable(f.x, 1, 8, ws, &packs), wi = readable(f.W_in, 2, 8, ws, &packs);
   const Mat16 wo = readable(f.W_out, 1, 8, ws, &packs);
-  // (a query does not know whether pre is asked for: it counts h)
-  if (!ws.counting && !pre && fused_ffn_takes(f.n, f.C, f.F, f.Co)) {
+  if (!keeps && fused_ffn_takes(f.n, f.C, f.F, f.Co)) {
+    if (ws.counting) return SUBMCONV_OK;
     SUBMCONV_TRY(run_packs(packs, stream));
     return fused_ffn(x, wi, f.F, b_in, wo, b_out, f.act, f.bf16, residual, ldr, out, f.Co, stream);
   }
   uint16_t* h = static_cast<uint16_t*>(ws.take(blocked_bytes(f.n, Fq)));
-  if (ws.counting || f.n == 0) return SUBMCONV_OK;
+  if (ws.counting) return SUBMCONV_OK;
   SUBMCONV_TRY(run_packs(packs, stream));
   SUBMCONV_TRY(gate_forward(x, wi, f.F, b_in, f.act, f.bf16, h, pre, stream));
   return linear_forward(blocked16(h, f.n, Fq), wo, b_out, kActNone, f.bf16, residual, ldr, out, f.Co,
@@ -308,6 +310,16 @@ int ffn_shape(int64_t n, int32_t cin, int32_t hidden, int32_t cout) {
   return check_shape("out", n, cout);
 }
 
+int64_t ffn_workspace(int64_t n, int32_t cin, int32_t hidden, int32_t cout, int32_t aligned, bool keeps) {
+  clear_error();
+  SUBMCONV_TRY(ffn_shape(n, cin, hidden, cout));
+  const Ffn f{n, cin, hidden, cout, shape_of(n, cin, aligned), shape_of(cin, 2 * hidden, aligned),
+              shape_of(hidden, cout, aligned), {}, kActSilu, false};
+  Arena ws;
+  SUBMCONV_TRY(ffn_forward(f, keeps, nullptr, nullptr, nullptr, 0, nullptr, nullptr, ws, nullptr));
+  return ws.used;
+}
+
 }  // namespace
 }  // namespace submconv
 
@@ -315,13 +327,13 @@ using namespace submconv;
 
 extern "C" int64_t submconv_gated_ffn_workspace_bytes(int64_t n, int32_t cin, int32_t hidden,
                                                       int32_t cout, int32_t aligned) {
-  clear_error();
-  SUBMCONV_TRY(ffn_shape(n, cin, hidden, cout));
-  const Ffn f{n, cin, hidden, cout, shape_of(n, cin, aligned), shape_of(cin, 2 * hidden, aligned),
-              shape_of(hidden, cout, aligned), {}, kActSilu, false};
-  Arena ws;
-  SUBMCONV_TRY(ffn_forward(f, nullptr, nullptr, nullptr, 0, nullptr, nullptr, ws, nullptr));
-  return ws.used;
+  return ffn_workspace(n, cin, hidden, cout, aligned, true);
+}
+
+extern "C" int64_t submconv_gated_ffn_inference_workspace_bytes(int64_t n, int32_t cin,
+                                                                int32_t hidden, int32_t cout,
+                                                                int32_t aligned) {
+  return ffn_workspace(n, cin, hidden, cout, aligned, false);
 }
 
 extern "C" int submconv_gated_ffn(const uint16_t* x, int64_t ldx, int64_t n, const uint16_t* W_in,
@@ -344,10 +356,10 @@ extern "C" int submconv_gated_ffn(const uint16_t* x, int64_t ldx, int64_t n, con
               Mat16{W_out, hidden, cout, cout}, {}, act, dtype == SUBMCONV_DTYPE_BF16};
   const int64_t lr = n == 1 ? round8(cout) : ldr;
   Arena count;
-  SUBMCONV_TRY(ffn_forward(f, b_in, b_out, residual, lr, out, pre, count, stream));
+  SUBMCONV_TRY(ffn_forward(f, pre != nullptr, b_in, b_out, residual, lr, out, pre, count, stream));
   SUBMCONV_TRY(check_workspace(workspace, workspace_bytes, count.used));
   Arena ws{false, static_cast<char*>(workspace)};
-  return ffn_forward(f, b_in, b_out, residual, lr, out, pre, ws, stream);
+  return ffn_forward(f, pre != nullptr, b_in, b_out, residual, lr, out, pre, ws, stream);
 }
 
 extern "C" int64_t submconv_gated_ffn_backward_workspace_bytes(int64_t n, int32_t cin,

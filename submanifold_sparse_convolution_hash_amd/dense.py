@@ -274,7 +274,8 @@ def gated_ffn(x: torch.Tensor, W_in: torch.Tensor, b_in: Optional[torch.Tensor],
     ldr = _rows(residual, "residual", (x.dtype,), cout, x) if residual is not None else 0
     out = x.new_empty((n, cout))
     pre = x.new_empty((n, 2 * hidden)) if return_pre else None
-    ws, nb = _workspace("submconv_gated_ffn_workspace_bytes", x, n, cin, hidden, cout,
+    query = "submconv_gated_ffn_workspace_bytes" if return_pre else "submconv_gated_ffn_inference_workspace_bytes"
+    ws, nb = _workspace(query, x, n, cin, hidden, cout,
                         _aligned((x, ldx), (W_in, 2 * hidden), (W_out, cout)))
     _call(dev, "submconv_gated_ffn", _ptr(x), ldx, n, _ptr(W_in), _ptr(b_in), _ptr(W_out), _ptr(b_out),
           _ptr(residual), ldr, _ptr(out), _ptr(pre), cin, hidden, cout, a, _DTYPES[x.dtype], _ptr(ws), nb)

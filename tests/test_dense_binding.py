@@ -44,3 +44,25 @@ def test_modules_record_only_where_something_requires_a_gradient(kind, monkeypat
     assert m(y) == "recorded"
     if kind != "LayerNorm":
         assert m(x, x) == "plain" and m(x, y) == "recorded"
+
+
+def test_workspace_of_the_gated_block():
+    """Where the hidden rows stay in registers no workspace is asked for them;
+    the query for calls with pre covers both."""
+    import submanifold_sparse_convolution_hash_amd as sc
+
+    lib = sc.load_library()
+    keep, alone = lib.submconv_gated_ffn_workspace_bytes, lib.submconv_gated_ffn_inference_workspace_bytes
+    assert keep(209715, 128, 512, 128, 1) >= 209715 * 512 * 2
+    assert alone(209715, 128, 512, 128, 1) == 0
+    assert alone(20000, 64, 256, 64, 1) == 0
+    # odd widths still go through padded copies, of x (104 columns) among others
+    assert 209715 * 104 * 2 <= alone(209715, 100, 267, 100, 0) < 209715 * 112 * 2
+    for n in (0, 1, 8, 9, 1000, 20000, 100000):
+        for cin, hidden, cout in ((64, 256, 64), (128, 512, 128), (129, 512, 128), (256, 1024, 256), (33, 2049, 20)):
+            for aligned in (0, 1):
+                a, k = alone(n, cin, hidden, cout, aligned), keep(n, cin, hidden, cout, aligned)
+                assert 0 <= a <= k
+                if max(cin, cout) > 128 or hidden > 2048:
+                    assert a == k
+    assert alone(-1, 8, 16, 8, 0) == -1 and alone(9, 8, 0, 8, 0) == -4
