@@ -207,14 +207,22 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_gated_ffn(Operand X, Operand
 
 }  // namespace
 
-// At 64 channels the two kernels are never faster (64 / 256: 1000 rows 11.2 us
-// against 8.8 here, 20000 rows 16.4 against 10.4, 209715 rows 87.7 against 43).
-// At 128 a workgroup walks the hidden channels longer than a few rows' tiles
-// take (128 / 512: 3000 rows 14.6 us against 23.2 here, 20000 rows 27.6 against
-// 22.2, 209715 rows 207 against 127).
+// A workgroup walks all hidden channels, 32 at a time, whatever the rows: 0.5 us a
+// chunk at 64 channels, 0.65 at 128, against 0.3 for the two kernels, which start
+// from one launch more and spread the hidden channels until they run out of
+// units. So the one kernel is taken for short walks, and for any from as many rows
+// as fill the units; without those the two are even near hidden 850 and 450. One
+// kernel against two, fp16, us:
+//   64 channels, hidden 64 / 512 / 1024 / 2048: 256 rows 4.5 / 11.2 / 19.1 / 34 against 9.3 / 13.5 /
+//   18.3 / 28, 4000 rows 4.6 / 11.4 / 19.1 / 34.3 against 9.5 / 14.1 / 20.3 / 34.5, 33000 rows 7.2 /
+//   20 / 35 / 65 against 12.4 / 37 / 60 / 106;
+//   128 channels, hidden 64 / 256 / 512 / 2048: 256 rows 5.5 / 9.4 / 14.8 / 46 against 10.0 / 12.0 /
+//   14.1 / 28, 8000 rows 5.8 / 9.9 / 15.2 / 47.1 against 10.4 / 12.8 / 17.1 / 47.6, 33000 rows 10 / 18 /
+//   29 / 95 against 13 / 25 / 43 / 129.
 bool fused_ffn_takes(int64_t rows, int64_t cin, int64_t hidden, int64_t cout) {
-  if (hidden > kFusedHidden) return false;
-  return (cin <= 64 && cout <= 64) || (cin <= 128 && cout <= 128 && rows >= 16384);
+  const int64_t most = std::max(cin, cout);
+  if (hidden > kFusedHidden || most > 128) return false;
+  return most <= 64 ? hidden <= 768 || rows >= 4096 : hidden <= 384 || rows >= 8192;
 }
 
 int fused_ffn(const Mat16& x, const Mat16& W_in, int64_t F, const float* b_in, const Mat16& W_out,

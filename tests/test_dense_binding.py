@@ -66,3 +66,19 @@ def test_workspace_of_the_gated_block():
                 if max(cin, cout) > 128 or hidden > 2048:
                     assert a == k
     assert alone(-1, 8, 16, 8, 0) == -1 and alone(9, 8, 0, 8, 0) == -4
+
+
+def test_one_kernel_or_two_by_the_length_of_the_walk():
+    """One workgroup walks all hidden channels in the one-kernel block: with many of
+    them and few rows two kernels are faster, with few of them one is (a workspace
+    without hidden rows tells which is taken)."""
+    import submanifold_sparse_convolution_hash_amd as sc
+
+    alone = sc.load_library().submconv_gated_ffn_inference_workspace_bytes
+    one = [(9, 64, 256), (300, 64, 512), (4096, 64, 2048), (300, 128, 64), (300, 128, 256), (8192, 128, 2048),
+           (20000, 128, 512)]
+    two = [(9, 64, 2048), (300, 64, 1024), (1000, 64, 2048), (300, 128, 512), (4000, 128, 1024), (9, 128, 2048)]
+    for n, c, f in one:
+        assert alone(n, c, f, c, 1) == 0, (n, c, f)
+    for n, c, f in two:
+        assert alone(n, c, f, c, 1) >= n * f * 2, (n, c, f)
