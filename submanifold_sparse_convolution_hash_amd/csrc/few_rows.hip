@@ -109,16 +109,20 @@ int launch_few(const X* x, int64_t ldx, int rows, const Mat16& W, int64_t N, con
   };
   // Strips of 128 bytes take whole memory lines; more rows hold too many sums a
   // thread for them until there are strips for every compute unit, and a narrow
-  // matrix has too few strips. With strips of 32 / 64 / 128 bytes, in us:
+  // matrix has too few strips, the more so the longer each one's walk along k is.
+  // With strips of 32 / 64 / 128 bytes, in us:
   // 1 row of 300 -> 77 5.9 / 6.5 / 7.9, 256 -> 1024 3.4 / 3.4 / 3.2, 1024 -> 4096
   // 7.6 / 5.5 / 4.8, 4096 -> 8192 43 / 21 / 12; 8 rows of 1024 -> 1024 8.4 / 8.4
-  // / 10.8, 1024 -> 4096 11.2 / 9.3 / 11.1, 512 -> 16384 27 / 15 / 8.7.
+  // / 10.8, 1024 -> 4096 11.2 / 9.3 / 11.1, 512 -> 16384 27 / 15 / 8.7. Long walks:
+  // 1 row of 4096 -> 320 8.0 / 8.0 / 9.9, 4096 -> 1024 14.9 / 15.9 / 15.8, 8192 -> 512
+  // 25.5 / 29.0 / 28.7, but 2048 -> 2048 9.7 / 9.8 / 9.7, 8192 -> 2048 26.7 / 20.7 /
+  // 20.5; 8 rows of 4096 -> 320 13.3 / 16.4 / 26, 4096 -> 1024 19.0 / 21.5 / 27.7.
   constexpr std::integral_constant<int, 1> one;
   constexpr std::integral_constant<int, 2> two;
   constexpr std::integral_constant<int, 4> four;
   constexpr std::integral_constant<int, 8> eight;
   static_assert(kFewRows == 8);
-  if (N <= 256) {
+  if (N <= 256 || (N <= 1024 && W.rows >= 4 * N)) {
     if (rows <= 1) go(one, two);
     else if (rows <= 2) go(two, two);
     else if (rows <= 4) go(four, two);

@@ -296,3 +296,18 @@ def test_gated_ffn_within_its_workspace(dev, n, cin, F, cout):
     z = x.double() @ Wi.double()
     _same(out[:n], (z[:, :F].clamp(min=0) * z[:, F:]) @ Wo.double(), "out")
     assert bool((out[n] == 7).all()) and bool((ws[nb:] == 9).all())
+
+
+@gpu
+@TYPES
+@pytest.mark.parametrize("n", [1, 2, 3, 5, 8])
+@pytest.mark.parametrize("cin,cout", [(1027, 257), (1028, 257), (4099, 1024), (4095, 1024), (4100, 1025), (8191, 300)])
+def test_linear_few_rows_of_a_long_k(dev, n, cin, cout, dtype):
+    """Either side of the rule that gives long walks along k narrow strips."""
+    sc = _sc()
+    mk = Whole(dev, n * cin)
+    x, W, b, res = mk.rows(n, cin, dtype, 2, 3), mk.mat(cin, cout, dtype, 2), mk.vec(cout, 9), mk.rows(n, cout, dtype, 9, 3)
+    out, pre = sc.linear(x, W, b, act="relu", residual=res, return_pre=True)
+    z = x.double() @ W.double() + b.double()
+    _same(pre, z, "pre")
+    _same(out, z.clamp(min=0) + res.double(), "out")
