@@ -594,7 +594,7 @@ int64_t submconv_linear_backward_workspace_bytes(int64_t n, int32_t cin, int32_t
  * and grad_w = x^T dz [cin,cout] of the data's type, grad_b = sum over rows of
  * dz (fp32 [cout]). Any of them may be NULL. pre [n,cout] as the forward wrote
  * it (not read for SUBMCONV_ACT_NONE). The residual's gradient is grad_out.
- * dz is rounded to the data's type before its two products.
+ * dz is rounded to the data's type before its two products, for any n.
  */
 int submconv_linear_backward(const uint16_t* grad_out, int64_t ldg, int64_t n, const uint16_t* x,
                              int64_t ldx, const uint16_t* W, const uint16_t* pre, uint16_t* grad_x,
@@ -616,7 +616,10 @@ int64_t submconv_gated_ffn_inference_workspace_bytes(int64_t n, int32_t cin, int
  * projection's; b_in [2*hidden] fp32 or NULL; W_out [hidden,cout]; b_out [cout]
  * fp32 or NULL; residual [n,cout] (row stride ldr) or NULL; out [n,cout];
  * pre [n,2*hidden] or NULL: [g | u] rounded to the data's type, for the
- * backward pass. h is rounded to the data's type between the two products.
+ * backward pass. From 9 rows on h is rounded to the data's type between the two
+ * products, as the matrix units' operands are: in fp16 an act(g) u past 65504 is
+ * infinite there. Up to 8 rows, whose products run without matrix units, h stays
+ * fp32 and such a value finite.
  */
 int submconv_gated_ffn(const uint16_t* x, int64_t ldx, int64_t n, const uint16_t* W_in,
                        const float* b_in, const uint16_t* W_out, const float* b_out,
@@ -635,7 +638,7 @@ int64_t submconv_gated_ffn_backward_workspace_bytes(int64_t n, int32_t cin, int3
  * grad_b_in = sums of [dg | du] (fp32 [2*hidden]), grad_b_out = sums of
  * grad_out (fp32 [cout]). Any of them may be NULL. h is formed again from pre
  * [n,2*hidden], as the forward wrote it. dg, du and h are rounded to the
- * data's type before their products.
+ * data's type before their products, for any n.
  */
 int submconv_gated_ffn_backward(const uint16_t* grad_out, int64_t ldg, int64_t n, const uint16_t* x,
                                 int64_t ldx, const uint16_t* W_in, const uint16_t* W_out,

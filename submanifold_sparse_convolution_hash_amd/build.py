@@ -23,8 +23,8 @@ FLAGS = ["--offload-arch=" + ARCH, "-O3", "-std=c++20", "-fPIC", "-Wall",
 # keep MFMA accumulators in VGPRs: most kernels read and write them through
 # LDS every step, which AGPRs would cost extra moves for
 VGPR_FORM = ["-mllvm", "-amdgpu-mfma-vgpr-form"]
-# sources whose MFMA accumulators stay in registers for a whole unit or tile
-# (64 to 128 per lane) are built without it: the accumulators take the AGPRs, the operands
+# sources whose MFMA accumulators stay in registers for a whole unit (64 to 128
+# per lane) are built without it: the accumulators take the AGPRs, the operands
 # the VGPRs
 AGPR_SOURCES = {"staged_wide.hip", "staged_bwd.hip"}
 

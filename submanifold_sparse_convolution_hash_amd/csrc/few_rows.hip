@@ -7,12 +7,16 @@
 // A workgroup owns a strip of LPR x 8 columns for all rows. Each thread walks
 // every (512 / LPR)-th row of W, 16 bytes at a time, straight from memory into
 // fp32 products with the rows of x, read beside it; the threads' sums are joined
-// by lane exchanges, then through LDS, in one fixed order.
+// by lane exchanges, then through LDS, in one fixed order. The gated block's
+// hidden rows pass between its two launches in fp32: nothing here needs them in 16
+// bits, and they are a few KB beside the weights.
 //
 // At 1 x 256 -> 1024 it takes 3.2 us, at 1 x 512 / 2048 (gated) 4.6 + 4.4, or
-// 5.2 + 6.6 with weights that no L2 holds. The MFMA tile kernels' rows are mostly empty and a workgroup walks all of k in
-// steps of a memory latency each: 8 rows here against 9 there take 6.9 and 6.4
-// us at 256 -> 1024, 8.4 and 13.0 at 1024 -> 1024, 17.0 and 39.7 at 4096 -> 1024.
+// 5.2 + 6.6 with weights that no L2 holds. The MFMA tile kernels' rows are mostly
+// empty here and a workgroup walks all of k in steps of a memory latency each: 8 rows here
+// against 9 there take 6.9 and 6.4 us at 256 -> 1024, 8.4 and 13.0 at 1024 -> 1024.
+// At a long k the rows from 9 on pay for it (4096 -> 1024 19 us at 8 rows, 40 at 9):
+// their products have no split over k.
 #include <algorithm>
 
 #include "dense_common.h"

@@ -263,7 +263,9 @@ def gated_ffn(x: torch.Tensor, W_in: torch.Tensor, b_in: Optional[torch.Tensor],
     """``(act(g) * u) W_out + b_out + residual`` with ``[g | u] = x W_in +
     b_in`` in x's dtype (fp16 or bf16): x [N,Cin], W_in [Cin,2*hidden] (gate
     columns first), W_out [hidden,Cout], fp32 biases. ``return_pre``: also
-    ``[g | u]``, which :func:`gated_ffn_backward` takes."""
+    ``[g | u]``, which :func:`gated_ffn_backward` takes. From 9 rows on ``act(g)
+    * u`` is rounded to x's dtype between the products (past 65504 it is infinite
+    in fp16); up to 8 rows it stays fp32."""
     ldx = _rows(x, "x", _DTYPES)
     n = x.shape[0]
     dev = x.device

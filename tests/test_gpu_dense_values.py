@@ -1,6 +1,6 @@
 """Values of the dense layers where fp32 formulas lose digits or range: the
 negative tail of the erf form of gelu, in bf16 which can hold it, bf16's
-largest numbers, and widths that 32 bits do not hold."""
+largest numbers, widths that 32 bits do not hold, and hidden values past fp16."""
 import numpy as np
 import pytest
 import torch
@@ -108,3 +108,22 @@ def test_more_columns_than_32_bits_are_refused(dev):
                  lambda: sc.gated_ffn(one, torch.empty((1, 2 * many), **h), None, tall)):
         with pytest.raises(ValueError):
             call()
+
+
+@gpu
+def test_range_of_the_hidden_rows(dev):
+    """Hidden values of 90000, which fp16 does not hold: up to 8 rows they stay fp32,
+    from 9 rows on they are operands of the data's type, as documented; bf16 holds
+    them (90000 to one rounding) at any count."""
+    sc = _sc()
+    c = 16
+    for dtype, n, ref in ((torch.float16, 8, 90000 / 64), (torch.float16, 9, float("inf")),
+                          (torch.bfloat16, 8, 90000 / 64), (torch.bfloat16, 9, 90000 / 64)):
+        x = torch.full((n, c), 300.0, dtype=dtype, device=dev)
+        eye = torch.eye(c, dtype=dtype, device=dev)
+        Wo = torch.full((c, c), 1 / 1024, dtype=dtype, device=dev)  # 16 equal terms
+        for pre in (False, True):
+            out = sc.gated_ffn(x, torch.cat([eye, eye], 1).contiguous(), None, Wo, act="relu", return_pre=pre)
+            out = (out[0] if pre else out).float()
+            # two roundings at most, of h and of the result
+            assert bool((out == ref).all()) if ref == float("inf") else bool(((out / ref - 1).abs() <= 2.1 * UB).all())
