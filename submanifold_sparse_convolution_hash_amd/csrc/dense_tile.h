@@ -108,15 +108,6 @@ __device__ __forceinline__ u32x4 load_piece(const uint16_t* row, int64_t n, int6
   return r;
 }
 
-// Rows of a tile of at most `most` that start at row m0 of M: none where m0 is
-// past the end (a later phase of a last tile).
-__host__ __device__ constexpr uint32_t rows_left(int64_t M, int64_t m0, int most) {
-  const int64_t left = M - m0;
-  return left <= 0 ? 0u : static_cast<uint32_t>(left < most ? left : most);
-}
-static_assert(rows_left(300, 256, 128) == 44 && rows_left(300, 128, 128) == 128, "rows of a tile");
-static_assert(rows_left(256, 256, 128) == 0 && rows_left(300, 384, 128) == 0, "no rows");
-
 // The rows m0 .. of a 16-bit matrix that an epilogue reads or writes, through
 // a buffer whose bound ends with the matrix: lanes outside it load zeros and
 // store nothing, without a branch. Stores are marked as not to be kept in the
@@ -138,8 +129,9 @@ struct RowsView {
                                       int64_t N, int tile_rows, bool vec_)
       : p(q ? q + m0 * ld_ : nullptr), ld(ld_), ld2(static_cast<uint32_t>(ld_) * 2u),
         n_end(static_cast<uint32_t>(N)), vec(vec_) {
-    rows = q ? rows_left(M, m0, tile_rows) : 0u;
-    r = tile_rsrc(p, rows ? static_cast<uint32_t>((rows - 1) * ld_ + N) * 2u : 0u);
+    const int64_t left = M - m0 < tile_rows ? M - m0 : tile_rows;
+    rows = q && left > 0 ? static_cast<uint32_t>(left) : 0u;
+    r = tile_rsrc(p, rows ? static_cast<uint32_t>((left - 1) * ld_ + N) * 2u : 0u);
   }
   __device__ __forceinline__ u32x4 load(uint32_t m, uint32_t n) const {
     if (vec)
@@ -268,6 +260,17 @@ constexpr int kBlockRows = 128;
 __host__ __device__ inline int64_t blocked_at(int64_t row, int64_t col, int64_t blocks) {
   return ((row / kBlockRows * blocks + col / 64) * kBlockRows + row % kBlockRows) * 64 + col % 64;
 }
+// Rows of a tile of at most `most` that start at row m0 of M: none where m0 is
+// past the end (a later phase of a last tile). RowsView counts by itself: through
+// this its stores compiled to slower code (209715 x 128 -> 512 with
+// pre-activations 95 -> 97, gated 128 / 512 255 -> 279 us).
+__host__ __device__ constexpr uint32_t rows_left(int64_t M, int64_t m0, int most) {
+  const int64_t left = M - m0;
+  return left <= 0 ? 0u : static_cast<uint32_t>(left < most ? left : most);
+}
+static_assert(rows_left(300, 256, 128) == 44 && rows_left(300, 128, 128) == 128, "rows of a tile");
+static_assert(rows_left(256, 256, 128) == 0 && rows_left(300, 384, 128) == 0, "no rows");
+
 // Stores 8 columns at tile row `m`, column n < n_end (a multiple of 64) of the
 // block row that starts at tile row 0.
 struct BlockView {
