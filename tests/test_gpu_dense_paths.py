@@ -82,7 +82,7 @@ def _same(got, ref, what):
 # odd widths, through copies; 66001 x 512 -> 520: the 256 x 256 forward; the
 # others few tiles, dx split over k, narrow weight gradients.
 LINEAR = [(33001, 136, 264, 8), (33001, 136, 264, 0), (40001, 72, 130, 3), (66001, 512, 520, 0), (300, 200, 1030, 0),
-          (9001, 128, 128, 0), (1000, 520, 1000, 5)]
+          (9001, 128, 128, 0), (1000, 520, 1000, 5), (300, 200, 1032, 0)]
 
 
 @gpu
@@ -111,9 +111,10 @@ def test_linear_whole_numbers(dev, shape, act, dtype):
 
 
 # 20011 x 136 / 328 -> 136: two buffers in both gate kernels, dx on blocked rows with
-# three, both weight gradients on 256 x 256 tiles, one with h blocked; the
-# others odd widths, and few tiles.
-GATED = [(20011, 136, 328, 136, 0), (20011, 136, 328, 72, 8), (24001, 100, 267, 131, 3), (1001, 96, 200, 64, 1)]
+# three, both weight gradients on 256 x 256 tiles, one with h blocked; 33001 x 64 /
+# 512 -> 512: the second product on 256 x 256 tiles; the others odd widths, and few
+# tiles.
+GATED = [(20011, 136, 328, 136, 0), (33001, 64, 512, 512, 0), (20011, 136, 328, 72, 8), (24001, 100, 267, 131, 3), (1001, 96, 200, 64, 1)]
 
 
 @gpu
@@ -249,6 +250,25 @@ def test_norm_rows_past_32_bits(dev):
     terms = y.double().abs().sum(0)
     assert bool(((gb.double() - y.double().sum(0)).abs() <= (n / 1024 + 2000) * V * terms).all())
     assert bool(gw.isfinite().all())
+
+
+@gpu
+def test_linear_of_more_rows_than_32_bits_count_pieces_of(dev):
+    """540 million rows of an odd width: a padded copy of more than 2^30 pieces and
+    2^33 elements; rows around element 2^31 and 2^32 of input, copy and result, and
+    both ends."""
+    sc = _sc()
+    n, cin, cout, half = 540_000_000, 9, 8, torch.float16
+    g = torch.Generator(device=dev).manual_seed(3)
+    x = torch.empty((n, cin), dtype=half, device=dev)
+    for part in x.split(1 << 26):
+        part.copy_(torch.randint(-2, 3, part.shape, generator=g, device=dev, dtype=torch.int8))
+    mk = Whole(dev, 4)
+    W, b = mk.mat(cin, cout, half, 2), mk.vec(cout, 9)
+    out = sc.linear(x, W, b)
+    edges = [e // w for e in (2 ** 31, 2 ** 32, 2 ** 33) for w in (9, 16, 8) if e // w < n - 1]
+    at = torch.tensor([0, 1, n - 2, n - 1] + [e + d for e in edges for d in (-1, 0, 1)], device=dev)
+    _same(out[at], x[at].double() @ W.double() + b.double(), "out")
 
 
 @gpu
