@@ -24,8 +24,9 @@ namespace {
 
 // ---- forward: h = act(x W_g + b_g) (x W_u + b_u) ----
 //
-// Bound by its per-tile work at few channels (209715 x 128 / 512 fp16 155 us: a
-// tile of 128 rows has two steps of k, then exp and reciprocal of 64 columns).
+// Bound by its per-tile work at few channels (209715 x 128 / 512 fp16 155 us
+// without pre, 177-207 with it, which writes 644 MB: a tile of 128 rows has two
+// steps of k, then exp and reciprocal of 64 columns).
 
 struct GateEpi {
   const float* bias;  // [2F] or null

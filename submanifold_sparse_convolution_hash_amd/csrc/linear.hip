@@ -64,10 +64,10 @@ int launch_linear(const Operand& A, const Operand& B, int64_t K, int64_t N, bool
 // as 128 x 128, but is alone on its compute unit, where nothing covers its
 // epilogue or its wait for memory. It is taken where a product has many
 // products per element moved (K N / (K + N)) and enough tiles for every unit.
-// Measured, 128 against 256: 209715 x 2048 -> 256 (228) 284 against 287 us,
-// 65536 x 1024 -> 1024 (512) 154 against 140, 8192^3 1229 against 920;
-// 209715 x 1024 -> 256 (205) 150 against 156, 100003 x 1024 -> 256 67.5 against
-// 72, 209715 x 512 -> 128 (102) 51 against 80.
+// Measured alone, repeated on the same operands, 128 against 256: 209715 x 2048 ->
+// 256 (228) 284 against 287 us, 65536 x 1024 -> 1024 (512) 154 against 140, 8192^3
+// 1229 against 920; 209715 x 1024 -> 256 (205) 150 against 156, 100003 x 1024 -> 256
+// 67.5 against 72, 209715 x 512 -> 128 (102) 51 against 80.
 bool wide_tile(int64_t M, int64_t K, int64_t N) {
   return N >= 256 && K * N / (K + N) >= 240 && div_up(M, 256) * div_up(N, 256) >= 256;
 }
