@@ -121,6 +121,9 @@ int launch_few(const X* x, int64_t ldx, int rows, const Mat16& W, int64_t N, con
   // 1 row of 4096 -> 320 8.0 / 8.0 / 9.9, 4096 -> 1024 14.9 / 15.9 / 15.8, 8192 -> 512
   // 25.5 / 29.0 / 28.7, but 2048 -> 2048 9.7 / 9.8 / 9.7, 8192 -> 2048 26.7 / 20.7 /
   // 20.5; 8 rows of 4096 -> 320 13.3 / 16.4 / 26, 4096 -> 1024 19.0 / 21.5 / 27.7.
+  // (The gated block's second product, one row, both launches, narrow against not: 512
+  // / 4096 22.0 against 24.7, 1024 / 4096 26.3 against 29.0; with all weights in L2 512 /
+  // 2048 7.9 against 9.7, but 1024 / 4096 18.4 against 14.5.)
   constexpr std::integral_constant<int, 1> one;
   constexpr std::integral_constant<int, 2> two;
   constexpr std::integral_constant<int, 4> four;
