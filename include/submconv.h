@@ -648,6 +648,136 @@ int submconv_gated_ffn_backward(const uint16_t* grad_out, int64_t ldg, int64_t n
                                 int32_t dtype, void* workspace, int64_t workspace_bytes,
                                 hipStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Operators on the rows of items packed one after the other: group norm with
+ * an activation, rotary positions, attention among the rows of an item.
+ *
+ * `offsets` [items + 1] int32 on the device, ascending from 0: item b has the
+ * rows offsets[b] .. offsets[b + 1] - 1 (none is fine). NULL, for items = 1
+ * only: one item of all n rows. Rows from offsets[items] on belong to no item
+ * and are written as zeros. Nothing waits for the offsets: they are not
+ * checked, but cut to 0 .. n, so that no access leaves the tensors; if they
+ * descend, the results mean nothing. items up to 65535, rows up to 2^31 - 1.
+ * Everything else as for the dense layers: asynchronous, no allocation, sums
+ * in one order, each stored value rounded once.
+ * ---------------------------------------------------------------------- */
+
+/*
+ * submconv_item_offsets -- offsets [items + 1] of sites whose batch index is
+ * the first of `ld` int32 of each row of coords (coords [n,4]: ld = 4), rows in
+ * the order of their item. status [1] int32, device: 0, or the sum of 1 (an
+ * index outside 0 .. items - 1) and 2 (rows out of order); offsets then mean
+ * nothing.
+ */
+int submconv_item_offsets(const int32_t* coords, int64_t ld, int64_t n, int32_t items,
+                          int32_t* offsets, int32_t* status, hipStream_t stream);
+
+/* Workspace of submconv_group_norm (0 is possible); negative on a bad argument. */
+int64_t submconv_group_norm_workspace_bytes(int64_t n, int32_t cdim, int32_t groups, int32_t items,
+                                            int32_t dtype);
+
+/*
+ * submconv_group_norm -- y = act((x - m) r weight + bias), m and r = 1 /
+ * sqrt(mean (x - m)^2 + eps) over an item's rows and each of `groups` runs of
+ * cdim / groups channels. x [n,cdim] of `dtype` (SUBMCONV_DTYPE_F16, _BF16 or
+ * _F32), row stride ldx; y [n,cdim]. weight and bias [cdim] fp32, either NULL
+ * for 1 and 0. mean and rstd [items,groups] fp32 receive m and r, either may be
+ * NULL; an empty item has m = 0. cdim up to 8192. y may be x itself where ldx
+ * is cdim.
+ */
+int submconv_group_norm(const void* x, int64_t ldx, int64_t n, int32_t cdim, int32_t groups,
+                        const int32_t* offsets, int32_t items, const float* weight,
+                        const float* bias, float eps, int32_t act, void* y, float* mean,
+                        float* rstd, int32_t dtype, void* workspace, int64_t workspace_bytes,
+                        hipStream_t stream);
+
+/* Workspace of submconv_group_norm_backward with every gradient asked for. */
+int64_t submconv_group_norm_backward_workspace_bytes(int64_t n, int32_t cdim, int32_t groups,
+                                                     int32_t items, int32_t dtype);
+
+/*
+ * submconv_group_norm_backward -- with xh = (x - mean) rstd, z = xh weight +
+ * bias, dz = grad_out act'(z) and d = dz weight: grad_x = rstd (d - mean(d) - xh
+ * mean(d xh)), the means over the item's rows and the group's channels;
+ * grad_weight = sum over all items' rows of dz xh, grad_bias = sum of dz (fp32
+ * [cdim]). mean and rstd as the forward wrote them. Any of the three results
+ * may be NULL.
+ */
+int submconv_group_norm_backward(const void* grad_out, int64_t ldg, const void* x, int64_t ldx,
+                                 int64_t n, int32_t cdim, int32_t groups, const int32_t* offsets,
+                                 int32_t items, const float* mean, const float* rstd,
+                                 const float* weight, const float* bias, int32_t act, void* grad_x,
+                                 float* grad_weight, float* grad_bias, int32_t dtype,
+                                 void* workspace, int64_t workspace_bytes, hipStream_t stream);
+
+/*
+ * submconv_rotary -- turns pairs of columns by the angle of their row's
+ * position. x [n,heads,dim] of `dtype` (fp16, bf16 or fp32) with ldx elements
+ * between rows and hx between heads; out likewise, and may be x itself with
+ * the same strides. positions int32, ldp elements between rows, ap between the
+ * `axes` (1 to 4) of a row; freqs [nfreqs] fp64, radians per position. Pair p =
+ * axis nfreqs + f turns by t = position[axis] freqs[f]:
+ * (u, v) -> amplitude (u cos t - v sin t, v cos t + u sin t), by -t where
+ * `inverse`. Its columns are 2 p and 2 p + 1 where `interleaved`, else p and
+ * axes nfreqs + p. Columns from 2 axes nfreqs (at most dim) on are copied.
+ * Angles are formed in fp64.
+ */
+int submconv_rotary(const void* x, int64_t ldx, int64_t hx, int64_t n, int32_t heads, int32_t dim,
+                    const int32_t* positions, int64_t ldp, int64_t ap, int32_t axes,
+                    const double* freqs, int32_t nfreqs, int32_t interleaved, int32_t inverse,
+                    float amplitude, void* out, int64_t ldo, int64_t ho, int32_t dtype,
+                    hipStream_t stream);
+
+/* Workspace of submconv_attention (0 is possible); negative on a bad argument. */
+int64_t submconv_attention_workspace_bytes(int64_t nq, int64_t nk, int32_t heads, int32_t kv_heads,
+                                           int32_t dim, int32_t items);
+
+/*
+ * submconv_attention -- out = softmax(scale q k^T) v of each item's queries
+ * over its keys. q [nq,heads,dim], k and v [nk,kv_heads,dim] fp16 or bf16 with
+ * ld. elements between rows and h. between heads: starts on 16 bytes, strides
+ * in multiples of 8, row strides up to 2^22; dim a multiple of 8 up to 128.
+ * heads is a multiple of kv_heads, and heads / kv_heads neighbouring heads share
+ * a key head. q_offsets and k_offsets: the items' rows of either side (NULL for
+ * one item); k_lengths [items] int32 or NULL: how many of an item's keys are
+ * attended. `causal`: query i of an item with Lq queries and Lk keys sees keys j
+ * <= i + Lk - Lq; the others' values have to be finite all the same. A query
+ * that sees no key has out = 0 and lse = -inf. out [nq,heads,dim] dense; lse
+ * [nq,heads] fp32 or NULL: log of the sum of exp(scale q k). scale > 0. Scores,
+ * their maximum and sum and out are fp32; the weights are rounded to the
+ * data's type between the two products.
+ */
+int submconv_attention(const uint16_t* q, int64_t ldq, int64_t hq, int64_t nq, const uint16_t* k,
+                       int64_t ldk, int64_t hk, const uint16_t* v, int64_t ldv, int64_t hv,
+                       int64_t nk, int32_t heads, int32_t kv_heads, int32_t dim,
+                       const int32_t* q_offsets, const int32_t* k_offsets, const int32_t* k_lengths,
+                       int32_t items, float scale, int32_t causal, uint16_t* out, float* lse,
+                       int32_t dtype, void* workspace, int64_t workspace_bytes, hipStream_t stream);
+
+/* Workspace of submconv_attention_backward with every gradient asked for. */
+int64_t submconv_attention_backward_workspace_bytes(int64_t nq, int64_t nk, int32_t heads,
+                                                    int32_t kv_heads, int32_t dim, int32_t items);
+
+/*
+ * submconv_attention_backward -- with p = exp(scale q k^T - lse), dp = grad_out
+ * v^T and ds = p (dp - rowsum(grad_out out)): grad_q = scale ds k [nq,heads,dim],
+ * grad_k = scale ds^T q and grad_v = p^T grad_out [nk,kv_heads,dim], summed over
+ * the heads that share a key head; dense, of the data's type. out and lse as
+ * the forward wrote them, grad_out with the strides of q's kind, the rest as
+ * the forward's. Any gradient may be NULL. p and ds are rounded to the data's
+ * type before their products (in fp16 times powers of two that keep small ones
+ * from being lost).
+ */
+int submconv_attention_backward(const uint16_t* grad_out, int64_t ldg, int64_t hg,
+                                const uint16_t* out, const float* lse, const uint16_t* q,
+                                int64_t ldq, int64_t hq, int64_t nq, const uint16_t* k, int64_t ldk,
+                                int64_t hk, const uint16_t* v, int64_t ldv, int64_t hv, int64_t nk,
+                                int32_t heads, int32_t kv_heads, int32_t dim,
+                                const int32_t* q_offsets, const int32_t* k_offsets,
+                                const int32_t* k_lengths, int32_t items, float scale, int32_t causal,
+                                uint16_t* grad_q, uint16_t* grad_k, uint16_t* grad_v, int32_t dtype,
+                                void* workspace, int64_t workspace_bytes, hipStream_t stream);
+
 /* Message for a status code (static string). */
 const char* submconv_status_string(int status);
 

@@ -29,7 +29,9 @@ __all__ = [
     "abi_version", "release_scratch", "FLAG_MORTON", "downsample", "subdivide", "MaskedPlan", "masked_plan",
     "forward_masked", "layer_norm", "layer_norm_backward", "linear", "linear_backward", "gated_ffn",
     "gated_ffn_backward", "LayerNormFunction", "LinearFunction", "GatedFeedForwardFunction", "LayerNorm",
-    "Linear", "GatedFeedForward", "SparseConvBlock",
+    "Linear", "GatedFeedForward", "SparseConvBlock", "item_offsets", "group_norm", "group_norm_backward", "rotary",
+    "rotary_frequencies", "attention", "attention_backward", "GroupNormFunction", "RotaryFunction",
+    "AttentionFunction", "GroupNorm",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -117,6 +119,22 @@ def load_library():
         "submconv_gated_ffn_backward_workspace_bytes": ([I64, I32, I32, I32, I32], I64),
         "submconv_gated_ffn_backward": ([P, I64, I64, P, I64, P, P, P, P, P, P, P, P, I32, I32, I32, I32, I32, P,
                                          I64, P], ctypes.c_int),
+        "submconv_item_offsets": ([P, I64, I64, I32, P, P, P], ctypes.c_int),
+        "submconv_group_norm_workspace_bytes": ([I64, I32, I32, I32, I32], I64),
+        "submconv_group_norm": ([P, I64, I64, I32, I32, P, I32, P, P, ctypes.c_float, I32, P, P, P, I32, P, I64, P],
+                                ctypes.c_int),
+        "submconv_group_norm_backward_workspace_bytes": ([I64, I32, I32, I32, I32], I64),
+        "submconv_group_norm_backward": ([P, I64, P, I64, I64, I32, I32, P, I32, P, P, P, P, I32, P, P, P, I32, P,
+                                          I64, P], ctypes.c_int),
+        "submconv_rotary": ([P, I64, I64, I64, I32, I32, P, I64, I64, I32, P, I32, I32, I32, ctypes.c_float, P, I64,
+                             I64, I32, P], ctypes.c_int),
+        "submconv_attention_workspace_bytes": ([I64, I64, I32, I32, I32, I32], I64),
+        "submconv_attention": ([P, I64, I64, I64, P, I64, I64, P, I64, I64, I64, I32, I32, I32, P, P, P, I32,
+                                ctypes.c_float, I32, P, P, I32, P, I64, P], ctypes.c_int),
+        "submconv_attention_backward_workspace_bytes": ([I64, I64, I32, I32, I32, I32], I64),
+        "submconv_attention_backward": ([P, I64, I64, P, P, P, I64, I64, I64, P, I64, I64, P, I64, I64, I64, I32, I32,
+                                         I32, P, P, P, I32, ctypes.c_float, I32, P, P, P, I32, P, I64, P],
+                                        ctypes.c_int),
         "submconv_status_string": ([ctypes.c_int], ctypes.c_char_p),
         "submconv_last_error": ([], ctypes.c_char_p),
         "submconv_abi_version": ([], ctypes.c_int),
@@ -655,4 +673,7 @@ class SubMConv3d(torch.nn.Module):
 from .dense import (  # noqa: E402  (dense.py uses this module's helpers)
     GatedFeedForward, GatedFeedForwardFunction, LayerNorm, LayerNormFunction, Linear, LinearFunction, gated_ffn,
     gated_ffn_backward, layer_norm, layer_norm_backward, linear, linear_backward)
+from .packed import (  # noqa: E402
+    AttentionFunction, GroupNorm, GroupNormFunction, RotaryFunction, attention, attention_backward, group_norm,
+    group_norm_backward, item_offsets, rotary, rotary_frequencies)
 from .blocks import SparseConvBlock  # noqa: E402

@@ -14,7 +14,8 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libsubmconv.so")
 SOURCES = ["map_build.hip", "forward.hip", "backward.hip", "coord_ops.hip", "masked.hip",
            "staged.hip", "staged_wide.hip", "staged_bwd.hip", "linear.hip", "gated_ffn.hip", "gated_fused.hip",
-           "few_rows.hip", "layer_norm.hip"]
+           "few_rows.hip", "layer_norm.hip", "items.hip", "group_norm.hip", "rotary.hip", "attention.hip",
+           "attention_grad.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 FLAGS = ["--offload-arch=" + ARCH, "-O3", "-std=c++20", "-fPIC", "-Wall",

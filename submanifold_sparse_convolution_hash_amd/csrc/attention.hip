@@ -1,0 +1,354 @@
+// Attention among the rows of packed items, forward. Per query i of an item and
+// head, over the keys j that it sees (all of the item's, or with the causal mask
+// those up to its own place counted from the end, j <= i + Lk - Lq):
+//
+//   s_j = scale q_i . k_j,  lse_i = log sum_j exp s_j,  o_i = sum_j exp(s_j - lse_i) v_j
+//
+// A query that sees no key has o = 0 and lse = -inf.
+//
+// One pass over the keys with a running maximum and sum. The `group` query heads
+// that share a key head are rows of one matrix, row = token group + head, so that
+// a few tokens still fill a tile and keys are read once for all of them. A wave
+// owns 32 such rows; it forms scores^T = K Q^T, so that a lane holds all of its
+// scores of one row: the maximum and the sum need one exchange between the halves
+// of the wave, and the rounded weights are at once the operand of O^T = V^T P^T.
+// Products, maximum, sum and O are fp32; weights are rounded to 16 bits for the
+// second product, as its operands have to be.
+#include <algorithm>
+
+#include "attention_tile.h"
+
+namespace submconv {
+namespace {
+
+struct AttnOut {
+  uint16_t* out;    // [nq][heads][D]
+  float* lse;       // [nq][heads] or null
+  float* part;      // [splits][nq][heads][D], where the keys are split
+  float* part_lse;  // [splits][nq][heads]
+  int32_t splits;
+  int64_t slots;  // tiles, times the splits
+};
+
+// The maximum is raised, and what was summed scaled down, only once a score
+// passes it by this many powers of two: weights stay below 2^8, which 16 bits
+// hold as exactly as any other, and the sums' 32 bits have room.
+constexpr float kSlack = 8.0f;
+
+template <bool BF16, int DP, int NW>
+__global__ __launch_bounds__(NW * 64, NW == 1 ? 1 : 2) void k_attention(Attention a, AttnOut o) {
+  constexpr int T = 32 * NW, SHIFT = NW == 1 ? 5 : NW == 2 ? 6 : NW == 4 ? 7 : 8;
+  static_assert(T == 1 << SHIFT, "rows");
+  using H = HeadTile<DP>;
+  using L = TileLoad<DP, NW>;
+  constexpr int KS = DP / 16, DB = DP / 32;
+  __shared__ __attribute__((aligned(16))) char smem[2][2][H::BYTES];
+  const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const Place at = place_of(blockIdx.x, o.slots, a.kv_heads);
+  // long walks first: under the causal mask an item's last tiles see most keys
+  const int64_t slot = (o.slots - 1 - at.slot) / o.splits;
+  const int split = static_cast<int>((o.slots - 1 - at.slot) % o.splits);
+  const ItemTile t = find_item(a.qi, a.group, SHIFT, slot);
+  const Extent x = extent_of(a, t.item);
+  const int64_t rows = static_cast<int64_t>(x.q_rows) * a.group, r_first = t.tile * T;
+  if (t.tile < 0 || r_first >= rows) return;
+
+  // this lane's row
+  const int64_t r = r_first + wave * 32 + (lane & 31);
+  const bool live = r < rows;
+  const int32_t token = static_cast<int32_t>((live ? r : rows - 1) / a.group);
+  const int head = at.head * a.group + static_cast<int>((live ? r : rows - 1) % a.group);
+  const int32_t see = keys_of(a, x, token);
+  const int32_t wave_token = static_cast<int32_t>(min(r_first + wave * 32, rows - 1) / a.group);
+  const int32_t see_least = keys_of(a, x, wave_token);  // of the wave's rows: the first's
+  const int32_t see_most = keys_of(a, x, static_cast<int32_t>(min(r_first + T, rows) - 1) / a.group);
+  const int tiles = (see_most + kTileKeys - 1) / kTileKeys;
+  const int first = static_cast<int>(static_cast<int64_t>(tiles) * split / o.splits);
+  const int last = static_cast<int>(static_cast<int64_t>(tiles) * (split + 1) / o.splits);
+
+  half8 q[KS];
+  {
+    const uint16_t* p = a.q.p + (x.q0 + token) * a.q.ld + head * a.q.hs;
+#pragma unroll
+    for (int kk = 0; kk < KS; ++kk) {
+      const int c = kk * 16 + h * 8;
+      q[kk] = half8{};
+      if (c < a.D) q[kk] = *reinterpret_cast<const half8*>(p + c);
+    }
+  }
+  const HeadRows kr{a.k.p + x.k0 * a.k.ld + at.head * a.k.hs, a.k.ld, x.Lk};
+  const HeadRows vr{a.v.p + x.k0 * a.v.ld + at.head * a.v.hs, a.v.ld, x.Lk};
+  L lk, lv;
+  lk.init(a.k.ld, a.D, wave, lane);
+  lv.init(a.v.ld, a.D, wave, lane);
+  const uint32_t lds = lds_addr(&smem[0][0][0]);
+  auto issue = [&](int tile) {
+    const uint32_t to = lds + (tile & 1) * 2 * H::BYTES;
+    lk.issue(kr, static_cast<int64_t>(tile) * kTileKeys, a.D, to, wave);
+    lv.issue(vr, static_cast<int64_t>(tile) * kTileKeys, a.D, to + H::BYTES, wave);
+  };
+
+  const float c = a.scale * kLog2e;
+  float m = -kInf, mc = 0.0f, sum = 0.0f;  // mc = m c, 0 while m is -inf
+  float16v acc[DB];
+#pragma unroll
+  for (int j = 0; j < DB; ++j) acc[j] = float16v{};
+  if (first < last) issue(first);
+  for (int tile = first; tile < last; ++tile) {
+    // this tile has landed and all waves are past the last one
+    wait_loads<0>();
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    if (tile + 1 < last) issue(tile + 1);
+    const char* tk = smem[tile & 1][0];
+    const char* tv = smem[tile & 1][1];
+    float16v s[2] = {};
+#pragma unroll
+    for (int kk = 0; kk < KS; ++kk)
+#pragma unroll
+      for (int b = 0; b < 2; ++b) s[b] = mfma32<BF16>(H::rows(tk, b * 32, kk, lane), q[kk], s[b]);
+    const int j0 = tile * kTileKeys;
+    if (j0 + kTileKeys > see_least) {
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (j0 + b * 32 + 8 * (i / 4) + 4 * h + i % 4 >= see) s[b][i] = -kInf;
+    }
+    float top = s[0][0];
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int i = b == 0 ? 1 : 0; i < 16; ++i) top = fmaxf(top, s[b][i]);
+    top = halves_max(top);
+    const bool raise = top * c > mc + kSlack || (m == -kInf && top > -kInf);
+    if (__ballot(raise)) {
+      const float next = raise ? top : m;
+      const float nc = next == -kInf ? 0.0f : next * c;
+      const float f = m == -kInf ? 0.0f : __builtin_amdgcn_exp2f(mc - nc);
+      m = next;
+      mc = nc;
+      sum *= f;
+#pragma unroll
+      for (int j = 0; j < DB; ++j)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc[j][i] *= f;
+    }
+    half8 p[4];
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        s[b][i] = __builtin_amdgcn_exp2f(s[b][i] * c - mc);
+        sum += s[b][i];
+      }
+      p[2 * b] = operand_of<BF16>(s[b], 0);
+      p[2 * b + 1] = operand_of<BF16>(s[b], 8);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int j = 0; j < DB; ++j) acc[j] = mfma32<BF16>(H::columns(tv, k * 16, j, lane), p[k], acc[j]);
+  }
+  sum = halves_sum(sum);
+  const float inv = sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;  // (a NaN stays one)
+  const float lse = sum == 0.0f ? -kInf : (mc + __log2f(sum)) * kLn2;
+  if (!live) return;
+  const int64_t heads = static_cast<int64_t>(a.kv_heads) * a.group;
+  int64_t to = (x.q0 + token) * heads + head;
+  if (o.splits == 1) {
+    if (o.lse && h == 0) o.lse[to] = lse;
+    uint16_t* out = o.out + to * a.D;
+#pragma unroll
+    for (int j = 0; j < DB; ++j)
+#pragma unroll
+      for (int i = 0; i < 16; i += 8) {
+        float4v u, w;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          u[e] = acc[j][i + e] * inv;
+          w[e] = acc[j][i + 4 + e] * inv;
+        }
+        const u32x4 v = eight_rows<BF16>(u, w);
+        const int d = j * 32 + i * 2 + h * 8;
+        if (d < a.D) *reinterpret_cast<u32x4*>(out + d) = v;
+      }
+    return;
+  }
+  to += split * a.qi.n * heads;
+  if (h == 0) o.part_lse[to] = lse;
+  float* part = o.part + to * a.D;
+#pragma unroll
+  for (int j = 0; j < DB; ++j)
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) {
+      const int d = j * 32 + i * 2 + h * 4;
+      float4v u;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) u[e] = acc[j][i + e] * inv;
+      if (d < a.D) *reinterpret_cast<float4v*>(part + d) = u;
+    }
+}
+
+// Joins the splits: o = sum_s w_s o_s, w_s = exp(lse_s - lse). Four columns a
+// thread; rows [nq heads].
+template <bool BF16>
+__global__ __launch_bounds__(256) void k_attention_join(const float* __restrict__ part,
+                                                        const float* __restrict__ part_lse, int64_t rows, int D,
+                                                        int splits, uint16_t* __restrict__ out,
+                                                        float* __restrict__ lse) {
+  const int64_t id = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  const int pieces = D / 4;
+  const int64_t row = id / pieces;
+  const int d = static_cast<int>(id % pieces) * 4;
+  if (row >= rows) return;
+  float top = -kInf;
+  for (int s = 0; s < splits; ++s) top = fmaxf(top, part_lse[s * rows + row]);
+  const float base = top == -kInf ? 0.0f : top;
+  float total = 0.0f;
+  float4v v = {};
+#pragma unroll 4
+  for (int s = 0; s < splits; ++s) {
+    const float w = __builtin_amdgcn_exp2f((part_lse[s * rows + row] - base) * kLog2e);
+    const float4v u = *reinterpret_cast<const float4v*>(part + (s * rows + row) * D + d);
+    total += w;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] += w * u[e];
+  }
+  const float inv = total > 0.0f ? 1.0f / total : total == 0.0f ? 0.0f : total;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) v[e] *= inv;
+  *reinterpret_cast<u32x2*>(out + row * D + d) = pack4<BF16>(v);
+  if (lse && d == 0) lse[row] = total == 0.0f ? -kInf : top + __log2f(total) * kLn2;
+}
+
+// ---- dispatch ----
+
+struct Plan {
+  int waves, splits;
+  int64_t slots;
+};
+
+// One wave a workgroup where the items have few rows on average, else four. The
+// keys are split over workgroups where the tiles alone leave units idle: up to
+// four workgroups a unit, each with at least four tiles of keys on average.
+Plan plan_of(const Attention& a) {
+  Plan p;
+  const int64_t mean_rows = (a.qi.n * a.group + a.qi.items - 1) / a.qi.items;
+  p.waves = mean_rows <= 32 ? 1 : 4;
+  const int64_t tile = p.waves * 32, tiles = (mean_rows + tile - 1) / tile * a.qi.items;
+  const int64_t key_tiles = (a.ki.n / a.qi.items + kTileKeys - 1) / kTileKeys;
+  const int64_t want = (p.waves == 1 ? 1024 : 512) / std::max<int64_t>(1, tiles * a.kv_heads);
+  p.splits = static_cast<int>(std::clamp<int64_t>(std::min(want, key_tiles / 4), 1, 64));
+  p.slots = item_slots(a.qi, a.group, p.waves == 1 ? 5 : 7) * p.splits;
+  return p;
+}
+
+int attention_forward(const Attention& a, bool bf16, uint16_t* out, float* lse, Arena& ws, hipStream_t stream) {
+  const Plan p = plan_of(a);
+  const int64_t rows = a.qi.n * a.group * a.kv_heads;
+  AttnOut o{out, lse, nullptr, nullptr, p.splits, p.slots};
+  if (p.splits > 1) {
+    o.part = static_cast<float*>(ws.take(rows * p.splits * a.D * 4));
+    o.part_lse = static_cast<float*>(ws.take(rows * p.splits * 4));
+  }
+  if (ws.counting) return SUBMCONV_OK;
+  const int64_t blocks = p.slots * a.kv_heads;
+  if (blocks > INT32_MAX) return set_error(SUBMCONV_ERR_UNSUPPORTED_SHAPE, "%lld tiles", (long long)blocks);
+  auto go = [&](auto dp, auto nw) {
+    if (bf16) k_attention<true, dp, nw><<<static_cast<unsigned>(blocks), nw * 64, 0, stream>>>(a, o);
+    else k_attention<false, dp, nw><<<static_cast<unsigned>(blocks), nw * 64, 0, stream>>>(a, o);
+  };
+  auto by_width = [&](auto nw) {
+    if (a.D <= 32) go(std::integral_constant<int, 32>{}, nw);
+    else if (a.D <= 64) go(std::integral_constant<int, 64>{}, nw);
+    else if (a.D <= 96) go(std::integral_constant<int, 96>{}, nw);
+    else go(std::integral_constant<int, 128>{}, nw);
+  };
+  if (p.waves == 1) by_width(std::integral_constant<int, 1>{});
+  else by_width(std::integral_constant<int, 4>{});
+  SUBMCONV_HIP_CHECK(hipGetLastError());
+  if (p.splits > 1) {
+    const int64_t n = rows * (a.D / 4);
+    const unsigned grid = static_cast<unsigned>((n + 255) / 256);
+    if (bf16) k_attention_join<true><<<grid, 256, 0, stream>>>(o.part, o.part_lse, rows, a.D, p.splits, out, lse);
+    else k_attention_join<false><<<grid, 256, 0, stream>>>(o.part, o.part_lse, rows, a.D, p.splits, out, lse);
+    SUBMCONV_HIP_CHECK(hipGetLastError());
+  }
+  return SUBMCONV_OK;
+}
+
+}  // namespace
+
+int check_strided(const char* name, const Strided& s, int64_t n, int32_t heads, int32_t D) {
+  if (n > 0 && !s.p) return set_error(SUBMCONV_ERR_INVALID_ARG, "%s is NULL", name);
+  if (reinterpret_cast<uintptr_t>(s.p) & 15)
+    return set_error(SUBMCONV_ERR_INVALID_ARG, "%s does not start on 16 bytes", name);
+  if ((n > 1 && s.ld % 8) || (heads > 1 && s.hs % 8))
+    return set_error(SUBMCONV_ERR_INVALID_ARG, "%s: strides %lld, %lld are not multiples of 8", name,
+                     (long long)s.ld, (long long)s.hs);
+  if ((heads > 1 && s.hs < D) || (n > 1 && s.ld < D))
+    return set_error(SUBMCONV_ERR_INVALID_ARG, "%s: strides %lld, %lld below %d columns", name, (long long)s.ld,
+                     (long long)s.hs, D);
+  if (n > 1 && s.ld > kMaxLd)
+    return set_error(SUBMCONV_ERR_UNSUPPORTED_SHAPE, "%s: row stride %lld above %lld", name, (long long)s.ld,
+                     (long long)kMaxLd);
+  return SUBMCONV_OK;
+}
+
+int check_attention(const Attention& a, int64_t nq, int64_t nk, int32_t heads, int32_t dtype) {
+  if (dtype != SUBMCONV_DTYPE_F16 && dtype != SUBMCONV_DTYPE_BF16)
+    return set_error(SUBMCONV_ERR_INVALID_ARG, "dtype = %d", dtype);
+  if (nq < 0 || nk < 0 || nq > INT32_MAX || nk > INT32_MAX)
+    return set_error(SUBMCONV_ERR_INVALID_ARG, "%lld queries, %lld keys", (long long)nq, (long long)nk);
+  if (a.kv_heads < 1 || heads < a.kv_heads || heads % a.kv_heads || heads > 65536)
+    return set_error(SUBMCONV_ERR_INVALID_ARG, "%d heads on %d key heads", heads, a.kv_heads);
+  if (a.D < 8 || a.D > 128 || a.D % 8)
+    return set_error(SUBMCONV_ERR_UNSUPPORTED_SHAPE, "%d columns a head, multiples of 8 up to 128 are supported", a.D);
+  if (a.qi.items < 1 || a.qi.items > 65535)
+    return set_error(SUBMCONV_ERR_INVALID_ARG, "%d items, 1 to 65535 are supported", a.qi.items);
+  if ((!a.qi.offsets || !a.ki.offsets) && a.qi.items != 1)
+    return set_error(SUBMCONV_ERR_INVALID_ARG, "%d items without offsets", a.qi.items);
+  if (!(a.scale > 0.0f) || a.scale > 3e38f) return set_error(SUBMCONV_ERR_INVALID_ARG, "scale = %g", a.scale);
+  return SUBMCONV_OK;
+}
+
+}  // namespace submconv
+
+using namespace submconv;
+
+extern "C" int64_t submconv_attention_workspace_bytes(int64_t nq, int64_t nk, int32_t heads, int32_t kv_heads,
+                                                      int32_t dim, int32_t items) {
+  clear_error();
+  const Attention a{{}, {}, {}, {reinterpret_cast<const int32_t*>(4), items, nq},
+                    {reinterpret_cast<const int32_t*>(4), items, nk}, nullptr,
+                    kv_heads > 0 ? heads / kv_heads : 0, kv_heads, dim, 1.0f, 0};
+  SUBMCONV_TRY(check_attention(a, nq, nk, heads, SUBMCONV_DTYPE_F16));
+  Arena ws;
+  SUBMCONV_TRY(attention_forward(a, false, nullptr, nullptr, ws, nullptr));
+  return ws.used;
+}
+
+extern "C" int submconv_attention(const uint16_t* q, int64_t ldq, int64_t hq, int64_t nq, const uint16_t* k,
+                                  int64_t ldk, int64_t hk, const uint16_t* v, int64_t ldv, int64_t hv, int64_t nk,
+                                  int32_t heads, int32_t kv_heads, int32_t dim, const int32_t* q_offsets,
+                                  const int32_t* k_offsets, const int32_t* k_lengths, int32_t items, float scale,
+                                  int32_t causal, uint16_t* out, float* lse, int32_t dtype, void* workspace,
+                                  int64_t workspace_bytes, hipStream_t stream) {
+  clear_error();
+  const Attention a{strided(q, nq, heads, dim, ldq, hq), strided(k, nk, kv_heads, dim, ldk, hk),
+                    strided(v, nk, kv_heads, dim, ldv, hv), Items{q_offsets, items, nq}, Items{k_offsets, items, nk},
+                    k_lengths, kv_heads > 0 ? heads / kv_heads : 0, kv_heads, dim, scale, causal};
+  SUBMCONV_TRY(check_attention(a, nq, nk, heads, dtype));
+  SUBMCONV_TRY(check_strided("q", a.q, nq, heads, dim));
+  SUBMCONV_TRY(check_strided("k", a.k, nk, kv_heads, dim));
+  SUBMCONV_TRY(check_strided("v", a.v, nk, kv_heads, dim));
+  SUBMCONV_TRY(check_strided("out", strided(out, nq, 1, dim, dim, dim), nq, 1, dim));
+  if (nq == 0) return SUBMCONV_OK;
+  const bool bf16 = dtype == SUBMCONV_DTYPE_BF16;
+  Arena need, ws{false, static_cast<char*>(workspace)};
+  SUBMCONV_TRY(attention_forward(a, bf16, out, lse, need, stream));
+  SUBMCONV_TRY(check_workspace(workspace, workspace_bytes, need.used));
+  return attention_forward(a, bf16, out, lse, ws, stream);
+}

@@ -1,0 +1,74 @@
+// Rows of several items packed one after the other: offsets [items + 1] int32
+// on the device, ascending from 0; item b's rows are offsets[b] .. offsets[b +
+// 1] - 1. Rows from offsets[items] on belong to no item; here they are the rows
+// of one item more, number `items`, for which every operator writes zeros. A
+// null pointer: one item of all rows.
+//
+// A launch knows the number of rows and of items, not their lengths, and
+// nothing waits for those. Its workgroups are numbered slots: an item of L rows,
+// `per` units a row, takes the slots from floor(start per / tile) + b on, at
+// most floor(end per / tile) + b of them, which is never fewer than ceil(L per /
+// tile). So total = floor(n per / tile) + items + 1 slots are enough for any
+// lengths, an item's first slot follows from its offset alone, and a slot finds
+// its item by a search that needs no prefix sums. Slots past an item's last tile
+// have nothing to do.
+//
+// Offsets that descend or leave 0 .. n are cut to it: their results mean
+// nothing, but no access leaves the tensors.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+namespace submconv {
+
+struct Items {
+  const int32_t* offsets;  // or null
+  int32_t items;
+  int64_t n;
+};
+// (tiles of 2^shift units)
+inline int64_t item_slots(const Items& it, int64_t per, int shift) {
+  return (it.n * per >> shift) + it.items + 1;
+}
+
+namespace {
+
+// First row of item b, 0 <= b <= items + 1.
+__device__ __forceinline__ int64_t item_start(const Items& it, int b) {
+  if (b == 0) return 0;
+  if (b > it.items || !it.offsets) return it.n;
+  const int64_t v = it.offsets[b];
+  return v < 0 ? 0 : v < it.n ? v : it.n;
+}
+
+struct ItemTile {
+  int32_t item;
+  int64_t row0, rows;  // of the item
+  int64_t tile;        // of the item; below 0 or past its last where the slot has nothing to do
+};
+
+// The item of a slot, by the lanes of each wave: 64 items a probe.
+__device__ __forceinline__ ItemTile find_item(const Items& it, int64_t per, int shift, int64_t slot) {
+  const int lane = threadIdx.x & 63;
+  int lo = 0, hi = it.items;
+  while (lo < hi) {
+    const int step = (hi - lo + 63) / 64;
+    const int b = lo + (lane + 1) * step;
+    const bool ok = b <= hi && (item_start(it, b) * per >> shift) + b <= slot;
+    const int c = __popcll(__ballot(ok));  // at most (hi - lo) / step of them have b <= hi
+    hi = min(hi, lo + (c + 1) * step - 1);
+    lo += c * step;
+  }
+  ItemTile r;
+  r.item = __builtin_amdgcn_readfirstlane(lo);
+  const int64_t s = item_start(it, r.item), e = item_start(it, r.item + 1);
+  r.row0 = s;
+  r.rows = e > s ? e - s : 0;
+  r.tile = slot - ((s * per >> shift) + r.item);
+  return r;
+}
+
+}  // namespace
+}  // namespace submconv
