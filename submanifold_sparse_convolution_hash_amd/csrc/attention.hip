@@ -46,10 +46,9 @@ __global__ __launch_bounds__(NW * 64, NW == 1 ? 1 : 2) void k_attention(Attentio
   const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const Place at = place_of(blockIdx.x, o.slots, a.kv_heads);
-  // long walks first: under the causal mask an item's last tiles see most keys
-  const int64_t slot = (o.slots - 1 - at.slot) / o.splits;
-  const int split = static_cast<int>((o.slots - 1 - at.slot) % o.splits);
-  const ItemTile t = find_item(a.qi, a.group, SHIFT, slot);
+  const Walk w = walk_of(a.qi, a.group, SHIFT, o.slots, o.splits, at.slot, a.causal, false);
+  const ItemTile t = w.t;
+  const int split = w.split;
   const Extent x = extent_of(a, t.item);
   const int64_t rows = static_cast<int64_t>(x.q_rows) * a.group, r_first = t.tile * T;
   if (t.tile < 0 || r_first >= rows) return;
@@ -77,14 +76,15 @@ __global__ __launch_bounds__(NW * 64, NW == 1 ? 1 : 2) void k_attention(Attentio
       if (c < a.D) q[kk] = *reinterpret_cast<const half8*>(p + c);
     }
   }
+  settle(q);
   const HeadRows kr{a.k.p + x.k0 * a.k.ld + at.head * a.k.hs, a.k.ld, x.Lk};
   const HeadRows vr{a.v.p + x.k0 * a.v.ld + at.head * a.v.hs, a.v.ld, x.Lk};
   L lk, lv;
   lk.init(a.k.ld, a.D, wave, lane);
   lv.init(a.v.ld, a.D, wave, lane);
   const uint32_t lds = lds_addr(&smem[0][0][0]);
-  auto issue = [&](int tile) {
-    const uint32_t to = lds + (tile & 1) * 2 * H::BYTES;
+  auto issue = [&](int tile, int buf) {
+    const uint32_t to = lds + buf * 2 * H::BYTES;
     lk.issue(kr, static_cast<int64_t>(tile) * kTileKeys, a.D, to, wave);
     lv.issue(vr, static_cast<int64_t>(tile) * kTileKeys, a.D, to + H::BYTES, wave);
   };
@@ -94,15 +94,16 @@ __global__ __launch_bounds__(NW * 64, NW == 1 ? 1 : 2) void k_attention(Attentio
   float16v acc[DB];
 #pragma unroll
   for (int j = 0; j < DB; ++j) acc[j] = float16v{};
-  if (first < last) issue(first);
-  for (int tile = first; tile < last; ++tile) {
+  // One tile, of the buffer whose number is a constant: its addresses are then
+  // offsets in the reads.
+  auto step = [&](int tile, auto buf) {
     // this tile has landed and all waves are past the last one
     wait_loads<0>();
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    if (tile + 1 < last) issue(tile + 1);
-    const char* tk = smem[tile & 1][0];
-    const char* tv = smem[tile & 1][1];
+    if (tile + 1 < last) issue(tile + 1, buf ^ 1);
+    const char* tk = smem[buf][0];
+    const char* tv = smem[buf][1];
     float16v s[2] = {};
 #pragma unroll
     for (int kk = 0; kk < KS; ++kk)
@@ -150,6 +151,11 @@ __global__ __launch_bounds__(NW * 64, NW == 1 ? 1 : 2) void k_attention(Attentio
     for (int k = 0; k < 4; ++k)
 #pragma unroll
       for (int j = 0; j < DB; ++j) acc[j] = mfma32<BF16>(H::columns(tv, k * 16, j, lane), p[k], acc[j]);
+  };
+  if (first < last) issue(first, 0);
+  for (int tile = first; tile < last; tile += 2) {
+    step(tile, std::integral_constant<int, 0>{});
+    if (tile + 1 < last) step(tile + 1, std::integral_constant<int, 1>{});
   }
   sum = halves_sum(sum);
   const float inv = sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;  // (a NaN stays one)

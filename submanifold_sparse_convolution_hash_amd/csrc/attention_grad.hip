@@ -29,7 +29,7 @@ struct AttnGrad {
   Strided dout;
   const uint16_t* out;  // [nq][heads][D]
   const float* lse;     // [nq][heads]
-  float* row_lse;       // [heads][nq]: lse log2(e), written by k_attention_dq
+  float* row_base;      // [heads][nq], written by k_attention_dq: the weights are exp2(score log2(e) + base)
   float* row_delta;     // [heads][nq]
   uint16_t *dq, *dk, *dv;
   float *dq_part, *dk_part, *dv_part;  // [splits][rows][D] where split
@@ -105,9 +105,9 @@ __global__ __launch_bounds__(NW * 64, NW == 1 ? 1 : 2) void k_attention_dq(Atten
   const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const Place at = place_of(blockIdx.x, o.slots, a.kv_heads);
-  const int64_t slot = (o.slots - 1 - at.slot) / o.splits;  // long walks first
-  const int split = static_cast<int>((o.slots - 1 - at.slot) % o.splits);
-  const ItemTile t = find_item(a.qi, a.group, SHIFT, slot);
+  const Walk w = walk_of(a.qi, a.group, SHIFT, o.slots, o.splits, at.slot, a.causal, false);
+  const ItemTile t = w.t;
+  const int split = w.split;
   const Extent x = extent_of(a, t.item);
   const int64_t rows = static_cast<int64_t>(x.q_rows) * a.group, r_first = t.tile * T;
   if (t.tile < 0 || r_first >= rows) return;
@@ -146,12 +146,14 @@ __global__ __launch_bounds__(NW * 64, NW == 1 ? 1 : 2) void k_attention_dq(Atten
     }
     delta = halves_sum(delta);
   }
-  const float lse2 = o.lse[row] * kLog2e;
+  float base = Range<BF16>::kPLog2 - o.lse[row] * kLog2e;
   if (live && h == 0 && split == 0) {
-    o.row_lse[head * a.qi.n + x.q0 + token] = lse2;
+    o.row_base[head * a.qi.n + x.q0 + token] = base;
     o.row_delta[head * a.qi.n + x.q0 + token] = delta;
   }
   if (!o.dq && !o.dq_part) return;
+  settle(q);
+  settle(dy);
   const HeadRows kr{a.k.p + x.k0 * a.k.ld + at.head * a.k.hs, a.k.ld, x.Lk};
   const HeadRows vr{a.v.p + x.k0 * a.v.ld + at.head * a.v.hs, a.v.ld, x.Lk};
   L lk, lv;
@@ -163,7 +165,8 @@ __global__ __launch_bounds__(NW * 64, NW == 1 ? 1 : 2) void k_attention_dq(Atten
     lk.issue(kr, static_cast<int64_t>(tile) * kTileKeys, a.D, to, wave);
     lv.issue(vr, static_cast<int64_t>(tile) * kTileKeys, a.D, to + H::BYTES, wave);
   };
-  const float c = a.scale * kLog2e, base = Range<BF16>::kPLog2 - lse2;
+  const float c = a.scale * kLog2e;
+  asm volatile("" : "+v"(base), "+v"(delta));
   Range<BF16> range;
   float16v acc[DB];
 #pragma unroll
@@ -207,32 +210,40 @@ __global__ __launch_bounds__(NW * 64, NW == 1 ? 1 : 2) void k_attention_dq(Atten
                       o.dq_part ? o.dq_part + split * a.qi.n * heads * a.D : nullptr, row, a.D, h);
 }
 
-// 32 keys a wave; the walk is over the group's query heads and their tiles of 64
-// queries.
+// 32 keys a wave, 128 a workgroup; the walk is over the group's query heads and
+// their tiles of 64 queries. Up to 64 columns a wave takes a tile's two blocks of
+// 32 queries in turn. Past that the sums (128 registers at 128 columns) leave room
+// for K but not for V beside them at two waves a SIMD: V stays in LDS, eight waves
+// make a workgroup, two of them share 32 keys and take one block of queries each,
+// and their sums are added through LDS at the end.
 template <bool BF16, int DP>
-__global__ __launch_bounds__(256, DP > 64 ? 1 : 2) void k_attention_dkv(Attention a, AttnGrad o) {
-  constexpr int NW = 4, T = 32 * NW, SHIFT = 7;
+__global__ __launch_bounds__(DP > 64 ? 512 : 256, 2) void k_attention_dkv(Attention a, AttnGrad o) {
+  constexpr bool PAIRED = DP > 64;
+  constexpr int NW = PAIRED ? 8 : 4, T = 128, SHIFT = 7;
   using H = HeadTile<DP>;
   using L = TileLoad<DP, NW>;
   constexpr int KS = DP / 16, DB = DP / 32;
-  __shared__ __attribute__((aligned(16))) char smem[2][2][H::BYTES];
-  __shared__ __attribute__((aligned(16))) float stats[2][2][kTileKeys];  // lse log2(e) and delta of a tile's queries
+  constexpr int STAGES = PAIRED ? 3 : 2;  // tiles of queries in LDS
+  __shared__ __attribute__((aligned(16))) char smem[STAGES][2][H::BYTES];
+  __shared__ __attribute__((aligned(16))) char vmem[PAIRED ? 2 * H::BYTES : 16];  // V of the workgroup's keys
+  __shared__ __attribute__((aligned(16))) float stats[STAGES][2][kTileKeys];  // base and delta of a tile's queries
   const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int part = wave & 3, half = wave >> 2;  // the wave's keys; its block of queries where PAIRED
   const Place at = place_of(blockIdx.x, o.slots, a.kv_heads);
-  const int64_t slot = at.slot / o.splits;  // (an item's first keys are seen by most queries)
-  const int split = static_cast<int>(at.slot % o.splits);
-  const ItemTile t = find_item(a.ki, 1, SHIFT, slot);
+  const Walk w = walk_of(a.ki, 1, SHIFT, o.slots, o.splits, at.slot, a.causal, true);
+  const ItemTile t = w.t;
+  const int split = w.split;
   const Extent x = extent_of(a, t.item);
   const int64_t k_first = t.tile * T;
   if (t.tile < 0 || k_first >= x.k_rows) return;
 
-  const int32_t j = static_cast<int32_t>(k_first) + wave * 32 + (lane & 31);  // this lane's key
+  const int32_t j = static_cast<int32_t>(k_first) + part * 32 + (lane & 31);  // this lane's key
   const bool seen = j < x.Lk;
   // Query i sees key j from i = j - (Lk - Lq) on under the causal mask.
-  const int32_t lag = a.causal ? x.Lk - x.Lq : INT32_MAX;
+  const int32_t lag = x.Lk - x.Lq;
   const int32_t from = a.causal ? max(0, j - lag) : 0;
-  const int32_t wave_last = static_cast<int32_t>(k_first) + wave * 32 + 31;
+  const int32_t wave_last = static_cast<int32_t>(k_first) + part * 32 + 31;
   const int32_t from_most = a.causal ? max(0, wave_last - lag) : 0;
   const bool whole = wave_last < x.Lk;
   const int32_t i_first = a.causal ? max(0, static_cast<int32_t>(k_first) - lag) : 0;
@@ -242,7 +253,7 @@ __global__ __launch_bounds__(256, DP > 64 ? 1 : 2) void k_attention_dkv(Attentio
   const int first = static_cast<int>(static_cast<int64_t>(walk) * split / o.splits);
   const int last = static_cast<int>(static_cast<int64_t>(walk) * (split + 1) / o.splits);
 
-  half8 kf[KS], vf[KS];
+  half8 kf[KS], vf[PAIRED ? 1 : KS];
   {
     const int64_t at_key = seen ? j : 0;
     const uint16_t* pk = a.k.p + (x.k0 + at_key) * a.k.ld + at.head * a.k.hs;
@@ -250,26 +261,37 @@ __global__ __launch_bounds__(256, DP > 64 ? 1 : 2) void k_attention_dkv(Attentio
 #pragma unroll
     for (int kk = 0; kk < KS; ++kk) {
       const int c = kk * 16 + h * 8;
-      kf[kk] = vf[kk] = half8{};
-      if (seen && c < a.D) {
-        kf[kk] = *reinterpret_cast<const half8*>(pk + c);
-        vf[kk] = *reinterpret_cast<const half8*>(pv + c);
+      kf[kk] = half8{};
+      if (seen && c < a.D) kf[kk] = *reinterpret_cast<const half8*>(pk + c);
+      if constexpr (!PAIRED) {
+        vf[kk] = half8{};
+        if (seen && c < a.D) vf[kk] = *reinterpret_cast<const half8*>(pv + c);
       }
     }
   }
+  settle(kf);
+  if constexpr (!PAIRED) settle(vf);
   L lq, ld;
   lq.init(a.q.ld, a.D, wave, lane);
   ld.init(o.dout.ld, a.D, wave, lane);
   const uint32_t lds = lds_addr(&smem[0][0][0]);
   const uint32_t lds_stats = lds_addr(reinterpret_cast<const char*>(&stats[0][0][0]));
+  if (PAIRED && first < last) {
+    L lv;
+    lv.init(a.v.ld, a.D, wave, lane);
+    const HeadRows vr{a.v.p + x.k0 * a.v.ld + at.head * a.v.hs, a.v.ld, x.Lk};
+    const uint32_t to = lds_addr(&vmem[0]);
+    lv.issue(vr, k_first, a.D, to, wave);
+    lv.issue(vr, k_first + kTileKeys, a.D, to + H::BYTES, wave);
+  }
   auto issue = [&](int head, int tile, int buf) {
     const int64_t row0 = static_cast<int64_t>(tile) * kTileKeys;
     const HeadRows qr{a.q.p + x.q0 * a.q.ld + head * a.q.hs, a.q.ld, x.Lq};
     const HeadRows dr{o.dout.p + x.q0 * o.dout.ld + head * o.dout.hs, o.dout.ld, x.Lq};
     lq.issue(qr, row0, a.D, lds + buf * 2 * H::BYTES, wave);
     ld.issue(dr, row0, a.D, lds + buf * 2 * H::BYTES + H::BYTES, wave);
-    if (wave < 2) {  // one wave the lse, one the delta; zeros past the last query
-      const float* p = (wave == 0 ? o.row_lse : o.row_delta) + head * a.qi.n + x.q0 + row0;
+    if (wave < 2) {  // one wave the bases, one the deltas; zeros past the last query
+      const float* p = (wave == 0 ? o.row_base : o.row_delta) + head * a.qi.n + x.q0 + row0;
       rsrc4 r = load_rsrc(p, rows_left(x.Lq, row0, kTileKeys) * 4u);
       settle_rsrc(r);
       load_word_to_lds(r, lane * 4, lds_stats + (buf * 2 + wave) * kTileKeys * 4);
@@ -280,42 +302,67 @@ __global__ __launch_bounds__(256, DP > 64 ? 1 : 2) void k_attention_dkv(Attentio
   float16v dk[DB], dv[DB];
 #pragma unroll
   for (int i = 0; i < DB; ++i) dk[i] = dv[i] = float16v{};
-  int head = at.head * a.group, tile = first_tile;  // of the step
+  // From the item's last queries down: with the causal mask an item's keys start
+  // from queries of their own, and this way their workgroups read the same ones at
+  // the same time.
+  struct Step {
+    int head, tile;
+  };
+  auto next = [&](Step& w) {
+    if (w.tile-- == first_tile) {
+      w.tile = first_tile + q_tiles - 1;
+      ++w.head;
+    }
+  };
+  Step at_step{at.head * a.group, first_tile + q_tiles - 1};
   if (first < last) {
-    head += first / q_tiles;
-    tile += first % q_tiles;
-    issue(head, tile, 0);
+    at_step.head += first / q_tiles;
+    at_step.tile -= first % q_tiles;
   }
+  Step ahead = at_step;
+  for (int i = 0; i < STAGES - 1; ++i)
+    if (first + i < last) {
+      issue(ahead.head, ahead.tile, i);
+      next(ahead);
+    }
+  int buf = 0;
   for (int u = first; u < last; ++u) {
-    const int buf = (u - first) & 1;
-    // this tile has landed and all waves are past the last one
-    wait_loads<0>();
+    // this tile has landed (the next one may still be on its way) and all waves
+    // are past the last one
+    if (STAGES == 3 && u + 1 < last) {
+      if (wave < 2) wait_loads<2 * L::N + 1>();
+      else wait_loads<2 * L::N>();
+    } else {
+      wait_loads<0>();
+    }
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    const int32_t i0 = tile * kTileKeys;
-    if (++tile == first_tile + q_tiles) {
-      tile = first_tile;
-      ++head;
+    const int32_t i0 = at_step.tile * kTileKeys;
+    next(at_step);
+    if (u + STAGES - 1 < last) {
+      issue(ahead.head, ahead.tile, buf == 0 ? STAGES - 1 : buf - 1);
+      next(ahead);
     }
-    if (u + 1 < last) issue(head, tile, buf ^ 1);
     const char* tq = smem[buf][0];
     const char* td = smem[buf][1];
-#pragma unroll
-    for (int b = 0; b < 2; ++b) {
+    auto block = [&](int b) {
       float16v s = {}, dp = {};
 #pragma unroll
       for (int kk = 0; kk < KS; ++kk) {
         s = mfma32<BF16>(H::rows(tq, b * 32, kk, lane), kf[kk], s);
-        dp = mfma32<BF16>(H::rows(td, b * 32, kk, lane), vf[kk], dp);
+        if constexpr (PAIRED)
+          dp = mfma32<BF16>(H::rows(td, b * 32, kk, lane), H::rows(vmem, part * 32, kk, lane), dp);
+        else
+          dp = mfma32<BF16>(H::rows(td, b * 32, kk, lane), vf[kk], dp);
       }
 #pragma unroll
       for (int i = 0; i < 16; i += 4) {
         const int at_row = b * 32 + 2 * i + 4 * h;
-        const float4v lse2 = *reinterpret_cast<const float4v*>(&stats[buf][0][at_row]);
+        const float4v base = *reinterpret_cast<const float4v*>(&stats[buf][0][at_row]);
         const float4v delta = *reinterpret_cast<const float4v*>(&stats[buf][1][at_row]);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          s[i + e] = __builtin_amdgcn_exp2f(s[i + e] * c + (Range<BF16>::kPLog2 - lse2[e]));
+          s[i + e] = __builtin_amdgcn_exp2f(s[i + e] * c + base[e]);
           dp[i + e] = s[i + e] * (dp[i + e] - delta[e]);
         }
       }
@@ -337,15 +384,42 @@ __global__ __launch_bounds__(256, DP > 64 ? 1 : 2) void k_attention_dkv(Attentio
           dk[i] = mfma32<BF16>(H::columns(tq, b * 32 + k * 16, i, lane), ds, dk[i]);
         }
       }
+    };
+    if constexpr (PAIRED) {
+      block(half);
+    } else {
+      block(0);
+      block(1);
     }
+    buf = buf + 1 == STAGES ? 0 : buf + 1;
   }
-  if (j >= x.k_rows) return;
   const int64_t row = (x.k0 + j) * a.kv_heads + at.head;
   const int64_t plane = split * a.ki.n * a.kv_heads * a.D;
-  if (o.dk || o.dk_part)
-    store_columns<BF16>(dk, a.scale * range.back(), o.dk, o.dk_part ? o.dk_part + plane : nullptr, row, a.D, h);
-  if (o.dv || o.dv_part)
-    store_columns<BF16>(dv, 1.0f / Range<BF16>::kP, o.dv, o.dv_part ? o.dv_part + plane : nullptr, row, a.D, h);
+  auto finish = [&](float16v (&acc)[DB], float f, uint16_t* out, float* part_out) {
+    if (!out && !part_out) return;
+    if constexpr (PAIRED) {
+      // the second waves' sums, [part][register][lane]
+      float* const sums = reinterpret_cast<float*>(&smem[0][0][0]);
+      static_assert(4 * DB * 16 * 64 * 4 <= sizeof(smem), "sums fit the tiles");
+      __syncthreads();
+      if (half == 1) {
+#pragma unroll
+        for (int i = 0; i < DB; ++i)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) sums[((part * DB + i) * 16 + e) * 64 + lane] = acc[i][e] * f;
+      }
+      __syncthreads();
+      if (half == 1) return;
+#pragma unroll
+      for (int i = 0; i < DB; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[i][e] = acc[i][e] * f + sums[((part * DB + i) * 16 + e) * 64 + lane];
+      f = 1.0f;
+    }
+    if (j < x.k_rows) store_columns<BF16>(acc, f, out, part_out ? part_out + plane : nullptr, row, a.D, h);
+  };
+  finish(dk, a.scale * range.back(), o.dk, o.dk_part);
+  finish(dv, 1.0f / Range<BF16>::kP, o.dv, o.dv_part);
 }
 
 // ---- dispatch ----
@@ -360,7 +434,7 @@ int attention_backward(const Attention& a, const AttnGrad& g, bool bf16, Arena& 
   const int64_t items = a.qi.items, q_rows = a.qi.n * a.group * a.kv_heads, k_rows = a.ki.n * a.kv_heads;
   const int64_t mean_q = (a.qi.n + items - 1) / items, mean_k = (a.ki.n + items - 1) / items;
   AttnGrad o = g;
-  o.row_lse = static_cast<float*>(ws.take(q_rows * 4));
+  o.row_base = static_cast<float*>(ws.take(q_rows * 4));
   o.row_delta = static_cast<float*>(ws.take(q_rows * 4));
   PlaneList planes;
   auto join = [&](uint16_t*& out, float*& part, int64_t rows, int splits) {
@@ -388,7 +462,7 @@ int attention_backward(const Attention& a, const AttnGrad& g, bool bf16, Arena& 
       SUBMCONV_HIP_CHECK(hipGetLastError());
     }
     if (keys) {
-      k_attention_dkv<B, dp><<<static_cast<unsigned>(k_blocks), 256, 0, stream>>>(a, ok);
+      k_attention_dkv<B, dp><<<static_cast<unsigned>(k_blocks), dp > 64 ? 512 : 256, 0, stream>>>(a, ok);
       SUBMCONV_HIP_CHECK(hipGetLastError());
     }
     return SUBMCONV_OK;

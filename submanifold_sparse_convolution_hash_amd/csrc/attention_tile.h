@@ -96,6 +96,15 @@ struct TileLoad {
   }
 };
 
+// Waits for operands that were loaded to registers. Without it the compiler,
+// which does not count the loads to LDS, waits for all loads in flight at the
+// operands' first use, in every turn of a loop: the next tile's among them.
+template <int N>
+__device__ __forceinline__ void settle(half8 (&v)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+v"(v[i]));
+}
+
 // 4 bytes a lane, as load_to_lds.
 __device__ __forceinline__ void load_word_to_lds(rsrc4 r, uint32_t voff, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(
@@ -165,6 +174,28 @@ __device__ __forceinline__ Place place_of(int64_t b, int64_t slots, int heads) {
   const int rest = heads % 8;
   b -= full * 8 * slots;
   return Place{b / rest, full * 8 + static_cast<int>(b % rest)};
+}
+
+// A workgroup's tile and split, longest walks first: a tile sees the more keys
+// the further behind it lies in its item under the causal mask (of_keys: a tile
+// of keys is seen by the more queries the further it lies from the item's end).
+// Without it all of an item's walks are as long.
+struct Walk {
+  ItemTile t;
+  int split;
+};
+__device__ __forceinline__ Walk walk_of(const Items& it, int64_t per, int shift, int64_t slots, int splits,
+                                        int64_t slot, bool causal, bool of_keys) {
+  Walk w;
+  if (causal && it.items > 1 && it.items <= kOrderedItems) {
+    w.t = find_item_longest(it, per, shift, slot / splits, of_keys);
+    w.split = static_cast<int>(slot % splits);
+    return w;
+  }
+  const int64_t s = of_keys ? slot : slots - 1 - slot;
+  w.t = find_item(it, per, shift, s / splits);
+  w.split = static_cast<int>(s % splits);
+  return w;
 }
 
 // Registers i and i + 4 .. of a result's rows (4 of them each), rounded: lane c

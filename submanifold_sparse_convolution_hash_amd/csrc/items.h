@@ -70,5 +70,53 @@ __device__ __forceinline__ ItemTile find_item(const Items& it, int64_t per, int 
   return r;
 }
 
+// The same tiles in the order of their place in their item, `from_end` counted
+// from the last tile, furthest first: the order of work under a causal mask, so
+// that the longest walks start first whatever the items' lengths. index: 0 ..;
+// the rows of no item come last. Up to 64 items: one a lane.
+constexpr int kOrderedItems = 64;
+__device__ __forceinline__ ItemTile find_item_longest(const Items& it, int64_t per, int shift, int64_t index,
+                                                      bool from_end) {
+  const int lane = threadIdx.x & 63;
+  int n = 0;  // tiles of item `lane`
+  if (lane < it.items) {
+    const int64_t s = item_start(it, lane), e = item_start(it, lane + 1);
+    if (e > s) n = static_cast<int>(((e - s) * per + (int64_t{1} << shift) - 1) >> shift);
+  }
+  int most = 0, total = 0;
+  for (int i = 0; i < it.items; ++i) {
+    const int v = __builtin_amdgcn_readlane(n, i);
+    most = max(most, v);
+    total += v;
+  }
+  ItemTile r;
+  if (index >= total) {
+    r.item = it.items;
+    r.tile = index - total;
+  } else {
+    // tiles whose place is past p; the smallest p with at most `index` of them
+    auto past = [&](int p) {
+      int sum = 0;
+      for (int i = 0; i < it.items; ++i) sum += max(0, __builtin_amdgcn_readlane(n, i) - p);
+      return sum;
+    };
+    int lo = 0, hi = most;  // past(lo) > index >= past(hi)
+    while (hi - lo > 1) {
+      const int step = (hi - lo + 63) / 64, p = lo + (lane + 1) * step;
+      const int c = __popcll(__ballot(p < hi && past(p) > index));
+      lo += c * step;
+      hi = min(hi, lo + step);
+    }
+    uint64_t have = __ballot(n >= hi);  // (hi >= 1: lanes without an item have none)
+    for (int k = static_cast<int>(index) - past(hi); k > 0; --k) have &= have - 1;
+    r.item = __builtin_amdgcn_readfirstlane(__ffsll(static_cast<unsigned long long>(have)) - 1);
+    r.tile = from_end ? __builtin_amdgcn_readlane(n, r.item) - hi : hi - 1;
+  }
+  const int64_t s = item_start(it, r.item), e = item_start(it, r.item + 1);
+  r.row0 = s;
+  r.rows = e > s ? e - s : 0;
+  return r;
+}
+
 }  // namespace
 }  // namespace submconv
