@@ -712,7 +712,8 @@ int submconv_group_norm_backward(const void* grad_out, int64_t ldg, const void* 
 
 /*
  * submconv_rotary -- turns pairs of columns by the angle of their row's
- * position. x [n,heads,dim] of `dtype` (fp16, bf16 or fp32) with ldx elements
+ * position. x [n,heads,dim] of `dtype` (fp16, bf16 or fp32; up to 65536 heads,
+ * dim up to 8192) with ldx elements
  * between rows and hx between heads; out likewise, and may be x itself with
  * the same strides. positions int32, ldp elements between rows, ap between the
  * `axes` (1 to 4) of a row; freqs [nfreqs] fp64, radians per position. Pair p =
