@@ -112,18 +112,32 @@ __global__ __launch_bounds__(NW * 64, NW == 1 ? 1 : 2) void k_attention_dq(Atten
   const int64_t rows = static_cast<int64_t>(x.q_rows) * a.group, r_first = t.tile * T;
   if (t.tile < 0 || r_first >= rows) return;
 
-  const int64_t r = r_first + wave * 32 + (lane & 31);
-  const bool live = r < rows;
-  const int32_t token = static_cast<int32_t>((live ? r : rows - 1) / a.group);
-  const int head = at.head * a.group + static_cast<int>((live ? r : rows - 1) % a.group);
+  const TileRows at_row(r_first, rows, T, a.group);
+  const int i = wave * 32 + (lane & 31);
+  const bool live = i < at_row.count;
+  const int32_t token = at_row.token(i);
+  const int head = at.head * a.group + at_row.head(i);
   const int32_t see = keys_of(a, x, token);
-  const int32_t see_least = keys_of(a, x, static_cast<int32_t>(min(r_first + wave * 32, rows - 1) / a.group));
-  const int32_t see_most = keys_of(a, x, static_cast<int32_t>((min(r_first + T, rows) - 1) / a.group));
+  const int32_t see_least = keys_of(a, x, at_row.token(wave * 32));  // of the wave's rows: the first's
+  const int32_t see_wave = keys_of(a, x, at_row.token(wave * 32 + 31));
+  const int32_t see_most = keys_of(a, x, at_row.token(T - 1));
   const int tiles = o.dq || o.dq_part ? (see_most + kTileKeys - 1) / kTileKeys : 0;
   const int first = static_cast<int>(static_cast<int64_t>(tiles) * split / o.splits);
   const int last = static_cast<int>(static_cast<int64_t>(tiles) * (split + 1) / o.splits);
   const int64_t heads = static_cast<int64_t>(a.kv_heads) * a.group, row = (x.q0 + token) * heads + head;
 
+  const HeadRows kr{a.k.p + x.k0 * a.k.ld + at.head * a.k.hs, a.k.ld, x.Lk};
+  const HeadRows vr{a.v.p + x.k0 * a.v.ld + at.head * a.v.hs, a.v.ld, x.Lk};
+  L lk, lv;
+  lk.init(a.k.ld, a.D, wave, lane);
+  lv.init(a.v.ld, a.D, wave, lane);
+  const uint32_t lds = lds_addr(&smem[0][0][0]);
+  auto issue = [&](int tile) {
+    const uint32_t to = lds + (tile & 1) * 2 * H::BYTES;
+    lk.issue(kr, static_cast<int64_t>(tile) * kTileKeys, a.D, to, wave);
+    lv.issue(vr, static_cast<int64_t>(tile) * kTileKeys, a.D, to + H::BYTES, wave);
+  };
+  if (first < last) issue(first);  // on its way beside the rows' operands
   half8 q[KS], dy[KS];
   float delta = 0.0f;
   {
@@ -151,27 +165,15 @@ __global__ __launch_bounds__(NW * 64, NW == 1 ? 1 : 2) void k_attention_dq(Atten
     o.row_base[head * a.qi.n + x.q0 + token] = base;
     o.row_delta[head * a.qi.n + x.q0 + token] = delta;
   }
-  if (!o.dq && !o.dq_part) return;
+  if (!o.dq && !o.dq_part) return;  // (then there is no tile to wait for either)
   settle(q);
   settle(dy);
-  const HeadRows kr{a.k.p + x.k0 * a.k.ld + at.head * a.k.hs, a.k.ld, x.Lk};
-  const HeadRows vr{a.v.p + x.k0 * a.v.ld + at.head * a.v.hs, a.v.ld, x.Lk};
-  L lk, lv;
-  lk.init(a.k.ld, a.D, wave, lane);
-  lv.init(a.v.ld, a.D, wave, lane);
-  const uint32_t lds = lds_addr(&smem[0][0][0]);
-  auto issue = [&](int tile) {
-    const uint32_t to = lds + (tile & 1) * 2 * H::BYTES;
-    lk.issue(kr, static_cast<int64_t>(tile) * kTileKeys, a.D, to, wave);
-    lv.issue(vr, static_cast<int64_t>(tile) * kTileKeys, a.D, to + H::BYTES, wave);
-  };
   const float c = a.scale * kLog2e;
   asm volatile("" : "+v"(base), "+v"(delta));
   Range<BF16> range;
   float16v acc[DB];
 #pragma unroll
   for (int j = 0; j < DB; ++j) acc[j] = float16v{};
-  if (first < last) issue(first);
   for (int tile = first; tile < last; ++tile) {
     // this tile has landed and all waves are past the last one
     wait_loads<0>();
@@ -182,6 +184,8 @@ __global__ __launch_bounds__(NW * 64, NW == 1 ? 1 : 2) void k_attention_dq(Atten
     const char* tv = smem[tile & 1][1];
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
+      const int j0 = tile * kTileKeys + b * 32;
+      if (j0 >= see_wave) break;  // no row of this wave sees the block
       float16v s = {}, dp = {};
 #pragma unroll
       for (int kk = 0; kk < KS; ++kk) {
@@ -190,7 +194,6 @@ __global__ __launch_bounds__(NW * 64, NW == 1 ? 1 : 2) void k_attention_dq(Atten
       }
 #pragma unroll
       for (int i = 0; i < 16; ++i) s[i] = __builtin_amdgcn_exp2f(s[i] * c + base) * (dp[i] - delta);
-      const int j0 = tile * kTileKeys + b * 32;
       if (j0 + 32 > see_least) {
 #pragma unroll
         for (int i = 0; i < 16; ++i)
@@ -253,24 +256,6 @@ __global__ __launch_bounds__(DP > 64 ? 512 : 256, 2) void k_attention_dkv(Attent
   const int first = static_cast<int>(static_cast<int64_t>(walk) * split / o.splits);
   const int last = static_cast<int>(static_cast<int64_t>(walk) * (split + 1) / o.splits);
 
-  half8 kf[KS], vf[PAIRED ? 1 : KS];
-  {
-    const int64_t at_key = seen ? j : 0;
-    const uint16_t* pk = a.k.p + (x.k0 + at_key) * a.k.ld + at.head * a.k.hs;
-    const uint16_t* pv = a.v.p + (x.k0 + at_key) * a.v.ld + at.head * a.v.hs;
-#pragma unroll
-    for (int kk = 0; kk < KS; ++kk) {
-      const int c = kk * 16 + h * 8;
-      kf[kk] = half8{};
-      if (seen && c < a.D) kf[kk] = *reinterpret_cast<const half8*>(pk + c);
-      if constexpr (!PAIRED) {
-        vf[kk] = half8{};
-        if (seen && c < a.D) vf[kk] = *reinterpret_cast<const half8*>(pv + c);
-      }
-    }
-  }
-  settle(kf);
-  if constexpr (!PAIRED) settle(vf);
   L lq, ld;
   lq.init(a.q.ld, a.D, wave, lane);
   ld.init(o.dout.ld, a.D, wave, lane);
@@ -325,6 +310,24 @@ __global__ __launch_bounds__(DP > 64 ? 512 : 256, 2) void k_attention_dkv(Attent
       issue(ahead.head, ahead.tile, i);
       next(ahead);
     }
+  half8 kf[KS], vf[PAIRED ? 1 : KS];
+  {
+    const int64_t at_key = seen ? j : 0;
+    const uint16_t* pk = a.k.p + (x.k0 + at_key) * a.k.ld + at.head * a.k.hs;
+    const uint16_t* pv = a.v.p + (x.k0 + at_key) * a.v.ld + at.head * a.v.hs;
+#pragma unroll
+    for (int kk = 0; kk < KS; ++kk) {
+      const int c = kk * 16 + h * 8;
+      kf[kk] = half8{};
+      if (seen && c < a.D) kf[kk] = *reinterpret_cast<const half8*>(pk + c);
+      if constexpr (!PAIRED) {
+        vf[kk] = half8{};
+        if (seen && c < a.D) vf[kk] = *reinterpret_cast<const half8*>(pv + c);
+      }
+    }
+  }
+  settle(kf);
+  if constexpr (!PAIRED) settle(vf);
   int buf = 0;
   for (int u = first; u < last; ++u) {
     // this tile has landed (the next one may still be on its way) and all waves

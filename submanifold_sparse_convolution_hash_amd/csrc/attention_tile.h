@@ -151,6 +151,24 @@ __device__ __forceinline__ Extent extent_of(const Attention& a, int item) {
   return x;
 }
 
+// Rows of a tile, row = token group + head of the group: `count` of them from the
+// tile's first on (32-bit divisions but for the first).
+struct TileRows {
+  int64_t token0;
+  uint32_t rest, group;
+  int count;
+  __device__ __forceinline__ TileRows(int64_t first, int64_t rows, int most, int32_t group_)
+      : token0(group_ == 1 ? first : first / group_),
+        rest(static_cast<uint32_t>(first - token0 * group_)),
+        group(static_cast<uint32_t>(group_)),
+        count(static_cast<int>(min(rows - first, static_cast<int64_t>(most)))) {}
+  // of the tile's row i, or its last one
+  __device__ __forceinline__ int32_t token(int i) const {
+    return static_cast<int32_t>(token0) + static_cast<int32_t>((rest + min(i, count - 1)) / group);
+  }
+  __device__ __forceinline__ int head(int i) const { return static_cast<int>((rest + min(i, count - 1)) % group); }
+};
+
 // Number of the item's keys that its token sees.
 __device__ __forceinline__ int32_t keys_of(const Attention& a, const Extent& x, int32_t token) {
   if (!a.causal) return x.Lk;
