@@ -31,7 +31,7 @@ __all__ = [
     "gated_ffn_backward", "LayerNormFunction", "LinearFunction", "GatedFeedForwardFunction", "LayerNorm",
     "Linear", "GatedFeedForward", "SparseConvBlock", "item_offsets", "group_norm", "group_norm_backward", "rotary",
     "rotary_frequencies", "attention", "attention_backward", "GroupNormFunction", "RotaryFunction",
-    "AttentionFunction", "GroupNorm",
+    "AttentionFunction", "GroupNorm", "SparseAttention", "SparseAttentionBlock",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -674,6 +674,6 @@ from .dense import (  # noqa: E402  (dense.py uses this module's helpers)
     GatedFeedForward, GatedFeedForwardFunction, LayerNorm, LayerNormFunction, Linear, LinearFunction, gated_ffn,
     gated_ffn_backward, layer_norm, layer_norm_backward, linear, linear_backward)
 from .packed import (  # noqa: E402
-    AttentionFunction, GroupNorm, GroupNormFunction, RotaryFunction, attention, attention_backward, group_norm,
-    group_norm_backward, item_offsets, rotary, rotary_frequencies)
-from .blocks import SparseConvBlock  # noqa: E402
+    AttentionFunction, GroupNorm, GroupNormFunction, RotaryFunction, SparseAttention, attention, attention_backward,
+    group_norm, group_norm_backward, item_offsets, rotary, rotary_frequencies)
+from .blocks import SparseAttentionBlock, SparseConvBlock  # noqa: E402

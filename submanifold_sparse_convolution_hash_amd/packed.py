@@ -21,12 +21,12 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import _DTYPES, SubmconvError
-from .dense import (_INT32_MAX, _NORM_DTYPES, _act, _call, _dense, _init_matrix, _optional, _ptr, _recorded, _rows,
+from .dense import (_INT32_MAX, _NORM_DTYPES, Linear, _act, _call, _dense, _optional, _ptr, _recorded, _rows,
                     _workspace)
 
 __all__ = [
     "item_offsets", "group_norm", "group_norm_backward", "rotary", "rotary_frequencies", "attention",
-    "attention_backward", "GroupNormFunction", "RotaryFunction", "AttentionFunction", "GroupNorm",
+    "attention_backward", "GroupNormFunction", "RotaryFunction", "AttentionFunction", "GroupNorm", "SparseAttention",
 ]
 
 
@@ -265,7 +265,7 @@ def _attention_args(q, k, v, offsets, k_offsets, k_lengths, scale):
         raise ValueError(f"{heads} query heads do not share {kv_heads} key heads")
     items = _items(offsets, "offsets", dev)
     if k_offsets is None:
-        if nk != nq:
+        if nk != nq and offsets is not None:
             raise ValueError(f"{nq} queries and {nk} keys: k_offsets are needed")
         k_offsets = offsets
     elif _items(k_offsets, "k_offsets", dev) != items:
@@ -287,7 +287,8 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, offsets: Option
     strides in multiples of 8; Hq is a multiple of Hk, neighbouring query heads
     share a key head.
 
-    ``offsets`` are the queries' items, ``k_offsets`` the keys' (None: the same),
+    ``offsets`` are the queries' items, ``k_offsets`` the keys' (None: the same, or
+    with no offsets either one item of all queries and all keys),
     ``k_lengths`` [items] int32 how many of an item's keys are there (None: all; a
     cache with room). ``causal``: the last query of an item sees all of its keys,
     each earlier one a key less; the keys and values that a query does not see
@@ -397,3 +398,74 @@ class GroupNorm(torch.nn.Module):
         if _recorded(x, self.weight, self.bias):
             return GroupNormFunction.apply(x, self.weight, self.bias, self.groups, self.eps, self.act, offsets)
         return group_norm(x, self.groups, self.weight, self.bias, self.eps, self.act, offsets)
+
+
+class SparseAttention(torch.nn.Module):
+    """Attention with its projections on the rows of packed items: among an item's
+    rows, or, with ``context`` (its row width), over an item's rows of another
+    tensor. ``channels`` is the row width, ``heads`` of ``dim`` columns (default
+    channels / heads), ``kv_heads`` (default heads) of keys and values. With
+    ``rotary`` columns of a head and ``axes`` coordinates, queries and keys are
+    turned by their rows' positions (not over a context)."""
+
+    def __init__(self, channels: int, heads: int, dim: Optional[int] = None, kv_heads: Optional[int] = None,
+                 context: Optional[int] = None, rotary: int = 0, axes: int = 3, causal: bool = False,
+                 interleaved: bool = True, device=None, dtype=torch.float16):
+        super().__init__()
+        kv_heads = heads if kv_heads is None else kv_heads
+        if dim is None:
+            if channels % heads:
+                raise ValueError(f"{channels} channels do not make {heads} heads")
+            dim = channels // heads
+        if heads < 1 or kv_heads < 1 or heads % kv_heads:
+            raise ValueError(f"{heads} query heads do not share {kv_heads} key heads")
+        if dim < 8 or dim > 128 or dim % 8:
+            raise ValueError(f"{dim} columns a head: multiples of 8 up to 128 are supported")
+        if rotary > dim or rotary and context is not None:
+            raise ValueError(f"{rotary} of {dim} columns turn" + (" over a context" if context is not None else ""))
+        self.heads, self.kv_heads, self.dim, self.causal, self.interleaved = heads, kv_heads, dim, causal, interleaved
+        self.own = context is None
+        if self.own:
+            self.proj_in = Linear(channels, (heads + 2 * kv_heads) * dim, device=device, dtype=dtype)
+        else:
+            self.proj_in = Linear(channels, heads * dim, device=device, dtype=dtype)
+            self.proj_context = Linear(context, 2 * kv_heads * dim, device=device, dtype=dtype)
+        self.proj_out = Linear(heads * dim, channels, device=device, dtype=dtype)
+        self.register_buffer("freqs", rotary_frequencies(rotary, axes, device=device) if rotary else None)
+
+    def _apply(self, fn, recurse=True):
+        freqs = self.freqs
+        super()._apply(fn, recurse)
+        if freqs is not None:  # moves with the module, and stays in 64 bits whatever its type
+            self.freqs = freqs.to(self.freqs.device)
+        return self
+
+    def forward(self, x: torch.Tensor, offsets: Optional[torch.Tensor] = None,
+                positions: Optional[torch.Tensor] = None, context: Optional[torch.Tensor] = None,
+                context_offsets: Optional[torch.Tensor] = None, residual: Optional[torch.Tensor] = None) -> torch.Tensor:
+        h, hk, d = self.heads, self.kv_heads, self.dim
+        rows = self.proj_in(x).view(x.shape[0], -1, d)
+        if self.own:
+            q, k, v = rows[:, :h], rows[:, h:h + hk], rows[:, h + hk:]
+            if self.freqs is not None:
+                if positions is None:
+                    raise ValueError("positions are needed to turn queries and keys")
+                both = rows[:, :h + hk]
+                if _recorded(both):
+                    both = RotaryFunction.apply(both, positions, self.freqs, self.interleaved, 1.0)
+                else:
+                    rotary(both, positions, self.freqs, self.interleaved, out=both)
+                q, k = both[:, :h], both[:, h:]
+            context_offsets = None
+        else:
+            if context is None:
+                raise ValueError("a context is needed")
+            q = rows
+            k, v = self.proj_context(context).view(context.shape[0], 2 * hk, d).split([hk, hk], 1)
+            if context_offsets is None and offsets is not None:
+                raise ValueError("context_offsets are needed")
+        if _recorded(q, k, v):
+            out = AttentionFunction.apply(q, k, v, offsets, context_offsets, None, self.causal, None)
+        else:
+            out = attention(q, k, v, offsets, context_offsets, None, self.causal)
+        return self.proj_out(out.view(x.shape[0], h * d), residual=residual)

@@ -148,3 +148,13 @@ def test_group_norm_module_records_only_where_something_requires_a_gradient(monk
         packed.GroupNorm(3, 8)
     with pytest.raises(ValueError):
         packed.GroupNorm(2, 8, act="other")
+
+
+@pytest.mark.parametrize("kw", [dict(heads=3), dict(heads=4, kv_heads=3), dict(heads=0), dict(heads=16, dim=4),
+                                dict(heads=2, dim=136), dict(heads=4, dim=20), dict(heads=4, rotary=18),
+                                dict(heads=4, rotary=10), dict(heads=4, rotary=12, context=8)])
+def test_attention_module_refuses(kw):
+    import submanifold_sparse_convolution_hash_amd as sc
+
+    with pytest.raises((ValueError, ZeroDivisionError)):
+        sc.SparseAttention(64, **kw)
