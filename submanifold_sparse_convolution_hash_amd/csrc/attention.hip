@@ -45,7 +45,7 @@ __global__ __launch_bounds__(NW * 64, NW == 1 ? 1 : 2) void k_attention(Attentio
   __shared__ __attribute__((aligned(16))) char smem[2][2][H::BYTES];
   const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const Place at = place_of(blockIdx.x, o.slots, a.kv_heads);
+  const Place at = place_of(blockIdx.x, o.slots, a.kv_heads, a.causal, true);
   const Walk w = walk_of(a.qi, a.group, SHIFT, o.slots, o.splits, at.slot, a.causal, false);
   const ItemTile t = w.t;
   const int split = w.split;
@@ -198,51 +198,58 @@ __global__ __launch_bounds__(NW * 64, NW == 1 ? 1 : 2) void k_attention(Attentio
 }
 
 // Joins the splits: o = sum_s w_s o_s, w_s = exp(lse_s - lse). A wave has one row
-// of [nq heads]: lane s the weight of split s, then pieces of four columns, the
-// splits shared among up to eight groups of lanes, whose loads are all on their way
-// before the weights are known. 128 rows of 64 columns, 32 splits: 4.6 us
+// of [nq heads]: its lanes the weights of the splits, then pieces of four columns,
+// the splits shared among up to eight groups of lanes, whose first loads are on
+// their way before the weights are known. 128 rows of 64 columns, 32 splits: 4.6 us
 // (16 splits joined by a thread per four columns: 7.2).
-constexpr int kMostSplits = 64, kJoinGroups = 8;
+constexpr int kJoinGroups = 8;
 template <bool BF16>
 __global__ __launch_bounds__(256) void k_attention_join(const float* __restrict__ part,
                                                         const float* __restrict__ part_lse, int64_t rows, int D,
                                                         int splits, uint16_t* __restrict__ out,
                                                         float* __restrict__ lse) {
-  constexpr int AHEAD = kMostSplits / kJoinGroups;
-  const int lane = threadIdx.x & 63;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
+  constexpr int AHEAD = 8, PER = kMostSplits / 64;
+  __shared__ float weights[4][kMostSplits];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + wave;
   if (row >= rows) return;
   const int pieces = D / 4, groups = min(64 / pieces, kJoinGroups);
   const int piece = lane % pieces, group = lane / pieces;
   const bool on = group < groups;
-  const float l = lane < splits ? part_lse[lane * rows + row] : -kInf;
+  float l[PER], top = -kInf, total = 0.0f;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    l[i] = lane + i * 64 < splits ? part_lse[(lane + i * 64) * rows + row] : -kInf;
+    top = fmaxf(top, l[i]);
+  }
+  auto load = [&](int s) {
+    return on && s < splits ? *reinterpret_cast<const float4v*>(part + (s * rows + row) * D + piece * 4) : float4v{};
+  };
   float4v u[AHEAD];
 #pragma unroll
-  for (int i = 0; i < AHEAD; ++i) {
-    const int s = group + i * groups;
-    u[i] = float4v{};
-    if (on && s < splits) u[i] = *reinterpret_cast<const float4v*>(part + (s * rows + row) * D + piece * 4);
-  }
-  float top = l;
+  for (int i = 0; i < AHEAD; ++i) u[i] = load(group + i * groups);
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
-  const float w = __builtin_amdgcn_exp2f((l - (top == -kInf ? 0.0f : top)) * kLog2e);
-  const float total = lanes_sum<64>(w);
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const float w = __builtin_amdgcn_exp2f((l[i] - (top == -kInf ? 0.0f : top)) * kLog2e);
+    weights[wave][lane + i * 64] = w;  // read by this wave alone
+    total += w;
+  }
+  total = lanes_sum<64>(total);
   float4v v = {};
-  for (int i = 0; i * groups < splits; ++i) {
-    const int s = group + i * groups;
-    const float f = __shfl(w, s & 63, 64);
-    float4v t = u[0];
-    if (i >= AHEAD) {  // fewer groups than eight: wide heads
-      t = float4v{};
-      if (on && s < splits) t = *reinterpret_cast<const float4v*>(part + (s * rows + row) * D + piece * 4);
-    } else {
+  for (int i = 0; i * groups < splits; i += AHEAD) {
 #pragma unroll
-      for (int k = 1; k < AHEAD; ++k)
-        if (i == k) t = u[k];
+    for (int k = 0; k < AHEAD; ++k) {
+      const int s = group + (i + k) * groups;
+      const float f = s < splits ? weights[wave][s] : 0.0f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] += s < splits ? f * u[k][e] : 0.0f;
     }
+    if ((i + AHEAD) * groups < splits) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] += s < splits ? f * t[e] : 0.0f;
+      for (int k = 0; k < AHEAD; ++k) u[k] = load(group + (i + AHEAD + k) * groups);
+    }
   }
   const float inv = total > 0.0f ? 1.0f / total : total == 0.0f ? 0.0f : total;
 #pragma unroll
@@ -262,18 +269,20 @@ struct Plan {
   int64_t slots;
 };
 
-// One wave a workgroup where the items have few rows on average, else four. The
-// keys are split over workgroups where the tiles alone leave units idle: two
-// workgroups of four waves a unit, or eight of one, whose loads wait for each
-// other; each with at least four tiles of keys on average, or two.
+// One wave a workgroup where the items have at most 32 rows on average, else four,
+// two workgroups a unit: a step of 64 keys takes them 0.8 us at 64 columns and 1.2
+// at 128. A single wave waits for its loads, 1.3 to 1.6 us a step; as many
+// workgroups of one run on a unit at once as its LDS holds their tiles.
 Plan plan_of(const Attention& a) {
   Plan p;
   const int64_t mean_rows = (a.qi.n * a.group + a.qi.items - 1) / a.qi.items;
   p.waves = mean_rows <= 32 ? 1 : 4;
-  const int64_t tile = p.waves * 32, tiles = (mean_rows + tile - 1) / tile * a.qi.items;
-  const int64_t key_tiles = (a.ki.n / a.qi.items + kTileKeys - 1) / kTileKeys;
-  const int64_t want = (p.waves == 1 ? 2048 : 512) / std::max<int64_t>(1, tiles * a.kv_heads);
-  p.splits = static_cast<int>(std::clamp<int64_t>(std::min(want, key_tiles / (p.waves == 1 ? 2 : 4)), 1, kMostSplits));
+  const int64_t tile = p.waves * 32;
+  const int64_t tiles = std::max<int64_t>(1, (mean_rows + tile - 1) / tile * a.qi.items * a.kv_heads);
+  const int64_t steps = (a.ki.n / a.qi.items + kTileKeys - 1) / kTileKeys;
+  const int64_t floats = a.qi.n * a.group * a.kv_heads * a.D;
+  if (p.waves == 1) p.splits = splits_of(tiles, steps, 1.0 + 0.005 * a.D, a.D > 64 ? 512 : a.D > 32 ? 1280 : 2560, floats);
+  else p.splits = splits_of(tiles, steps, 0.35 + 0.0066 * a.D, 512, floats);
   p.slots = item_slots(a.qi, a.group, p.waves == 1 ? 5 : 7) * p.splits;
   return p;
 }
