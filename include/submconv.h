@@ -731,7 +731,7 @@ int submconv_rotary(const void* x, int64_t ldx, int64_t hx, int64_t n, int32_t h
 
 /* Workspace of submconv_attention (0 is possible); negative on a bad argument. */
 int64_t submconv_attention_workspace_bytes(int64_t nq, int64_t nk, int32_t heads, int32_t kv_heads,
-                                           int32_t dim, int32_t items);
+                                           int32_t dim, int32_t items, int32_t causal);
 
 /*
  * submconv_attention -- out = softmax(scale q k^T) v of each item's queries
@@ -757,7 +757,8 @@ int submconv_attention(const uint16_t* q, int64_t ldq, int64_t hq, int64_t nq, c
 
 /* Workspace of submconv_attention_backward with every gradient asked for. */
 int64_t submconv_attention_backward_workspace_bytes(int64_t nq, int64_t nk, int32_t heads,
-                                                    int32_t kv_heads, int32_t dim, int32_t items);
+                                                    int32_t kv_heads, int32_t dim, int32_t items,
+                                                    int32_t causal);
 
 /*
  * submconv_attention_backward -- with p = exp(scale q k^T - lse), dp = grad_out

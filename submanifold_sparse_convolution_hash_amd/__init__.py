@@ -128,10 +128,10 @@ def load_library():
                                           I64, P], ctypes.c_int),
         "submconv_rotary": ([P, I64, I64, I64, I32, I32, P, I64, I64, I32, P, I32, I32, I32, ctypes.c_float, P, I64,
                              I64, I32, P], ctypes.c_int),
-        "submconv_attention_workspace_bytes": ([I64, I64, I32, I32, I32, I32], I64),
+        "submconv_attention_workspace_bytes": ([I64, I64, I32, I32, I32, I32, I32], I64),
         "submconv_attention": ([P, I64, I64, I64, P, I64, I64, P, I64, I64, I64, I32, I32, I32, P, P, P, I32,
                                 ctypes.c_float, I32, P, P, I32, P, I64, P], ctypes.c_int),
-        "submconv_attention_backward_workspace_bytes": ([I64, I64, I32, I32, I32, I32], I64),
+        "submconv_attention_backward_workspace_bytes": ([I64, I64, I32, I32, I32, I32, I32], I64),
         "submconv_attention_backward": ([P, I64, I64, P, P, P, I64, I64, I64, P, I64, I64, P, I64, I64, I64, I32, I32,
                                          I32, P, P, P, I32, ctypes.c_float, I32, P, P, P, I32, P, I64, P],
                                         ctypes.c_int),

@@ -281,8 +281,8 @@ Plan plan_of(const Attention& a) {
   const int64_t tiles = std::max<int64_t>(1, (mean_rows + tile - 1) / tile * a.qi.items * a.kv_heads);
   const int64_t steps = (a.ki.n / a.qi.items + kTileKeys - 1) / kTileKeys;
   const int64_t floats = a.qi.n * a.group * a.kv_heads * a.D;
-  if (p.waves == 1) p.splits = splits_of(tiles, steps, 1.0 + 0.005 * a.D, a.D > 64 ? 512 : a.D > 32 ? 1280 : 2560, floats);
-  else p.splits = splits_of(tiles, steps, 0.35 + 0.0066 * a.D, 512, floats);
+  if (p.waves == 1) p.splits = splits_of(tiles, steps, 1.0 + 0.005 * a.D, 1.0, seen_share(a), a.D > 64 ? 512 : a.D > 32 ? 1280 : 2560, floats);
+  else p.splits = splits_of(tiles, steps, 0.35 + 0.0066 * a.D, 1.4, seen_share(a), 512, floats);
   p.slots = item_slots(a.qi, a.group, p.waves == 1 ? 5 : 7) * p.splits;
   return p;
 }
@@ -360,11 +360,11 @@ int check_attention(const Attention& a, int64_t nq, int64_t nk, int32_t heads, i
 using namespace submconv;
 
 extern "C" int64_t submconv_attention_workspace_bytes(int64_t nq, int64_t nk, int32_t heads, int32_t kv_heads,
-                                                      int32_t dim, int32_t items) {
+                                                      int32_t dim, int32_t items, int32_t causal) {
   clear_error();
   const Attention a{{}, {}, {}, {reinterpret_cast<const int32_t*>(4), items, nq},
                     {reinterpret_cast<const int32_t*>(4), items, nk}, nullptr,
-                    kv_heads > 0 ? heads / kv_heads : 0, kv_heads, dim, 1.0f, 0};
+                    kv_heads > 0 ? heads / kv_heads : 0, kv_heads, dim, 1.0f, causal};
   SUBMCONV_TRY(check_attention(a, nq, nk, heads, SUBMCONV_DTYPE_F16));
   Arena ws;
   SUBMCONV_TRY(attention_forward(a, false, nullptr, nullptr, ws, nullptr));

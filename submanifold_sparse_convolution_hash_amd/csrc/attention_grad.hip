@@ -444,8 +444,9 @@ int attention_backward(const Attention& a, const AttnGrad& g, bool bf16, Arena& 
   // (steps of 64 keys or queries, measured: 1.1 and 1.6 us at 64 columns, 1.8 and 2.4 at 128)
   const int64_t q_tiles = (mean_q * a.group + 127) / 128 * items * a.kv_heads;
   const int64_t k_tiles = (mean_k + 127) / 128 * items * a.kv_heads;
-  oq.splits = splits_of(q_tiles, (mean_k + 63) / 64, 0.5 + 0.01 * a.D, 512, q_rows * a.D);
-  ok.splits = splits_of(k_tiles, (mean_q + 63) / 64 * a.group, 0.7 + 0.0132 * a.D, a.D > 96 ? 256 : 512, 2 * k_rows * a.D);
+  oq.splits = splits_of(q_tiles, (mean_k + 63) / 64, 0.5 + 0.01 * a.D, 1.0, seen_share(a), 512, q_rows * a.D);
+  ok.splits = splits_of(k_tiles, (mean_q + 63) / 64 * a.group, 0.7 + 0.0132 * a.D, 1.0, seen_share(a), a.D > 96 ? 256 : 512,
+                        2 * k_rows * a.D);
   oq.slots = item_slots(a.qi, a.group, 7) * oq.splits;
   ok.slots = item_slots(a.ki, 1, 7) * ok.splits;
   join(oq.dq, oq.dq_part, q_rows, oq.splits);
@@ -483,11 +484,12 @@ int attention_backward(const Attention& a, const AttnGrad& g, bool bf16, Arena& 
 using namespace submconv;
 
 extern "C" int64_t submconv_attention_backward_workspace_bytes(int64_t nq, int64_t nk, int32_t heads,
-                                                               int32_t kv_heads, int32_t dim, int32_t items) {
+                                                               int32_t kv_heads, int32_t dim, int32_t items,
+                                                               int32_t causal) {
   clear_error();
   const Attention a{{}, {}, {}, {reinterpret_cast<const int32_t*>(4), items, nq},
                     {reinterpret_cast<const int32_t*>(4), items, nk}, nullptr,
-                    kv_heads > 0 ? heads / kv_heads : 0, kv_heads, dim, 1.0f, 0};
+                    kv_heads > 0 ? heads / kv_heads : 0, kv_heads, dim, 1.0f, causal};
   SUBMCONV_TRY(check_attention(a, nq, nk, heads, SUBMCONV_DTYPE_F16));
   Arena ws;
   SUBMCONV_TRY(attention_backward(a, AttnGrad{}, false, ws, nullptr));

@@ -17,6 +17,8 @@
 // that order, and scores never leave the registers.
 #pragma once
 
+#include <algorithm>
+
 #include "dense_common.h"
 #include "dense_tile.h"
 #include "items.h"
@@ -255,25 +257,35 @@ __device__ __forceinline__ float halves_sum(float x) {
 
 // Into how many runs a walk is split, each to its own fp32 sums, which a last launch
 // joins: the least of what walks and joins take, as measured. `tiles` workgroups
-// start in 4 us and walk `steps` steps of step_us each, `places` of them at once;
-// the sums of one run are written and read at 2.5 TB/s, and the join's launch takes
+// start in 4 us and walk up to `steps` steps of step_us each, `seen` of them on
+// average (the causal mask), `places` of them at once, which then share their
+// units and take `full` times as long: what counts is the longest walk or all of
+// them in turn; the sums of one run are written and read at 2.5 TB/s, and the join's launch takes
 // 6 us. 300 rows of 8 heads of 64 on 4000 keys: 55 us in one run, 20 in eight; 2048
 // rows of 16 heads of 128: 48 in one, 70 in two.
 constexpr int kMostSplits = 256;
-inline int splits_of(int64_t tiles, int64_t steps, double step_us, int64_t places, int64_t run_floats) {
+inline int splits_of(int64_t tiles, int64_t steps, double step_us, double full, double seen,
+                     int64_t places, int64_t run_floats) {
   const double join_us = static_cast<double>(run_floats) * 8 / 2.5e6;
   int best = 1;
   double least = 0.0;
   for (int s = 1; s <= kMostSplits && (s == 1 || 2 * s <= steps); ++s) {
     const double rounds = static_cast<double>(tiles) * s / static_cast<double>(places);
-    const double us = (4.0 + static_cast<double>((steps + s - 1) / s) * step_us) * (rounds > 1.0 ? rounds : 1.0) +
-                      (s > 1 ? 6.0 + s * join_us : 0.0);
+    const double walk = static_cast<double>((steps + s - 1) / s) * step_us;
+    const double us = std::max(4.0 + walk, rounds * (4.0 + full * seen * walk)) + (s > 1 ? 6.0 + s * join_us : 0.0);
     if (s == 1 || us < least) {
       least = us;
       best = s;
     }
   }
   return best;
+}
+
+// The share of an item's pairs of rows and keys that are seen, on average.
+inline double seen_share(const Attention& a) {
+  const double q = static_cast<double>(a.qi.n), k = static_cast<double>(a.ki.n);
+  if (!a.causal || q < 1.0 || k < 1.0) return 1.0;
+  return k >= q ? 1.0 - 0.5 * q / k : 0.5 * k / q;
 }
 
 // Host side of the checks, shared by both directions.

@@ -299,7 +299,7 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, offsets: Option
     args, (nq, nk, heads, kv_heads, d, items) = _attention_args(q, k, v, offsets, k_offsets, k_lengths, scale)
     out = q.new_empty((nq, heads, d))
     lse = q.new_empty((nq, heads), dtype=torch.float32) if return_lse else None
-    ws, nb = _workspace("submconv_attention_workspace_bytes", q, nq, nk, heads, kv_heads, d, items)
+    ws, nb = _workspace("submconv_attention_workspace_bytes", q, nq, nk, heads, kv_heads, d, items, int(bool(causal)))
     _call(q.device, "submconv_attention", *args, int(bool(causal)), _ptr(out), _ptr(lse), _DTYPES[q.dtype], _ptr(ws),
           nb)
     return (out, lse) if return_lse else out
@@ -318,7 +318,8 @@ def attention_backward(grad_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor,
     gq = q.new_empty((nq, heads, d)) if needs[0] else None
     gk = q.new_empty((nk, kv_heads, d)) if needs[1] else None
     gv = q.new_empty((nk, kv_heads, d)) if needs[2] else None
-    ws, nb = _workspace("submconv_attention_backward_workspace_bytes", q, nq, nk, heads, kv_heads, d, items)
+    ws, nb = _workspace("submconv_attention_backward_workspace_bytes", q, nq, nk, heads, kv_heads, d, items,
+                        int(bool(causal)))
     _call(q.device, "submconv_attention_backward", _ptr(grad_out), ldg, hg, _ptr(out), _ptr(lse), *args,
           int(bool(causal)), _ptr(gq), _ptr(gk), _ptr(gv), _DTYPES[q.dtype], _ptr(ws), nb)
     return gq, gk, gv

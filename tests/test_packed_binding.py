@@ -104,9 +104,9 @@ def test_attention_refuses_more(lib):
     assert _attn(lib, True, nb=0) == -1 and _attn(lib, True, ws=None) == -1
     assert _attn(lib, nk=100000, nb=0) == -1  # the keys are split: a workspace is needed
     q = lib.submconv_attention_workspace_bytes
-    assert q(20000, 20000, 12, 12, 64, 1) == 0 and q(1, 30000, 16, 4, 64, 1) > 0
-    assert q(10, 10, 3, 2, 64, 1) == -1 and q(10, 10, 2, 2, 60, 1) == -4
-    assert lib.submconv_attention_backward_workspace_bytes(10, 10, 2, 0, 64, 1) == -1
+    assert q(20000, 20000, 12, 12, 64, 1, 0) == 0 and q(1, 30000, 16, 4, 64, 1, 1) > 0
+    assert q(10, 10, 3, 2, 64, 1, 0) == -1 and q(10, 10, 2, 2, 60, 1, 0) == -4
+    assert lib.submconv_attention_backward_workspace_bytes(10, 10, 2, 0, 64, 1, 0) == -1
 
 
 def test_host_tensors_are_refused():
