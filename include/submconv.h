@@ -657,7 +657,7 @@ int submconv_gated_ffn_backward(const uint16_t* grad_out, int64_t ldg, int64_t n
  * only: one item of all n rows. Rows from offsets[items] on belong to no item
  * and are written as zeros. Nothing waits for the offsets: they are not
  * checked, but cut to 0 .. n, so that no access leaves the tensors; if they
- * descend, the results mean nothing. items up to 65535, rows up to 2^31 - 1.
+ * descend, the results mean nothing. items up to 65535, rows up to 2^31 - 1025.
  * Everything else as for the dense layers: asynchronous, no allocation, sums
  * in one order, each stored value rounded once.
  * ---------------------------------------------------------------------- */
@@ -682,8 +682,7 @@ int64_t submconv_group_norm_workspace_bytes(int64_t n, int32_t cdim, int32_t gro
  * cdim / groups channels. x [n,cdim] of `dtype` (SUBMCONV_DTYPE_F16, _BF16 or
  * _F32), row stride ldx; y [n,cdim]. weight and bias [cdim] fp32, either NULL
  * for 1 and 0. mean and rstd [items,groups] fp32 receive m and r, either may be
- * NULL; an empty item has m = 0. cdim up to 8192. y may be x itself where ldx
- * is cdim.
+ * NULL; an empty item has m = 0. cdim up to 8192.
  */
 int submconv_group_norm(const void* x, int64_t ldx, int64_t n, int32_t cdim, int32_t groups,
                         const int32_t* offsets, int32_t items, const float* weight,
@@ -715,7 +714,7 @@ int submconv_group_norm_backward(const void* grad_out, int64_t ldg, const void* 
  * position. x [n,heads,dim] of `dtype` (fp16, bf16 or fp32; up to 65536 heads,
  * dim up to 8192) with ldx elements
  * between rows and hx between heads; out likewise, and may be x itself with
- * the same strides. positions int32, ldp elements between rows, ap between the
+ * the same strides, but not overlap it otherwise. positions int32, ldp elements between rows, ap between the
  * `axes` (1 to 4) of a row; freqs [nfreqs] fp64, radians per position. Pair p =
  * axis nfreqs + f turns by t = position[axis] freqs[f]:
  * (u, v) -> amplitude (u cos t - v sin t, v cos t + u sin t), by -t where

@@ -338,10 +338,13 @@ int check_strided(const char* name, const Strided& s, int64_t n, int32_t heads, 
   return SUBMCONV_OK;
 }
 
+// (a tile's row numbers past the last one stay within 32 bits)
+constexpr int64_t kMostRows = INT32_MAX - 1024;
+
 int check_attention(const Attention& a, int64_t nq, int64_t nk, int32_t heads, int32_t dtype) {
   if (dtype != SUBMCONV_DTYPE_F16 && dtype != SUBMCONV_DTYPE_BF16)
     return set_error(SUBMCONV_ERR_INVALID_ARG, "dtype = %d", dtype);
-  if (nq < 0 || nk < 0 || nq > INT32_MAX || nk > INT32_MAX)
+  if (nq < 0 || nk < 0 || nq > kMostRows || nk > kMostRows)
     return set_error(SUBMCONV_ERR_INVALID_ARG, "%lld queries, %lld keys", (long long)nq, (long long)nk);
   if (a.kv_heads < 1 || heads < a.kv_heads || heads % a.kv_heads || heads > 65536)
     return set_error(SUBMCONV_ERR_INVALID_ARG, "%d heads on %d key heads", heads, a.kv_heads);

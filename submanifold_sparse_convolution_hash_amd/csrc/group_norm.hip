@@ -192,39 +192,55 @@ __global__ __launch_bounds__(kGroupThreads) void k_group_moments(const T* __rest
   });
 }
 
-// A workgroup joins the chunks of one item and group, as chunk_moments its
-// threads' parts: up to kChunks of them, which a thread keeps in registers.
-constexpr int kChunks = 2049;
-__global__ __launch_bounds__(kGroupThreads) void k_group_join(const float2* __restrict__ partial, Items it, int G,
+// NT threads join the chunks of one item and group, as chunk_moments its threads'
+// parts: four waves up to kFewItems items, whose chunks they keep in registers,
+// else one wave, which reads most items' few chunks once and others' in turn.
+constexpr int kChunks = 2049, kFewItems = 16;
+template <int NT>
+__global__ __launch_bounds__(NT) void k_group_join(const float2* __restrict__ partial, Items it, int G,
                                                               int cpg, int shift, float eps,
                                                               float* __restrict__ mean, float* __restrict__ rstd) {
-  constexpr int MOST = (kChunks + kGroupThreads - 1) / kGroupThreads;
-  __shared__ float sums[2][kGroupThreads / 64];
+  constexpr int MOST = NT == 64 ? 1 : (kChunks + NT - 1) / NT;
+  __shared__ float sums[2][NT / 64];
   const int item = blockIdx.y, k = blockIdx.x;
   const int64_t s = item_start(it, item), e = item_start(it, item + 1);
   const int64_t rows = e > s ? e - s : 0, slot = (s >> shift) + item, chunk = int64_t{1} << shift;
-  auto all = [&](float v, float (&to)[kGroupThreads / 64]) {
+  auto all = [&](float v, float (&to)[NT / 64]) {
     v = lanes_sum<64>(v);
+    if constexpr (NT == 64) return v;
     if ((threadIdx.x & 63) == 0) to[threadIdx.x >> 6] = v;
     __syncthreads();
-    return (to[0] + to[1]) + (to[2] + to[3]);
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NT / 64; ++i) sum += to[i];
+    return sum;
   };
   float2 p[MOST];
-  float n[MOST], total = 0.0f, q = 0.0f;
+  float n[MOST];
+  auto read = [&](int64_t first) {
+#pragma unroll
+    for (int i = 0; i < MOST; ++i) {
+      const int64_t c = first + threadIdx.x + i * NT, left = rows - c * chunk;
+      n[i] = left > 0 ? static_cast<float>(min(chunk, left) * cpg) : 0.0f;
+      p[i] = left > 0 ? partial[(slot + c) * G + k] : float2{0.0f, 0.0f};
+    }
+  };
+  const bool once = rows <= MOST * NT * chunk;
   const float near = rows ? partial[slot * G + k].x : 0.0f;
+  float total = 0.0f, q = 0.0f;
+  for (int64_t first = 0; first * chunk < rows; first += MOST * NT) {
+    read(first);
 #pragma unroll
-  for (int i = 0; i < MOST; ++i) {
-    const int64_t c = threadIdx.x + i * kGroupThreads, left = rows - c * chunk;
-    n[i] = left > 0 ? static_cast<float>(min(chunk, left) * cpg) : 0.0f;
-    p[i] = left > 0 ? partial[(slot + c) * G + k] : float2{0.0f, 0.0f};
+    for (int i = 0; i < MOST; ++i) total += n[i] > 0.0f ? n[i] * (p[i].x - near) : 0.0f;
   }
-#pragma unroll
-  for (int i = 0; i < MOST; ++i) total += n[i] > 0.0f ? n[i] * (p[i].x - near) : 0.0f;
   const float inv = rows ? 1.0f / (static_cast<float>(rows) * static_cast<float>(cpg)) : 0.0f;
   const float m = near + all(total, sums[0]) * inv;
+  for (int64_t first = 0; first * chunk < rows; first += MOST * NT) {
+    if (!once) read(first);
 #pragma unroll
-  for (int i = 0; i < MOST; ++i)
-    if (n[i] > 0.0f) q += p[i].y + n[i] * ((p[i].x - m) * (p[i].x - m));
+    for (int i = 0; i < MOST; ++i)
+      if (n[i] > 0.0f) q += p[i].y + n[i] * ((p[i].x - m) * (p[i].x - m));
+  }
   q = all(q, sums[1]) * inv;
   if (threadIdx.x == 0) {
     const int64_t at = static_cast<int64_t>(item) * G + k;
@@ -534,13 +550,14 @@ __global__ __launch_bounds__(kGroupThreads, 4) void k_group_sums(const T* __rest
   });
 }
 
-// Sums of an item's chunks: 16 columns of the 2 C a workgroup, 64 chunks at a
+// Sums of an item's chunks: 16 columns of the 2 C a workgroup, NT / 16 chunks at a
 // time. sz and sx [items][C].
-constexpr int kJoinThreads = 1024, kJoinCols = 16;
-__global__ __launch_bounds__(kJoinThreads) void k_group_join_sums(const float* __restrict__ partial, Items it, int C,
+constexpr int kJoinCols = 16;
+template <int NT>
+__global__ __launch_bounds__(NT) void k_group_join_sums(const float* __restrict__ partial, Items it, int C,
                                                                   int shift, float* __restrict__ sz,
                                                                   float* __restrict__ sx) {
-  constexpr int LANES = kJoinThreads / kJoinCols;
+  constexpr int LANES = NT / kJoinCols;
   __shared__ float lds[LANES][kJoinCols];
   const int item = blockIdx.y, q = threadIdx.x % kJoinCols, t = threadIdx.x / kJoinCols;
   const int col = blockIdx.x * kJoinCols + q;
@@ -561,33 +578,19 @@ __global__ __launch_bounds__(kJoinThreads) void k_group_join_sums(const float* _
   else sx[static_cast<int64_t>(item) * C + col - C] = sum;
 }
 
-// dx of a chunk, and in workgroups from `slots` on 256 columns' dw and db, the
-// sums over the items.
+// dx of a chunk, the chunks from the last on (see k_group_apply).
 template <typename T>
 __global__ __launch_bounds__(kGroupThreads) void k_group_dx(const T* __restrict__ dy, int64_t ldg,
                                                             const T* __restrict__ x, int64_t ldx, Items it, int C,
-                                                            int cpg, Lanes g, int shift, int64_t slots,
+                                                            int cpg, Lanes g, int shift,
                                                             const float* __restrict__ mean,
                                                             const float* __restrict__ rstd,
                                                             const float* __restrict__ w, const float* __restrict__ b,
                                                             int act, const float* __restrict__ sz,
-                                                            const float* __restrict__ sx, T* __restrict__ dx,
-                                                            float* __restrict__ dw, float* __restrict__ db) {
+                                                            const float* __restrict__ sx, T* __restrict__ dx) {
   extern __shared__ float lds[];
   const int64_t G = C / cpg;
-  if (blockIdx.x >= slots) {
-    const int64_t c = (blockIdx.x - slots) * kGroupThreads + threadIdx.x;
-    if (c >= C) return;
-    float a = 0.0f, q = 0.0f;
-    for (int64_t i = 0; i < it.items; ++i) {
-      a += sz[i * C + c];
-      q += sx[i * C + c];
-    }
-    if (dw) dw[c] = q;
-    if (db) db[c] = a;
-    return;
-  }
-  const ItemTile t = find_item(it, 1, shift, slots - 1 - blockIdx.x);
+  const ItemTile t = find_item(it, 1, shift, gridDim.x - 1 - blockIdx.x);
   const int64_t r0 = t.tile << shift;
   if (t.tile < 0 || r0 >= t.rows) return;
   const int rows = static_cast<int>(min(t.rows - r0, int64_t{1} << shift));
@@ -719,11 +722,21 @@ int group_forward(const GroupShape& s, const void* xp, int64_t ldx, const float*
   k_group_moments<T><<<grid, kGroupThreads, lanes_lds(g, kVec<T>) * 4, stream>>>(x, ldx, s.it, s.C, s.cpg, g, shift,
                                                                                  partial);
   SUBMCONV_HIP_CHECK(hipGetLastError());
-  k_group_join<<<dim3(s.G, s.it.items), kGroupThreads, 0, stream>>>(partial, s.it, s.G, s.cpg, shift, eps, mean, rstd);
+  const dim3 join(s.G, s.it.items);
+  if (s.it.items <= kFewItems) k_group_join<256><<<join, 256, 0, stream>>>(partial, s.it, s.G, s.cpg, shift, eps, mean, rstd);
+  else k_group_join<64><<<join, 64, 0, stream>>>(partial, s.it, s.G, s.cpg, shift, eps, mean, rstd);
   SUBMCONV_HIP_CHECK(hipGetLastError());
   k_group_apply<T><<<grid, kGroupThreads, 0, stream>>>(x, ldx, s.it, s.C, s.cpg, g, shift, mean, rstd, w, b, act, y);
   SUBMCONV_HIP_CHECK(hipGetLastError());
   return SUBMCONV_OK;
+}
+
+// dw and db from the items' sums [items][C].
+int sum_items(const GroupShape& s, const float* sz, const float* sx, float* dw, float* db, hipStream_t stream) {
+  SumList list;
+  if (db) list.job[list.count++] = SumJob{sz, s.it.items, s.C, s.C, 1, db};
+  if (dw) list.job[list.count++] = SumJob{sx, s.it.items, s.C, s.C, 1, dw};
+  return list.count ? run_sums(list, stream) : SUBMCONV_OK;
 }
 
 template <typename T>
@@ -746,10 +759,7 @@ int group_backward(const GroupShape& s, const void* gp, int64_t ldg, const void*
     k_group_norm_grad<T><<<grid, kGroupThreads, lanes_lds(g, kVec<T>) * 4, stream>>>(
         dy, ldg, x, ldx, s.it, s.C, s.cpg, gpw, g, mean, rstd, w, b, act, dx, sz, sx);
     SUBMCONV_HIP_CHECK(hipGetLastError());
-    SumList list;
-    if (!one && db) list.job[list.count++] = SumJob{sz, s.it.items, s.C, s.C, 1, db};
-    if (!one && dw) list.job[list.count++] = SumJob{sx, s.it.items, s.C, s.C, 1, dw};
-    return list.count ? run_sums(list, stream) : SUBMCONV_OK;
+    return one ? SUBMCONV_OK : sum_items(s, sz, sx, dw, db, stream);
   }
   const Lanes g = lanes_of(s.C, kVec<T>);
   const int shift = chunk_shift(s.it.n, g.rl);
@@ -763,15 +773,15 @@ int group_backward(const GroupShape& s, const void* gp, int64_t ldg, const void*
       dy, ldg, x, ldx, s.it, s.C, s.cpg, g, shift, mean, rstd, w, b, act, partial);
   SUBMCONV_HIP_CHECK(hipGetLastError());
   const dim3 join((2 * s.C + kJoinCols - 1) / kJoinCols, s.it.items);
-  k_group_join_sums<<<join, kJoinThreads, 0, stream>>>(partial, s.it, s.C, shift, sz, sx);
+  if (s.it.items <= kFewItems) k_group_join_sums<1024><<<join, 1024, 0, stream>>>(partial, s.it, s.C, shift, sz, sx);
+  else k_group_join_sums<128><<<join, 128, 0, stream>>>(partial, s.it, s.C, shift, sz, sx);
   SUBMCONV_HIP_CHECK(hipGetLastError());
-  const int64_t rows = dx ? slots : 0, cols = !one && (dw || db) ? (s.C + kGroupThreads - 1) / kGroupThreads : 0;
-  if (rows + cols == 0) return SUBMCONV_OK;
-  k_group_dx<T><<<static_cast<unsigned>(rows + cols), kGroupThreads, 2 * s.G * 4, stream>>>(
-      dy, ldg, x, ldx, s.it, s.C, s.cpg, g, shift, rows, mean, rstd, w, b, act, sz, sx, dx, one ? nullptr : dw,
-      one ? nullptr : db);
-  SUBMCONV_HIP_CHECK(hipGetLastError());
-  return SUBMCONV_OK;
+  if (dx) {
+    k_group_dx<T><<<static_cast<unsigned>(slots), kGroupThreads, 2 * s.G * 4, stream>>>(
+        dy, ldg, x, ldx, s.it, s.C, s.cpg, g, shift, mean, rstd, w, b, act, sz, sx, dx);
+    SUBMCONV_HIP_CHECK(hipGetLastError());
+  }
+  return one ? SUBMCONV_OK : sum_items(s, sz, sx, dw, db, stream);
 }
 
 template <typename F>

@@ -226,10 +226,11 @@ int rotate(const void* x, void* out, Rotary a, bool interleaved, hipStream_t str
 int check_heads(const char* name, const void* p, int64_t n, int32_t heads, int32_t dim, int64_t ld, int64_t hs,
                 int32_t dtype) {
   if (n > 0 && !p) return set_error(SUBMCONV_ERR_INVALID_ARG, "%s is NULL", name);
-  if (heads > 1 && hs < dim)
-    return set_error(SUBMCONV_ERR_INVALID_ARG, "%s: head stride %lld below %d columns", name, (long long)hs, dim);
-  if (n > 1 && ld < (heads - 1) * (heads > 1 ? hs : 0) + dim)
-    return set_error(SUBMCONV_ERR_INVALID_ARG, "%s: row stride %lld below a row's columns", name, (long long)ld);
+  const bool rows_of_heads = hs >= dim && ld >= (heads - 1) * hs + dim;
+  const bool heads_of_rows = ld >= dim && hs >= (n - 1) * ld + dim;
+  if ((heads > 1 && hs < dim) || (n > 1 && ld < dim) || (heads > 1 && n > 1 && !rows_of_heads && !heads_of_rows))
+    return set_error(SUBMCONV_ERR_INVALID_ARG, "%s: rows or heads overlap with strides %lld and %lld", name,
+                     (long long)ld, (long long)hs);
   if (reinterpret_cast<uintptr_t>(p) & (dtype == SUBMCONV_DTYPE_F32 ? 3 : 1))
     return set_error(SUBMCONV_ERR_INVALID_ARG, "%s is not aligned to its elements", name);
   return SUBMCONV_OK;

@@ -170,10 +170,12 @@ def _heads(t, name: str, dtypes, like=None) -> Tuple[int, int]:
         if t.shape != like.shape:
             raise ValueError(f"{name} must be {list(like.shape)}, got {tuple(t.shape)}")
     ld, hs, inner = t.stride()
-    if n > 0 and (d > 1 and inner != 1 or h > 1 and hs < d or n > 1 and ld < (h - 1) * hs * (h > 1) + d):
+    ld, hs = ld if n > 1 else h * d, hs if h > 1 else d
+    apart = hs >= d and ld >= (h - 1) * hs + d or ld >= d and hs >= (n - 1) * ld + d  # rows of heads, or heads of rows
+    if n > 0 and (d > 1 and inner != 1 or h > 1 and n > 1 and not apart or min(ld, hs) < d):
         raise ValueError(f"{name}: a head's columns must be next to each other, heads and rows must not overlap, "
                          f"got strides {t.stride()}")
-    return (ld if n > 1 else h * d), (hs if h > 1 else d)
+    return ld, hs
 
 
 def rotary_frequencies(dim: int, axes: int = 1, base: float = 10000.0, scaling: Optional[str] = None,
@@ -209,12 +211,14 @@ def rotary_frequencies(dim: int, axes: int = 1, base: float = 10000.0, scaling: 
 def rotary(x: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor, interleaved: bool = False,
            inverse: bool = False, amplitude: float = 1.0, out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Turns the pairs of the first ``2 axes F`` columns of each head of ``x``
-    ([N,H,D] fp16, bf16 or fp32, heads and rows with any strides) by ``position *
+    ([N,H,D] fp16, bf16 or fp32, rows of heads or heads of rows, of a wider tensor as
+    well) by ``position *
     freq`` and copies the others. ``positions`` int32 [N], or [N,axes] (up to 4
     axes; a slice of sites' coordinates is fine), ``freqs`` fp64 [F] in radians
     (:func:`rotary_frequencies`): pair ``p = axis F + f``, columns (2p, 2p + 1) where
     ``interleaved``, else (p, axes F + p). ``inverse`` turns back, which is the
-    gradient; ``amplitude`` scales what is turned. ``out`` may be x itself."""
+    gradient; ``amplitude`` scales what is turned. ``out`` may be x itself, but not
+    overlap it otherwise."""
     ldx, hx = _heads(x, "x", _NORM_DTYPES)
     n, h, d = x.shape
     dev = x.device

@@ -110,7 +110,8 @@ NORMS = [([1], 0, 8, 1, 0), ([7], 0, 32, 32, 0), ([64, 0], 3, 256, 32, 0), ([20,
          ([0, 0], 4, 16, 2, 0), ([700, 321], 0, 128, 32, 8), ([1023], 1, 64, 1, 0), ([5] * 90, 0, 24, 8, 1),
          ([3000], 0, 128, 32, 0), ([1500, 0, 2500, 1], 77, 60, 12, 3), ([2100], 9, 33, 3, 1), ([1100, 5], 0, 515, 5, 0),
          ([1300], 0, 2056, 8, 0), ([900, 200], 0, 4100, 1, 2), ([1025], 0, 8192, 64, 0), ([700, 700], 3, 8192, 8192, 0),
-         ([0, 1200, 0], 100, 20, 20, 0), ([3] * 400, 1, 8, 2, 0), ([0], 0, 16, 4, 0)]
+         ([0, 1200, 0], 100, 20, 20, 0), ([3] * 400, 1, 8, 2, 0), ([0], 0, 16, 4, 0),
+         ([40] * 100 + [0, 1, 5000], 3, 96, 8, 0), ([2] * 3000, 5, 40, 5, 0)]
 
 
 def _joins(lengths, c, groups):
@@ -422,6 +423,93 @@ def test_attention(dev, case, dtype):
         needs = [i == need for i in range(3)]
         some = sc.attention_backward(do, q, k, v, out, lse, off, koff, causal=causal, scale=float(scale), needs=needs)
         assert [t is not None for t in some] == needs and torch.equal(some[need], grads[need])
+
+
+@gpu
+@pytest.mark.parametrize("causal", [False, True])
+def test_attention_heads_of_rows(dev, causal):
+    """Tensors stored head by head, and a single row or head with any stride, give
+    what rows of heads give."""
+    sc = _sc()
+    n, h, hk, d = 150, 4, 2, 64
+    q, k, v, g = (_randn((n, a, d), torch.float16, dev, s) for a, s in ((h, 1), (hk, 2), (hk, 3), (h, 4)))
+    out, lse = sc.attention(q, k, v, causal=causal, return_lse=True)
+    grads = sc.attention_backward(g, q, k, v, out, lse, causal=causal)
+    tq, tk, tv, tg = (t.transpose(0, 1).contiguous().transpose(0, 1) for t in (q, k, v, g))
+    assert tq.stride() == (d, n * d, 1)
+    assert torch.equal(sc.attention(tq, tk, tv, causal=causal), out)
+    for a, b in zip(sc.attention_backward(tg, tq, tk, tv, out, lse, causal=causal), grads):
+        assert torch.equal(a, b)
+    at, f = torch.arange(n, dtype=torch.int32, device=dev), sc.rotary_frequencies(32, device=dev)
+    y = torch.empty_like(tq)
+    assert torch.equal(sc.rotary(tq, at, f, out=y), sc.rotary(q, at, f)) and y.stride() == tq.stride()
+    one = sc.attention(q[:1, :2], k[:1, :1], v[:1, :1])
+    odd = [torch.empty_strided(t.shape, (7, t.shape[2], 1), dtype=t.dtype, device=dev).copy_(t)
+           for t in (q[:1, :2], k[:1, :1], v[:1, :1])]
+    assert torch.equal(sc.attention(*odd), one)
+    with pytest.raises(ValueError, match="overlap"):
+        sc.attention(q, k[:, :1].expand(n, 2, d), v)
+
+
+@gpu
+def test_attention_with_nothing_on_a_side(dev):
+    sc = _sc()
+    h, hk, d = 4, 2, 32
+    some, none = torch.tensor([0, 3, 5], dtype=torch.int32, device=dev), torch.zeros(3, dtype=torch.int32, device=dev)
+    q, k = _randn((5, h, d), torch.float16, dev, 1), _randn((5, hk, d), torch.float16, dev, 2)
+    out, lse = sc.attention(q, k[:0], k[:0], some, none, return_lse=True)
+    assert not out.any() and torch.isneginf(lse).all()
+    dq, dk, dv = sc.attention_backward(q, q, k[:0], k[:0], out, lse, some, none)
+    assert not dq.any() and dk.shape == dv.shape == (0, hk, d)
+    out, lse = sc.attention(q[:0], k, k, none, some, return_lse=True)
+    assert out.shape == (0, h, d) and lse.shape == (0, h)
+    dq, dk, dv = sc.attention_backward(q[:0], q[:0], k, k, out, lse, none, some)
+    assert dq.shape == (0, h, d) and not dk.any() and not dv.any()
+    assert sc.attention(q[:0], k[:0], k[:0]).shape == (0, h, d)
+
+
+@gpu
+@pytest.mark.parametrize("items", [64, 65, 700])
+def test_attention_of_many_items(dev, items):
+    """Lengths of 0 to 40 in any order, under the causal mask: up to 64 items the
+    tiles go by their walks, past that item by item."""
+    sc = _sc()
+    g = _gen(items)
+    lengths = torch.randint(0, 41, (items,), generator=g).tolist()
+    lengths[items // 2] = 600
+    n, h, hk, d = sum(lengths) + 7, 4, 1, 32
+    q, k, v = (_randn((n, a, d), torch.float16, dev, s) for a, s in ((h, 1), (hk, 2), (hk, 3)))
+    off = _offsets(lengths, dev)
+    out, lse = sc.attention(q, k, v, off, causal=True, return_lse=True)
+    args = (d ** -0.5, True, off.tolist(), None)
+    ro, rl = op.attention(_np(q), _np(k), _np(v), *args)
+    do = _randn((n, h, d), torch.float16, dev, 4)
+    to, tl, tq, tk, tv = _bounds(_np(q), _np(k), _np(v), _np(out), _np(do), *args, None, torch.float16)
+    _check(out, ro, to + 2.0 ** -11 * np.abs(ro) + 2.0 ** -24, "out")
+    _check(lse, rl, tl, "lse")
+    grads = sc.attention_backward(do, q, k, v, out, lse, off, causal=True)
+    refs = op.attention_backward(_np(do), _np(q), _np(k), _np(v), _np(out), *args)
+    for got, ref, tol, what in zip(grads, refs, (tq, tk, tv), ("grad_q", "grad_k", "grad_v")):
+        _check(got, ref, tol + 2.0 ** -11 * np.abs(ref) + 2.0 ** -24, what)
+
+
+@gpu
+def test_attention_of_offsets_that_descend_stays_in_bounds(dev):
+    """What they mean is undefined; rows beside the tensors stay as they are, and
+    the kernels end. (Kernels cut offsets to 0 .. n, whatever they hold.)"""
+    sc = _sc()
+    n, h, d = 300, 2, 32
+    wide = _randn((n + 20, h, d), torch.float16, dev, 1)
+    q = wide[10:n + 10]
+    before = wide.clone()
+    for bad in ([0, 200, 100, 300], [5, -7, 2 ** 31 - 1, 40], [0, 400, 500, 600]):
+        off = torch.tensor(bad, dtype=torch.int32, device=dev)
+        for causal in (False, True):
+            out, lse = sc.attention(q, q, q, off, causal=causal, return_lse=True)
+            sc.attention_backward(q, q, q, q, out, torch.zeros_like(lse), off, causal=causal)
+        sc.group_norm(q.reshape(n, h * d), 2, offsets=off)
+    torch.cuda.synchronize()
+    assert torch.equal(wide, before)
 
 
 @gpu
