@@ -92,8 +92,12 @@ __device__ __forceinline__ int sum_width(int count) {
   return w;
 }
 __device__ __forceinline__ float width_sum(float v, int width) {
-  for (int o = 1; o < width; o <<= 1) v += __shfl_xor(v, o, 64);
-  return v;
+  if (width == 64) return lanes_sum<64>(v);
+  if (width == 32) return lanes_sum<32>(v);
+  if (width == 16) return lanes_sum<16>(v);
+  if (width == 8) return lanes_sum<8>(v);
+  if (width == 4) return lanes_sum<4>(v);
+  return width == 2 ? v + dpp<0xB1>(v) : v;
 }
 
 // The mean and the sum of squares about it of `rows` rows of columns 0 .. cols -
@@ -151,6 +155,11 @@ __device__ __forceinline__ void chunk_moments(const T* x, int64_t ldx, int rows,
     auto each = [&](auto&& take) {  // (row of threads i, channel c) of the group, every width-th
       int i = t / cpg, c = t - i * cpg;
       const int di = width / cpg, dc = width - di * cpg;
+      if (dc == 0) {  // always the same channel
+#pragma unroll 4
+        for (; i < g.rl; i += di) take(static_cast<float>(base + (i < more)), i * wide + k * cpg + c);
+        return;
+      }
       while (i < g.rl) {
         take(static_cast<float>(base + (i < more)), i * wide + k * cpg + c);
         i += di;
@@ -525,7 +534,7 @@ __device__ __forceinline__ void chunk_grads(const T* dy, int64_t ldg, const T* x
 
 // partial [slots][2][C]: each chunk's sums of dz and of dz xh.
 template <typename T>
-__global__ __launch_bounds__(kGroupThreads, 4) void k_group_sums(const T* __restrict__ dy, int64_t ldg,
+__global__ __launch_bounds__(kGroupThreads) void k_group_sums(const T* __restrict__ dy, int64_t ldg,
                                                               const T* __restrict__ x, int64_t ldx, Items it, int C,
                                                               int cpg, Lanes g, int shift,
                                                               const float* __restrict__ mean,
@@ -578,19 +587,35 @@ __global__ __launch_bounds__(NT) void k_group_join_sums(const float* __restrict_
   else sx[static_cast<int64_t>(item) * C + col - C] = sum;
 }
 
-// dx of a chunk, the chunks from the last on (see k_group_apply).
+// dx of a chunk, the chunks from the last on (see k_group_apply); in workgroups
+// from `slots` on 256 columns' dw and db, the sums over a few items (a launch of
+// their own would take 4 us).
 template <typename T>
 __global__ __launch_bounds__(kGroupThreads) void k_group_dx(const T* __restrict__ dy, int64_t ldg,
                                                             const T* __restrict__ x, int64_t ldx, Items it, int C,
-                                                            int cpg, Lanes g, int shift,
+                                                            int cpg, Lanes g, int shift, int64_t slots,
                                                             const float* __restrict__ mean,
                                                             const float* __restrict__ rstd,
                                                             const float* __restrict__ w, const float* __restrict__ b,
                                                             int act, const float* __restrict__ sz,
-                                                            const float* __restrict__ sx, T* __restrict__ dx) {
+                                                            const float* __restrict__ sx, T* __restrict__ dx,
+                                                            float* __restrict__ dw, float* __restrict__ db) {
   extern __shared__ float lds[];
   const int64_t G = C / cpg;
-  const ItemTile t = find_item(it, 1, shift, gridDim.x - 1 - blockIdx.x);
+  if (blockIdx.x >= slots) {
+    const int64_t c = (blockIdx.x - slots) * kGroupThreads + threadIdx.x;
+    if (c >= C) return;
+    float z = 0.0f, q = 0.0f;
+#pragma unroll 8
+    for (int64_t i = 0; i < it.items; ++i) {
+      z += sz[i * C + c];
+      q += sx[i * C + c];
+    }
+    if (dw) dw[c] = q;
+    if (db) db[c] = z;
+    return;
+  }
+  const ItemTile t = find_item(it, 1, shift, slots - 1 - blockIdx.x);
   const int64_t r0 = t.tile << shift;
   if (t.tile < 0 || r0 >= t.rows) return;
   const int rows = static_cast<int>(min(t.rows - r0, int64_t{1} << shift));
@@ -776,12 +801,15 @@ int group_backward(const GroupShape& s, const void* gp, int64_t ldg, const void*
   if (s.it.items <= kFewItems) k_group_join_sums<1024><<<join, 1024, 0, stream>>>(partial, s.it, s.C, shift, sz, sx);
   else k_group_join_sums<128><<<join, 128, 0, stream>>>(partial, s.it, s.C, shift, sz, sx);
   SUBMCONV_HIP_CHECK(hipGetLastError());
-  if (dx) {
-    k_group_dx<T><<<static_cast<unsigned>(slots), kGroupThreads, 2 * s.G * 4, stream>>>(
-        dy, ldg, x, ldx, s.it, s.C, s.cpg, g, shift, mean, rstd, w, b, act, sz, sx, dx);
+  const bool here = !one && s.it.items <= kFewItems && (dw || db);  // the sums over the items
+  const int64_t grid = (dx ? slots : 0) + (here ? (s.C + kGroupThreads - 1) / kGroupThreads : 0);
+  if (grid > 0) {
+    k_group_dx<T><<<static_cast<unsigned>(grid), kGroupThreads, 2 * s.G * 4, stream>>>(
+        dy, ldg, x, ldx, s.it, s.C, s.cpg, g, shift, dx ? slots : 0, mean, rstd, w, b, act, sz, sx, dx,
+        here ? dw : nullptr, here ? db : nullptr);
     SUBMCONV_HIP_CHECK(hipGetLastError());
   }
-  return one ? SUBMCONV_OK : sum_items(s, sz, sx, dw, db, stream);
+  return one || here ? SUBMCONV_OK : sum_items(s, sz, sx, dw, db, stream);
 }
 
 template <typename F>
