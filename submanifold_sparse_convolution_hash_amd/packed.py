@@ -71,7 +71,12 @@ def _items(offsets, name: str, device) -> int:
         raise TypeError(f"{name} must be a tensor")
     if offsets.dim() != 1 or offsets.shape[0] < 2:
         raise ValueError(f"{name} must be [items + 1], got {tuple(offsets.shape)}")
-    _dense(offsets, name, torch.int32, tuple(offsets.shape), device)
+    if offsets.dtype != torch.int32:
+        raise TypeError(f"{name} must be {torch.int32}, got {offsets.dtype}")
+    if offsets.device != device:
+        raise ValueError(f"{name} is on {offsets.device}, not on {device}")
+    if not offsets.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
     return offsets.shape[0] - 1
 
 
@@ -161,14 +166,16 @@ def _heads(t, name: str, dtypes, like=None) -> Tuple[int, int]:
         raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
     if t.dim() != 3:
         raise ValueError(f"{name} must have 3 dims (rows, heads, columns), got {tuple(t.shape)}")
-    n, h, d = t.shape
-    if max(h, d) > _INT32_MAX or h < 1 or d < 1:
-        raise ValueError(f"{name} is {tuple(t.shape)}")
+    n, h, d = shape = t.shape
     if like is not None:
         if t.device != like.device:
             raise ValueError(f"{name} is on {t.device}, not on {like.device}")
-        if t.shape != like.shape:
-            raise ValueError(f"{name} must be {list(like.shape)}, got {tuple(t.shape)}")
+        if shape != like.shape:
+            raise ValueError(f"{name} must be {list(like.shape)}, got {tuple(shape)}")
+    if not (0 < h <= _INT32_MAX and 0 < d <= _INT32_MAX):
+        raise ValueError(f"{name} is {tuple(shape)}")
+    if t.is_contiguous():
+        return h * d, d
     ld, hs, inner = t.stride()
     ld, hs = ld if n > 1 else h * d, hs if h > 1 else d
     apart = hs >= d and ld >= (h - 1) * hs + d or ld >= d and hs >= (n - 1) * ld + d  # rows of heads, or heads of rows
@@ -239,8 +246,9 @@ def rotary(x: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor, interl
     if f < 1 or 2 * axes * f > d:
         raise ValueError(f"{axes} axes of {f} pairs do not fit {d} columns")
     if out is None:
-        out = x.new_empty((n, h, d))
-    ldo, ho = _heads(out, "out", (x.dtype,), x)
+        out, ldo, ho = x.new_empty((n, h, d)), h * d, d
+    else:
+        ldo, ho = _heads(out, "out", (x.dtype,), x)
     _call(dev, "submconv_rotary", _ptr(x), ldx, hx, n, h, d, _ptr(positions), positions.stride(0), ap, axes,
           _ptr(freqs), f, int(bool(interleaved)), int(bool(inverse)), amplitude, _ptr(out), ldo, ho,
           _NORM_DTYPES[x.dtype])
