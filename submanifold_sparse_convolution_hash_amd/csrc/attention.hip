@@ -49,7 +49,7 @@ __global__ __launch_bounds__(NW * 64, NW == 1 ? 1 : 2) void k_attention(Attentio
   const Walk w = walk_of(a.qi, a.group, SHIFT, o.slots, o.splits, at.slot, a.causal, false);
   const ItemTile t = w.t;
   const int split = w.split;
-  const Extent x = extent_of(a, t.item);
+  const Extent x = extent_of(a, t, false);
   const int64_t rows = static_cast<int64_t>(x.q_rows) * a.group, r_first = t.tile * T;
   if (t.tile < 0 || r_first >= rows) return;
 

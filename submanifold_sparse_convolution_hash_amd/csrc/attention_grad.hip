@@ -108,7 +108,7 @@ __global__ __launch_bounds__(NW * 64, NW == 1 ? 1 : 2) void k_attention_dq(Atten
   const Walk w = walk_of(a.qi, a.group, SHIFT, o.slots, o.splits, at.slot, a.causal, false);
   const ItemTile t = w.t;
   const int split = w.split;
-  const Extent x = extent_of(a, t.item);
+  const Extent x = extent_of(a, t, false);
   const int64_t rows = static_cast<int64_t>(x.q_rows) * a.group, r_first = t.tile * T;
   if (t.tile < 0 || r_first >= rows) return;
 
@@ -237,7 +237,7 @@ __global__ __launch_bounds__(DP > 96 ? 512 : 256, 2) void k_attention_dkv(Attent
   const Walk w = walk_of(a.ki, 1, SHIFT, o.slots, o.splits, at.slot, a.causal, true);
   const ItemTile t = w.t;
   const int split = w.split;
-  const Extent x = extent_of(a, t.item);
+  const Extent x = extent_of(a, t, true);
   const int64_t k_first = t.tile * T;
   if (t.tile < 0 || k_first >= x.k_rows) return;
 

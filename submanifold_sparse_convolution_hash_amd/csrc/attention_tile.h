@@ -140,16 +140,23 @@ struct Extent {
   int64_t q0, k0;
   int32_t q_rows, k_rows, Lq, Lk;
 };
-__device__ __forceinline__ Extent extent_of(const Attention& a, int item) {
+// Of the item of a tile of queries, or of keys (of_keys).
+__device__ __forceinline__ Extent extent_of(const Attention& a, const ItemTile& t, bool of_keys) {
+  const int64_t s = t.row0, n = t.rows;
+  int64_t s2 = s, n2 = n;  // the other side's
+  if (a.qi.offsets != a.ki.offsets || a.qi.n != a.ki.n) {
+    const Items& other = of_keys ? a.qi : a.ki;
+    s2 = item_start(other, t.item);
+    const int64_t e2 = item_start(other, t.item + 1);
+    n2 = e2 > s2 ? e2 - s2 : 0;
+  }
   Extent x;
-  const int64_t qs = item_start(a.qi, item), qe = item_start(a.qi, item + 1);
-  const int64_t ks = item_start(a.ki, item), ke = item_start(a.ki, item + 1);
-  x.q0 = qs;
-  x.k0 = ks;
-  x.q_rows = x.Lq = qe > qs ? static_cast<int32_t>(qe - qs) : 0;
-  x.k_rows = x.Lk = ke > ks ? static_cast<int32_t>(ke - ks) : 0;
-  if (item == a.qi.items) x.Lk = 0, x.Lq = 0;
-  else if (a.k_lengths) x.Lk = min(x.Lk, max(a.k_lengths[item], 0));
+  x.q0 = of_keys ? s2 : s;
+  x.k0 = of_keys ? s : s2;
+  x.q_rows = x.Lq = static_cast<int32_t>(of_keys ? n2 : n);
+  x.k_rows = x.Lk = static_cast<int32_t>(of_keys ? n : n2);
+  if (t.item == a.qi.items) x.Lk = 0, x.Lq = 0;
+  else if (a.k_lengths) x.Lk = min(x.Lk, max(a.k_lengths[t.item], 0));
   return x;
 }
 

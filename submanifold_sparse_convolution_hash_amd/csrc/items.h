@@ -49,24 +49,35 @@ struct ItemTile {
   int64_t tile;        // of the item; below 0 or past its last where the slot has nothing to do
 };
 
-// The item of a slot, by the lanes of each wave: 64 items a probe.
+// The item of a slot, by the lanes of each wave: 64 items a probe. Up to 63 items
+// one probe is all that is read.
 __device__ __forceinline__ ItemTile find_item(const Items& it, int64_t per, int shift, int64_t slot) {
   const int lane = threadIdx.x & 63;
-  int lo = 0, hi = it.items;
-  while (lo < hi) {
-    const int step = (hi - lo + 63) / 64;
-    const int b = lo + (lane + 1) * step;
-    const bool ok = b <= hi && (item_start(it, b) * per >> shift) + b <= slot;
-    const int c = __popcll(__ballot(ok));  // at most (hi - lo) / step of them have b <= hi
-    hi = min(hi, lo + (c + 1) * step - 1);
-    lo += c * step;
-  }
   ItemTile r;
-  r.item = __builtin_amdgcn_readfirstlane(lo);
-  const int64_t s = item_start(it, r.item), e = item_start(it, r.item + 1);
-  r.row0 = s;
-  r.rows = e > s ? e - s : 0;
-  r.tile = slot - ((s * per >> shift) + r.item);
+  if (it.items < 64) {
+    const int b = lane + 1;
+    const int v = static_cast<int>(item_start(it, b));  // (n is below 2^31)
+    const int c = __popcll(__ballot(b <= it.items && (v * per >> shift) + b <= slot));
+    r.item = c;
+    r.row0 = c > 0 ? __builtin_amdgcn_readlane(v, c - 1) : 0;
+    const int64_t e = __builtin_amdgcn_readlane(v, c);
+    r.rows = e > r.row0 ? e - r.row0 : 0;
+  } else {
+    int lo = 0, hi = it.items;
+    while (lo < hi) {
+      const int step = (hi - lo + 63) / 64;
+      const int b = lo + (lane + 1) * step;
+      const bool ok = b <= hi && (item_start(it, b) * per >> shift) + b <= slot;
+      const int c = __popcll(__ballot(ok));  // at most (hi - lo) / step of them have b <= hi
+      hi = min(hi, lo + (c + 1) * step - 1);
+      lo += c * step;
+    }
+    r.item = __builtin_amdgcn_readfirstlane(lo);
+    r.row0 = item_start(it, r.item);
+    const int64_t e = item_start(it, r.item + 1);
+    r.rows = e > r.row0 ? e - r.row0 : 0;
+  }
+  r.tile = slot - ((r.row0 * per >> shift) + r.item);
   return r;
 }
 
