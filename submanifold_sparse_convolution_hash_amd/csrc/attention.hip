@@ -28,6 +28,7 @@ struct AttnOut {
   float* part_lse;  // [splits][nq][heads]
   int32_t splits;
   int64_t slots;  // tiles, times the splits
+  bool by_slot;   // see place_of
 };
 
 // The maximum is raised, and what was summed scaled down, only once a score
@@ -45,7 +46,7 @@ __global__ __launch_bounds__(NW * 64, NW == 1 ? 1 : 2) void k_attention(Attentio
   __shared__ __attribute__((aligned(16))) char smem[2][2][H::BYTES];
   const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const Place at = place_of(blockIdx.x, o.slots, a.kv_heads, a.causal, true);
+  const Place at = place_of(blockIdx.x, o.slots, a.kv_heads, a.causal, true, o.by_slot);
   const Walk w = walk_of(a.qi, a.group, SHIFT, o.slots, o.splits, at.slot, a.causal, false);
   const ItemTile t = w.t;
   const int split = w.split;
@@ -290,7 +291,7 @@ Plan plan_of(const Attention& a) {
 int attention_forward(const Attention& a, bool bf16, uint16_t* out, float* lse, Arena& ws, hipStream_t stream) {
   const Plan p = plan_of(a);
   const int64_t rows = a.qi.n * a.group * a.kv_heads;
-  AttnOut o{out, lse, nullptr, nullptr, p.splits, p.slots};
+  AttnOut o{out, lse, nullptr, nullptr, p.splits, p.slots, few_keys(a)};
   if (p.splits > 1) {
     o.part = static_cast<float*>(ws.take(rows * p.splits * a.D * 4));
     o.part_lse = static_cast<float*>(ws.take(rows * p.splits * 4));

@@ -35,6 +35,7 @@ struct AttnGrad {
   float *dq_part, *dk_part, *dv_part;  // [splits][rows][D] where split
   int32_t splits;
   int64_t slots;  // tiles, times the splits
+  bool by_slot;   // see place_of
 };
 
 // Power of two that a column's ds are taken times.
@@ -104,7 +105,7 @@ __global__ __launch_bounds__(NW * 64, NW == 1 ? 1 : 2) void k_attention_dq(Atten
   __shared__ __attribute__((aligned(16))) char smem[2][2][H::BYTES];
   const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const Place at = place_of(blockIdx.x, o.slots, a.kv_heads, a.causal, true);
+  const Place at = place_of(blockIdx.x, o.slots, a.kv_heads, a.causal, true, o.by_slot);
   const Walk w = walk_of(a.qi, a.group, SHIFT, o.slots, o.splits, at.slot, a.causal, false);
   const ItemTile t = w.t;
   const int split = w.split;
@@ -233,7 +234,7 @@ __global__ __launch_bounds__(DP > 96 ? 512 : 256, 2) void k_attention_dkv(Attent
   const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int part = wave & 3, half = wave >> 2;  // the wave's keys; its block of queries where PAIRED
-  const Place at = place_of(blockIdx.x, o.slots, a.kv_heads, a.causal, !PAIRED);
+  const Place at = place_of(blockIdx.x, o.slots, a.kv_heads, a.causal, !PAIRED, o.by_slot);
   const Walk w = walk_of(a.ki, 1, SHIFT, o.slots, o.splits, at.slot, a.causal, true);
   const ItemTile t = w.t;
   const int split = w.split;
@@ -431,6 +432,7 @@ int attention_backward(const Attention& a, const AttnGrad& g, bool bf16, Arena& 
   const int64_t items = a.qi.items, q_rows = a.qi.n * a.group * a.kv_heads, k_rows = a.ki.n * a.kv_heads;
   const int64_t mean_q = (a.qi.n + items - 1) / items, mean_k = (a.ki.n + items - 1) / items;
   AttnGrad o = g;
+  o.by_slot = few_keys(a);
   o.row_base = static_cast<float*>(ws.take(q_rows * 4));
   o.row_delta = static_cast<float*>(ws.take(q_rows * 4));
   PlaneList planes;
