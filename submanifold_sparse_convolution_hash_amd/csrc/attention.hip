@@ -14,6 +14,18 @@
 // of the wave, and the rounded weights are at once the operand of O^T = V^T P^T.
 // Products, maximum, sum and O are fp32; weights are rounded to 16 bits for the
 // second product, as its operands have to be.
+//
+// 8192 rows of 8 heads of 128 bf16 255-268 us, 1030-1080 TFLOP/s; 20011 rows of two
+// items, 12 heads of 64 fp16 760 us, 810; 8192 causal rows of four items, 16 / 4
+// heads of 128 89 us, 830. Bound by the vector units (68 % busy at 64 columns, where
+// exp2 takes half of what the matrix units take) and by power: the clock falls to
+// 1.7-1.9 GHz, and zeros in place of random numbers take a quarter less time (a
+// library product of 8192^3 reaches 1240 TFLOP/s here). So what counts is the work
+// per score: scale and maximum go into one multiply-add, the sums are scaled only
+// when the maximum rises (kSlack), masks are applied in tiles that need them. 64
+// rows a wave, which read LDS half as often, took 735 us in place of 760 at 64
+// columns and left small inputs half the workgroups; priorities around the products
+// (s_setprio) and more chains in maximum and sum changed nothing.
 #include <algorithm>
 
 #include "attention_tile.h"

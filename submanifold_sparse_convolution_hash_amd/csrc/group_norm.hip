@@ -15,6 +15,12 @@
 // joined in a fixed order: results repeat bit for bit. Means and squares about
 // the mean are joined pairwise (n, mean, square sum), so that a mean of many
 // deviations costs no digits.
+//
+// 209715 x 128 in 32 groups, silu: fp16 forward 18 + 5 + 27 us (54 + 0 + 107 MB at
+// the memory), bf16 gradient of four items 34 + 4 + 42 (107 + 0 + 161 MB); 209715 x
+// 512 fp16 131 and 230 us, 4.9 and 4.7 TB/s, a copy's rate. At 128 channels the
+// three launches' starts and ends weigh: every workgroup is resident at once and
+// has one batch of rows.
 #include <algorithm>
 
 #include "dense_common.h"
