@@ -459,16 +459,15 @@ class SparseAttention(torch.nn.Module):
         h, hk, d = self.heads, self.kv_heads, self.dim
         rows = self.proj_in(x).view(x.shape[0], -1, d)
         if self.own:
-            q, k, v = rows[:, :h], rows[:, h:h + hk], rows[:, h + hk:]
+            both, v = rows.split([h + hk, hk], 1)
             if self.freqs is not None:
                 if positions is None:
                     raise ValueError("positions are needed to turn queries and keys")
-                both = rows[:, :h + hk]
                 if _recorded(both):
                     both = RotaryFunction.apply(both, positions, self.freqs, self.interleaved, 1.0)
                 else:
                     rotary(both, positions, self.freqs, self.interleaved, out=both)
-                q, k = both[:, :h], both[:, h:]
+            q, k = both.split([h, hk], 1)
             context_offsets = None
         else:
             if context is None:
