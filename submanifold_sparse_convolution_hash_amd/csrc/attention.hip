@@ -48,17 +48,23 @@ struct AttnOut {
 // hold as exactly as any other, and the sums' 32 bits have room.
 constexpr float kSlack = 8.0f;
 
-template <bool BF16, int DP, int NW>
-__global__ __launch_bounds__(NW * 64, NW == 1 ? 1 : 2) void k_attention(Attention a, AttnOut o) {
-  constexpr int T = 32 * NW, SHIFT = NW == 1 ? 5 : NW == 2 ? 6 : NW == 4 ? 7 : 8;
+// KG = 2: two groups of NW waves have the same rows and take every other tile of
+// keys, each with its own buffers; what they have is joined through LDS. For the
+// same waves on a unit this halves the walk of a workgroup that would be alone on
+// it: 2048 causal rows of 16 heads of 128 48.5 -> 40.5 us.
+template <bool BF16, int DP, int NW, int KG>
+__global__ __launch_bounds__(NW * KG * 64, NW == 1 ? 1 : 2) void k_attention(Attention a, AttnOut o) {
+  constexpr int T = 32 * NW, SHIFT = NW == 1 ? 5 : 7;
   static_assert(T == 1 << SHIFT, "rows");
   using H = HeadTile<DP>;
   using L = TileLoad<DP, NW>;
   constexpr int KS = DP / 16, DB = DP / 32;
-  __shared__ __attribute__((aligned(16))) char smem[2][2][H::BYTES];
+  __shared__ __attribute__((aligned(16))) char tiles_of[KG][2][2][H::BYTES];
   const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const Place at = place_of(blockIdx.x, o.slots, a.kv_heads, a.causal, true, o.by_slot);
+  const int wave_of = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wave = wave_of % NW, kg = wave_of / NW;
+  char(&smem)[2][2][H::BYTES] = tiles_of[kg];
+  const Place at = place_of(blockIdx.x, o.slots, a.kv_heads, a.causal, KG == 1, o.by_slot);
   const Walk w = walk_of(a.qi, a.group, SHIFT, o.slots, o.splits, at.slot, a.causal, false);
   const ItemTile t = w.t;
   const int split = w.split;
@@ -91,7 +97,7 @@ __global__ __launch_bounds__(NW * 64, NW == 1 ? 1 : 2) void k_attention(Attentio
     lv.issue(vr, static_cast<int64_t>(tile) * kTileKeys, a.D, to + H::BYTES, wave);
   };
 
-  if (first < last) issue(first, 0);  // on its way beside the queries
+  if (first + kg < last) issue(first + kg, 0);  // on its way beside the queries
   half8 q[KS];
   {
     const uint16_t* p = a.q.p + (x.q0 + token) * a.q.ld + head * a.q.hs;
@@ -115,7 +121,8 @@ __global__ __launch_bounds__(NW * 64, NW == 1 ? 1 : 2) void k_attention(Attentio
     wait_loads<0>();
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    if (tile + 1 < last) issue(tile + 1, buf ^ 1);
+    if (tile + KG < last) issue(tile + KG, buf ^ 1);
+    if (KG > 1 && tile >= last) return;  // (the other group has one more)
     const char* tk = smem[buf][0];
     const char* tv = smem[buf][1];
     float16v s[2] = {};
@@ -166,9 +173,34 @@ __global__ __launch_bounds__(NW * 64, NW == 1 ? 1 : 2) void k_attention(Attentio
 #pragma unroll
       for (int j = 0; j < DB; ++j) acc[j] = mfma32<BF16>(H::columns(tv, k * 16, j, lane), p[k], acc[j]);
   };
-  for (int tile = first; tile < last; tile += 2) {
-    step(tile, std::integral_constant<int, 0>{});
-    if (tile + 1 < last) step(tile + 1, std::integral_constant<int, 1>{});
+  for (int tile = first; tile < last; tile += 2 * KG) {
+    step(tile + kg, std::integral_constant<int, 0>{});
+    if (tile + KG < last) step(tile + KG + kg, std::integral_constant<int, 1>{});
+  }
+  if constexpr (KG > 1) {
+    static_assert(KG == 2 && NW * DB * 16 * 64 * 4 <= sizeof(smem), "sums fit the tiles");
+    __shared__ float tops[2][NW * 64];
+    float* const sums = reinterpret_cast<float*>(&tiles_of[1][0][0][0]);
+    __syncthreads();
+    if (kg == 1) {
+      tops[0][wave * 64 + lane] = m == -kInf ? -kInf : mc;
+      tops[1][wave * 64 + lane] = sum;
+#pragma unroll
+      for (int j = 0; j < DB; ++j)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) sums[((wave * DB + j) * 16 + i) * 64 + lane] = acc[j][i];
+    }
+    __syncthreads();
+    if (kg == 1) return;
+    const float other = tops[0][wave * 64 + lane], mine = m == -kInf ? -kInf : mc;
+    const float top = fmaxf(mine, other), base = top == -kInf ? 0.0f : top;
+    const float f = __builtin_amdgcn_exp2f(mine - base), g = __builtin_amdgcn_exp2f(other - base);
+    mc = base;
+    sum = sum * f + tops[1][wave * 64 + lane] * g;
+#pragma unroll
+    for (int j = 0; j < DB; ++j)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) acc[j][i] = acc[j][i] * f + sums[((wave * DB + j) * 16 + i) * 64 + lane] * g;
   }
   sum = halves_sum(sum);
   const float inv = sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;  // (a NaN stays one)
@@ -278,14 +310,16 @@ __global__ __launch_bounds__(256) void k_attention_join(const float* __restrict_
 // ---- dispatch ----
 
 struct Plan {
-  int waves, splits;
+  int waves, groups, splits;
   int64_t slots;
 };
 
 // One wave a workgroup where the items have at most 32 rows on average, else four,
-// two workgroups a unit: a step of 64 keys takes them 0.8 us at 64 columns and 1.2
-// at 128. A single wave waits for its loads, 1.3 to 1.6 us a step; as many
-// workgroups of one run on a unit at once as its LDS holds their tiles.
+// two workgroups a unit: a step of 64 keys takes them 0.9 us at 64 columns and 1.4
+// at 128. Or twice four, one workgroup a unit, where that is faster: their start and
+// join take 6 us, their steps 1.45 times as long, and they walk half as far. A single
+// wave waits for its loads, 1.3 to 1.6 us a step; as many workgroups of one run on
+// a unit at once as its LDS holds their tiles.
 Plan plan_of(const Attention& a) {
   Plan p;
   const int64_t mean_rows = (a.qi.n * a.group + a.qi.items - 1) / a.qi.items;
@@ -294,8 +328,18 @@ Plan plan_of(const Attention& a) {
   const int64_t tiles = std::max<int64_t>(1, (mean_rows + tile - 1) / tile * a.qi.items * a.kv_heads);
   const int64_t steps = (a.ki.n / a.qi.items + kTileKeys - 1) / kTileKeys;
   const int64_t floats = a.qi.n * a.group * a.kv_heads * a.D;
-  if (p.waves == 1) p.splits = splits_of(tiles, steps, 1.0 + 0.005 * a.D, 1.0, seen_share(a), a.D > 64 ? 512 : a.D > 32 ? 1280 : 2560, floats);
-  else p.splits = splits_of(tiles, steps, 0.35 + 0.0066 * a.D, 1.4, seen_share(a), 512, floats);
+  const double seen = seen_share(a), step = 0.46 + 0.007 * a.D;
+  Splits s;
+  if (p.waves == 1) {
+    s = splits_of(tiles, steps, 4.0, 1.0 + 0.005 * a.D, 1.0, seen, a.D > 64 ? 512 : a.D > 32 ? 1280 : 2560, floats);
+    p.groups = 1;
+  } else {
+    s = splits_of(tiles, steps, 4.0, step, 1.4, seen, 512, floats);
+    const Splits two = splits_of(tiles, (steps + 1) / 2, 6.0, 1.45 * step, 1.15, seen, 256, floats);
+    p.groups = two.us < s.us ? 2 : 1;
+    if (p.groups == 2) s = two;
+  }
+  p.splits = s.splits;
   p.slots = item_slots(a.qi, a.group, p.waves == 1 ? 5 : 7) * p.splits;
   return p;
 }
@@ -311,18 +355,23 @@ int attention_forward(const Attention& a, bool bf16, uint16_t* out, float* lse, 
   if (ws.counting) return SUBMCONV_OK;
   const int64_t blocks = p.slots * a.kv_heads;
   if (blocks > INT32_MAX) return set_error(SUBMCONV_ERR_UNSUPPORTED_SHAPE, "%lld tiles", (long long)blocks);
-  auto go = [&](auto dp, auto nw) {
-    if (bf16) k_attention<true, dp, nw><<<static_cast<unsigned>(blocks), nw * 64, 0, stream>>>(a, o);
-    else k_attention<false, dp, nw><<<static_cast<unsigned>(blocks), nw * 64, 0, stream>>>(a, o);
+  using One = std::integral_constant<int, 1>;
+  using Two = std::integral_constant<int, 2>;
+  using Four = std::integral_constant<int, 4>;
+  auto go = [&](auto dp, auto nw, auto kg) {
+    const unsigned grid = static_cast<unsigned>(blocks);
+    if (bf16) k_attention<true, dp, nw, kg><<<grid, nw * kg * 64, 0, stream>>>(a, o);
+    else k_attention<false, dp, nw, kg><<<grid, nw * kg * 64, 0, stream>>>(a, o);
   };
-  auto by_width = [&](auto nw) {
-    if (a.D <= 32) go(std::integral_constant<int, 32>{}, nw);
-    else if (a.D <= 64) go(std::integral_constant<int, 64>{}, nw);
-    else if (a.D <= 96) go(std::integral_constant<int, 96>{}, nw);
-    else go(std::integral_constant<int, 128>{}, nw);
+  auto by_width = [&](auto nw, auto kg) {
+    if (a.D <= 32) go(std::integral_constant<int, 32>{}, nw, kg);
+    else if (a.D <= 64) go(std::integral_constant<int, 64>{}, nw, kg);
+    else if (a.D <= 96) go(std::integral_constant<int, 96>{}, nw, kg);
+    else go(std::integral_constant<int, 128>{}, nw, kg);
   };
-  if (p.waves == 1) by_width(std::integral_constant<int, 1>{});
-  else by_width(std::integral_constant<int, 4>{});
+  if (p.waves == 1) by_width(One{}, One{});
+  else if (p.groups == 1) by_width(Four{}, One{});
+  else by_width(Four{}, Two{});
   SUBMCONV_HIP_CHECK(hipGetLastError());
   if (p.splits > 1) {
     const unsigned grid = static_cast<unsigned>((rows + 3) / 4);

@@ -450,9 +450,10 @@ int attention_backward(const Attention& a, const AttnGrad& g, bool bf16, Arena& 
   // (steps of 64 keys or queries, measured: 1.1 and 2.3 us at 64 columns, 1.8 and 2.4, two waves a block, at 128)
   const int64_t q_tiles = (mean_q * a.group + 127) / 128 * items * a.kv_heads;
   const int64_t k_tiles = (mean_k + 127) / 128 * items * a.kv_heads;
-  oq.splits = splits_of(q_tiles, (mean_k + 63) / 64, 0.5 + 0.01 * a.D, 1.0, seen_share(a), 512, q_rows * a.D);
-  ok.splits = splits_of(k_tiles, (mean_q + 63) / 64 * a.group, a.D > 96 ? 2.4 : 1.0 + 0.02 * a.D, 1.0, seen_share(a), a.D > 96 ? 256 : 512,
-                        2 * k_rows * a.D);
+  oq.splits = splits_of(q_tiles, (mean_k + 63) / 64, 4.0, 0.5 + 0.01 * a.D, 1.0, seen_share(a), 512, q_rows * a.D).splits;
+  ok.splits = splits_of(k_tiles, (mean_q + 63) / 64 * a.group, 4.0, a.D > 96 ? 2.4 : 1.0 + 0.02 * a.D, 1.0,
+                        seen_share(a), a.D > 96 ? 256 : 512, 2 * k_rows * a.D)
+                  .splits;
   oq.slots = item_slots(a.qi, a.group, 7) * oq.splits;
   ok.slots = item_slots(a.ki, 1, 7) * ok.splits;
   join(oq.dq, oq.dq_part, q_rows, oq.splits);

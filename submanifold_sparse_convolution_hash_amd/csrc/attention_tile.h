@@ -277,26 +277,27 @@ __device__ __forceinline__ float halves_sum(float x) {
 
 // Into how many runs a walk is split, each to its own fp32 sums, which a last launch
 // joins: the least of what walks and joins take, as measured. `tiles` workgroups
-// start in 4 us and walk up to `steps` steps of step_us each, `seen` of them on
+// start in start_us and walk up to `steps` steps of step_us each, `seen` of them on
 // average (the causal mask), `places` of them at once, which then share their
 // units and take `full` times as long: what counts is the longest walk or all of
 // them in turn; the sums of one run are written and read at 2.5 TB/s, and the join's launch takes
 // 6 us. 300 rows of 8 heads of 64 on 4000 keys: 55 us in one run, 20 in eight; 2048
 // rows of 16 heads of 128: 48 in one, 70 in two.
 constexpr int kMostSplits = 256;
-inline int splits_of(int64_t tiles, int64_t steps, double step_us, double full, double seen,
-                     int64_t places, int64_t run_floats) {
+struct Splits {
+  int splits;
+  double us;
+};
+inline Splits splits_of(int64_t tiles, int64_t steps, double start_us, double step_us, double full, double seen,
+                        int64_t places, int64_t run_floats) {
   const double join_us = static_cast<double>(run_floats) * 8 / 2.5e6;
-  int best = 1;
-  double least = 0.0;
+  Splits best{1, 0.0};
   for (int s = 1; s <= kMostSplits && (s == 1 || 2 * s <= steps); ++s) {
     const double rounds = static_cast<double>(tiles) * s / static_cast<double>(places);
     const double walk = static_cast<double>((steps + s - 1) / s) * step_us;
-    const double us = std::max(4.0 + walk, rounds * (4.0 + full * seen * walk)) + (s > 1 ? 6.0 + s * join_us : 0.0);
-    if (s == 1 || us < least) {
-      least = us;
-      best = s;
-    }
+    const double us = std::max(start_us + walk, rounds * (start_us + full * seen * walk)) +
+                      (s > 1 ? 6.0 + s * join_us : 0.0);
+    if (s == 1 || us < best.us) best = Splits{s, us};
   }
   return best;
 }

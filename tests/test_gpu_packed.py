@@ -543,6 +543,50 @@ def test_attention_over_caches_with_room(dev, causal):
         _check(got, ref, tol + 2.0 ** -8 * np.abs(ref), what)  # zeros where nothing is used
 
 
+# Walks long and rows few enough that two groups of waves share a workgroup's keys.
+# rows per item, keys per item, heads, key heads, columns, causal
+PAIRED = [
+    ([1300, 1, 1700], [1345, 70, 1410], 2, 2, 64, False),  # 22, 2 and 23 tiles of keys
+    ([1300, 0, 1700], [1280, 9, 1473], 4, 2, 128, True),
+    ([1500], [1473], 2, 2, 32, False), ([900, 700], [1700, 1400], 4, 4, 96, True),
+    ([1100], [6011], 2, 2, 128, False),                    # and in several runs
+    ([700, 500, 600], [0, 5000, 64], 2, 1, 72, False),     # an item without keys, one of one tile
+    ([1800], [1000], 4, 4, 64, True),                      # rows that see nothing
+]
+
+
+@gpu
+@pytest.mark.parametrize("dtype", TYPES[:2], ids=IDS[:2])
+@pytest.mark.parametrize("case", range(len(PAIRED)))
+def test_attention_of_two_groups_of_waves(dev, case, dtype):
+    sc = _sc()
+    lengths, keys, h, hk, d, causal = PAIRED[case]
+    n, nk = sum(lengths) + 2, sum(keys) + 3
+    q = _randn((n, h, d), dtype, dev, case, 1.3)
+    k, v = _randn((nk, 2 * hk, d), dtype, dev, case + 1000, 1.3).split([hk, hk], 1)
+    k[nk - 3:], v[nk - 3:] = float("nan"), float("inf")
+    # maxima that come late: the last keys' scores are the largest
+    k[: nk - 3] *= (torch.arange(nk - 3, device=dev)[:, None, None] * (2.0 / nk)).to(dtype)
+    off, koff = _offsets(lengths, dev), _offsets(keys, dev)
+    out, lse = sc.attention(q, k, v, off, koff, causal=causal, return_lse=True)
+    for _ in range(2):
+        again, l2 = sc.attention(q, k, v, off, koff, causal=causal, return_lse=True)
+        assert torch.equal(out, again) and torch.equal(lse, l2)
+    args = (np.float64(np.float32(d ** -0.5)), causal, off.tolist(), koff.tolist())
+    ro, rl = op.attention(_np(q), _clean(k), _clean(v), *args)
+    to, tl = _bounds(_np(q), _clean(k), _clean(v), None, None, *args, None, dtype)[:2]
+    _check(out, ro, to + U[dtype] * np.abs(ro) + TINY[dtype], "out")
+    _check(lse, rl, tl, "lse")
+    # a row of NaN is one, and its neighbours in the tile do not see it
+    row = lengths[0] // 2
+    q[row] = float("nan")
+    bad, lbad = sc.attention(q, k, v, off, koff, causal=causal, return_lse=True)
+    sees = koff[1].item() - max(lengths[0] - 1 - row, 0) > 0 if causal else keys[0] > 0
+    assert torch.isnan(bad[row]).all() == sees and torch.isnan(lbad[row]).all() == sees
+    bad[row], lbad[row] = out[row], lse[row]
+    assert torch.equal(bad, out) and torch.equal(lbad, lse)
+
+
 @gpu
 @pytest.mark.parametrize("dtype", TYPES[:2], ids=IDS[:2])
 def test_attention_extreme_scores(dev, dtype):
