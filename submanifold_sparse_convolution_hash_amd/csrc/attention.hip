@@ -416,7 +416,7 @@ int check_attention(const Attention& a, int64_t nq, int64_t nk, int32_t heads, i
     return set_error(SUBMCONV_ERR_INVALID_ARG, "%d items, 1 to 65535 are supported", a.qi.items);
   if ((!a.qi.offsets || !a.ki.offsets) && a.qi.items != 1)
     return set_error(SUBMCONV_ERR_INVALID_ARG, "%d items without offsets", a.qi.items);
-  if (!(a.scale > 0.0f) || a.scale > 3e38f) return set_error(SUBMCONV_ERR_INVALID_ARG, "scale = %g", a.scale);
+  if (!(a.scale > 0.0f) || a.scale > 2e38f) return set_error(SUBMCONV_ERR_INVALID_ARG, "scale = %g", a.scale);
   return SUBMCONV_OK;
 }
 

@@ -18,6 +18,7 @@ __global__ __launch_bounds__(256) void k_item_offsets(const int32_t* __restrict_
   if (i < n && (here < 0 || here >= items)) bad |= 1;
   if (i > 0 && i < n && here < before) bad |= 2;
   if (bad) atomicOr(status, bad);
+  if (before >= items) return;  // (refused; before + 1 may pass 32 bits)
   const int32_t last = here < items ? here : items;
   for (int32_t b = before < -1 ? 0 : before + 1; b <= last; ++b) offsets[b] = static_cast<int32_t>(i);
 }

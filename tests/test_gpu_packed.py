@@ -101,6 +101,18 @@ def test_item_offsets_refuses_what_is_not_sorted(dev):
             sc.item_offsets(bad, 2)
 
 
+@gpu
+@pytest.mark.parametrize("row", [0, 298, 299, 300])
+@pytest.mark.parametrize("value", [2, 65535, 2 ** 31 - 1, -2 ** 31])
+def test_item_offsets_refuses_an_index_anywhere(dev, row, value):
+    sc = _sc()
+    coords = torch.zeros((600, 4), dtype=torch.int32, device=dev)
+    coords[300:, 0] = 1
+    coords[row, 0] = value
+    with pytest.raises(sc.SubmconvError, match="outside"):
+        sc.item_offsets(coords, 2)
+
+
 # ---------------------------------------------------------------------------
 # group norm
 # ---------------------------------------------------------------------------
