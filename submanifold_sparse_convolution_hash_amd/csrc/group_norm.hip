@@ -33,6 +33,7 @@ namespace {
 
 constexpr int kGroupThreads = 256;
 constexpr int kGroupChannels = 8192;
+constexpr int kUnits = 256;  // compute units
 // rows of a thread in flight, of one tensor or of two
 constexpr int kRowsAhead = 8, kGradRowsAhead = 4;
 
@@ -191,16 +192,16 @@ __device__ __forceinline__ void chunk_moments(const T* x, int64_t ldx, int rows,
 
 // ---- forward ----
 
-// partial [slots][G] {mean, square sum} of each chunk of 2^shift rows.
+// partial [slots][G] {mean, square sum} of each chunk of `chunk` rows.
 template <typename T>
 __global__ __launch_bounds__(kGroupThreads) void k_group_moments(const T* __restrict__ x, int64_t ldx, Items it,
-                                                                 int C, int cpg, Lanes g, int shift,
+                                                                 int C, int cpg, Lanes g, uint32_t chunk,
                                                                  float2* __restrict__ partial) {
   extern __shared__ float lds[];
-  const ItemTile t = find_item(it, 1, shift, blockIdx.x);
-  const int64_t r0 = t.tile << shift;
+  const ItemTile t = find_chunk(it, chunk, blockIdx.x);
+  const int64_t r0 = t.tile * chunk;
   if (t.item == it.items || t.tile < 0 || r0 >= t.rows) return;
-  const int rows = static_cast<int>(min(t.rows - r0, int64_t{1} << shift)), G = C / cpg;
+  const int rows = static_cast<int>(min(t.rows - r0, static_cast<int64_t>(chunk))), G = C / cpg;
   Piece<T> v[kRowsAhead];
   chunk_moments<T>(x + (t.row0 + r0) * ldx, ldx, rows, C, cpg, g, lds, v, [&](int k, float mean, float squares) {
     partial[static_cast<int64_t>(blockIdx.x) * G + k] = float2{mean, squares};
@@ -210,16 +211,16 @@ __global__ __launch_bounds__(kGroupThreads) void k_group_moments(const T* __rest
 // NT threads join the chunks of one item and group, as chunk_moments its threads'
 // parts: four waves up to kFewItems items, whose chunks they keep in registers,
 // else one wave, which reads most items' few chunks once and others' in turn.
-constexpr int kChunks = 2049, kFewItems = 16;
+constexpr int kChunks = 8 * kUnits + 1, kFewItems = 16;
 template <int NT>
 __global__ __launch_bounds__(NT) void k_group_join(const float2* __restrict__ partial, Items it, int G,
-                                                              int cpg, int shift, float eps,
+                                                              int cpg, uint32_t chunk, float eps,
                                                               float* __restrict__ mean, float* __restrict__ rstd) {
   constexpr int MOST = NT == 64 ? 1 : (kChunks + NT - 1) / NT;
   __shared__ float sums[2][NT / 64];
   const int item = blockIdx.y, k = blockIdx.x;
   const int64_t s = item_start(it, item), e = item_start(it, item + 1);
-  const int64_t rows = e > s ? e - s : 0, slot = (s >> shift) + item, chunk = int64_t{1} << shift;
+  const int64_t rows = e > s ? e - s : 0, slot = static_cast<uint32_t>(s) / chunk + item;
   auto all = [&](float v, float (&to)[NT / 64]) {
     v = lanes_sum<64>(v);
     if constexpr (NT == 64) return v;
@@ -236,11 +237,11 @@ __global__ __launch_bounds__(NT) void k_group_join(const float2* __restrict__ pa
 #pragma unroll
     for (int i = 0; i < MOST; ++i) {
       const int64_t c = first + threadIdx.x + i * NT, left = rows - c * chunk;
-      n[i] = left > 0 ? static_cast<float>(min(chunk, left) * cpg) : 0.0f;
+      n[i] = left > 0 ? static_cast<float>(min(static_cast<int64_t>(chunk), left) * cpg) : 0.0f;
       p[i] = left > 0 ? partial[(slot + c) * G + k] : float2{0.0f, 0.0f};
     }
   };
-  const bool once = rows <= MOST * NT * chunk;
+  const bool once = rows <= static_cast<int64_t>(chunk) * (MOST * NT);
   const float near = rows ? partial[slot * G + k].x : 0.0f;
   float total = 0.0f, q = 0.0f;
   for (int64_t first = 0; first * chunk < rows; first += MOST * NT) {
@@ -332,16 +333,16 @@ __device__ __forceinline__ void chunk_zeros(T* y, int64_t ldy, int64_t rows, int
 // caches (209715 x 512 fp16, 215 MB: 131 us in place of 139; x 128: no change).
 template <typename T>
 __global__ __launch_bounds__(kGroupThreads) void k_group_apply(const T* __restrict__ x, int64_t ldx, Items it, int C,
-                                                               int cpg, Lanes g, int shift,
+                                                               int cpg, Lanes g, uint32_t chunk,
                                                                const float* __restrict__ mean,
                                                                const float* __restrict__ rstd,
                                                                const float* __restrict__ w,
                                                                const float* __restrict__ b, int act,
                                                                T* __restrict__ y) {
-  const ItemTile t = find_item(it, 1, shift, gridDim.x - 1 - blockIdx.x);
-  const int64_t r0 = t.tile << shift;
+  const ItemTile t = find_chunk(it, chunk, gridDim.x - 1 - blockIdx.x);
+  const int64_t r0 = t.tile * chunk;
   if (t.tile < 0 || r0 >= t.rows) return;
-  const int rows = static_cast<int>(min(t.rows - r0, int64_t{1} << shift));
+  const int rows = static_cast<int>(min(t.rows - r0, static_cast<int64_t>(chunk)));
   const int64_t at = t.row0 + r0;
   if (t.item == it.items) {
     chunk_zeros<T>(y + at * C, C, rows, C, g);
@@ -542,17 +543,17 @@ __device__ __forceinline__ void chunk_grads(const T* dy, int64_t ldg, const T* x
 template <typename T>
 __global__ __launch_bounds__(kGroupThreads) void k_group_sums(const T* __restrict__ dy, int64_t ldg,
                                                               const T* __restrict__ x, int64_t ldx, Items it, int C,
-                                                              int cpg, Lanes g, int shift,
+                                                              int cpg, Lanes g, uint32_t chunk,
                                                               const float* __restrict__ mean,
                                                               const float* __restrict__ rstd,
                                                               const float* __restrict__ w,
                                                               const float* __restrict__ b, int act,
                                                               float* __restrict__ partial) {
   extern __shared__ float lds[];
-  const ItemTile t = find_item(it, 1, shift, blockIdx.x);
-  const int64_t r0 = t.tile << shift;
+  const ItemTile t = find_chunk(it, chunk, blockIdx.x);
+  const int64_t r0 = t.tile * chunk;
   if (t.item == it.items || t.tile < 0 || r0 >= t.rows) return;
-  const int rows = static_cast<int>(min(t.rows - r0, int64_t{1} << shift));
+  const int rows = static_cast<int>(min(t.rows - r0, static_cast<int64_t>(chunk)));
   const int64_t at = t.row0 + r0, G = C / cpg;
   float* out = partial + static_cast<int64_t>(blockIdx.x) * 2 * C;
   with_act(act, [&](auto a) {
@@ -570,14 +571,15 @@ __global__ __launch_bounds__(kGroupThreads) void k_group_sums(const T* __restric
 constexpr int kJoinCols = 16;
 template <int NT>
 __global__ __launch_bounds__(NT) void k_group_join_sums(const float* __restrict__ partial, Items it, int C,
-                                                                  int shift, float* __restrict__ sz,
+                                                                  uint32_t chunk, float* __restrict__ sz,
                                                                   float* __restrict__ sx) {
   constexpr int LANES = NT / kJoinCols;
   __shared__ float lds[LANES][kJoinCols];
   const int item = blockIdx.y, q = threadIdx.x % kJoinCols, t = threadIdx.x / kJoinCols;
   const int col = blockIdx.x * kJoinCols + q;
   const int64_t s = item_start(it, item), e = item_start(it, item + 1), rows = e > s ? e - s : 0;
-  const int64_t slot = (s >> shift) + item, chunks = (rows + (int64_t{1} << shift) - 1) >> shift;
+  const int64_t slot = static_cast<uint32_t>(s) / chunk + item;
+  const int64_t chunks = static_cast<uint32_t>(rows + chunk - 1) / chunk;
   float sum = 0.0f;
   if (col < 2 * C) {
 #pragma unroll 8
@@ -599,7 +601,7 @@ __global__ __launch_bounds__(NT) void k_group_join_sums(const float* __restrict_
 template <typename T>
 __global__ __launch_bounds__(kGroupThreads) void k_group_dx(const T* __restrict__ dy, int64_t ldg,
                                                             const T* __restrict__ x, int64_t ldx, Items it, int C,
-                                                            int cpg, Lanes g, int shift, int64_t slots,
+                                                            int cpg, Lanes g, uint32_t chunk, int64_t slots,
                                                             const float* __restrict__ mean,
                                                             const float* __restrict__ rstd,
                                                             const float* __restrict__ w, const float* __restrict__ b,
@@ -621,10 +623,10 @@ __global__ __launch_bounds__(kGroupThreads) void k_group_dx(const T* __restrict_
     if (db) db[c] = z;
     return;
   }
-  const ItemTile t = find_item(it, 1, shift, slots - 1 - blockIdx.x);
-  const int64_t r0 = t.tile << shift;
+  const ItemTile t = find_chunk(it, chunk, slots - 1 - blockIdx.x);
+  const int64_t r0 = t.tile * chunk;
   if (t.tile < 0 || r0 >= t.rows) return;
-  const int rows = static_cast<int>(min(t.rows - r0, int64_t{1} << shift));
+  const int rows = static_cast<int>(min(t.rows - r0, static_cast<int64_t>(chunk)));
   const int64_t at = t.row0 + r0;
   if (t.item == it.items) {
     chunk_zeros<T>(dx + at * C, C, rows, C, g);
@@ -701,12 +703,18 @@ struct GroupShape {
   int C, G, cpg;
 };
 
-// Chunks of 2^shift rows, at most 2048 of them over all rows and an item's first:
-// at least a row for each row of threads.
-int chunk_shift(int64_t n, int rl) {
-  int shift = 3;
-  while ((n >> shift) >= kChunks || (1 << shift) < rl) ++shift;
-  return shift;
+// Rows of a chunk: two batches a thread, as long as that makes whole rounds of a
+// workgroup a unit, one to four of them (three for the gradients): each start costs
+// more than two batches do. 100000 x 96 fp16, forward / backward us: 256 chunks 28 /
+// 37, 768 27 / 36, 1024 30 / 45, 2048 45 / 57; 209715 x 128: 256 48 / 70, 512 45 / 63,
+// 768 45 / 64, 1024 43 / 69, 2048 51 / 83. Where the walk is more than the 256 MB that
+// the second one finds in the caches, eight rounds: 209715 x 1024, 1024 chunks 278 /
+// 465, 2048 262 / 428. At least a row for each row of threads.
+uint32_t chunk_rows(int64_t n, int C, int elem, const Lanes& g, bool grad) {
+  const int64_t two = std::max(1, 2 * kRowsAhead * g.rl / g.strips), round = two * kUnits;
+  const bool cached = n * C * elem * (grad ? 2 : 1) <= int64_t{256} << 20;
+  const int64_t chunks = kUnits * std::clamp<int64_t>((n + round / 2) / round, 1, !cached ? 8 : grad ? 3 : 4);
+  return static_cast<uint32_t>(std::max<int64_t>(std::max(8, g.rl), (n + chunks - 1) / chunks));
 }
 
 // A workgroup of the one-launch kernels takes columns of about 128 bytes, whole
@@ -742,22 +750,22 @@ int group_forward(const GroupShape& s, const void* xp, int64_t ldx, const float*
     return SUBMCONV_OK;
   }
   const Lanes g = lanes_of(s.C, kVec<T>);
-  const int shift = chunk_shift(s.it.n, g.rl);
-  const int64_t slots = item_slots(s.it, 1, shift), stats = static_cast<int64_t>(s.it.items) * s.G;
+  const uint32_t chunk = chunk_rows(s.it.n, s.C, sizeof(T), g, false);
+  const int64_t slots = chunk_slots(s.it, chunk), stats = static_cast<int64_t>(s.it.items) * s.G;
   float2* partial = static_cast<float2*>(ws.take(slots * s.G * 8));
   float* spare = static_cast<float*>(ws.take(2 * stats * 4));
   if (ws.counting) return SUBMCONV_OK;
   if (!mean) mean = spare;
   if (!rstd) rstd = spare + stats;
   const unsigned grid = static_cast<unsigned>(slots);
-  k_group_moments<T><<<grid, kGroupThreads, lanes_lds(g, kVec<T>) * 4, stream>>>(x, ldx, s.it, s.C, s.cpg, g, shift,
+  k_group_moments<T><<<grid, kGroupThreads, lanes_lds(g, kVec<T>) * 4, stream>>>(x, ldx, s.it, s.C, s.cpg, g, chunk,
                                                                                  partial);
   SUBMCONV_HIP_CHECK(hipGetLastError());
   const dim3 join(s.G, s.it.items);
-  if (s.it.items <= kFewItems) k_group_join<256><<<join, 256, 0, stream>>>(partial, s.it, s.G, s.cpg, shift, eps, mean, rstd);
-  else k_group_join<64><<<join, 64, 0, stream>>>(partial, s.it, s.G, s.cpg, shift, eps, mean, rstd);
+  if (s.it.items <= kFewItems) k_group_join<256><<<join, 256, 0, stream>>>(partial, s.it, s.G, s.cpg, chunk, eps, mean, rstd);
+  else k_group_join<64><<<join, 64, 0, stream>>>(partial, s.it, s.G, s.cpg, chunk, eps, mean, rstd);
   SUBMCONV_HIP_CHECK(hipGetLastError());
-  k_group_apply<T><<<grid, kGroupThreads, 0, stream>>>(x, ldx, s.it, s.C, s.cpg, g, shift, mean, rstd, w, b, act, y);
+  k_group_apply<T><<<grid, kGroupThreads, 0, stream>>>(x, ldx, s.it, s.C, s.cpg, g, chunk, mean, rstd, w, b, act, y);
   SUBMCONV_HIP_CHECK(hipGetLastError());
   return SUBMCONV_OK;
 }
@@ -793,25 +801,25 @@ int group_backward(const GroupShape& s, const void* gp, int64_t ldg, const void*
     return one ? SUBMCONV_OK : sum_items(s, sz, sx, dw, db, stream);
   }
   const Lanes g = lanes_of(s.C, kVec<T>);
-  const int shift = chunk_shift(s.it.n, g.rl);
-  const int64_t slots = item_slots(s.it, 1, shift);
+  const uint32_t chunk = chunk_rows(s.it.n, s.C, sizeof(T), g, true);
+  const int64_t slots = chunk_slots(s.it, chunk);
   float* partial = static_cast<float*>(ws.take(slots * 2 * s.C * 4));
   float* spare = static_cast<float*>(ws.take(2 * sums * 4));
   if (ws.counting) return SUBMCONV_OK;
   float* sz = one && db ? db : spare;
   float* sx = one && dw ? dw : spare + sums;
   k_group_sums<T><<<static_cast<unsigned>(slots), kGroupThreads, lanes_lds(g, kVec<T>) * 4, stream>>>(
-      dy, ldg, x, ldx, s.it, s.C, s.cpg, g, shift, mean, rstd, w, b, act, partial);
+      dy, ldg, x, ldx, s.it, s.C, s.cpg, g, chunk, mean, rstd, w, b, act, partial);
   SUBMCONV_HIP_CHECK(hipGetLastError());
   const dim3 join((2 * s.C + kJoinCols - 1) / kJoinCols, s.it.items);
-  if (s.it.items <= kFewItems) k_group_join_sums<1024><<<join, 1024, 0, stream>>>(partial, s.it, s.C, shift, sz, sx);
-  else k_group_join_sums<128><<<join, 128, 0, stream>>>(partial, s.it, s.C, shift, sz, sx);
+  if (s.it.items <= kFewItems) k_group_join_sums<1024><<<join, 1024, 0, stream>>>(partial, s.it, s.C, chunk, sz, sx);
+  else k_group_join_sums<128><<<join, 128, 0, stream>>>(partial, s.it, s.C, chunk, sz, sx);
   SUBMCONV_HIP_CHECK(hipGetLastError());
   const bool here = !one && s.it.items <= kFewItems && (dw || db);  // the sums over the items
   const int64_t grid = (dx ? slots : 0) + (here ? (s.C + kGroupThreads - 1) / kGroupThreads : 0);
   if (grid > 0) {
     k_group_dx<T><<<static_cast<unsigned>(grid), kGroupThreads, 2 * s.G * 4, stream>>>(
-        dy, ldg, x, ldx, s.it, s.C, s.cpg, g, shift, dx ? slots : 0, mean, rstd, w, b, act, sz, sx, dx,
+        dy, ldg, x, ldx, s.it, s.C, s.cpg, g, chunk, dx ? slots : 0, mean, rstd, w, b, act, sz, sx, dx,
         here ? dw : nullptr, here ? db : nullptr);
     SUBMCONV_HIP_CHECK(hipGetLastError());
   }

@@ -32,6 +32,7 @@ struct Items {
 inline int64_t item_slots(const Items& it, int64_t per, int shift) {
   return (it.n * per >> shift) + it.items + 1;
 }
+inline int64_t chunk_slots(const Items& it, uint32_t chunk) { return it.n / chunk + it.items + 1; }
 
 namespace {
 
@@ -50,14 +51,16 @@ struct ItemTile {
 };
 
 // The item of a slot, by the lanes of each wave: 64 items a probe. Up to 63 items
-// one probe is all that is read.
-__device__ __forceinline__ ItemTile find_item(const Items& it, int64_t per, int shift, int64_t slot) {
+// one probe is all that is read. tile_of: row -> number of its tile, were there
+// one item.
+template <typename F>
+__device__ __forceinline__ ItemTile find_item_by(const Items& it, int64_t slot, F&& tile_of) {
   const int lane = threadIdx.x & 63;
   ItemTile r;
   if (it.items < 64) {
     const int b = lane + 1;
     const int v = static_cast<int>(item_start(it, b));  // (n is below 2^31)
-    const int c = __popcll(__ballot(b <= it.items && (v * per >> shift) + b <= slot));
+    const int c = __popcll(__ballot(b <= it.items && tile_of(v) + b <= slot));
     r.item = c;
     r.row0 = c > 0 ? __builtin_amdgcn_readlane(v, c - 1) : 0;
     const int64_t e = __builtin_amdgcn_readlane(v, c);
@@ -67,7 +70,7 @@ __device__ __forceinline__ ItemTile find_item(const Items& it, int64_t per, int 
     while (lo < hi) {
       const int step = (hi - lo + 63) / 64;
       const int b = lo + (lane + 1) * step;
-      const bool ok = b <= hi && (item_start(it, b) * per >> shift) + b <= slot;
+      const bool ok = b <= hi && tile_of(item_start(it, b)) + b <= slot;
       const int c = __popcll(__ballot(ok));  // at most (hi - lo) / step of them have b <= hi
       hi = min(hi, lo + (c + 1) * step - 1);
       lo += c * step;
@@ -77,8 +80,15 @@ __device__ __forceinline__ ItemTile find_item(const Items& it, int64_t per, int 
     const int64_t e = item_start(it, r.item + 1);
     r.rows = e > r.row0 ? e - r.row0 : 0;
   }
-  r.tile = slot - ((r.row0 * per >> shift) + r.item);
+  r.tile = slot - (tile_of(r.row0) + r.item);
   return r;
+}
+__device__ __forceinline__ ItemTile find_item(const Items& it, int64_t per, int shift, int64_t slot) {
+  return find_item_by(it, slot, [&](int64_t v) { return v * per >> shift; });
+}
+// Tiles of `chunk` rows.
+__device__ __forceinline__ ItemTile find_chunk(const Items& it, uint32_t chunk, int64_t slot) {
+  return find_item_by(it, slot, [&](int64_t v) { return static_cast<int64_t>(static_cast<uint32_t>(v) / chunk); });
 }
 
 // The same tiles in the order of their place in their item, `from_end` counted
