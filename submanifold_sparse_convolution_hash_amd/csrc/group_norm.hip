@@ -10,17 +10,16 @@
 // Bound by memory: the statistics need all of an item before its first output,
 // so x (and dy) are read twice. The rows are cut into chunks of one item each:
 // a first launch leaves each chunk's sums, a second joins them, a third makes
-// the outputs. A thread keeps its 16 bytes of columns for all rows of its
+// the outputs (and joins the chunks itself, where an item has few). A thread keeps its 16 bytes of columns for all rows of its
 // chunk, so that sums per channel stay in registers. All sums are fp32 and
 // joined in a fixed order: results repeat bit for bit. Means and squares about
 // the mean are joined pairwise (n, mean, square sum), so that a mean of many
 // deviations costs no digits.
 //
-// 209715 x 128 in 32 groups, silu: fp16 forward 18 + 5 + 27 us (54 + 0 + 107 MB at
-// the memory), bf16 gradient of four items 34 + 4 + 42 (107 + 0 + 161 MB); 209715 x
-// 512 fp16 131 and 230 us, 4.9 and 4.7 TB/s, a copy's rate. At 128 channels the
-// three launches' starts and ends weigh: every workgroup is resident at once and
-// has one batch of rows.
+// 209715 x 128 in 32 groups, silu: fp16 forward 20 + 5 + 24 us (54 + 0 + 107 MB at
+// the memory), bf16 gradients 27 + 5 + 34 (107 + 0 + 161 MB, 3.9 and 4.7 TB/s); 209715
+// x 512 fp16 128 and 223 us, 5.0 and 4.8 TB/s, a copy's rate. At 128 channels the
+// three launches' starts and ends weigh.
 #include <algorithm>
 
 #include "dense_common.h"
@@ -265,6 +264,53 @@ __global__ __launch_bounds__(NT) void k_group_join(const float2* __restrict__ pa
   }
 }
 
+// The same by a workgroup for all groups of one item, from its first chunk's parts
+// on, to f(group, mean, variance) in one thread of each. A thread has up to BATCH
+// parts in registers, so that all of them are on their way at once; what is more is
+// read twice.
+template <typename F>
+__device__ __forceinline__ void item_moments(const float2* partial, int64_t rows, uint32_t chunk, int G, int cpg,
+                                             F&& f) {
+  constexpr int BATCH = 4;
+  const int width = sum_width(G), t = threadIdx.x % width;
+  const int chunks = static_cast<int>(static_cast<uint32_t>(rows + chunk - 1) / chunk);
+  const float whole = static_cast<float>(chunk) * static_cast<float>(cpg);
+  const float end = static_cast<float>(rows - (chunks - 1) * static_cast<int64_t>(chunk)) * static_cast<float>(cpg);
+  const float inv = 1.0f / (static_cast<float>(rows) * static_cast<float>(cpg));
+  for (int k = threadIdx.x / width; k < G; k += kGroupThreads / width) {
+    float2 p[BATCH];
+    auto read = [&](int first) {
+#pragma unroll
+      for (int i = 0; i < BATCH; ++i) {
+        const int c = min(first + i * width, chunks - 1);
+        p[i] = partial[static_cast<int64_t>(c) * G + k];
+      }
+    };
+    auto weight = [&](int c) { return c + 1 < chunks ? whole : c < chunks ? end : 0.0f; };
+    const float near = partial[k].x;
+    float s = 0.0f, q = 0.0f;
+    for (int first = t; first < chunks; first += BATCH * width) {
+      read(first);
+#pragma unroll
+      for (int i = 0; i < BATCH; ++i) {
+        const float n = weight(first + i * width);
+        s += n > 0.0f ? n * (p[i].x - near) : 0.0f;
+      }
+    }
+    const float mean = near + width_sum(s, width) * inv;
+    for (int first = t; first < chunks; first += BATCH * width) {
+      if (chunks > BATCH * width) read(first);
+#pragma unroll
+      for (int i = 0; i < BATCH; ++i) {
+        const float n = weight(first + i * width);
+        q += n > 0.0f ? p[i].y + n * ((p[i].x - mean) * (p[i].x - mean)) : 0.0f;
+      }
+    }
+    q = width_sum(q, width);
+    if (t == 0) f(k, mean, q * inv);
+  }
+}
+
 // What a thread's columns are normalised with. mean and rstd of the item.
 template <int VEC>
 struct Affine {
@@ -331,28 +377,63 @@ __device__ __forceinline__ void chunk_zeros(T* y, int64_t ldy, int64_t rows, int
 
 // The rows from the last on: what the statistics' walk read last is still in the
 // caches (209715 x 512 fp16, 215 MB: 131 us in place of 139; x 128: no change).
-template <typename T>
+// JOIN: a workgroup joins its item's chunks itself, while its first rows are on
+// their way, and an item's first one also writes mean and rstd where they are
+// wanted. Else they are read.
+template <typename T, bool JOIN>
 __global__ __launch_bounds__(kGroupThreads) void k_group_apply(const T* __restrict__ x, int64_t ldx, Items it, int C,
                                                                int cpg, Lanes g, uint32_t chunk,
-                                                               const float* __restrict__ mean,
-                                                               const float* __restrict__ rstd,
-                                                               const float* __restrict__ w,
+                                                               const float2* __restrict__ partial, float eps,
+                                                               float* mean, float* rstd, const float* __restrict__ w,
                                                                const float* __restrict__ b, int act,
                                                                T* __restrict__ y) {
-  const ItemTile t = find_chunk(it, chunk, gridDim.x - 1 - blockIdx.x);
+  extern __shared__ float lds[];  // [2][G] where JOIN
+  const int64_t slot = gridDim.x - 1 - blockIdx.x;
+  const ItemTile t = find_chunk(it, chunk, slot);
   const int64_t r0 = t.tile * chunk;
-  if (t.tile < 0 || r0 >= t.rows) return;
-  const int rows = static_cast<int>(min(t.rows - r0, static_cast<int64_t>(chunk)));
-  const int64_t at = t.row0 + r0;
-  if (t.item == it.items) {
-    chunk_zeros<T>(y + at * C, C, rows, C, g);
+  const int G = C / cpg;
+  if (t.tile < 0) return;
+  if (r0 >= t.rows) {
+    if (JOIN && t.tile == 0 && t.item < it.items)  // no rows
+      for (int k = threadIdx.x; k < G; k += kGroupThreads) {
+        const int64_t to = static_cast<int64_t>(t.item) * G + k;
+        if (mean) mean[to] = 0.0f;
+        if (rstd) rstd[to] = 1.0f / sqrtf(eps);
+      }
     return;
   }
-  const int64_t G = C / cpg;
+  const int rows = static_cast<int>(min(t.rows - r0, static_cast<int64_t>(chunk)));
+  const int64_t at = t.row0 + r0;
+  x += at * ldx;
+  y += at * C;
+  if (t.item == it.items) {
+    chunk_zeros<T>(y, C, rows, C, g);
+    return;
+  }
+  Piece<T> v[kRowsAhead];
+  const float *m = mean + static_cast<int64_t>(t.item) * G, *r = rstd + static_cast<int64_t>(t.item) * G;
+  bool have = false;
+  if constexpr (JOIN) {
+    const int l = threadIdx.x % g.lanes, rr = threadIdx.x / g.lanes;
+    have = g.strips == 1;
+    if (have && rr < g.rl && rr < rows)
+      read_rows(v, x, ldx, rr, g.rl, live_rows<kRowsAhead>(rows, rr, g.rl), l * kVec<T>, C);
+    auto keep = [&](int k, float group_mean, float variance) {
+      const float group_rstd = 1.0f / sqrtf(variance + eps);
+      lds[k] = group_mean;
+      lds[G + k] = group_rstd;
+      const int64_t to = static_cast<int64_t>(t.item) * G + k;
+      if (t.tile == 0 && mean) mean[to] = group_mean;
+      if (t.tile == 0 && rstd) rstd[to] = group_rstd;
+    };
+    const float2* p = partial + (slot - t.tile) * G;
+    item_moments(p, t.rows, chunk, G, cpg, keep);
+    __syncthreads();
+    m = lds;
+    r = lds + G;
+  }
   with_act(act, [&](auto a) {
-    Piece<T> v[kRowsAhead];
-    chunk_outputs<T, decltype(a)::value>(x + at * ldx, ldx, y + at * C, C, rows, C, cpg, g, mean + t.item * G,
-                                         rstd + t.item * G, w, b, v, false);
+    chunk_outputs<T, decltype(a)::value>(x, ldx, y, C, rows, C, cpg, g, m, r, w, b, v, have);
   });
 }
 
@@ -539,7 +620,9 @@ __device__ __forceinline__ void chunk_grads(const T* dy, int64_t ldg, const T* x
   }
 }
 
-// partial [slots][2][C]: each chunk's sums of dz and of dz xh.
+// partial [slots][2][C]: each chunk's sums of dz and of dz xh; zeros of a slot
+// without rows. groups [slots][2][G], or null: a chunk's sums of dz w and of dz w xh
+// over a group's columns.
 template <typename T>
 __global__ __launch_bounds__(kGroupThreads) void k_group_sums(const T* __restrict__ dy, int64_t ldg,
                                                               const T* __restrict__ x, int64_t ldx, Items it, int C,
@@ -548,22 +631,34 @@ __global__ __launch_bounds__(kGroupThreads) void k_group_sums(const T* __restric
                                                               const float* __restrict__ rstd,
                                                               const float* __restrict__ w,
                                                               const float* __restrict__ b, int act,
-                                                              float* __restrict__ partial) {
+                                                              float* __restrict__ partial,
+                                                              float* __restrict__ groups) {
   extern __shared__ float lds[];
   const ItemTile t = find_chunk(it, chunk, blockIdx.x);
   const int64_t r0 = t.tile * chunk;
-  if (t.item == it.items || t.tile < 0 || r0 >= t.rows) return;
+  float* out = partial + static_cast<int64_t>(blockIdx.x) * 2 * C;
+  if (t.item == it.items || t.tile < 0 || r0 >= t.rows) {
+    for (int c = threadIdx.x; c < 2 * C; c += kGroupThreads) out[c] = 0.0f;
+    return;
+  }
   const int rows = static_cast<int>(min(t.rows - r0, static_cast<int64_t>(chunk)));
   const int64_t at = t.row0 + r0, G = C / cpg;
-  float* out = partial + static_cast<int64_t>(blockIdx.x) * 2 * C;
+  float* const sz = lds;
+  float* const sx = lds + g.rl * g.lanes * kVec<T> * g.strips;
   with_act(act, [&](auto a) {
     Piece<T> v[kGradRowsAhead], d[kGradRowsAhead];
     chunk_sums<T, decltype(a)::value>(dy + at * ldg, ldg, x + at * ldx, ldx, rows, C, cpg, g, mean + t.item * G,
                                       rstd + t.item * G, w, b, lds, v, d, [&](int c, float z, float q) {
                                         out[c] = z;
                                         out[C + c] = q;
+                                        sz[c] = z;  // (its threads alone have read the column)
+                                        sx[c] = q;
                                       });
   });
+  if (!groups) return;
+  __syncthreads();
+  groups += static_cast<int64_t>(blockIdx.x) * 2 * G;
+  group_means(C, cpg, w, 1.0f, [&](int c) { return sz[c]; }, [&](int c) { return sx[c]; }, groups, groups + G);
 }
 
 // Sums of an item's chunks: 16 columns of the 2 C a workgroup, NT / 16 chunks at a
@@ -595,52 +690,91 @@ __global__ __launch_bounds__(NT) void k_group_join_sums(const float* __restrict_
   else sx[static_cast<int64_t>(item) * C + col - C] = sum;
 }
 
-// dx of a chunk, the chunks from the last on (see k_group_apply); in workgroups
-// from `slots` on 256 columns' dw and db, the sums over a few items (a launch of
-// their own would take 4 us).
-template <typename T>
+// dx of a chunk, the chunks from the last on (see k_group_apply). The first `sums`
+// workgroups have columns of dw and db (a launch of their own would take 4 us):
+// where JOIN 16 of the 2 C columns each, over all slots, else 256 each, over a few
+// items. JOIN: a workgroup joins its item's chunks itself, from their groups' sums,
+// while its first rows are on their way; else sz and sx [items][C] are read.
+template <typename T, bool JOIN>
 __global__ __launch_bounds__(kGroupThreads) void k_group_dx(const T* __restrict__ dy, int64_t ldg,
                                                             const T* __restrict__ x, int64_t ldx, Items it, int C,
-                                                            int cpg, Lanes g, uint32_t chunk, int64_t slots,
-                                                            const float* __restrict__ mean,
+                                                            int cpg, Lanes g, uint32_t chunk, int sums,
+                                                            int64_t slots, const float* __restrict__ mean,
                                                             const float* __restrict__ rstd,
                                                             const float* __restrict__ w, const float* __restrict__ b,
                                                             int act, const float* __restrict__ sz,
-                                                            const float* __restrict__ sx, T* __restrict__ dx,
+                                                            const float* __restrict__ sx,
+                                                            const float* __restrict__ partial,
+                                                            const float* __restrict__ groups, T* __restrict__ dx,
                                                             float* __restrict__ dw, float* __restrict__ db) {
   extern __shared__ float lds[];
-  const int64_t G = C / cpg;
-  if (blockIdx.x >= slots) {
-    const int64_t c = (blockIdx.x - slots) * kGroupThreads + threadIdx.x;
-    if (c >= C) return;
-    float z = 0.0f, q = 0.0f;
+  const int G = C / cpg;
+  if (blockIdx.x < sums) {
+    if constexpr (JOIN) {
+      constexpr int LANES = kGroupThreads / kJoinCols;
+      __shared__ float part[LANES][kJoinCols];
+      const int q = threadIdx.x % kJoinCols, t = threadIdx.x / kJoinCols;
+      const int col = blockIdx.x * kJoinCols + q;
+      float sum = 0.0f;
+      if (col < 2 * C) {
+#pragma unroll 16
+        for (int64_t i = t; i < slots; i += LANES) sum += partial[i * 2 * C + col];
+      }
+      part[t][q] = sum;
+      __syncthreads();
+      if (t != 0 || col >= 2 * C) return;
+      sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < LANES; ++i) sum += part[i][q];
+      if (col < C && db) db[col] = sum;
+      if (col >= C && dw) dw[col - C] = sum;
+    } else {
+      const int c = blockIdx.x * kGroupThreads + threadIdx.x;
+      if (c >= C) return;
+      float z = 0.0f, q = 0.0f;
 #pragma unroll 8
-    for (int64_t i = 0; i < it.items; ++i) {
-      z += sz[i * C + c];
-      q += sx[i * C + c];
+      for (int64_t i = 0; i < it.items; ++i) {
+        z += sz[i * C + c];
+        q += sx[i * C + c];
+      }
+      if (dw) dw[c] = q;
+      if (db) db[c] = z;
     }
-    if (dw) dw[c] = q;
-    if (db) db[c] = z;
     return;
   }
-  const ItemTile t = find_chunk(it, chunk, slots - 1 - blockIdx.x);
+  const int64_t slot = gridDim.x - 1 - blockIdx.x;
+  const ItemTile t = find_chunk(it, chunk, slot);
   const int64_t r0 = t.tile * chunk;
   if (t.tile < 0 || r0 >= t.rows) return;
   const int rows = static_cast<int>(min(t.rows - r0, static_cast<int64_t>(chunk)));
-  const int64_t at = t.row0 + r0;
+  const int64_t at = t.row0 + r0, stats = static_cast<int64_t>(t.item) * G;
   if (t.item == it.items) {
     chunk_zeros<T>(dx + at * C, C, rows, C, g);
     return;
   }
-  const float* z = sz + static_cast<int64_t>(t.item) * C;
-  const float* q = sx + static_cast<int64_t>(t.item) * C;
+  const float inv = 1.0f / (static_cast<float>(t.rows) * static_cast<float>(cpg));
   with_act(act, [&](auto a) {
     Piece<T> v[kGradRowsAhead], d[kGradRowsAhead];
     chunk_grads<T, decltype(a)::value>(
-        dy + at * ldg, ldg, x + at * ldx, ldx, dx + at * C, C, rows, C, cpg, g, mean + t.item * G, rstd + t.item * G, w,
-        b, lds, lds + G, v, d, false, [&] {
-          group_means(C, cpg, w, 1.0f / (static_cast<float>(t.rows) * static_cast<float>(cpg)),
-                      [&](int c) { return z[c]; }, [&](int c) { return q[c]; }, lds, lds + G);
+        dy + at * ldg, ldg, x + at * ldx, ldx, dx + at * C, C, rows, C, cpg, g, mean + stats, rstd + stats, w, b, lds,
+        lds + G, v, d, false, [&] {
+          if constexpr (JOIN) {
+            const float* p = groups + (slot - t.tile) * 2 * G;
+            const int chunks = static_cast<int>(static_cast<uint32_t>(t.rows + chunk - 1) / chunk);
+            const int width = sum_width(2 * G), l = threadIdx.x % width;
+            for (int k = threadIdx.x / width; k < 2 * G; k += kGroupThreads / width) {
+              float sum = 0.0f;
+#pragma unroll 16
+              for (int c = l; c < chunks; c += width) sum += p[static_cast<int64_t>(c) * 2 * G + k];
+              sum = width_sum(sum, width);
+              if (l == 0) lds[k] = sum * inv;
+            }
+            __syncthreads();
+          } else {
+            const float* z = sz + static_cast<int64_t>(t.item) * C;
+            const float* q = sx + static_cast<int64_t>(t.item) * C;
+            group_means(C, cpg, w, inv, [&](int c) { return z[c]; }, [&](int c) { return q[c]; }, lds, lds + G);
+          }
         });
   });
 }
@@ -717,6 +851,17 @@ uint32_t chunk_rows(int64_t n, int C, int elem, const Lanes& g, bool grad) {
   return static_cast<uint32_t>(std::max<int64_t>(std::max(8, g.rl), (n + chunks - 1) / chunks));
 }
 
+// Whether the workgroups of the outputs join their item's chunks themselves, in place
+// of a launch of 5 us: where an item has few on average. Each of them reads 8 bytes a
+// chunk and group, most of it from another die's cache. Forward / backward us, three
+// launches -> two: 20011 x 60 in 12 groups, 7 items (276 parts an item) 16 / 21 -> 13 /
+// 18; 100000 x 96 in 32, 100 items (256) 35 / 50 -> 32 / 44; one item, 100000 x 32 in 8
+// (2000) 17.4 / 21.0 -> 17.7 / 19.7, 1000 x 256 in 32 (4000) 16.0 / 20.6 -> 16.6 / 18.5,
+// 20000 x 320 in 32 (6700) 23 / 33 -> 25 / 35.
+bool joins_itself(const GroupShape& s, uint32_t chunk, bool grad) {
+  return (s.it.n / chunk / s.it.items + 1) * s.G <= (grad ? 4096 : 1024);
+}
+
 // A workgroup of the one-launch kernels takes columns of about 128 bytes, whole
 // groups, at most 256 of them.
 int groups_per_workgroup(const GroupShape& s, int elem) {
@@ -752,29 +897,38 @@ int group_forward(const GroupShape& s, const void* xp, int64_t ldx, const float*
   const Lanes g = lanes_of(s.C, kVec<T>);
   const uint32_t chunk = chunk_rows(s.it.n, s.C, sizeof(T), g, false);
   const int64_t slots = chunk_slots(s.it, chunk), stats = static_cast<int64_t>(s.it.items) * s.G;
+  const bool join = joins_itself(s, chunk, false);
   float2* partial = static_cast<float2*>(ws.take(slots * s.G * 8));
-  float* spare = static_cast<float*>(ws.take(2 * stats * 4));
+  float* spare = join ? nullptr : static_cast<float*>(ws.take(2 * stats * 4));
   if (ws.counting) return SUBMCONV_OK;
-  if (!mean) mean = spare;
-  if (!rstd) rstd = spare + stats;
   const unsigned grid = static_cast<unsigned>(slots);
   k_group_moments<T><<<grid, kGroupThreads, lanes_lds(g, kVec<T>) * 4, stream>>>(x, ldx, s.it, s.C, s.cpg, g, chunk,
                                                                                  partial);
   SUBMCONV_HIP_CHECK(hipGetLastError());
-  const dim3 join(s.G, s.it.items);
-  if (s.it.items <= kFewItems) k_group_join<256><<<join, 256, 0, stream>>>(partial, s.it, s.G, s.cpg, chunk, eps, mean, rstd);
-  else k_group_join<64><<<join, 64, 0, stream>>>(partial, s.it, s.G, s.cpg, chunk, eps, mean, rstd);
+  if (join) {
+    k_group_apply<T, true><<<grid, kGroupThreads, 2 * s.G * 4, stream>>>(x, ldx, s.it, s.C, s.cpg, g, chunk, partial,
+                                                                         eps, mean, rstd, w, b, act, y);
+    SUBMCONV_HIP_CHECK(hipGetLastError());
+    return SUBMCONV_OK;
+  }
+  if (!mean) mean = spare;
+  if (!rstd) rstd = spare + stats;
+  const dim3 of(s.G, s.it.items);
+  if (s.it.items <= kFewItems) k_group_join<256><<<of, 256, 0, stream>>>(partial, s.it, s.G, s.cpg, chunk, eps, mean, rstd);
+  else k_group_join<64><<<of, 64, 0, stream>>>(partial, s.it, s.G, s.cpg, chunk, eps, mean, rstd);
   SUBMCONV_HIP_CHECK(hipGetLastError());
-  k_group_apply<T><<<grid, kGroupThreads, 0, stream>>>(x, ldx, s.it, s.C, s.cpg, g, chunk, mean, rstd, w, b, act, y);
+  k_group_apply<T, false><<<grid, kGroupThreads, 0, stream>>>(x, ldx, s.it, s.C, s.cpg, g, chunk, nullptr, eps, mean,
+                                                              rstd, w, b, act, y);
   SUBMCONV_HIP_CHECK(hipGetLastError());
   return SUBMCONV_OK;
 }
 
-// dw and db from the items' sums [items][C].
-int sum_items(const GroupShape& s, const float* sz, const float* sx, float* dw, float* db, hipStream_t stream) {
+// dw and db from `parts` sums of each column, ld apart.
+int sum_parts(const GroupShape& s, int64_t parts, int64_t ld, const float* sz, const float* sx, float* dw, float* db,
+              hipStream_t stream) {
   SumList list;
-  if (db) list.job[list.count++] = SumJob{sz, s.it.items, s.C, s.C, 1, db};
-  if (dw) list.job[list.count++] = SumJob{sx, s.it.items, s.C, s.C, 1, dw};
+  if (db) list.job[list.count++] = SumJob{sz, parts, ld, s.C, 1, db};
+  if (dw) list.job[list.count++] = SumJob{sx, parts, ld, s.C, 1, dw};
   return list.count ? run_sums(list, stream) : SUBMCONV_OK;
 }
 
@@ -798,32 +952,46 @@ int group_backward(const GroupShape& s, const void* gp, int64_t ldg, const void*
     k_group_norm_grad<T><<<grid, kGroupThreads, lanes_lds(g, kVec<T>) * 4, stream>>>(
         dy, ldg, x, ldx, s.it, s.C, s.cpg, gpw, g, mean, rstd, w, b, act, dx, sz, sx);
     SUBMCONV_HIP_CHECK(hipGetLastError());
-    return one ? SUBMCONV_OK : sum_items(s, sz, sx, dw, db, stream);
+    return one ? SUBMCONV_OK : sum_parts(s, s.it.items, s.C, sz, sx, dw, db, stream);
   }
   const Lanes g = lanes_of(s.C, kVec<T>);
   const uint32_t chunk = chunk_rows(s.it.n, s.C, sizeof(T), g, true);
   const int64_t slots = chunk_slots(s.it, chunk);
+  const bool join = joins_itself(s, chunk, true);
   float* partial = static_cast<float*>(ws.take(slots * 2 * s.C * 4));
-  float* spare = static_cast<float*>(ws.take(2 * sums * 4));
+  float* groups = join ? static_cast<float*>(ws.take(slots * 2 * s.G * 4)) : nullptr;
+  float* spare = join ? nullptr : static_cast<float*>(ws.take(2 * sums * 4));
   if (ws.counting) return SUBMCONV_OK;
+  k_group_sums<T><<<static_cast<unsigned>(slots), kGroupThreads, lanes_lds(g, kVec<T>) * 4, stream>>>(
+      dy, ldg, x, ldx, s.it, s.C, s.cpg, g, chunk, mean, rstd, w, b, act, partial, dx ? groups : nullptr);
+  SUBMCONV_HIP_CHECK(hipGetLastError());
+  const int64_t tiles = dx ? slots : 0;
+  if (join) {
+    const bool here = (dw || db) && slots <= kChunks + kFewItems;  // the sums over the slots
+    const int extra = here ? (2 * s.C + kJoinCols - 1) / kJoinCols : 0;
+    if (tiles + extra > 0) {
+      k_group_dx<T, true><<<static_cast<unsigned>(tiles + extra), kGroupThreads, 2 * s.G * 4, stream>>>(
+          dy, ldg, x, ldx, s.it, s.C, s.cpg, g, chunk, extra, slots, mean, rstd, w, b, act, nullptr, nullptr, partial,
+          groups, dx, dw, db);
+      SUBMCONV_HIP_CHECK(hipGetLastError());
+    }
+    return here ? SUBMCONV_OK : sum_parts(s, slots, 2 * s.C, partial, partial + s.C, dw, db, stream);
+  }
   float* sz = one && db ? db : spare;
   float* sx = one && dw ? dw : spare + sums;
-  k_group_sums<T><<<static_cast<unsigned>(slots), kGroupThreads, lanes_lds(g, kVec<T>) * 4, stream>>>(
-      dy, ldg, x, ldx, s.it, s.C, s.cpg, g, chunk, mean, rstd, w, b, act, partial);
-  SUBMCONV_HIP_CHECK(hipGetLastError());
-  const dim3 join((2 * s.C + kJoinCols - 1) / kJoinCols, s.it.items);
-  if (s.it.items <= kFewItems) k_group_join_sums<1024><<<join, 1024, 0, stream>>>(partial, s.it, s.C, chunk, sz, sx);
-  else k_group_join_sums<128><<<join, 128, 0, stream>>>(partial, s.it, s.C, chunk, sz, sx);
+  const dim3 of((2 * s.C + kJoinCols - 1) / kJoinCols, s.it.items);
+  if (s.it.items <= kFewItems) k_group_join_sums<1024><<<of, 1024, 0, stream>>>(partial, s.it, s.C, chunk, sz, sx);
+  else k_group_join_sums<128><<<of, 128, 0, stream>>>(partial, s.it, s.C, chunk, sz, sx);
   SUBMCONV_HIP_CHECK(hipGetLastError());
   const bool here = !one && s.it.items <= kFewItems && (dw || db);  // the sums over the items
-  const int64_t grid = (dx ? slots : 0) + (here ? (s.C + kGroupThreads - 1) / kGroupThreads : 0);
-  if (grid > 0) {
-    k_group_dx<T><<<static_cast<unsigned>(grid), kGroupThreads, 2 * s.G * 4, stream>>>(
-        dy, ldg, x, ldx, s.it, s.C, s.cpg, g, chunk, dx ? slots : 0, mean, rstd, w, b, act, sz, sx, dx,
-        here ? dw : nullptr, here ? db : nullptr);
+  const int extra = here ? (s.C + kGroupThreads - 1) / kGroupThreads : 0;
+  if (tiles + extra > 0) {
+    k_group_dx<T, false><<<static_cast<unsigned>(tiles + extra), kGroupThreads, 2 * s.G * 4, stream>>>(
+        dy, ldg, x, ldx, s.it, s.C, s.cpg, g, chunk, extra, slots, mean, rstd, w, b, act, sz, sx, nullptr, nullptr, dx,
+        dw, db);
     SUBMCONV_HIP_CHECK(hipGetLastError());
   }
-  return one || here ? SUBMCONV_OK : sum_items(s, sz, sx, dw, db, stream);
+  return one || here ? SUBMCONV_OK : sum_parts(s, s.it.items, s.C, sz, sx, dw, db, stream);
 }
 
 template <typename F>
