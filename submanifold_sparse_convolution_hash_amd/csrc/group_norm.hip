@@ -10,11 +10,11 @@
 // Bound by memory: the statistics need all of an item before its first output,
 // so x (and dy) are read twice. The rows are cut into chunks of one item each:
 // a first launch leaves each chunk's sums, a second joins them, a third makes
-// the outputs (and joins the chunks itself, where an item has few). A thread keeps its 16 bytes of columns for all rows of its
-// chunk, so that sums per channel stay in registers. All sums are fp32 and
-// joined in a fixed order: results repeat bit for bit. Means and squares about
-// the mean are joined pairwise (n, mean, square sum), so that a mean of many
-// deviations costs no digits.
+// the outputs (and joins the chunks itself, where an item has few). A thread keeps
+// its 16 bytes of columns for all rows of its chunk, so that sums per channel stay
+// in registers. All sums are fp32 and joined in a fixed order: results repeat bit
+// for bit. Means and squares about the mean are joined pairwise (n, mean, square
+// sum), so that a mean of many deviations costs no digits.
 //
 // 209715 x 128 in 32 groups, silu: fp16 forward 20 + 5 + 24 us (54 + 0 + 107 MB at
 // the memory), bf16 gradients 27 + 5 + 34 (107 + 0 + 161 MB, 3.9 and 4.7 TB/s); 209715
@@ -844,10 +844,13 @@ struct GroupShape {
 // 768 45 / 64, 1024 43 / 69, 2048 51 / 83. Where the walk is more than the 256 MB that
 // the second one finds in the caches, eight rounds: 209715 x 1024, 1024 chunks 278 /
 // 465, 2048 262 / 428. At least a row for each row of threads.
-uint32_t chunk_rows(int64_t n, int C, int elem, const Lanes& g, bool grad) {
-  const int64_t two = std::max(1, 2 * kRowsAhead * g.rl / g.strips), round = two * kUnits;
-  const bool cached = n * C * elem * (grad ? 2 : 1) <= int64_t{256} << 20;
-  const int64_t chunks = kUnits * std::clamp<int64_t>((n + round / 2) / round, 1, !cached ? 8 : grad ? 3 : 4);
+uint32_t chunk_rows(const GroupShape& s, int elem, const Lanes& g, bool grad) {
+  const int64_t n = s.it.n, two = std::max(1, 2 * kRowsAhead * g.rl / g.strips), round = two * kUnits;
+  const bool cached = n * s.C * elem * (grad ? 2 : 1) <= int64_t{256} << 20;
+  // (the last chunk of an item is a part of one: they fit into the rounds as well; 100000 x
+  // 96 of 70 items 37 / 51 without, 30 / 42 with)
+  const int64_t chunks = kUnits * std::clamp<int64_t>((n + round / 2) / round, 1, !cached ? 8 : grad ? 3 : 4) -
+                         (s.it.items < kUnits / 2 ? s.it.items + 1 : 0);
   return static_cast<uint32_t>(std::max<int64_t>(std::max(8, g.rl), (n + chunks - 1) / chunks));
 }
 
@@ -895,7 +898,7 @@ int group_forward(const GroupShape& s, const void* xp, int64_t ldx, const float*
     return SUBMCONV_OK;
   }
   const Lanes g = lanes_of(s.C, kVec<T>);
-  const uint32_t chunk = chunk_rows(s.it.n, s.C, sizeof(T), g, false);
+  const uint32_t chunk = chunk_rows(s, sizeof(T), g, false);
   const int64_t slots = chunk_slots(s.it, chunk), stats = static_cast<int64_t>(s.it.items) * s.G;
   const bool join = joins_itself(s, chunk, false);
   float2* partial = static_cast<float2*>(ws.take(slots * s.G * 8));
@@ -955,7 +958,7 @@ int group_backward(const GroupShape& s, const void* gp, int64_t ldg, const void*
     return one ? SUBMCONV_OK : sum_parts(s, s.it.items, s.C, sz, sx, dw, db, stream);
   }
   const Lanes g = lanes_of(s.C, kVec<T>);
-  const uint32_t chunk = chunk_rows(s.it.n, s.C, sizeof(T), g, true);
+  const uint32_t chunk = chunk_rows(s, sizeof(T), g, true);
   const int64_t slots = chunk_slots(s.it, chunk);
   const bool join = joins_itself(s, chunk, true);
   float* partial = static_cast<float*>(ws.take(slots * 2 * s.C * 4));
