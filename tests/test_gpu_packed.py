@@ -123,7 +123,9 @@ NORMS = [([1], 0, 8, 1, 0), ([7], 0, 32, 32, 0), ([64, 0], 3, 256, 32, 0), ([20,
          ([3000], 0, 128, 32, 0), ([1500, 0, 2500, 1], 77, 60, 12, 3), ([2100], 9, 33, 3, 1), ([1100, 5], 0, 515, 5, 0),
          ([1300], 0, 2056, 8, 0), ([900, 200], 0, 4100, 1, 2), ([1025], 0, 8192, 64, 0), ([700, 700], 3, 8192, 8192, 0),
          ([0, 1200, 0], 100, 20, 20, 0), ([3] * 400, 1, 8, 2, 0), ([0], 0, 16, 4, 0),
-         ([40] * 100 + [0, 1, 5000], 3, 96, 8, 0), ([2] * 3000, 5, 40, 5, 0)]
+         ([40] * 100 + [0, 1, 5000], 3, 96, 8, 0), ([2] * 3000, 5, 40, 5, 0),
+         ([100] * 127, 0, 40, 5, 0), ([60] * 128, 2, 64, 8, 0), ([9000] + [1] * 126, 0, 16, 2, 0), ([20000], 5, 33, 11, 0),
+         ([0, 12000, 30], 0, 320, 32, 0)]
 
 
 def _joins(lengths, c, groups):
