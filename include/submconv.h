@@ -745,7 +745,8 @@ int64_t submconv_attention_workspace_bytes(int64_t nq, int64_t nk, int32_t heads
  * that sees no key has out = 0 and lse = -inf. out [nq,heads,dim] dense; lse
  * [nq,heads] fp32 or NULL: log of the sum of exp(scale q k). scale > 0. Scores,
  * their maximum and sum and out are fp32; the weights are rounded to the
- * data's type between the two products.
+ * data's type between the two products (in fp16 times a power of two, so that a
+ * weight loses at most 2^-32 of its row's largest below the normal numbers).
  */
 int submconv_attention(const uint16_t* q, int64_t ldq, int64_t hq, int64_t nq, const uint16_t* k,
                        int64_t ldk, int64_t hk, const uint16_t* v, int64_t ldv, int64_t hv,

@@ -44,9 +44,14 @@ struct AttnOut {
 };
 
 // The maximum is raised, and what was summed scaled down, only once a score
-// passes it by this many powers of two: weights stay below 2^8, which 16 bits
-// hold as exactly as any other, and the sums' 32 bits have room.
+// passes it by this many powers of two: weights stay below 2^8, which bf16
+// holds as exactly as any other, and the sums' 32 bits have room. In fp16 they are
+// taken times 2^7, up to 2^15 of its range, so that small ones beside a large one
+// keep their digits: a weight loses at most 2^-32 of the row's largest (2^-25
+// without, which 10^5 keys 17 below one of a small value lost altogether).
 constexpr float kSlack = 8.0f;
+template <bool BF16>
+constexpr float kUp = BF16 ? 0.0f : 7.0f;
 
 // KG = 2: two groups of NW waves have the same rows and take every other tile of
 // keys, each with its own buffers; what they have is joined through LDS. For the
@@ -110,7 +115,7 @@ __global__ __launch_bounds__(NW * KG * 64, NW == 1 ? 1 : 2) void k_attention(Att
   }
   settle(q);
   const float c = a.scale * kLog2e;
-  float m = -kInf, mc = 0.0f, sum = 0.0f;  // mc = m c, 0 while m is -inf
+  float m = -kInf, mc = 0.0f, sum = 0.0f;  // mc = m c - kUp, 0 while m is -inf
   float16v acc[DB];
 #pragma unroll
   for (int j = 0; j < DB; ++j) acc[j] = float16v{};
@@ -144,10 +149,10 @@ __global__ __launch_bounds__(NW * KG * 64, NW == 1 ? 1 : 2) void k_attention(Att
 #pragma unroll
       for (int i = b == 0 ? 1 : 0; i < 16; ++i) top = fmaxf(top, s[b][i]);
     top = halves_max(top);
-    const bool raise = top * c > mc + kSlack || (m == -kInf && top > -kInf);
+    const bool raise = top * c > mc + (kUp<BF16> + kSlack) || (m == -kInf && top > -kInf);
     if (__ballot(raise)) {
       const float next = raise ? top : m;
-      const float nc = next == -kInf ? 0.0f : next * c;
+      const float nc = next == -kInf ? 0.0f : next * c - kUp<BF16>;
       const float f = m == -kInf ? 0.0f : __builtin_amdgcn_exp2f(mc - nc);
       m = next;
       mc = nc;
