@@ -208,13 +208,17 @@ int rotate(const void* x, void* out, Rotary a, bool interleaved, hipStream_t str
   a.stride = interleaved ? a.turn_units * (VEC / 2) : a.turn_units * VEC;
   // As many rows as fill 512 pairs, where there are 2048 workgroups of them
   // (209715 x 8 x 64 with one axis: 79 us; 4096 pairs 105, 256 88). With few rows
-  // their heads are shared out as well, 256 pieces or more a workgroup.
+  // their heads are shared out as well, 256 pieces or more a workgroup. With very many
+  // rows no more workgroups than a launch can have.
   a.rows = static_cast<int>(std::clamp<int64_t>(a.n / 2048, 1, std::max(1, kRotaryRun / a.stride)));
+  while (!launch_fits((a.n + a.rows - 1) / a.rows, kRotaryThreads)) ++a.rows;
   const int64_t blocks = (a.n + a.rows - 1) / a.rows;
   const int64_t shares = std::clamp<int64_t>(256 / blocks, 1, std::max<int64_t>(1, int64_t{a.heads} * a.units / 256));
   a.share = static_cast<int>((a.heads + shares - 1) / shares);
   const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>((a.heads + a.share - 1) / a.share));
   const int lds = a.rows * a.stride * static_cast<int>(sizeof(float2));
+  if (lds > 65536)
+    return set_error(SUBMCONV_ERR_UNSUPPORTED_SHAPE, "%lld rows of %d pairs", (long long)a.n, a.pairs);
   const T* from = static_cast<const T*>(x);
   T* to = static_cast<T*>(out);
   if (interleaved) k_rotary<T, VEC, true><<<grid, kRotaryThreads, lds, stream>>>(from, to, a);

@@ -12,6 +12,12 @@
 
 namespace submconv {
 
+// Whether a launch can have this many workgroups along an axis: from 2^32 threads on
+// it is cut to the count's low 32 bits, without an error.
+inline bool launch_fits(int64_t blocks, int threads) {
+  return blocks <= INT32_MAX && blocks * threads < int64_t{1} << 32;
+}
+
 // Number of taps of a 3x3x3 kernel and the centre tap, k = 9(dx+1)+3(dy+1)+(dz+1).
 constexpr int kTaps3 = 27;
 constexpr int kCenterTap = 13;
