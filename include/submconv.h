@@ -657,7 +657,9 @@ int submconv_gated_ffn_backward(const uint16_t* grad_out, int64_t ldg, int64_t n
  * only: one item of all n rows. Rows from offsets[items] on belong to no item
  * and are written as zeros. Nothing waits for the offsets: they are not
  * checked, but cut to 0 .. n, so that no access leaves the tensors; if they
- * descend, the results mean nothing. items up to 65535, rows up to 2^31 - 1025.
+ * descend, the results mean nothing. items up to 65535, rows up to 2^31 - 1025;
+ * attention refuses more tiles of rows and heads than one launch can have (heads
+ * n near 2^31).
  * Everything else as for the dense layers: asynchronous, no allocation, sums
  * in one order, each stored value rounded once.
  * ---------------------------------------------------------------------- */

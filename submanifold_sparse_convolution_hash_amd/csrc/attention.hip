@@ -359,7 +359,8 @@ int attention_forward(const Attention& a, bool bf16, uint16_t* out, float* lse, 
   }
   if (ws.counting) return SUBMCONV_OK;
   const int64_t blocks = p.slots * a.kv_heads;
-  if (blocks > INT32_MAX) return set_error(SUBMCONV_ERR_UNSUPPORTED_SHAPE, "%lld tiles", (long long)blocks);
+  if (!launch_fits(blocks, p.waves * p.groups * 64))
+    return set_error(SUBMCONV_ERR_UNSUPPORTED_SHAPE, "too many tiles: %lld", (long long)blocks);
   using One = std::integral_constant<int, 1>;
   using Two = std::integral_constant<int, 2>;
   using Four = std::integral_constant<int, 4>;

@@ -461,7 +461,9 @@ int attention_backward(const Attention& a, const AttnGrad& g, bool bf16, Arena& 
   join(ok.dv, ok.dv_part, k_rows, ok.splits);
   if (ws.counting) return SUBMCONV_OK;
   const int64_t q_blocks = oq.slots * a.kv_heads, k_blocks = ok.slots * a.kv_heads;
-  if (std::max(q_blocks, k_blocks) > INT32_MAX) return set_error(SUBMCONV_ERR_UNSUPPORTED_SHAPE, "too many tiles");
+  if (!launch_fits(q_blocks, 256) || !launch_fits(k_blocks, a.D > 96 ? 512 : 256))
+    return set_error(SUBMCONV_ERR_UNSUPPORTED_SHAPE, "too many tiles: %lld and %lld", (long long)q_blocks,
+                     (long long)k_blocks);
   const bool keys = a.ki.n > 0 && (g.dk || g.dv);
   auto go = [&](auto b, auto dp) {
     constexpr bool B = decltype(b)::value;
