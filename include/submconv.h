@@ -119,7 +119,8 @@ typedef struct submconv_map_s* submconv_map_t;
  *
  * coords   [n,4] int32 (b,x,y,z), device. Sites must be distinct and satisfy
  *          0 <= b < batch, 0 <= x < grid[0], 0 <= y < grid[1], 0 <= z < grid[2].
- * n        number of sites (n = 0 gives an empty map).
+ * n        number of sites (n = 0 gives an empty map); from about 3.0e8 on (1.5e8
+ *          with sorted keys) a launch has too few threads, and they are refused.
  * batch    number of batch items (>= 1).
  * grid     host array of 3 positive extents.
  * flags    0 or SUBMCONV_FLAG_MORTON (iteration order only; results are the

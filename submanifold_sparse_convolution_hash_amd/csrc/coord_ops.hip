@@ -300,6 +300,8 @@ extern "C" int submconv_downsample_max(submconv_down_t plan, const uint16_t* fea
   if ((reinterpret_cast<uintptr_t>(feats) | reinterpret_cast<uintptr_t>(out)) & 15)
     return set_error(SUBMCONV_ERR_INVALID_ARG, "feats and out must be 16-byte aligned");
   const int64_t items = d.m * (cdim / 8);
+  if (!launch_fits((items + 255) / 256, 256))
+    return set_error(SUBMCONV_ERR_UNSUPPORTED_SHAPE, "too many features: %lld x %d", (long long)d.m, cdim);
   k_down_max<<<static_cast<unsigned>((items + 255) / 256), 256, 0, stream>>>(
       d.sorted_child, d.seg, d.m, reinterpret_cast<const _Float16*>(feats), cdim,
       reinterpret_cast<_Float16*>(out));
@@ -327,6 +329,8 @@ extern "C" int submconv_subdivide(const int32_t* coords, int64_t n, const uint16
     return set_error(SUBMCONV_ERR_INVALID_ARG, "feats and out_feats must be 16-byte aligned");
   if (n == 0) return SUBMCONV_OK;
   const int per = 8 * (1 + (feats ? cdim / 8 : 0));
+  if (n > INT32_MAX || !launch_fits((n * per + 255) / 256, 256))
+    return set_error(SUBMCONV_ERR_UNSUPPORTED_SHAPE, "too many features: 8 x %lld x %d", (long long)n, cdim);
   const int64_t items = n * per;
   k_subdivide<<<static_cast<unsigned>((items + 255) / 256), 256, 0, stream>>>(
       coords, n, reinterpret_cast<const _Float16*>(feats), cdim, out_coords,

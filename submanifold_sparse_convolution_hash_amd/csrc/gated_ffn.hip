@@ -188,8 +188,8 @@ int gate_forward(const Mat16& x, const Mat16& W, int64_t F, const float* bias, i
                  uint16_t* h, uint16_t* pre, hipStream_t stream) {
   const int64_t Fp = W.cols / 2, Fq = round64(F);
   const int64_t mt = div_up(x.rows, kGateTile), nt = div_up(Fq, kGateTile / 2);
-  if (mt * nt > INT32_MAX)
-    return set_error(SUBMCONV_ERR_UNSUPPORTED_SHAPE, "%lld output tiles", (long long)(mt * nt));
+  if (!launch_fits(mt * nt, 512))
+    return set_error(SUBMCONV_ERR_UNSUPPORTED_SHAPE, "too many output tiles: %lld", (long long)(mt * nt));
   const GateEpi e{bias, h, pre, F, Fq, act, F % 8 == 0 && aligned16(pre)};
   const Operand A{x.p, x.ld, x.rows, x.cols}, B{W.p, W.ld, Fp, W.rows};
   const dim3 grid(static_cast<unsigned>(mt * nt));
@@ -210,8 +210,8 @@ int gate_grad(const Mat16& dy, const Mat16& W, int64_t Fq, const uint16_t* pre, 
               uint16_t* dz, uint16_t* h, float* sums, hipStream_t stream) {
   const int64_t F = W.rows;
   const int64_t mt = gate_grad_tiles(dy.rows), nt = div_up(Fq, kGateTile);
-  if (mt * nt > INT32_MAX)
-    return set_error(SUBMCONV_ERR_UNSUPPORTED_SHAPE, "%lld output tiles", (long long)(mt * nt));
+  if (!launch_fits(mt * nt, 512))
+    return set_error(SUBMCONV_ERR_UNSUPPORTED_SHAPE, "too many output tiles: %lld", (long long)(mt * nt));
   const GateGradEpi e{pre, dz, h, sums, F, Fq, act, F % 8 == 0 && aligned16(pre)};
   const Operand A{dy.p, dy.ld, dy.rows, dy.cols}, B{W.p, W.ld, F, W.cols};
   const dim3 grid(static_cast<unsigned>(mt * nt));

@@ -234,6 +234,8 @@ int fused_ffn(const Mat16& x, const Mat16& W_in, int64_t F, const float* b_in, c
   const LinearEpi e{b_out, residual, ldr, out, cout, nullptr, kActNone,
                     cout % 8 == 0 && ldr % 8 == 0 && aligned16(residual),
                     cout % 8 == 0 && aligned16(out), false};
+  if (!launch_fits(div_up(x.rows, kWaves * 32), kWaves * 64))  // of 32 rows a wave
+    return set_error(SUBMCONV_ERR_UNSUPPORTED_SHAPE, "too many rows: %lld", (long long)x.rows);
   auto go = [&](auto width, auto fm) {
     const dim3 grid(static_cast<unsigned>(div_up(x.rows, kWaves * 16 * fm)));
     if (bf16)

@@ -49,8 +49,8 @@ template <bool B_ROW, bool A_TILED, int BM, int BN, int WM, int WN, int STAGES>
 int launch_linear(const Operand& A, const Operand& B, int64_t K, int64_t N, bool bf16,
                   const LinearEpi& e, hipStream_t stream) {
   const int64_t mt = div_up(A.rows, BM), nt = div_up(N, BN);
-  if (mt * nt > INT32_MAX)
-    return set_error(SUBMCONV_ERR_UNSUPPORTED_SHAPE, "%lld output tiles", (long long)(mt * nt));
+  if (!launch_fits(mt * nt, WM * WN * 64))
+    return set_error(SUBMCONV_ERR_UNSUPPORTED_SHAPE, "too many output tiles: %lld", (long long)(mt * nt));
   const dim3 grid(static_cast<unsigned>(mt * nt));
   if (bf16)
     k_linear<true, B_ROW, A_TILED, BM, BN, WM, WN, STAGES><<<grid, WM * WN * 64, 0, stream>>>(A, B, K, N, mt, nt, e);
@@ -457,7 +457,7 @@ int product_tn(const Mat16& x, const Mat16& dz, bool bf16, float* partial, uint1
   const int64_t runs = std::max<int64_t>(1, div_up(x.rows, run));
   const int64_t tile = grad_tile(x.rows, x.cols, dz.cols);
   const int64_t mt = div_up(x.cols, tile), nt = div_up(dz.cols, tile);
-  if (runs * mt * nt > INT32_MAX || div_up(x.cols * dz.cols, 256) > INT32_MAX)
+  if (!launch_fits(runs * mt * nt, 512) || !launch_fits(div_up(x.cols * dz.cols, 256), 256))
     return set_error(SUBMCONV_ERR_UNSUPPORTED_SHAPE, "weight gradient %lld x %lld",
                      (long long)x.cols, (long long)dz.cols);
   const Operand X{x.p, x.ld, x.cols, x.rows}, Z{dz.p, dz.ld, dz.cols, x.rows};

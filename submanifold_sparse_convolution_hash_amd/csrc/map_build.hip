@@ -651,6 +651,10 @@ extern "C" int submconv_build_map(const int32_t* coords, int64_t n, int32_t batc
   }
   const bool morton = (flags & SUBMCONV_FLAG_MORTON) != 0;
   const bool sorted_keys = (flags & SUBMCONV_FLAG_SORTED_KEYS) != 0;
+  // the neighbour query has a thread per row and tap
+  const int64_t query = sorted_keys ? (n * kTaps3 + 255) / 256 : (n + kTileRows - 1) / kTileRows * kQueryTaps;
+  if (!launch_fits(query, 256))
+    return set_error(SUBMCONV_ERR_UNSUPPORTED_SHAPE, "too many rows for one launch: n = %lld", (long long)n);
   int mbits = 0;
   if (morton) {
     mbits = bits_for(std::max(grid[0], std::max(grid[1], grid[2])));
@@ -1047,6 +1051,8 @@ extern "C" int submconv_map_export(submconv_map_t map, int32_t* kmap, hipStream_
   if (m.n == 0) return SUBMCONV_OK;
   if (!kmap) return set_error(SUBMCONV_ERR_INVALID_ARG, "kmap is NULL");
   const int B = 256;
+  if (!launch_fits((m.n * kTaps3 + B - 1) / B, B))
+    return set_error(SUBMCONV_ERR_UNSUPPORTED_SHAPE, "too many rows for one launch: n = %lld", (long long)m.n);
   k_export<<<grid_for(m.n * kTaps3, B), B, 0, stream>>>(m.nbr, m.order, m.n, kmap);
   SUBMCONV_HIP_CHECK(hipGetLastError());
   return SUBMCONV_OK;
