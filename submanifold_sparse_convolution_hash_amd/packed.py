@@ -419,7 +419,7 @@ class SparseAttention(torch.nn.Module):
     tensor. ``channels`` is the row width, ``heads`` of ``dim`` columns (default
     channels / heads), ``kv_heads`` (default heads) of keys and values. With
     ``rotary`` columns of a head and ``axes`` coordinates, queries and keys are
-    turned by their rows' positions (not over a context)."""
+    turned by their rows' positions [N,axes] (not over a context)."""
 
     def __init__(self, channels: int, heads: int, dim: Optional[int] = None, kv_heads: Optional[int] = None,
                  context: Optional[int] = None, rotary: int = 0, axes: int = 3, causal: bool = False,
@@ -437,7 +437,7 @@ class SparseAttention(torch.nn.Module):
         if rotary > dim or rotary and context is not None:
             raise ValueError(f"{rotary} of {dim} columns turn" + (" over a context" if context is not None else ""))
         self.heads, self.kv_heads, self.dim, self.causal, self.interleaved = heads, kv_heads, dim, causal, interleaved
-        self.own = context is None
+        self.own, self.axes = context is None, axes
         if self.own:
             self.proj_in = Linear(channels, (heads + 2 * kv_heads) * dim, device=device, dtype=dtype)
         else:
@@ -456,13 +456,18 @@ class SparseAttention(torch.nn.Module):
     def forward(self, x: torch.Tensor, offsets: Optional[torch.Tensor] = None,
                 positions: Optional[torch.Tensor] = None, context: Optional[torch.Tensor] = None,
                 context_offsets: Optional[torch.Tensor] = None, residual: Optional[torch.Tensor] = None) -> torch.Tensor:
+        if self.freqs is not None:
+            if positions is None:
+                raise ValueError("positions are needed to turn queries and keys")
+            if not isinstance(positions, torch.Tensor):
+                raise TypeError("positions must be a tensor")
+            if positions.dim() not in (1, 2) or (positions.shape[1] if positions.dim() == 2 else 1) != self.axes:
+                raise ValueError(f"positions must be [N,{self.axes}], the module's axes, got {tuple(positions.shape)}")
         h, hk, d = self.heads, self.kv_heads, self.dim
         rows = self.proj_in(x).view(x.shape[0], -1, d)
         if self.own:
             both, v = rows.split([h + hk, hk], 1)
             if self.freqs is not None:
-                if positions is None:
-                    raise ValueError("positions are needed to turn queries and keys")
                 if _recorded(both):
                     both = RotaryFunction.apply(both, positions, self.freqs, self.interleaved, 1.0)
                 else:

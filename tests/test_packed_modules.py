@@ -1,0 +1,20 @@
+"""The attention modules' own checks, without a GPU."""
+import pytest
+import torch
+
+
+def _sc():
+    import submanifold_sparse_convolution_hash_amd as sc
+    return sc
+
+
+@pytest.mark.parametrize("axes,shape", [(3, (5, 4)), (3, (5, 2)), (3, (5, 1)), (3, (5,)), (1, (5, 2)), (2, (5, 3)),
+                                        (1, (5, 1, 1)), (1, ())])
+def test_positions_have_the_modules_axes(axes, shape):
+    """A batch index among them, or an axis too few, would turn other columns."""
+    m = _sc().SparseAttention(64, 1, rotary=12, axes=axes)
+    x = torch.zeros((5, 64), dtype=torch.float16)
+    with pytest.raises(ValueError, match="axes"):
+        m(x, positions=torch.zeros(shape, dtype=torch.int32))
+    with pytest.raises(TypeError, match="positions"):
+        m(x, positions=[1, 2, 3])
