@@ -77,6 +77,8 @@ class SparseAttentionBlock(torch.nn.Module):
     def forward(self, x: torch.Tensor, offsets: Optional[torch.Tensor] = None,
                 positions: Optional[torch.Tensor] = None, context: Optional[torch.Tensor] = None,
                 context_offsets: Optional[torch.Tensor] = None) -> torch.Tensor:
+        if self.over_context is None and not (context is None and context_offsets is None):
+            raise ValueError("the block was made without a context")
         h = self.attention(self.norm(x, offsets), offsets, positions, residual=x)
         if self.over_context is not None:
             h = self.over_context(self.norm_context(h), offsets, context=context, context_offsets=context_offsets,

@@ -456,6 +456,8 @@ class SparseAttention(torch.nn.Module):
     def forward(self, x: torch.Tensor, offsets: Optional[torch.Tensor] = None,
                 positions: Optional[torch.Tensor] = None, context: Optional[torch.Tensor] = None,
                 context_offsets: Optional[torch.Tensor] = None, residual: Optional[torch.Tensor] = None) -> torch.Tensor:
+        if self.own and not (context is None and context_offsets is None):
+            raise ValueError("the module attends among an item's rows: it has no use for a context")
         if self.freqs is not None:
             if positions is None:
                 raise ValueError("positions are needed to turn queries and keys")
@@ -473,7 +475,6 @@ class SparseAttention(torch.nn.Module):
                 else:
                     rotary(both, positions, self.freqs, self.interleaved, out=both)
             q, k = both.split([h, hk], 1)
-            context_offsets = None
         else:
             if context is None:
                 raise ValueError("a context is needed")

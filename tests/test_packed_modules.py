@@ -18,3 +18,14 @@ def test_positions_have_the_modules_axes(axes, shape):
         m(x, positions=torch.zeros(shape, dtype=torch.int32))
     with pytest.raises(TypeError, match="positions"):
         m(x, positions=[1, 2, 3])
+
+
+@pytest.mark.parametrize("what", [dict(context=torch.zeros((2, 8), dtype=torch.float16)),
+                                  dict(context_offsets=torch.zeros(2, dtype=torch.int32))])
+def test_a_context_that_nothing_would_read_is_refused(what):
+    sc = _sc()
+    x = torch.zeros((5, 64), dtype=torch.float16)
+    with pytest.raises(ValueError, match="context"):
+        sc.SparseAttention(64, 2)(x, **what)
+    with pytest.raises(ValueError, match="context"):
+        sc.SparseAttentionBlock(64, 32, heads=2, groups=8)(x, **what)
