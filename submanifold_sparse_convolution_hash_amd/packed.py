@@ -466,7 +466,7 @@ class SparseAttention(torch.nn.Module):
             if positions.dim() not in (1, 2) or (positions.shape[1] if positions.dim() == 2 else 1) != self.axes:
                 raise ValueError(f"positions must be [N,{self.axes}], the module's axes, got {tuple(positions.shape)}")
         h, hk, d = self.heads, self.kv_heads, self.dim
-        rows = self.proj_in(x).view(x.shape[0], -1, d)
+        rows = self.proj_in(x).view(x.shape[0], h + 2 * hk if self.own else h, d)
         if self.own:
             both, v = rows.split([h + hk, hk], 1)
             if self.freqs is not None:

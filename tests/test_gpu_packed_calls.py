@@ -46,3 +46,46 @@ def test_rotary_of_more_rows_than_a_launch_has_workgroups(dev):
             assert torch.equal(x[p], w), p
             x[p] = 0.0
         assert not x.any()  # the rows between them, which were zeros
+
+
+@gpu
+@pytest.mark.parametrize("items", [None, 1, 3])
+@pytest.mark.parametrize("context_rows", [None, 0, 7])
+def test_block_without_rows(dev, items, context_rows):
+    """No sites: an output of no rows, gradients of zero."""
+    sc = _sc()
+    width = None if context_rows is None else 24
+    m = sc.SparseAttentionBlock(64, 96, heads=4, kv_heads=2, groups=8, context=width, rotary=12, device=dev)
+    x = torch.zeros((0, 64), dtype=torch.float16, device=dev, requires_grad=True)
+    at = torch.zeros((0, 3), dtype=torch.int32, device=dev)
+    off = None if items is None else torch.zeros(items + 1, dtype=torch.int32, device=dev)
+    extra = ()
+    if context_rows is not None:
+        ctx = _randn((context_rows, width), torch.float16, dev, 1).requires_grad_()
+        coff = None if items is None else torch.tensor([0] * items + [context_rows], dtype=torch.int32, device=dev)
+        extra = (ctx, coff)
+    with torch.no_grad():
+        assert m(x, off, at, *extra).shape == (0, 64)
+    y = m(x, off, at, *extra)
+    assert y.shape == (0, 64) and y.requires_grad
+    y.backward(torch.zeros_like(y))
+    assert x.grad.shape == (0, 64)
+    for name, p in m.named_parameters():
+        assert p.grad is not None and p.grad.shape == p.shape and not p.grad.any(), name
+    if context_rows is not None:
+        assert ctx.grad.shape == ctx.shape and not ctx.grad.any()
+
+
+@gpu
+def test_attention_over_a_context_without_rows(dev):
+    """Sites that attend to nothing get the last product's bias."""
+    sc = _sc()
+    m = sc.SparseAttention(32, 2, context=16, device=dev)
+    m.proj_out.bias.data += torch.linspace(-1, 1, 32, device=dev)
+    x = _randn((9, 32), torch.float16, dev, 2).requires_grad_()
+    ctx = torch.zeros((0, 16), dtype=torch.float16, device=dev, requires_grad=True)
+    y = m(x, context=ctx)
+    assert torch.equal(y, m.proj_out.bias.data.half().expand(9, 32))
+    y.backward(torch.ones_like(y))
+    assert not x.grad.any() and ctx.grad.shape == (0, 16)
+    assert not m.proj_in.weight.grad.any() and not m.proj_context.weight.grad.any()
