@@ -391,7 +391,10 @@ class AttentionFunction(torch.autograd.Function):
     @staticmethod
     @once_differentiable
     def backward(ctx, grad_out):
-        grads = attention_backward(grad_out.contiguous(), *ctx.saved_tensors, *ctx.how, ctx.needs_input_grad[:3])
+        grad_out = grad_out.contiguous()
+        if grad_out.data_ptr() % 16:  # a piece of a tensor that autograd took apart
+            grad_out = grad_out.clone()
+        grads = attention_backward(grad_out, *ctx.saved_tensors, *ctx.how, ctx.needs_input_grad[:3])
         return (*grads, None, None, None, None, None)
 
 

@@ -89,3 +89,21 @@ def test_attention_over_a_context_without_rows(dev):
     y.backward(torch.ones_like(y))
     assert not x.grad.any() and ctx.grad.shape == (0, 16)
     assert not m.proj_in.weight.grad.any() and not m.proj_context.weight.grad.any()
+
+
+@gpu
+@pytest.mark.parametrize("start", [1, 3, 8])
+def test_attention_gradient_that_starts_anywhere(dev, start):
+    """The gradient of a tensor that was joined with others is a piece of theirs."""
+    sc = _sc()
+    q, k, v = (_randn((50, h, 40), torch.float16, dev, h).requires_grad_() for h in (4, 2, 2))
+    other = torch.zeros(start, dtype=torch.float16, device=dev, requires_grad=True)
+    out = sc.AttentionFunction.apply(q, k, v, None, None, None, True, None)
+    g = _randn((start + out.numel(),), torch.float16, dev, 7)
+    torch.cat([other, out.flatten()]).backward(g)
+    with torch.no_grad():
+        o, lse = sc.attention(q, k, v, causal=True, return_lse=True)
+        want = sc.attention_backward(g[start:].clone().view_as(o), q, k, v, o, lse, causal=True)
+    assert torch.equal(o, out)
+    for t, w in zip((q, k, v), want):
+        assert torch.equal(t.grad, w)
