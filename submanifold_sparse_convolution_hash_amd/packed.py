@@ -440,7 +440,7 @@ class SparseAttention(torch.nn.Module):
         if rotary > dim or rotary and context is not None:
             raise ValueError(f"{rotary} of {dim} columns turn" + (" over a context" if context is not None else ""))
         self.heads, self.kv_heads, self.dim, self.causal, self.interleaved = heads, kv_heads, dim, causal, interleaved
-        self.own, self.axes = context is None, axes
+        self.own, self.rotary, self.axes = context is None, rotary, axes
         if self.own:
             self.proj_in = Linear(channels, (heads + 2 * kv_heads) * dim, device=device, dtype=dtype)
         else:
@@ -453,6 +453,8 @@ class SparseAttention(torch.nn.Module):
         freqs = self.freqs
         super()._apply(fn, recurse)
         if freqs is not None:  # moves with the module, and stays in 64 bits whatever its type
+            if freqs.is_meta and not self.freqs.is_meta:  # it has memory now, but no values
+                freqs = rotary_frequencies(self.rotary, self.axes, device="cpu")
             self.freqs = freqs.to(self.freqs.device)
         return self
 

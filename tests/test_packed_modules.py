@@ -29,3 +29,23 @@ def test_a_context_that_nothing_would_read_is_refused(what):
         sc.SparseAttention(64, 2)(x, **what)
     with pytest.raises(ValueError, match="context"):
         sc.SparseAttentionBlock(64, 32, heads=2, groups=8)(x, **what)
+
+
+def test_made_without_memory_and_given_some_later():
+    """On the meta device first: the frequencies are there after to_empty, in 64 bits,
+    whatever types the module went through."""
+    sc = _sc()
+    want = sc.rotary_frequencies(12, 3)
+    m = sc.SparseAttention(64, 2, rotary=12, device="meta")
+    assert m.freqs.is_meta and m.freqs.dtype == torch.float64
+    m = m.to(torch.bfloat16)
+    assert m.freqs.is_meta and m.freqs.dtype == torch.float64
+    m = m.to_empty(device="cpu")
+    assert m.proj_in.weight.device.type == "cpu" and m.proj_in.weight.dtype == torch.bfloat16
+    assert m.freqs.dtype == torch.float64 and torch.equal(m.freqs, want)
+    m = m.to_empty(device="cpu")  # frequencies that are there stay
+    assert torch.equal(m.freqs, want)
+    with torch.device("meta"):
+        block = sc.SparseAttentionBlock(64, 96, heads=4, groups=8, context=24, rotary=6, axes=1)
+    block = block.to_empty(device="cpu")
+    assert torch.equal(block.attention.freqs, sc.rotary_frequencies(6, 1)) and block.over_context.freqs is None
