@@ -429,12 +429,12 @@ class SparseAttention(torch.nn.Module):
                  interleaved: bool = True, device=None, dtype=torch.float16):
         super().__init__()
         kv_heads = heads if kv_heads is None else kv_heads
+        if heads < 1 or kv_heads < 1 or heads % kv_heads:
+            raise ValueError(f"{heads} query heads do not share {kv_heads} key heads")
         if dim is None:
             if channels % heads:
                 raise ValueError(f"{channels} channels do not make {heads} heads")
             dim = channels // heads
-        if heads < 1 or kv_heads < 1 or heads % kv_heads:
-            raise ValueError(f"{heads} query heads do not share {kv_heads} key heads")
         if dim < 8 or dim > 128 or dim % 8:
             raise ValueError(f"{dim} columns a head: multiples of 8 up to 128 are supported")
         if rotary > dim or rotary and context is not None:

@@ -49,3 +49,9 @@ def test_made_without_memory_and_given_some_later():
         block = sc.SparseAttentionBlock(64, 96, heads=4, groups=8, context=24, rotary=6, axes=1)
     block = block.to_empty(device="cpu")
     assert torch.equal(block.attention.freqs, sc.rotary_frequencies(6, 1)) and block.over_context.freqs is None
+
+
+@pytest.mark.parametrize("kw", [dict(heads=0), dict(heads=-4), dict(heads=0, dim=16), dict(heads=4, kv_heads=0)])
+def test_no_heads_are_refused(kw):
+    with pytest.raises(ValueError):
+        _sc().SparseAttention(64, **kw)
