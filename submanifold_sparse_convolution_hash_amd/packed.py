@@ -29,6 +29,8 @@ __all__ = [
     "attention_backward", "GroupNormFunction", "RotaryFunction", "AttentionFunction", "GroupNorm", "SparseAttention",
 ]
 
+_MOST_ITEMS = 65535
+
 
 def item_offsets(coords: torch.Tensor, batch: Optional[int] = None) -> torch.Tensor:
     """Row offsets [batch + 1] int32 of the items of sites ``coords`` ([N,4] int32
@@ -45,8 +47,12 @@ def item_offsets(coords: torch.Tensor, batch: Optional[int] = None) -> torch.Ten
     n = coords.shape[0]
     if batch is None:
         batch = int(coords[:, 0].max().item()) + 1 if n else 1
-    out = coords.new_empty((max(0, batch) + 2,))
-    _call(coords.device, "submconv_item_offsets", _ptr(coords), coords.stride(0), n, _count(batch, "batch"), _ptr(out),
+    else:
+        batch = _count(batch, "batch")
+    if not 1 <= batch <= _MOST_ITEMS:  # before there is memory for them
+        raise SubmconvError(-1, f"{batch} items, 1 to {_MOST_ITEMS} are supported")
+    out = coords.new_empty((batch + 2,))
+    _call(coords.device, "submconv_item_offsets", _ptr(coords), coords.stride(0), n, batch, _ptr(out),
           out[-1:].data_ptr())
     bad = int(out[-1].item())
     if bad & 1:

@@ -107,3 +107,17 @@ def test_attention_gradient_that_starts_anywhere(dev, start):
     assert torch.equal(o, out)
     for t, w in zip((q, k, v), want):
         assert torch.equal(t.grad, w)
+
+
+@gpu
+@pytest.mark.parametrize("index", [65535, 2 ** 31 - 2, 2 ** 31 - 1])
+def test_item_offsets_allocates_nothing_for_an_index_past_every_batch(dev, index):
+    sc = _sc()
+    coords = torch.zeros((600, 4), dtype=torch.int32, device=dev)
+    coords[599, 0] = index
+    torch.cuda.synchronize()
+    torch.cuda.reset_peak_memory_stats()
+    before = torch.cuda.memory_allocated()
+    with pytest.raises(sc.SubmconvError, match="items"):
+        sc.item_offsets(coords)
+    assert torch.cuda.max_memory_allocated() - before < 1 << 20
