@@ -855,14 +855,21 @@ uint32_t chunk_rows(const GroupShape& s, int elem, const Lanes& g, bool grad) {
 }
 
 // Whether the workgroups of the outputs join their item's chunks themselves, in place
-// of a launch of 5 us: where an item has few on average. Each of them reads 8 bytes a
-// chunk and group, most of it from another die's cache. Forward / backward us, three
-// launches -> two: 20011 x 60 in 12 groups, 7 items (276 parts an item) 16 / 21 -> 13 /
-// 18; 100000 x 96 in 32, 100 items (256) 35 / 50 -> 32 / 44; one item, 100000 x 32 in 8
-// (2000) 17.4 / 21.0 -> 17.7 / 19.7, 1000 x 256 in 32 (4000) 16.0 / 20.6 -> 16.6 / 18.5,
-// 20000 x 320 in 32 (6700) 23 / 33 -> 25 / 35.
+// of a launch of 5 us: where an item has few on average, and would not have too many
+// had one item nearly all rows. Each workgroup reads 8 bytes a chunk and group, most of
+// it from another die's cache. Forward / backward us, three launches -> two, for the parts
+// (chunks times groups) of an item on average and of all items:
+//   20011 x 60 in 12 groups of 7 items, 276 and 1900: 16 / 21 -> 13 / 18; 100000 x 96 in
+//   32 of 100 items, 80 and 4960: 34 / 51 -> 30 / 45; one item, 100000 x 32 in 8, 2000:
+//   17.4 / 21.0 -> 17.7 / 19.7, 1000 x 256 in 32, 4000: 16.0 / 20.6 -> 16.6 / 18.5, 20000 x
+//   320 in 32, 6700: 23 / 33 -> 25 / 35.
+//   16 items, equal ones and one with nearly all rows: 50000 x 96 in 32, 7650: 21.7 / 27.0
+//   -> 18.8 / 25.1 and 21.5 / 28.1 -> 24.5 / 29.1; 100000 x 128 in 32, 15800: 30.8 / 43.2 ->
+//   27.8 / 42.7 and 30.9 / 45.5 -> 46.5 / 48.5; 100000 x 320 in 32, 24000: backward 73 -> 74
+//   and 75 -> 83; of 100 items, 29400: forward 53 -> 58 and 61 -> 131.
 bool joins_itself(const GroupShape& s, uint32_t chunk, bool grad) {
-  return (s.it.n / chunk / s.it.items + 1) * s.G <= (grad ? 4096 : 1024);
+  const int64_t chunks = s.it.n / chunk;
+  return (chunks / s.it.items + 1) * s.G <= (grad ? 4096 : 1024) && (chunks + 1) * s.G <= (grad ? 16384 : 8192);
 }
 
 // A workgroup of the one-launch kernels takes columns of about 128 bytes, whole
