@@ -99,9 +99,9 @@ __device__ __forceinline__ void store_columns(const float16v (&acc)[DB], float f
     }
 }
 
-template <bool BF16, int DP, int NW>
-__global__ __launch_bounds__(NW * 64, NW == 1 ? 1 : 2) void k_attention_dq(Attention a, AttnGrad o) {
-  constexpr int T = 32 * NW, SHIFT = NW == 1 ? 5 : 7;
+template <bool BF16, int DP>
+__global__ __launch_bounds__(256, 2) void k_attention_dq(Attention a, AttnGrad o) {
+  constexpr int NW = 4, T = 32 * NW, SHIFT = 7;
   static_assert(T == 1 << SHIFT, "rows");
   using H = HeadTile<DP>;
   using L = TileLoad<DP, NW>;
@@ -219,7 +219,7 @@ __global__ __launch_bounds__(NW * 64, NW == 1 ? 1 : 2) void k_attention_dq(Atten
 }
 
 // 32 keys a wave, 128 a workgroup; the walk is over the group's query heads and
-// their tiles of 64 queries. Up to 64 columns a wave takes a tile's two blocks of
+// their tiles of 64 queries. Up to 96 columns a wave takes a tile's two blocks of
 // 32 queries in turn. Past that the sums (128 registers at 128 columns) leave room
 // for K but not for V beside them at two waves a SIMD: V stays in LDS, eight waves
 // make a workgroup, two of them share 32 keys and take one block of queries each,
@@ -468,7 +468,7 @@ int attention_backward(const Attention& a, const AttnGrad& g, bool bf16, Arena& 
   auto go = [&](auto b, auto dp) {
     constexpr bool B = decltype(b)::value;
     if (a.qi.n > 0) {
-      k_attention_dq<B, dp, 4><<<static_cast<unsigned>(q_blocks), 256, 0, stream>>>(a, oq);
+      k_attention_dq<B, dp><<<static_cast<unsigned>(q_blocks), 256, 0, stream>>>(a, oq);
       SUBMCONV_HIP_CHECK(hipGetLastError());
     }
     if (keys) {
