@@ -16,8 +16,8 @@
 // second product, as its operands have to be.
 //
 // 8192 rows of 8 heads of 128 bf16 255-268 us, 1030-1080 TFLOP/s; 20011 rows of two
-// items, 12 heads of 64 fp16 760 us, 810; 8192 causal rows of four items, 16 / 4
-// heads of 128 89 us, 830. Bound by the vector units (68 % busy at 64 columns, where
+// items, 12 heads of 64 fp16 734-760 us, 810-840; 8192 causal rows of four items, 16 / 4
+// heads of 128 86-89 us, 830-860. Bound by the vector units (68 % busy at 64 columns, where
 // exp2 takes half of what the matrix units take) and by power: the clock falls to
 // 1.7-1.9 GHz, and zeros in place of random numbers take a quarter less time (a
 // library product of 8192^3 reaches 1240 TFLOP/s here). So what counts is the work
