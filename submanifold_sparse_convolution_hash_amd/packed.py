@@ -255,6 +255,7 @@ def rotary(x: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor, interl
         out, ldo, ho = x.new_empty((n, h, d)), h * d, d
     else:
         ldo, ho = _heads(out, "out", (x.dtype,), x)
+        torch.autograd.graph.increment_version(out)  # a change in place, for autograd's checks
     _call(dev, "submconv_rotary", _ptr(x), ldx, hx, n, h, d, _ptr(positions), positions.stride(0), ap, axes,
           _ptr(freqs), f, int(bool(interleaved)), int(bool(inverse)), amplitude, _ptr(out), ldo, ho,
           _NORM_DTYPES[x.dtype])

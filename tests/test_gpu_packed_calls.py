@@ -121,3 +121,62 @@ def test_item_offsets_allocates_nothing_for_an_index_past_every_batch(dev, index
     with pytest.raises(sc.SubmconvError, match="items"):
         sc.item_offsets(coords)
     assert torch.cuda.max_memory_allocated() - before < 1 << 20
+
+
+@gpu
+def test_rotary_in_place_is_seen_by_autograd(dev):
+    """A tensor that a recorded operation keeps for its gradient is turned in place:
+    the backward pass refuses it, as after any change in place."""
+    sc = _sc()
+    at, f = torch.arange(9, dtype=torch.int32, device=dev), sc.rotary_frequencies(32, device=dev)
+    x = _randn((9, 2, 32), torch.float32, dev, 1)
+    w = torch.ones_like(x, requires_grad=True)
+    y = (x * w).sum()
+    sc.rotary(x, at, f)  # elsewhere: x is as it was
+    y.backward(retain_graph=True)
+    sc.rotary(x, at, f, out=x)
+    with pytest.raises(RuntimeError, match="inplace"):
+        y.backward()
+    with torch.inference_mode():  # tensors without a version
+        z = x.clone()
+        assert sc.rotary(z, at, f, out=z) is z
+
+
+@gpu
+@pytest.mark.parametrize("rows", [3, 40])
+def test_most_items(dev, rows):
+    """65535 items, as many as there may be, of one length, the last of them without
+    rows: the same as a batch of matrices in fp64."""
+    sc = _sc()
+    items, h, d = 65535, 2, 16
+    n = (items - 1) * rows
+    off = (torch.arange(items + 1, device=dev).clamp(max=items - 1) * rows).to(torch.int32)
+    x = _randn((n, h * d), torch.float32, dev, rows)
+    w, b = (_randn((h * d,), torch.float32, dev, s) for s in (1, 2))
+    y, mean, rstd = sc.group_norm(x, 4, w, b, offsets=off, return_stats=True)
+    t = x.double().view(items - 1, rows, 4, -1)
+    m, v = t.mean((1, 3), keepdim=True), t.var((1, 3), keepdim=True, correction=0)
+    xh = (t - m) * (v + 1e-5).rsqrt()
+    # a few roundings of values below 8, and of a deviation that may be small
+    e = 2.0 ** -24 * 64 * (1 + (v + 1e-5).rsqrt())
+    bound = (e * 8 * w.abs().double().view(4, -1) + 2.0 ** -20 * (1 + b.abs().double().view(4, -1))).expand_as(t)
+    assert ((y.double().view_as(t) - (xh * w.double().view(4, -1) + b.double().view(4, -1))).abs() <= bound).all()
+    assert mean[-1].eq(0).all() and (mean[:-1].double() - m[:, 0, :, 0]).abs().max().item() <= 2.0 ** -24 * 64 * 8
+    g = _randn((n, h * d), torch.float32, dev, 5)
+    _, gw, gb = sc.group_norm_backward(g, x, mean, rstd, w, b, offsets=off)
+    gd = g.double()
+    terms = gd * xh.flatten(2).reshape(n, -1)
+    # sums in parts: some hundreds of steps, 2^-24 of the sum of sizes each
+    assert ((gb.double() - gd.sum(0)).abs() <= 2.0 ** -24 * 2000 * gd.abs().sum(0)).all()
+    assert ((gw.double() - terms.sum(0)).abs() <= 2.0 ** -24 * 2000 * (gd.abs() * 8).sum(0)).all()
+    q = x.half().view(n, h, d)
+    out, lse = sc.attention(q, q, q, off, causal=True, return_lse=True)
+    p = q.double().view(items - 1, rows, h, d).transpose(1, 2)
+    s = p @ p.transpose(2, 3).contiguous() * d ** -0.5
+    s = s.masked_fill(torch.ones((rows, rows), dtype=torch.bool, device=dev).triu(1), float("-inf"))
+    want = torch.softmax(s, 3) @ p
+    size = torch.softmax(s, 3) @ p.abs()
+    err = (out.double().view(items - 1, rows, h, d).transpose(1, 2) - want).abs()
+    # a weight's rounding, its score's and the sums', the stored value's
+    assert (err <= 2.0 ** -11 * size + 2.0 ** -15 * size + 2.0 ** -11 * want.abs() + 2.0 ** -24).all()
+    assert (lse.double().view(items - 1, rows, h).transpose(1, 2) - s.logsumexp(3)).abs().max().item() <= 2.0 ** -16
