@@ -47,8 +47,9 @@ struct AttnOut {
 // passes it by this many powers of two: weights stay below 2^8, which bf16
 // holds as exactly as any other, and the sums' 32 bits have room. In fp16 they are
 // taken times 2^7, up to 2^15 of its range, so that small ones beside a large one
-// keep their digits: a weight loses at most 2^-32 of the row's largest (2^-25
-// without, which 10^5 keys 17 below one of a small value lost altogether).
+// keep their digits: a weight loses at most 2^-32 of the row's largest. (As they
+// are it is 2^-25: beside one key of value 0 whose score leads by 17, the output of
+// all others was 0.)
 constexpr float kSlack = 8.0f;
 template <bool BF16>
 constexpr float kUp = BF16 ? 0.0f : 7.0f;
